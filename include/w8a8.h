@@ -576,6 +576,127 @@ w8a8_status w8a8_probe_dp4a_rate(int64_t iters, int64_t *macs_out, w8a8_stream_t
 /* Library version: major * 10000 + minor * 100 + patch. */
 int w8a8_version(void);
 
+/* ---------------------------------------------------------------------------
+ * The router's gate: expert ids and weights, as w8a8_moe_ffn takes them, from
+ * the router's logits ("each token goes to the experts its router picked",
+ * Hunyuan-770B page §1.3).
+ *   logits [T, ld] FP32 or BF16 (logits_dtype; the first E columns);
+ *   bias   [E] float or NULL: added to the scores for the choice, not to the
+ *          weights (balance between experts);
+ *   ids    [T, k] int32, w [T, k] float.
+ * Scores are s = softmax(x) over the E experts or s = 1 / (1 + e^-x); the keys
+ * are s + bias. The E experts form n_group equal runs; the topk_group groups
+ * with the largest score stay, a group's score being its largest key or, with
+ * a bias, the sum of its two largest. Of their experts the k largest keys are
+ * picked, largest first; equal keys (groups) in the order of their index.
+ * Without a bias keys are compared by the logits (the order of the scores).
+ * The weights are the picked scores, divided by their sum when renormalize is
+ * set, times scale.
+ * A logit of -inf or NaN marks an expert that is never picked; a token with
+ * fewer than k experts to pick has id -1 and weight 0 in its last places
+ * (w8a8_moe_route does not route those). +inf counts as the largest finite
+ * number. Choices are exact: two keys that 32-bit arithmetic cannot tell apart
+ * are compared in 64 bits.
+ * 1 <= E <= 1024, 1 <= n_group <= 64 dividing E, 1 <= topk_group <= n_group,
+ * 1 <= k <= 64 and k <= topk_group * E / n_group, ld >= E. T == 0 is a no-op.
+ */
+typedef enum { W8A8_GATE_SOFTMAX = 0, W8A8_GATE_SIGMOID = 1 } w8a8_gate_score;
+
+w8a8_status w8a8_moe_gate(const void *logits, w8a8_dtype logits_dtype, int64_t ld, int64_t T,
+                          int64_t E, int64_t k, w8a8_gate_score score, const float *bias,
+                          int64_t n_group, int64_t topk_group, int renormalize, float scale,
+                          int32_t *ids, float *w, w8a8_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The paged KV cache. The cache of a layer is a pool of P pages,
+ *   [P, Hkv, page, 128]  INT8 codes with one float scale per vector
+ *                        [P, Hkv, page], or BF16 values, for K and for V;
+ * row b of block_table [B, W] names the pages that hold request b's positions
+ * in order (position p: page block_table[b, p / page], offset p % page). The
+ * slot of a position is its page * page + its offset.
+ *
+ * Brings the block tables of B requests from the lengths they hold to the
+ * lengths asked for, and places the new tokens. On the device; one call serves
+ * every layer.
+ *   block_table [B, W]  in/out: the first ceil(lens / page) entries of a row
+ *                       are its pages; entries given back become -1;
+ *   lens        [B]     in/out: positions held;
+ *   target      [B]     positions asked for: more (the request brings target -
+ *                       lens new tokens), fewer (a rejected guess; 0: it
+ *                       leaves) or as many;
+ *   free_pages  [P], n_free [1]  in/out: the stack of free pages, the first
+ *                       n_free entries of the array, the last one on top;
+ *   cu_new      [B + 1] out: new tokens asked for by the requests before b;
+ *   kv_lens     [B]     out: target, or 0 for a request that is refused;
+ *   slots, positions [n_tokens] out: of each new token, in request order; -1
+ *                       for those of refused requests and past cu_new[B].
+ * Pages are given back first, in request order and by rising index, then
+ * taken, in request order. A request that needs pages is refused, and keeps
+ * its lens and pages, when it and those before it need more than there are, when
+ * its target does not fit its row, or when its tokens end past n_tokens; one
+ * whose lens or target is negative, or whose lens does not fit its row, too.
+ * Entries of free_pages at and past n_free are left as they are.
+ * 0 <= B <= 4096, W >= 1, P >= 1, page >= 1, n_tokens >= 0, W * page and
+ * P * page below 2^31.
+ */
+w8a8_status w8a8_paged_kv_plan(int32_t *block_table, int32_t *lens, const int32_t *target,
+                               int32_t *free_pages, int32_t *n_free, int64_t B, int64_t W,
+                               int64_t P, int64_t page, int64_t n_tokens, int32_t *cu_new,
+                               int32_t *kv_lens, int32_t *slots, int32_t *positions,
+                               w8a8_stream_t stream);
+
+/*
+ * Writes the new tokens' K and V vectors into their slots (page §3.4: every
+ * key and value vector gets its own scale when it is written).
+ *   k, v [T, Hkv, 128] BF16 with the given strides in elements (parts of one
+ *        projection's rows may be given as they are);
+ *   slots [T]: a token whose slot is outside [0, P * page) is not written.
+ * INT8 pages: k_cache, v_cache int8 and both scales given; codes and scales as
+ * w8a8_quant_act would make them of each vector. BF16 pages: both scales NULL.
+ * Two tokens of one call must not share a slot. Inputs must be finite.
+ * Pointers to k, v and the caches 16-byte aligned, strides multiples of 8;
+ * P * Hkv * page < 2^31, page >= 1, Hkv <= 65535. T == 0 is a no-op.
+ */
+w8a8_status w8a8_paged_kv_write(const void *k_bf16, int64_t k_token_stride, int64_t k_head_stride,
+                                const void *v_bf16, int64_t v_token_stride, int64_t v_head_stride,
+                                const int32_t *slots, int64_t T, int64_t Hkv, int64_t head_dim,
+                                int64_t P, int64_t page, void *k_cache, float *k_scale,
+                                void *v_cache, float *v_scale, w8a8_stream_t stream);
+
+/*
+ * Attention of each request's new tokens over its pages: prompts, chunks of
+ * prompts over what is cached of them, guessed tokens and single tokens, in
+ * one call. The new tokens' own K and V have been written.
+ *   q        [T, Hq, 128] BF16 with the given strides in elements;
+ *   kv_lens  [B] positions, the new tokens' included; cu_new [B + 1]: request
+ *            b's new tokens are rows cu_new[b] .. cu_new[b + 1] - 1 of q;
+ *   out      [T, Hq, 128] BF16 or FP32.
+ * Token i of a request's n stands at position p = kv_len - n + i and sees the
+ * keys of positions max(0, p - window + 1) .. p (window 0: from 0). Query
+ * head h uses kv head h / (Hq / Hkv). A token that sees nothing (p < 0), and
+ * rows of q that belong to no request, get zeros. Nothing outside the
+ * positions that some new token sees is read; what those hold must be finite.
+ * A table entry outside [0, P) there reads as absent: its positions are masked,
+ * and w8a8_device_error() tells of it. A length past W * page is cut to it.
+ * Sums and softmax statistics are FP32. Up to 16 query rows per item the
+ * probabilities keep 22 (BF16 pages: 24) bits, as in the contiguous-cache
+ * calls.
+ * Pointers to q, out, the caches and the scales 16-byte aligned, strides
+ * multiples of 8; Hq a multiple of Hkv, Hq / Hkv <= 16; page a multiple of 8;
+ * P * Hkv * page, W * page and T below 2^31; workspace 16-byte aligned.
+ * T == 0 is a no-op; B >= 1.
+ */
+size_t w8a8_attention_paged_workspace_size(int64_t T, int64_t B, int64_t Hq, int64_t Hkv);
+
+w8a8_status w8a8_attention_paged(const void *q_bf16, int64_t q_token_stride, int64_t q_head_stride,
+                                 const void *k_cache, const float *k_scale, const void *v_cache,
+                                 const float *v_scale, const int32_t *block_table,
+                                 const int32_t *kv_lens, const int32_t *cu_new, int64_t T,
+                                 int64_t B, int64_t W, int64_t Hq, int64_t Hkv, int64_t head_dim,
+                                 int64_t P, int64_t page, float softmax_scale, int64_t window,
+                                 void *out, w8a8_dtype out_dtype, void *workspace,
+                                 size_t workspace_bytes, w8a8_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

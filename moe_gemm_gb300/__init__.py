@@ -10,6 +10,8 @@ Functions (names match the C entry points):
   quant_weight(w_f32)                     -> (qw int8 [N,K], sw f32 [N,K/128])
   gemm(qa, sa, qw, sw, out_dtype, ...)    -> y [M,N]  (+ partials when debug)
   grouped_gemm(qa, sa, offsets, qw, sw, out_dtype, ...) -> y [R,N]
+Serving: moe_gate (expert ids and weights for moe_ffn), and the paged KV cache:
+paged_kv_plan (block tables and slots), paged_kv_write, attention_paged.
 """
 from __future__ import annotations
 
@@ -95,6 +97,17 @@ def _load() -> ctypes.CDLL:
     lib.w8a8_rmsnorm_quant.argtypes = [vp, i64, vp, ctypes.c_float, i32, i64, i64, vp, i64, vp, vp]
     lib.w8a8_rmsnorm_linear.argtypes = [vp, i64, vp, ctypes.c_float, vp, vp, vp, i32, i64, i64,
                                         i64, vp, ctypes.c_size_t, vp]
+    lib.w8a8_moe_gate.argtypes = [vp, i32, i64, i64, i64, i64, i32, vp, i64, i64, i32,
+                                  ctypes.c_float, vp, vp, vp]
+    lib.w8a8_paged_kv_plan.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, vp, vp, vp, vp,
+                                       vp]
+    lib.w8a8_paged_kv_write.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, i64, i64, i64, i64,
+                                        vp, vp, vp, vp, vp]
+    lib.w8a8_attention_paged_workspace_size.argtypes = [i64, i64, i64, i64]
+    lib.w8a8_attention_paged_workspace_size.restype = ctypes.c_size_t
+    lib.w8a8_attention_paged.argtypes = [vp, i64, i64, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64,
+                                         i64, i64, i64, i64, i64, ctypes.c_float, i64, vp, i32, vp,
+                                         ctypes.c_size_t, vp]
     lib.w8a8_version.restype = i32
     for name in ("w8a8_quant_act", "w8a8_quant_weight", "w8a8_gemm", "w8a8_grouped_gemm",
                  "w8a8_gemm_noalloc", "w8a8_device_error", "w8a8_selftest_wait_timeout",
@@ -105,7 +118,8 @@ def _load() -> ctypes.CDLL:
                  "w8a8_grouped_gemm_ex", "w8a8_linear_ex", "w8a8_w8a16_gemm",
                  "w8a8_w8a16_grouped_gemm", "w8a8_kv_quant", "w8a8_attention_decode_int8kv",
                  "w8a8_attention_decode_bf16kv", "w8a8_rmsnorm", "w8a8_rmsnorm_quant",
-                 "w8a8_rmsnorm_linear"):
+                 "w8a8_rmsnorm_linear", "w8a8_moe_gate", "w8a8_paged_kv_plan",
+                 "w8a8_paged_kv_write", "w8a8_attention_paged"):
         getattr(lib, name).restype = i32
     return lib
 
@@ -167,6 +181,16 @@ def _on_device(device: torch.device, stream: Optional[torch.cuda.Stream]):
     if stream is not None and stream.device != device:
         raise ValueError(f"stream belongs to {stream.device}, the operands to {device}")
     return torch.cuda.device(device)
+
+
+def _empty(shape, dtype: torch.dtype, device: torch.device,
+           stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """An uninitialised tensor whose memory belongs to the stream that the call
+    runs on: the allocator may hand it out again only in that stream's order."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def quant_act(a: torch.Tensor, qa: Optional[torch.Tensor] = None,
@@ -653,7 +677,173 @@ def attention_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     return out
 
 
+# ------------------------------------------- paged KV cache and its attention
+def paged_kv_plan(block_table: torch.Tensor, lens: torch.Tensor, target: torch.Tensor,
+                  free_pages: torch.Tensor, n_free: torch.Tensor, page_size: int, n_tokens: int,
+                  stream: Optional[torch.cuda.Stream] = None
+                  ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Brings the block tables [B, W] from the lengths they hold, lens [B], to
+    those asked for, target [B]: pages of requests that shrink go back to the
+    stack free_pages [P] (its first n_free [1] entries), requests that grow take
+    theirs off it; block_table, lens, free_pages and n_free are updated in place
+    (all int32). n_tokens: the new tokens of the call, as packed by the caller.
+    Returns (cu_new [B + 1], kv_lens [B], slots [n_tokens], positions
+    [n_tokens]); a request that cannot get its pages keeps what it holds and has
+    kv_lens 0 and slots -1."""
+    _require(block_table, torch.int32, "block_table", 2)
+    dev = block_table.device
+    B, W = block_table.shape
+    _require(lens, torch.int32, "lens", 1, (B,), dev)
+    _require(target, torch.int32, "target", 1, (B,), dev)
+    _require(free_pages, torch.int32, "free_pages", 1, device=dev)
+    _require(n_free, torch.int32, "n_free", 1, (1,), dev)
+    out = _empty((2 * B + 1 + 2 * max(n_tokens, 0),), torch.int32, dev, stream)
+    cu_new, kv_lens = out[:B + 1], out[B + 1:2 * B + 1]
+    slots, positions = out[2 * B + 1:2 * B + 1 + n_tokens], out[2 * B + 1 + n_tokens:]
+    with _on_device(dev, stream):
+        _check(_lib.w8a8_paged_kv_plan(
+            _ptr(block_table), _ptr(lens), _ptr(target), _ptr(free_pages), _ptr(n_free), B, W,
+            free_pages.numel(), page_size, n_tokens, _ptr(cu_new), _ptr(kv_lens), _ptr(slots),
+            _ptr(positions), _stream(stream)), "w8a8_paged_kv_plan")
+    return cu_new, kv_lens, slots, positions
+
+
+def _require_heads(x: torch.Tensor, name: str, device: Optional[torch.device] = None) -> None:
+    if (not x.is_cuda or x.dtype != torch.bfloat16 or x.dim() != 3 or x.shape[2] != HEAD_DIM
+            or x.stride(2) != 1 or (device is not None and x.device != device)):
+        raise ValueError(f"{name}: expected a CUDA bf16 [T, heads, {HEAD_DIM}] tensor with unit "
+                         f"stride in the last dimension")
+
+
+def _require_pages(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: Optional[torch.Tensor],
+                   v_scale: Optional[torch.Tensor], device: torch.device):
+    """Checks a paged cache; returns (P, Hkv, page)."""
+    if k_cache.dtype not in (torch.int8, torch.bfloat16):
+        raise ValueError("k_cache: expected int8 or bf16 pages")
+    _require(k_cache, k_cache.dtype, "k_cache", 4, device=device)
+    P, Hkv, page, d = k_cache.shape
+    if d != HEAD_DIM:
+        raise ValueError(f"k_cache must be [P, Hkv, page, {HEAD_DIM}]")
+    _require(v_cache, k_cache.dtype, "v_cache", 4, tuple(k_cache.shape), device)
+    if k_cache.dtype == torch.int8:
+        if k_scale is None or v_scale is None:
+            raise ValueError("INT8 pages need k_scale and v_scale")
+        _require(k_scale, torch.float32, "k_scale", 3, (P, Hkv, page), device)
+        _require(v_scale, torch.float32, "v_scale", 3, (P, Hkv, page), device)
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("BF16 pages take no scales")
+    return P, Hkv, page
+
+
+def paged_kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
+                   v_cache: torch.Tensor, k_scale: Optional[torch.Tensor] = None,
+                   v_scale: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Writes K and V vectors k, v [T, Hkv, 128] (BF16; views of a fused
+    projection's rows are taken as they are) into slots [T] of the pages
+    k_cache, v_cache [P, Hkv, page, 128]: INT8 with one scale per vector in
+    k_scale, v_scale [P, Hkv, page], or BF16. Tokens with slot -1 are skipped."""
+    _require_heads(k, "k")
+    dev = k.device
+    _require_heads(v, "v", dev)
+    T, Hkv, d = k.shape
+    if v.shape != k.shape:
+        raise ValueError(f"v: expected shape {tuple(k.shape)}, got {tuple(v.shape)}")
+    P, heads, page = _require_pages(k_cache, v_cache, k_scale, v_scale, dev)
+    if heads != Hkv:
+        raise ValueError(f"the cache has {heads} kv heads, k has {Hkv}")
+    _require(slots, torch.int32, "slots", 1, (T,), dev)
+    with _on_device(dev, stream):
+        _check(_lib.w8a8_paged_kv_write(
+            _ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0), v.stride(1), _ptr(slots), T,
+            Hkv, d, P, page, _ptr(k_cache), _ptr(k_scale), _ptr(v_cache), _ptr(v_scale),
+            _stream(stream)), "w8a8_paged_kv_write")
+
+
+def attention_paged_workspace_size(T: int, B: int, Hq: int, Hkv: int) -> int:
+    return int(_lib.w8a8_attention_paged_workspace_size(T, B, Hq, Hkv))
+
+
+def attention_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    block_table: torch.Tensor, kv_lens: torch.Tensor, cu_new: torch.Tensor,
+                    softmax_scale: float, k_scale: Optional[torch.Tensor] = None,
+                    v_scale: Optional[torch.Tensor] = None, window: int = 0,
+                    out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Causal attention of each request's new tokens, rows cu_new[b] ..
+    cu_new[b + 1] - 1 of q [T, Hq, 128] (BF16), over its kv_lens[b] positions
+    (the new tokens' included) in the pages that block_table [B, W] names; with
+    a window, over the last `window` positions. Single tokens, guessed tokens,
+    chunks and whole prompts may be mixed. INT8 pages with k_scale, v_scale, or
+    BF16 pages without."""
+    _require_heads(q, "q")
+    dev = q.device
+    T, Hq, d = q.shape
+    P, Hkv, page = _require_pages(k_cache, v_cache, k_scale, v_scale, dev)
+    _require(block_table, torch.int32, "block_table", 2, device=dev)
+    B, W = block_table.shape
+    _require(kv_lens, torch.int32, "kv_lens", 1, (B,), dev)
+    _require(cu_new, torch.int32, "cu_new", 1, (B + 1,), dev)
+    code = _dtype_code(out_dtype)
+    if out is None:
+        out = _empty((T, Hq, d), out_dtype, dev, stream)
+    else:
+        _require(out, out_dtype, "out", 3, (T, Hq, d), dev)
+    if workspace is None:
+        workspace = _empty((max(attention_paged_workspace_size(T, B, Hq, Hkv), 1),),
+                           torch.uint8, dev, stream)
+    else:
+        _require_workspace(workspace, dev)
+    with _on_device(dev, stream):
+        _check(_lib.w8a8_attention_paged(
+            _ptr(q), q.stride(0), q.stride(1), _ptr(k_cache), _ptr(k_scale), _ptr(v_cache),
+            _ptr(v_scale), _ptr(block_table), _ptr(kv_lens), _ptr(cu_new), T, B, W, Hq, Hkv, d, P,
+            page, float(softmax_scale), window, _ptr(out), code, _ptr(workspace),
+            workspace.numel(), _stream(stream)), "w8a8_attention_paged")
+    return out
+
+
 # ------------------------------------------------------------ MoE expert FFN
+GATE_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def moe_gate(logits: torch.Tensor, k: int, scoring: str = "softmax",
+             bias: Optional[torch.Tensor] = None, n_group: int = 1, topk_group: int = 1,
+             renormalize: bool = True, scale: float = 1.0,
+             topk_ids: Optional[torch.Tensor] = None, topk_w: Optional[torch.Tensor] = None,
+             stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The router's choice: (topk_ids int32 [T, k], topk_w float32 [T, k]), as
+    moe_ffn takes them, from logits [T, E] (FP32 or BF16). Scores are
+    softmax(logits) or the sigmoid; the k largest of scores + bias among the
+    topk_group best of n_group expert groups are picked, and weighted by their
+    scores (over their sum with renormalize), times scale."""
+    if (not logits.is_cuda or logits.dtype not in (torch.float32, torch.bfloat16)
+            or logits.dim() != 2 or logits.stride(1) != 1):
+        raise ValueError("logits: expected a CUDA fp32 or bf16 [T, E] tensor with unit column "
+                         "stride")
+    if scoring not in GATE_SCORES:
+        raise ValueError(f"scoring: one of {sorted(GATE_SCORES)}")
+    dev = logits.device
+    T, E = logits.shape
+    if bias is not None:
+        _require(bias, torch.float32, "bias", 1, (E,), dev)
+    if topk_ids is None:
+        topk_ids = _empty((T, k), torch.int32, dev, stream)
+    else:
+        _require(topk_ids, torch.int32, "topk_ids", 2, (T, k), dev)
+    if topk_w is None:
+        topk_w = _empty((T, k), torch.float32, dev, stream)
+    else:
+        _require(topk_w, torch.float32, "topk_w", 2, (T, k), dev)
+    with _on_device(dev, stream):
+        _check(_lib.w8a8_moe_gate(
+            _ptr(logits), _dtype_code(logits.dtype), logits.stride(0), T, E, k,
+            GATE_SCORES[scoring], _ptr(bias), n_group, topk_group, int(renormalize), float(scale),
+            _ptr(topk_ids), _ptr(topk_w), _stream(stream)), "w8a8_moe_gate")
+    return topk_ids, topk_w
+
+
 def moe_route(topk_ids: torch.Tensor, E: int, stream: Optional[torch.cuda.Stream] = None):
     """Routing of topk_ids [T, k] (int32): returns (offsets [E+1], row_of
     [T*k], token_of_row [T*k], pair_of_row [T*k]), all int32 on the device."""

@@ -5,6 +5,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 #include <mutex>
 
 #include "../../include/w8a8.h"
@@ -674,6 +675,186 @@ w8a8_status w8a8_attention_decode_bf16kv(const void *q_bf16, const void *k_cache
     return run_attention(q_bf16, k_cache, nullptr, v_cache, nullptr, lens, B, Hq, Hkv, S_max,
                          head_dim, softmax_scale, out, out_dtype, workspace, workspace_bytes,
                          false, stream);
+}
+
+w8a8_status w8a8_moe_gate(const void *logits, w8a8_dtype logits_dtype, int64_t ld, int64_t T,
+                          int64_t E, int64_t k, w8a8_gate_score score, const float *bias,
+                          int64_t n_group, int64_t topk_group, int renormalize, float scale,
+                          int32_t *ids, float *w, w8a8_stream_t stream) {
+    if (logits_dtype != W8A8_BF16 && logits_dtype != W8A8_FP32) return W8A8_ERR_INVALID_ARG;
+    if (score != W8A8_GATE_SOFTMAX && score != W8A8_GATE_SIGMOID) return W8A8_ERR_INVALID_ARG;
+    if (T < 0 || E < 1 || E > w8a8::kMaxExperts || n_group < 1 ||
+        n_group > w8a8::kGateMaxGroups || E % n_group != 0 || topk_group < 1 ||
+        topk_group > n_group || k < 1 || k > w8a8::kMoeMaxTopK || k > topk_group * (E / n_group) ||
+        ld < E || !std::isfinite(scale))
+        return W8A8_ERR_INVALID_ARG;
+    if (T > kMaxElems / ld || T > kMaxElems / k) return W8A8_ERR_INVALID_ARG;
+    if (T == 0) return W8A8_OK;
+    if (!logits || !ids || !w || !aligned(logits, logits_dtype == W8A8_FP32 ? 4 : 2) ||
+        !aligned(bias, 4) || !aligned(ids, 4) || !aligned(w, 4))
+        return W8A8_ERR_INVALID_ARG;
+    w8a8::DeviceInfo info;
+    w8a8_status st = check_device(&info);
+    if (st != W8A8_OK) return st;
+    w8a8::GateProblem p;
+    p.logits = logits;
+    p.fp32 = logits_dtype == W8A8_FP32;
+    p.ldx = ld;
+    p.T = T;
+    p.E = E;
+    p.k = k;
+    p.n_group = n_group;
+    p.topk_group = topk_group;
+    p.bias = bias;
+    p.sigmoid = score == W8A8_GATE_SIGMOID;
+    p.renormalize = renormalize != 0;
+    p.scale = scale;
+    p.ids = ids;
+    p.w = w;
+    return from_cuda(w8a8::launch_moe_gate(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+w8a8_status w8a8_paged_kv_plan(int32_t *block_table, int32_t *lens, const int32_t *target,
+                               int32_t *free_pages, int32_t *n_free, int64_t B, int64_t W,
+                               int64_t P, int64_t page, int64_t n_tokens, int32_t *cu_new,
+                               int32_t *kv_lens, int32_t *slots, int32_t *positions,
+                               w8a8_stream_t stream) {
+    if (B < 0 || B > w8a8::kPagedMaxRequests || W < 1 || P < 1 || page < 1 || n_tokens < 0 ||
+        n_tokens > kMaxElems || W > kMaxElems / page || P > kMaxElems / page)
+        return W8A8_ERR_INVALID_ARG;
+    if (!free_pages || !n_free || !cu_new ||
+        (B > 0 && (!block_table || !lens || !target || !kv_lens)) ||
+        (n_tokens > 0 && (!slots || !positions)))
+        return W8A8_ERR_INVALID_ARG;
+    for (const void *q : {static_cast<const void *>(block_table), static_cast<const void *>(lens),
+                          static_cast<const void *>(target), static_cast<const void *>(free_pages),
+                          static_cast<const void *>(n_free), static_cast<const void *>(cu_new),
+                          static_cast<const void *>(kv_lens), static_cast<const void *>(slots),
+                          static_cast<const void *>(positions)})
+        if (!aligned(q, 4)) return W8A8_ERR_INVALID_ARG;
+    w8a8::DeviceInfo info;
+    w8a8_status st = check_device(&info);
+    if (st != W8A8_OK) return st;
+    w8a8::PagedPlanProblem p;
+    p.block_table = block_table;
+    p.lens = lens;
+    p.target = target;
+    p.free_pages = free_pages;
+    p.n_free = n_free;
+    p.B = B;
+    p.W = W;
+    p.P = P;
+    p.page = page;
+    p.n_tokens = n_tokens;
+    p.cu_new = cu_new;
+    p.kv_lens = kv_lens;
+    p.slots = slots;
+    p.positions = positions;
+    return from_cuda(w8a8::launch_paged_kv_plan(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+w8a8_status w8a8_paged_kv_write(const void *k_bf16, int64_t k_token_stride, int64_t k_head_stride,
+                                const void *v_bf16, int64_t v_token_stride, int64_t v_head_stride,
+                                const int32_t *slots, int64_t T, int64_t Hkv, int64_t head_dim,
+                                int64_t P, int64_t page, void *k_cache, float *k_scale,
+                                void *v_cache, float *v_scale, w8a8_stream_t stream) {
+    if (T < 0 || Hkv < 1 || Hkv > 65535 || head_dim != w8a8::kAttnHeadDim || P < 1 || page < 1 ||
+        P > kMaxElems / page || P * page > kMaxElems / Hkv || T > kMaxElems / Hkv)
+        return W8A8_ERR_INVALID_ARG;
+    for (const int64_t s : {k_token_stride, k_head_stride, v_token_stride, v_head_stride})
+        if (s < 0 || s % 8 != 0 || s > kMaxElems) return W8A8_ERR_INVALID_ARG;
+    if ((k_scale == nullptr) != (v_scale == nullptr)) return W8A8_ERR_INVALID_ARG;
+    if (T == 0) return W8A8_OK;
+    if (!k_bf16 || !v_bf16 || !slots || !k_cache || !v_cache || !aligned(k_bf16, 16) ||
+        !aligned(v_bf16, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !aligned(slots, 4) || !aligned(k_scale, 4) || !aligned(v_scale, 4))
+        return W8A8_ERR_INVALID_ARG;
+    w8a8::DeviceInfo info;
+    w8a8_status st = check_device(&info);
+    if (st != W8A8_OK) return st;
+    w8a8::PagedWriteProblem p;
+    p.k = static_cast<const uint16_t *>(k_bf16);
+    p.v = static_cast<const uint16_t *>(v_bf16);
+    p.kt = k_token_stride;
+    p.kh = k_head_stride;
+    p.vt = v_token_stride;
+    p.vh = v_head_stride;
+    p.slots = slots;
+    p.T = T;
+    p.Hkv = Hkv;
+    p.P = P;
+    p.page = page;
+    p.int8 = k_scale != nullptr;
+    p.kc = k_cache;
+    p.vc = v_cache;
+    p.ks = k_scale;
+    p.vs = v_scale;
+    return from_cuda(w8a8::launch_paged_kv_write(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t w8a8_attention_paged_workspace_size(int64_t T, int64_t B, int64_t Hq, int64_t Hkv) {
+    if (T <= 0 || B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return 0;
+    return w8a8::paged_attn_workspace_bytes(T, B, Hq, Hkv);
+}
+
+w8a8_status w8a8_attention_paged(const void *q_bf16, int64_t q_token_stride, int64_t q_head_stride,
+                                 const void *k_cache, const float *k_scale, const void *v_cache,
+                                 const float *v_scale, const int32_t *block_table,
+                                 const int32_t *kv_lens, const int32_t *cu_new, int64_t T,
+                                 int64_t B, int64_t W, int64_t Hq, int64_t Hkv, int64_t head_dim,
+                                 int64_t P, int64_t page, float softmax_scale, int64_t window,
+                                 void *out, w8a8_dtype out_dtype, void *workspace,
+                                 size_t workspace_bytes, w8a8_stream_t stream) {
+    if (out_dtype != W8A8_BF16 && out_dtype != W8A8_FP32) return W8A8_ERR_INVALID_ARG;
+    if (T < 0 || B < 1 || B > 65535 || W < 1 || Hq < 1 || Hkv < 1 || Hkv > 65535 ||
+        Hq % Hkv != 0 || Hq / Hkv > w8a8::kPagedMaxGroup || head_dim != w8a8::kAttnHeadDim ||
+        P < 1 || page < 8 || page % 8 != 0 || window < 0 || !(softmax_scale > 0.0f) ||
+        !std::isfinite(softmax_scale))
+        return W8A8_ERR_INVALID_ARG;
+    // positions, rows of the cache and tokens are 32-bit (a tile past the last
+    // position included); byte offsets are 64-bit
+    if (T > kMaxElems / Hq || W > (kMaxElems - 256) / page || P > kMaxElems / page ||
+        P * page > kMaxElems / Hkv || window > kMaxElems)
+        return W8A8_ERR_INVALID_ARG;
+    for (const int64_t s : {q_token_stride, q_head_stride})
+        if (s < 0 || s % 8 != 0 || s > kMaxElems) return W8A8_ERR_INVALID_ARG;
+    if ((k_scale == nullptr) != (v_scale == nullptr)) return W8A8_ERR_INVALID_ARG;
+    if (T == 0) return W8A8_OK;
+    if (!q_bf16 || !k_cache || !v_cache || !block_table || !kv_lens || !cu_new || !out ||
+        !aligned(q_bf16, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !aligned(k_scale, 16) || !aligned(v_scale, 16) || !aligned(out, 16) ||
+        !aligned(block_table, 4) || !aligned(kv_lens, 4) || !aligned(cu_new, 4))
+        return W8A8_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 16) ||
+        workspace_bytes < w8a8::paged_attn_workspace_bytes(T, B, Hq, Hkv))
+        return W8A8_ERR_WORKSPACE;
+    w8a8::DeviceInfo info;
+    w8a8_status st = check_device(&info);
+    if (st != W8A8_OK) return st;
+    w8a8::PagedAttnProblem p;
+    p.q = static_cast<const uint16_t *>(q_bf16);
+    p.qt = q_token_stride;
+    p.qh = q_head_stride;
+    p.kc = k_cache;
+    p.vc = v_cache;
+    p.ks = k_scale;
+    p.vs = v_scale;
+    p.block_table = block_table;
+    p.kv_lens = kv_lens;
+    p.cu_new = cu_new;
+    p.T = T;
+    p.B = B;
+    p.W = W;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.P = P;
+    p.page = page;
+    p.scale = softmax_scale;
+    p.window = window;
+    p.out = out;
+    p.out_fp32 = out_dtype == W8A8_FP32;
+    p.workspace = workspace;
+    return from_cuda(w8a8::launch_paged_attention(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 namespace {

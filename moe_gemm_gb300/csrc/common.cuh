@@ -13,7 +13,7 @@ namespace w8a8 {
 // error word (first writer wins). Layout of the 64-bit code:
 //   bits 56..63 kernel id, 48..55 role, 32..47 wait site, 0..31 CTA index.
 
-enum KernelId : unsigned { KID_GEMM = 1, KID_SELFTEST = 2, KID_QUANT = 3 };
+enum KernelId : unsigned { KID_GEMM = 1, KID_SELFTEST = 2, KID_QUANT = 3, KID_ATTN = 4 };
 enum Role : unsigned {
     ROLE_PRODUCER = 1, ROLE_MMA = 2, ROLE_CONVERT = 3, ROLE_EPILOGUE = 4, ROLE_SELFTEST = 5
 };

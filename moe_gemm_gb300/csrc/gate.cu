@@ -1,0 +1,401 @@
+// The router's gate, on sm_103a: from the router's logits x [T, E] to the
+// top-k expert ids and weights that the expert FFN takes ("Deploying Hunyuan
+// 770B in INT8 on domestic accelerators", §1.3: each token goes to the experts
+// its router picked).
+//
+//   score  s = softmax(x) or 1 / (1 + e^-x); key = s + bias (s without a bias);
+//   groups the E experts form n_group equal runs; a group's score is its largest
+//          key (with a bias, the sum of its two largest); the topk_group best
+//          groups stay;
+//   pick   the k largest keys of the groups that stay, largest first, ties to
+//          the lower expert;
+//   weight s of the picked (renormalize: over their sum), times a factor.
+//
+// One warp per token. Lane l holds experts [V l, V l + V), so a token's logits
+// are one coalesced read, lane order is expert order (a tie goes to the first
+// lane that holds the maximum) and, in the usual layouts, a group is a run of
+// lanes. A pick is one warp-wide unsigned maximum (redux) over keys mapped to
+// ordered integers.
+//
+// Whole numbers depend on comparisons, so they are made exact:
+//  * without a bias the logits themselves are compared: softmax and sigmoid
+//    keep their order;
+//  * with a bias, keys in 32 bits decide unless two compared keys are closer
+//    than their error bound; such a token (measured: well under 1 % of them) is
+//    decided again with scores in 64 bits.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace w8a8 {
+namespace {
+
+constexpr unsigned kFull = 0xFFFFFFFFu;
+constexpr int kGateWarps = 4;
+
+// Ordered integers: a < b as numbers <=> ord(a) < ord(b); 0 is kept for "not
+// available" (the mapping of -infinity is above 0). -0 counts as +0.
+__device__ __forceinline__ uint32_t ord(float v) {
+    const uint32_t u = __float_as_uint(v + 0.0f);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ uint64_t ord(double v) {
+    const uint64_t u = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
+    return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+}
+__device__ __forceinline__ float unord(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+
+__device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(kFull, v); }
+__device__ __forceinline__ uint64_t warp_max(uint64_t v) {
+    const uint32_t hi = static_cast<uint32_t>(v >> 32);
+    const uint32_t mh = __reduce_max_sync(kFull, hi);
+    const uint32_t ml = __reduce_max_sync(kFull, hi == mh ? static_cast<uint32_t>(v) : 0u);
+    return (static_cast<uint64_t>(mh) << 32) | ml;
+}
+
+template <typename R>
+struct KeyOf;
+template <>
+struct KeyOf<float> { using type = uint32_t; };
+template <>
+struct KeyOf<double> { using type = uint64_t; };
+
+__device__ __forceinline__ float load_logit(const float *p) { return __ldg(p); }
+__device__ __forceinline__ float load_logit(const uint16_t *p) {
+    return __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16);
+}
+
+struct GateArgs {
+    const float *bias;
+    int64_t ldx;
+    int T, E, k, n_group, topk_group;
+    int sigmoid, renormalize;
+    float scale;
+    int32_t *ids;
+    float *w;
+};
+
+// Out of line: it runs for few tokens, and once per expert of a lane.
+__device__ __noinline__ double exp_f64(double v) { return exp(v); }
+
+// The picks of one token: pick j and its logit are held by lane j & 31, in
+// element j >> 5 (id -1: none).
+struct Picks {
+    int id[2];
+    float x[2];
+};
+
+// The two largest of the union of {a1 >= a2} and {b1 >= b2}.
+template <typename R>
+__device__ __forceinline__ void top2_merge(R &a1, R &a2, R b1, R b2) {
+    const R lo = fmin(a1, b1);
+    a1 = fmax(a1, b1);
+    a2 = fmax(lo, fmax(a2, b2));
+}
+
+// Marks the experts outside the topk_group best groups as not available
+// (kr = -inf there). Returns false when the last group kept and the first one
+// left out are within `tol` of one another (relative to 1 and to their size).
+template <typename R, int V>
+__device__ __forceinline__ bool keep_groups(R (&kr)[V], const GateArgs &a, int lane, bool sum2,
+                                            R tol) {
+    const int size = a.E / a.n_group;
+    const R none = -INFINITY;
+    R gs[2] = {none, none};   // lane l: the scores of groups l and l + 32
+    const int run = size / V;
+    if (size % V == 0 && (run & (run - 1)) == 0) {
+        // a group is a run of a power of two lanes: every group at once
+        R m1 = none, m2 = none;
+#pragma unroll
+        for (int i = 0; i < V; ++i) top2_merge<R>(m1, m2, kr[i], none);
+        for (int o = 1; o < run; o <<= 1)
+            top2_merge<R>(m1, m2, __shfl_xor_sync(kFull, m1, o), __shfl_xor_sync(kFull, m2, o));
+        const R s = sum2 && m2 > none ? m1 + m2 : m1;
+        gs[0] = __shfl_sync(kFull, s, (lane * run) & 31);
+        if (lane >= a.n_group) gs[0] = none;
+    } else {
+        for (int g = 0; g < a.n_group; ++g) {
+            R m1 = none, m2 = none;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int e = lane * V + i;
+                top2_merge<R>(m1, m2, e >= g * size && e < (g + 1) * size ? kr[i] : none, none);
+            }
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1)
+                top2_merge<R>(m1, m2, __shfl_xor_sync(kFull, m1, o), __shfl_xor_sync(kFull, m2, o));
+            const R s = sum2 && m2 > none ? m1 + m2 : m1;
+            if (lane == (g & 31)) {
+                if (g < 32) gs[0] = s;
+                else gs[1] = s;
+            }
+        }
+    }
+    // rank of each group: those with a larger score, or an equal one and a lower index
+    int rank[2] = {0, 0};
+    for (int g = 0; g < a.n_group; ++g) {
+        const R s = __shfl_sync(kFull, g < 32 ? gs[0] : gs[1], g & 31);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int mine = lane + 32 * h;
+            rank[h] += (s > gs[h] || (s == gs[h] && g < mine)) ? 1 : 0;
+        }
+    }
+    bool clear = true;
+    unsigned kept[2];
+    R worst_in = INFINITY, best_out = none;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const bool exists = lane + 32 * h < a.n_group;
+        const bool in = exists && rank[h] < a.topk_group;
+        kept[h] = __ballot_sync(kFull, in);
+        if (in) worst_in = fmin(worst_in, gs[h]);
+        if (exists && !in) best_out = fmax(best_out, gs[h]);
+    }
+    if (tol > R(0)) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            worst_in = fmin(worst_in, __shfl_xor_sync(kFull, worst_in, o));
+            best_out = fmax(best_out, __shfl_xor_sync(kFull, best_out, o));
+        }
+        // (an unavailable group, -inf, is never close to an available one)
+        clear = !(worst_in - best_out <= tol * fmax(R(1), fabs(worst_in)));
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int g = min((lane * V + i) / size, 63);
+        if (!((kept[g >> 5] >> (g & 31)) & 1u)) kr[i] = none;
+    }
+    return clear;
+}
+
+// Picks the k largest of the available keys (kr > -inf). Returns false when
+// two keys whose order decides are within tol of one another.
+template <typename R, int V>
+__device__ __forceinline__ bool pick(R (&kr)[V], const float (&x)[V], const GateArgs &a, int lane,
+                                     R tol, Picks &out) {
+    using K = typename KeyOf<R>::type;
+    K key[V];
+    K best = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        key[i] = kr[i] > R(-INFINITY) ? ord(kr[i]) : K(0);
+        best = best > key[i] ? best : key[i];
+    }
+    out.id[0] = out.id[1] = -1;
+    out.x[0] = out.x[1] = 0.0f;
+    float last = INFINITY;
+    bool clear = true;
+    const int rounds = tol > R(0) ? a.k + 1 : a.k;   // the first key left out decides too
+    for (int j = 0; j < rounds; ++j) {
+        const K mx = warp_max(best);
+        if (mx == 0) break;
+        if constexpr (sizeof(K) == 4) {
+            if (tol > R(0)) {
+                const float v = unord(mx);
+                if (last - v <= tol * fmaxf(1.0f, fabsf(v))) clear = false;
+                last = v;
+            }
+        }
+        if (j == a.k) break;
+        const int owner = __ffs(__ballot_sync(kFull, best == mx)) - 1;
+        int at = 0;
+        float xv = 0.0f;
+        if (lane == owner) {
+#pragma unroll
+            for (int i = V - 1; i >= 0; --i)
+                if (key[i] == mx) {
+                    at = i;
+                    xv = x[i];
+                }
+            best = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (i == at) key[i] = 0;
+                best = best > key[i] ? best : key[i];
+            }
+        }
+        const int id = __shfl_sync(kFull, lane * V + at, owner);
+        const float xs = __shfl_sync(kFull, xv, owner);
+        if (lane == (j & 31)) {
+            if (j < 32) {
+                out.id[0] = id;
+                out.x[0] = xs;
+            } else {
+                out.id[1] = id;
+                out.x[1] = xs;
+            }
+        }
+    }
+    return clear;
+}
+
+template <int V, typename Tin>
+__global__ void __launch_bounds__(kGateWarps * 32)
+moe_gate_kernel(const Tin *__restrict__ logits, const GateArgs a) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + (threadIdx.x >> 5);
+    if (t >= a.T) return;
+    const Tin *row = logits + t * a.ldx;
+    // logits: NaN and -inf mark experts that are never picked; +inf counts as
+    // the largest finite number
+    float x[V];
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = lane * V + i;
+        const float v = e < a.E ? load_logit(row + e) : -INFINITY;
+        x[i] = v == v ? fminf(v, 3.402823466e38f) : -INFINITY;
+        m = fmaxf(m, x[i]);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    if (m == -INFINITY) m = 0.0f;   // no expert is available
+    // sum of e^(x - m): softmax's denominator
+    float sum = 1.0f;
+    if (!a.sigmoid && (a.bias != nullptr || !a.renormalize)) {
+        sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum += expf(x[i] - m);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    }
+    Picks p;
+    if (a.bias == nullptr) {
+        float kr[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) kr[i] = x[i];
+        if (a.topk_group < a.n_group) keep_groups<float, V>(kr, a, lane, false, 0.0f);
+        pick<float, V>(kr, x, a, lane, 0.0f, p);
+    } else {
+        // A 32-bit key is off by at most: sigmoid, 4 roundings of a number <= 1
+        // and the sum's; softmax, those of its sum of E terms as well, relative
+        // to the score. 2^-20 and 2^-18 cover twice that (two keys compared).
+        const float tol = a.sigmoid ? 0x1p-20f : 0x1p-20f + 0x1p-18f / fmaxf(sum, 1.0f);
+        float kr[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = lane * V + i;
+            const float s = a.sigmoid ? __fdiv_rn(1.0f, 1.0f + expf(-x[i]))
+                                      : __fdiv_rn(expf(x[i] - m), sum);
+            kr[i] = x[i] > -INFINITY ? s + __ldg(a.bias + e) : -INFINITY;
+        }
+        bool clear = true;
+        if (a.topk_group < a.n_group)
+            clear = keep_groups<float, V>(kr, a, lane, true, 2.0f * tol);
+        if (clear) clear = pick<float, V>(kr, x, a, lane, tol, p);
+        if (!clear) {   // (the same in every lane)
+            double kd[V];
+            double dsum = 0.0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                kd[i] = exp_f64(a.sigmoid ? -static_cast<double>(x[i])
+                                          : static_cast<double>(x[i]) - static_cast<double>(m));
+                dsum += kd[i];
+            }
+            if (!a.sigmoid) {
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) dsum += __shfl_xor_sync(kFull, dsum, o);
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int e = lane * V + i;
+                const double s = a.sigmoid ? 1.0 / (1.0 + kd[i]) : kd[i] / dsum;
+                kd[i] = x[i] > -INFINITY ? s + static_cast<double>(__ldg(a.bias + e)) : -INFINITY;
+            }
+            if (a.topk_group < a.n_group) keep_groups<double, V>(kd, a, lane, true, 0.0);
+            pick<double, V>(kd, x, a, lane, 0.0, p);
+        }
+    }
+    // weights. Renormalised softmax: e^(x - x_max) over the picked; sigmoid as
+    // e^min(x, 0) / (1 + e^-|x|), with the common factor e^r taken out before
+    // it can underflow (r = 0 when any picked logit is positive).
+    float xm = -INFINITY;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        if (p.id[h] >= 0) xm = fmaxf(xm, p.x[h]);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) xm = fmaxf(xm, __shfl_xor_sync(kFull, xm, o));
+    const float r = a.sigmoid ? (a.renormalize ? fminf(xm, 0.0f) : 0.0f)
+                              : (a.renormalize ? xm : m);
+    float num[2], den = 0.0f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        num[h] = 0.0f;
+        if (p.id[h] >= 0) {
+            if (a.sigmoid)
+                num[h] = __fdiv_rn(expf(fminf(p.x[h], 0.0f) - r), 1.0f + expf(-fabsf(p.x[h])));
+            else
+                num[h] = expf(p.x[h] - r);
+        }
+        den += num[h];
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) den += __shfl_xor_sync(kFull, den, o);
+    if (!a.renormalize) den = a.sigmoid ? 1.0f : sum;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int j = lane + 32 * h;
+        if (j < a.k) {
+            a.ids[t * a.k + j] = p.id[h];
+            a.w[t * a.k + j] = p.id[h] >= 0 ? __fdiv_rn(num[h], den) * a.scale : 0.0f;
+        }
+    }
+}
+
+template <int V, typename Tin>
+cudaError_t launch_v(const Tin *x, const GateArgs &a, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((a.T + kGateWarps - 1) / kGateWarps));
+    cfg.blockDim = dim3(kGateWarps * 32);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, moe_gate_kernel<V, Tin>, x, a);
+    if (e != cudaSuccess) return e;
+    return cudaGetLastError();
+}
+
+template <typename Tin>
+cudaError_t launch_any(const void *logits, const GateArgs &a, cudaStream_t stream) {
+    const Tin *x = static_cast<const Tin *>(logits);
+    if (a.E <= 32) return launch_v<1>(x, a, stream);
+    if (a.E <= 64) return launch_v<2>(x, a, stream);
+    if (a.E <= 128) return launch_v<4>(x, a, stream);
+    if (a.E <= 256) return launch_v<8>(x, a, stream);
+    if (a.E <= 512) return launch_v<16>(x, a, stream);
+    return launch_v<32>(x, a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_moe_gate(const GateProblem &p, cudaStream_t stream) {
+    GateArgs a;
+    a.bias = p.bias;
+    a.ldx = p.ldx;
+    a.T = static_cast<int>(p.T);
+    a.E = static_cast<int>(p.E);
+    a.k = static_cast<int>(p.k);
+    a.n_group = static_cast<int>(p.n_group);
+    a.topk_group = static_cast<int>(p.topk_group);
+    a.sigmoid = p.sigmoid ? 1 : 0;
+    a.renormalize = p.renormalize ? 1 : 0;
+    a.scale = p.scale;
+    a.ids = p.ids;
+    a.w = p.w;
+    return p.fp32 ? launch_any<float>(p.logits, a, stream)
+                  : launch_any<uint16_t>(p.logits, a, stream);
+}
+
+}  // namespace w8a8

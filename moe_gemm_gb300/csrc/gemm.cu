@@ -58,6 +58,7 @@
 #include "common.cuh"
 #include "quant_math.cuh"
 #include "internal.h"
+#include "tensor_map.h"
 
 namespace w8a8 {
 
@@ -2302,6 +2303,8 @@ cudaError_t launch_selftest_wait(unsigned long long limit_ns, cudaStream_t strea
     selftest_wait_kernel<<<1, 32, 0, stream>>>(err, limit_ns);
     return cudaGetLastError();
 }
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encode_fn() { return get_encode_fn(); }
 
 cudaError_t device_error_word(unsigned long long **out) {
     return cudaGetSymbolAddress(reinterpret_cast<void **>(out), g_device_error);

@@ -156,6 +156,62 @@ cudaError_t launch_attention_decode(const AttnProblem &p, cudaStream_t stream);
 cudaError_t launch_kv_quant(const uint16_t *x, int64_t n, const int32_t *dst_rows, int8_t *cache,
                             float *scales, cudaStream_t stream);
 
+// The router's gate (gate.cu): top-k ids and weights from logits [T, E].
+struct GateProblem {
+    const void *logits;     // [T, ldx] FP32 or BF16
+    bool fp32;
+    int64_t ldx, T, E, k, n_group, topk_group;
+    const float *bias;      // [E] or null
+    bool sigmoid, renormalize;
+    float scale;
+    int32_t *ids;           // [T, k]
+    float *w;               // [T, k]
+};
+constexpr int kGateMaxGroups = 64;
+cudaError_t launch_moe_gate(const GateProblem &p, cudaStream_t stream);
+
+// The paged KV cache (paged_kv.cu): pages [P, Hkv, page, 128].
+constexpr int64_t kPagedMaxRequests = 4096;
+struct PagedPlanProblem {
+    int32_t *block_table, *lens;
+    const int32_t *target;
+    int32_t *free_pages, *n_free;
+    int64_t B, W, P, page, n_tokens;
+    int32_t *cu_new, *kv_lens, *slots, *positions;
+};
+cudaError_t launch_paged_kv_plan(const PagedPlanProblem &p, cudaStream_t stream);
+
+struct PagedWriteProblem {
+    const uint16_t *k, *v;           // BF16 [T, Hkv, 128]
+    int64_t kt, kh, vt, vh;          // token and head strides (elements)
+    const int32_t *slots;            // [T]
+    int64_t T, Hkv, P, page;
+    bool int8;
+    void *kc, *vc;
+    float *ks, *vs;                  // INT8: [P, Hkv, page]
+};
+cudaError_t launch_paged_kv_write(const PagedWriteProblem &p, cudaStream_t stream);
+
+// Attention of each request's new tokens over its pages (paged_attention.cu).
+struct PagedAttnProblem {
+    const uint16_t *q;               // BF16 [T, Hq, 128]
+    int64_t qt, qh;                  // token and head strides (elements)
+    const void *kc, *vc;
+    const float *ks, *vs;            // INT8 pages: [P, Hkv, page]; null: BF16 pages
+    const int32_t *block_table;      // [B, W]
+    const int32_t *kv_lens;          // [B]
+    const int32_t *cu_new;           // [B + 1]
+    int64_t T, B, W, Hq, Hkv, P, page;
+    float scale;
+    int64_t window;                  // 0: none
+    void *out;                       // [T, Hq, 128]
+    bool out_fp32;
+    void *workspace;
+};
+constexpr int kPagedMaxGroup = 16;   // Hq / Hkv
+size_t paged_attn_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hkv);
+cudaError_t launch_paged_attention(const PagedAttnProblem &p, cudaStream_t stream);
+
 // Maximum number of experts a grouped call may have.
 constexpr int kMaxExperts = 1024;
 
