@@ -13,8 +13,10 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libw8a8.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.cu", "quant.cu", "gemm.cu", "probe.cu", "moe.cu", "attention.cu",
-           "gate.cu", "paged_kv.cu", "paged_attention.cu"]
+           "gate.cu", "paged_kv.cu", "paged_attention.cu",
+           "paged_attention_tiles.cu"]
 HEADERS = ["common.cuh", "quant_math.cuh", "attention_math.cuh", "paged_schedule.cuh",
+           "paged_attention.cuh",
            "tensor_map.h", "internal.h"]
 GENCODE = "-gencode=arch=compute_103a,code=sm_103a"
 NVCC_FLAGS = [GENCODE, "-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC",

@@ -12,6 +12,8 @@
 // the work is shared out as paged_schedule.cuh says.
 //  * paged_rows_kernel: up to 16 query rows per item (mma.sync), for calls of
 //    few new tokens per request: an HBM stream of the cache.
+//  * paged_tiles_kernel (paged_attention_tiles.cu): up to 256 query rows per item
+//    on the tcgen05 tensor cores, for calls with more.
 //  * paged_combine_kernel joins the shares of items that were divided.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -22,6 +24,7 @@
 #include "attention_math.cuh"
 #include "common.cuh"
 #include "internal.h"
+#include "paged_attention.cuh"
 #include "paged_schedule.cuh"
 #include "tensor_map.h"
 
@@ -35,112 +38,11 @@ constexpr int kRowThreads = (kRowWarps + 1) * 32;   // and a warp that loads
 constexpr int kRowStages = 2;
 constexpr float kNegInf = -INFINITY;
 
-// ------------------------------------------------------------- cache loading
-struct PagedCache {
-    const int32_t *table;   // [B, W]
-    const float *ks, *vs;   // INT8: [P, Hkv, page]
-    int W, P, Hkv, page;
-    int box;                // rows of one TMA box: gcd(page, 128)
-};
+// The kernel of a call, by the query rows that a request and kv head have on
+// average: up to 16 fit one item of the rows kernel, which reads the cache
+// once; more take the tiles kernel.
+bool uses_tiles(int64_t T, int64_t B, int64_t G) { return T * G > kRowsMax * B; }
 
-// One tile of 128 positions of one (request, kv head) in shared memory: K and
-// V rows of 128 bytes with the 128-byte swizzle (16-byte piece c of row r at
-// piece c ^ (r & 7)); BF16 rows are two such halves, 64 dimensions each.
-template <bool kInt8>
-struct Tile {
-    static constexpr int kHalves = kInt8 ? 1 : 2;
-    static constexpr int kBytes = kHalves * kTilePositions * 128;   // of K, or of V
-};
-
-// Which positions of a tile hold keys of the request: bit i of word i / 32.
-// Positions outside [lo, hi), and those of pages whose table entry is not a
-// page, are masked for every query and not loaded.
-struct TileMask {
-    uint32_t w[4];
-};
-
-// The loading warp's part for one tile: finds the pages of the tile's boxes
-// (lane i: box i), issues their copies to `bar`, and returns the mask. The
-// boxes outside [lo, hi) keep whatever their shared memory held.
-template <bool kInt8>
-__device__ __forceinline__ TileMask load_tile(const PagedCache &c, const CUtensorMap *km,
-                                              const CUtensorMap *vm, int b, int h, int tile, int lo,
-                                              int hi, uint32_t k_dst, uint32_t v_dst,
-                                              uint32_t ks_dst, uint32_t vs_dst, uint32_t bar,
-                                              unsigned long long *err) {
-    const int lane = threadIdx.x & 31;
-    const int pos = tile * kTilePositions + lane * c.box;
-    const int boxes = kTilePositions / c.box;
-    bool use = lane < boxes && pos < hi && pos + c.box > lo;
-    int64_t row = 0;
-    if (use) {
-        const int pg = pos / c.page;
-        const int id = __ldg(c.table + static_cast<int64_t>(b) * c.W + pg);
-        if (id < 0 || id >= c.P) {
-            use = false;
-            record_device_error(err, KID_ATTN, ROLE_PRODUCER, 9);
-        } else {
-            row = (static_cast<int64_t>(id) * c.Hkv + h) * c.page + (pos - pg * c.page);
-        }
-    }
-    const unsigned used = __ballot_sync(0xFFFFFFFFu, use);
-    const uint32_t per_box = static_cast<uint32_t>(c.box) * (kInt8 ? 2 * 128 + 8 : 4 * 128);
-    if (lane == 0) mbar_arrive_expect_tx(bar, __popc(used) * per_box);
-    __syncwarp();
-    if (use) {
-        const uint32_t off = static_cast<uint32_t>(lane * c.box) * 128;
-#pragma unroll
-        for (int half = 0; half < Tile<kInt8>::kHalves; ++half) {
-            const uint32_t o = off + half * kTilePositions * 128;
-            tma_load_2d(k_dst + o, km, half * 64, static_cast<int>(row), bar);
-            tma_load_2d(v_dst + o, vm, half * 64, static_cast<int>(row), bar);
-        }
-        if constexpr (kInt8) {
-            bulk_g2s(ks_dst + lane * c.box * 4, c.ks + row, c.box * 4, bar);
-            bulk_g2s(vs_dst + lane * c.box * 4, c.vs + row, c.box * 4, bar);
-        }
-    }
-    // the mask: lane l answers for positions 4 l .. 4 l + 3
-    uint32_t nib = 0;
-    const bool page_ok = (used >> (4 * lane / c.box)) & 1u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int p = tile * kTilePositions + 4 * lane + i;
-        if (page_ok && p >= lo && p < hi) nib |= 1u << i;
-    }
-    uint32_t word = nib << (4 * (lane & 7));
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) word |= __shfl_xor_sync(0xFFFFFFFFu, word, o);
-    TileMask m;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m.w[i] = __shfl_sync(0xFFFFFFFFu, word, 8 * i);
-    return m;
-}
-
-// The positions of a request that any of its new tokens may see: nothing
-// outside them is read.
-__device__ __forceinline__ void request_span(const PagedSchedule &s, const PagedRequest &r, int &lo,
-                                             int &hi) {
-    lo = s.window > 0 ? max(r.base - s.window + 1, 0) : 0;
-    hi = r.kv;
-}
-
-// ------------------------------------------------------------------ workspace
-// Of every CTA two slots; a slot holds, of up to `rows` query rows, the sums
-// sum_j e^(s_j - m) v_j (rows x 128), then m, then sum_j e^(s_j - m).
-__device__ __forceinline__ float *slot_of(float *ws, int rows, int cta, int slot) {
-    return ws + (static_cast<int64_t>(cta) * 2 + slot) * rows * (kHeadDim + 2);
-}
-
-struct PagedOut {
-    void *out;              // [T, Hq, 128]
-    int fp32, Hq, G;
-};
-
-__device__ __forceinline__ int64_t out_row(const PagedOut &o, const PagedRequest &r, int h,
-                                           int tok0, int row) {
-    return (static_cast<int64_t>(r.t0) + tok0 + row / o.G) * o.Hq + h * o.G + row % o.G;
-}
 
 // ------------------------------------------------------------ the rows kernel
 struct RowsArgs {
@@ -227,7 +129,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant_
     const PagedSchedule &s = a.s;
     if (tid == 0) {
         for (int i = 0; i < kRowStages; ++i) {
-            mbar_init(smem_u32(&sm.full[i]), 2);   // the copies, and the mask
+            mbar_init(smem_u32(&sm.full[i]), 1);
             mbar_init(smem_u32(&sm.empty[i]), kRowWarps * 32);
         }
         sm.abort_flag = 0;
@@ -254,13 +156,20 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant_
                                    a.err, ROLE_PRODUCER, 1, kWaitLimitNs, KID_ATTN);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
-                const TileMask m = load_tile<kInt8>(
-                    a.c, &km, &vm, w.b, w.h, p.tile0 + x, lo, hi, smem_u32(sm.stage[st].k),
-                    smem_u32(sm.stage[st].v), smem_u32(sm.ks[st]), smem_u32(sm.vs[st]),
-                    smem_u32(&sm.full[st]), a.err);
-                if (lane == 0) sm.mask[st] = m;
+                const TileBoxes tb = find_boxes(a.c, w.b, w.h, p.tile0 + x, lo, hi, a.err);
+                const uint32_t bar = smem_u32(&sm.full[st]);
+                if (lane == 0) {
+                    sm.mask[st] = tb.mask;
+                    mbar_arrive_expect_tx(bar, 2 * tile_bytes<kInt8>(a.c, tb) +
+                                                   (kInt8 ? 2 * scale_bytes(a.c, tb) : 0));
+                }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sm.full[st]));
+                copy_boxes<kInt8>(a.c, tb, &km, smem_u32(sm.stage[st].k), bar);
+                copy_boxes<kInt8>(a.c, tb, &vm, smem_u32(sm.stage[st].v), bar);
+                if constexpr (kInt8) {
+                    copy_scales(a.c, tb, a.c.ks, smem_u32(sm.ks[st]), bar);
+                    copy_scales(a.c, tb, a.c.vs, smem_u32(sm.vs[st]), bar);
+                }
             }
             if (!ok) break;
         }
@@ -589,50 +498,7 @@ cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, int threads, size_t
     return cudaGetLastError();
 }
 
-// The cache as rows of 128 (bytes or BF16 values): a box is 128 bytes wide.
-bool encode_cache(CUtensorMap *map, const void *ptr, bool int8, int64_t rows, int box) {
-    auto fn = tensor_map_encode_fn();
-    if (fn == nullptr) return false;
-    cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(rows)};
-    cuuint64_t strides[1] = {int8 ? 128u : 256u};
-    cuuint32_t bx[2] = {int8 ? 128u : 64u, static_cast<cuuint32_t>(box)};
-    cuuint32_t estr[2] = {1, 1};
-    return fn(map, int8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-              const_cast<void *>(ptr), dims, strides, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
-
-PagedSchedule schedule_of(const PagedAttnProblem &p, int rows) {
-    PagedSchedule s;
-    s.cu = p.cu_new;
-    s.kv = p.kv_lens;
-    s.B = static_cast<int>(p.B);
-    s.T = static_cast<int>(p.T);
-    s.Hkv = static_cast<int>(p.Hkv);
-    s.tile_tokens = rows / static_cast<int>(p.Hq / p.Hkv);
-    s.capacity = p.W * p.page;
-    // a window that reaches past the first position of any row masks nothing
-    s.window = p.window >= s.capacity ? 0 : static_cast<int>(p.window);
-    s.overhead = kTilePositions;
-    s.min_share = 2 * kTilePositions;
-    return s;
-}
-
-PagedCache cache_of(const PagedAttnProblem &p) {
-    PagedCache c;
-    c.table = p.block_table;
-    c.ks = p.ks;
-    c.vs = p.vs;
-    c.W = static_cast<int>(p.W);
-    c.P = static_cast<int>(p.P);
-    c.Hkv = static_cast<int>(p.Hkv);
-    c.page = static_cast<int>(p.page);
-    c.box = gcd(c.page, kTilePositions);
-    return c;
-}
 
 cudaError_t launch_combine(const PagedSchedule &s, const PagedOut &o, const float *ws, int rows,
                            int max_ctas, cudaStream_t stream) {
@@ -668,12 +534,10 @@ cudaError_t launch_rows(const PagedAttnProblem &p, const CUtensorMap &km, const 
     int ctas = per_sm[dev] * num_sms;
     if (ctas > kMaxCtas) ctas = kMaxCtas;
     RowsArgs a;
-    a.s = schedule_of(p, 8 * NT);
-    a.c = cache_of(p);
-    a.o.out = p.out;
-    a.o.fp32 = p.out_fp32 ? 1 : 0;
-    a.o.Hq = static_cast<int>(p.Hq);
-    a.o.G = static_cast<int>(p.Hq / p.Hkv);
+    const PagedSetup u = paged_setup(p, 8 * NT);
+    a.s = u.s;
+    a.c = u.c;
+    a.o = u.o;
     a.q = p.q;
     a.qt = p.qt;
     a.qh = p.qh;
@@ -687,8 +551,55 @@ cudaError_t launch_rows(const PagedAttnProblem &p, const CUtensorMap &km, const 
 
 }  // namespace
 
-size_t paged_attn_workspace_bytes(int64_t, int64_t, int64_t, int64_t) {
-    return static_cast<size_t>(kMaxCtas) * 2 * kRowsMax * (kHeadDim + 2) * sizeof(float);
+PagedSetup paged_setup(const PagedAttnProblem &p, int rows) {
+    PagedSetup u;
+    u.o.out = p.out;
+    u.o.fp32 = p.out_fp32 ? 1 : 0;
+    u.o.Hq = static_cast<int>(p.Hq);
+    u.o.G = static_cast<int>(p.Hq / p.Hkv);
+    u.s.cu = p.cu_new;
+    u.s.kv = p.kv_lens;
+    u.s.B = static_cast<int>(p.B);
+    u.s.T = static_cast<int>(p.T);
+    u.s.Hkv = static_cast<int>(p.Hkv);
+    // (an item of the tiles kernel is two halves of whole tokens)
+    u.s.tile_tokens = rows == kPagedTileRows ? 2 * (rows / 2 / u.o.G) : rows / u.o.G;
+    u.s.capacity = p.W * p.page;
+    // a window that reaches past the first position of any row masks nothing
+    u.s.window = p.window >= u.s.capacity ? 0 : static_cast<int>(p.window);
+    u.s.overhead = kTilePositions;
+    u.s.min_share = 2 * kTilePositions;
+    u.c.table = p.block_table;
+    u.c.ks = p.ks;
+    u.c.vs = p.vs;
+    u.c.W = static_cast<int>(p.W);
+    u.c.P = static_cast<int>(p.P);
+    u.c.Hkv = static_cast<int>(p.Hkv);
+    u.c.page = static_cast<int>(p.page);
+    u.c.box = gcd(u.c.page, kTilePositions);
+    return u;
+}
+
+bool paged_encode_cache(CUtensorMap *map, const void *ptr, bool int8, const PagedAttnProblem &p) {
+    auto fn = tensor_map_encode_fn();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(p.P * p.Hkv * p.page)};
+    cuuint64_t strides[1] = {int8 ? 128u : 256u};
+    cuuint32_t bx[2] = {int8 ? 128u : 64u,
+                        static_cast<cuuint32_t>(gcd(static_cast<int>(p.page), kTilePositions))};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(map, int8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+              const_cast<void *>(ptr), dims, strides, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t paged_attn_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hkv) {
+    if (T <= 0 || B <= 0) return 0;
+    const size_t slots = uses_tiles(T, B, Hq / Hkv)
+                             ? static_cast<size_t>(kPagedTileCtas) * 2 * kPagedTileRows
+                             : static_cast<size_t>(kMaxCtas) * 2 * kRowsMax;
+    return slots * (kHeadDim + 2) * sizeof(float);
 }
 
 cudaError_t launch_paged_attention(const PagedAttnProblem &p, cudaStream_t stream) {
@@ -698,13 +609,21 @@ cudaError_t launch_paged_attention(const PagedAttnProblem &p, cudaStream_t strea
     unsigned long long *err = nullptr;
     e = device_error_word(&err);
     if (e != cudaSuccess) return e;
+    const int64_t G = p.Hq / p.Hkv;
+    // (the tiles kernel copies q by tensor map, which takes rows apart from one
+    // another; the rows kernel takes any strides)
+    if (uses_tiles(p.T, p.B, G) && p.qt >= kHeadDim && p.qh >= kHeadDim) {
+        const PagedSetup u = paged_setup(p, kPagedTileRows);
+        const int ctas = info.num_sms < kPagedTileCtas ? info.num_sms : kPagedTileCtas;
+        e = launch_paged_tiles(p, u, ctas, err, stream);
+        if (e != cudaSuccess) return e;
+        return launch_combine(u.s, u.o, static_cast<float *>(p.workspace), kPagedTileRows, ctas,
+                              stream);
+    }
     const bool int8 = p.ks != nullptr;
     CUtensorMap km, vm;
-    const int box = gcd(static_cast<int>(p.page), kTilePositions);
-    const int64_t rows = p.P * p.Hkv * p.page;
-    if (!encode_cache(&km, p.kc, int8, rows, box) || !encode_cache(&vm, p.vc, int8, rows, box))
+    if (!paged_encode_cache(&km, p.kc, int8, p) || !paged_encode_cache(&vm, p.vc, int8, p))
         return cudaErrorInvalidValue;
-    const int64_t G = p.Hq / p.Hkv;
     // An item takes whole tokens: 8 rows when the group fits and the call has
     // about one token per request, else 16.
     const bool one = G <= 8 && p.T <= p.B;

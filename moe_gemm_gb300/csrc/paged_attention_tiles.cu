@@ -1,0 +1,830 @@
+// Attention over the paged cache for calls with many query rows, on the
+// tcgen05 tensor cores of sm_103a (the operator: paged_attention.cu).
+//
+// An item is 256 query rows of one (request, kv head): two halves of 128 rows
+// (whole tokens x the G query heads that share the kv head), whose products
+// alternate on the tensor core so that one half's softmax runs beside the
+// other half's products. Per tile of 128 positions and half:
+//
+//   S = Q K^T         128 x 128 x 128, both operands in shared memory
+//   softmax           one thread per row: S from tensor memory, running
+//                     maximum and sum, P back to tensor memory over S
+//   O += P V          128 x 128 x 128, P from tensor memory, V as it lies
+//                     (N-major), O stays in tensor memory for the whole item
+//
+// Tensor memory: S0, S1, O0, O1 of 128 columns each (all 512).
+//
+// The reference that the running maximum gives the exponentials moves only
+// when a tile's maximum passes it by more than 8 (in log2): weights are then up
+// to 2^8 instead of 1, which costs no accuracy, and O is rescaled a few times
+// per item instead of at every tile. Sums and statistics are FP32.
+//
+// BF16 pages: P is rounded to BF16 for the product (half a step 2^-8 of each
+// weight; V is BF16, and both operands have one type).
+// INT8 pages: a converter warpgroup widens the codes to fp16 (exact) into
+// shared memory. Scores are S * (k scale); a weight carries its v scale,
+//   P_j = 2^(s_j + log2 vs_j - m), m the running maximum of s_j + log2 vs_j,
+// so P is at most 2^8 whatever the scales' range, and is rounded to fp16 (half a step
+// 2^-11); the denominator adds P_j / vs_j. q goes to fp16 too, each row scaled
+// by a power of two that the scores take back exactly. Scales below 2^-100
+// count as 2^-100.
+//
+// Warps: 0-3 and 4-7 softmax of the halves, 8 issues the products, 9 loads,
+// 12-15 convert (INT8).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "attention_math.cuh"
+#include "common.cuh"
+#include "internal.h"
+#include "paged_attention.cuh"
+#include "paged_schedule.cuh"
+#include "quant_math.cuh"
+#include "tensor_map.h"
+
+namespace w8a8 {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kHalfRows = 128;
+constexpr int kInfo = 4;             // tiles whose mask and scales are kept
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.0f;       // log2 by which weights may pass 1
+constexpr int kOperandBytes = 128 * 128 * 2;
+// Registers of a softmax thread and of the others: 2 x 128 x 192 + 2 x 128 x
+// 64 = the 512 x 128 that the block is launched with.
+constexpr int kSoftmaxRegs = 192, kOtherRegs = 64;
+
+struct TilesArgs {
+    PagedSchedule s;
+    PagedCache c;
+    PagedOut o;
+    int half_tokens;        // whole tokens of a half: 128 / G
+    float scale_log2;       // softmax scale * log2(e)
+    float *ws;
+    unsigned long long *err;
+};
+
+template <bool kInt8>
+struct TilesSmem {
+    // BF16 operands are copied straight into 5 slots; INT8 codes land in 3 raw
+    // slots and are widened into 3.
+    static constexpr int kOps = kInt8 ? 3 : 5;
+    static constexpr int kRaws = 3;
+    uint8_t q[2][kOperandBytes];
+    uint8_t op[kOps][kOperandBytes];
+    uint8_t raw[kInt8 ? kRaws : 1][kInt8 ? kOperandBytes / 2 : 16];
+    float rks[kInfo][kInt8 ? 128 : 4], rvs[kInfo][kInt8 ? 128 : 4];   // scales as stored
+    float ks[kInfo][kInt8 ? 128 : 4];    // k scale
+    float lv[kInfo][kInt8 ? 128 : 4];    // log2 of the v scale, -inf: masked for every query
+    float iv[kInfo][kInt8 ? 128 : 4];    // 1 / v scale
+    float qinv[2][kHalfRows];
+    TileMask mask[kInfo];
+    uint64_t op_full[kOps], op_empty[kOps], raw_full[kRaws], raw_empty[kRaws];
+    uint64_t info_full[kInfo];
+    uint64_t q_land[2], q_full[2], q_empty[2];
+    uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
+    uint64_t fix, drain;
+    uint32_t tmem;
+    volatile int abort_flag;
+};
+
+// D[tmem] (+)= A[smem] * B[smem], kind::f16, cta_group::1.
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Descriptor of an N-major operand tile with the 128-byte swizzle: rows of k
+// (128 bytes: 64 values of n), 8-row groups 1024 bytes apart (stride offset),
+// the next 64 values of n 16 KB further (leading offset).
+__device__ __forceinline__ uint64_t smem_desc_nmajor(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFF) >> 4);
+    d |= static_cast<uint64_t>((kOperandBytes / 2) >> 4) << 16;
+    d |= static_cast<uint64_t>(1024 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+constexpr uint32_t kBNMajor = 1u << 16;   // instruction descriptor: B is N-major
+
+#define W8A8_R16(r, o)                                                                          \
+    "=r"(r[o + 0]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]),             \
+        "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7]), "=r"(r[o + 8]), "=r"(r[o + 9]),         \
+        "=r"(r[o + 10]), "=r"(r[o + 11]), "=r"(r[o + 12]), "=r"(r[o + 13]), "=r"(r[o + 14]),    \
+        "=r"(r[o + 15])
+#define W8A8_I16(r, o)                                                                          \
+    "r"(r[o + 0]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), "r"(r[o + 5]),   \
+        "r"(r[o + 6]), "r"(r[o + 7]), "r"(r[o + 8]), "r"(r[o + 9]), "r"(r[o + 10]),             \
+        "r"(r[o + 11]), "r"(r[o + 12]), "r"(r[o + 13]), "r"(r[o + 14]), "r"(r[o + 15])
+
+// 128 columns of the thread's lane, with the wait for them.
+__device__ __forceinline__ void tmem_ld_128cols_sync(uint32_t t, uint32_t (&r)[128]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%128];\n"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%129];\n"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95}, [%130];\n"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%131];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : W8A8_R16(r, 0), W8A8_R16(r, 16), W8A8_R16(r, 32), W8A8_R16(r, 48), W8A8_R16(r, 64),
+          W8A8_R16(r, 80), W8A8_R16(r, 96), W8A8_R16(r, 112)
+        : "r"(t), "r"(t + 32), "r"(t + 64), "r"(t + 96)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_32cols(uint32_t t, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::
+            W8A8_I16(r, 0),
+        W8A8_I16(r, 16), "r"(t)
+        : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ unsigned long long f2_fma(unsigned long long a, unsigned long long b,
+                                                     unsigned long long c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// The tiles that a half of an item sees within a piece: [from, upto), in tiles
+// of the request.
+struct HalfTiles {
+    bool exists;
+    int first, last;        // positions of its first and last token
+    int from, upto;
+};
+
+__device__ __forceinline__ HalfTiles half_tiles(const PagedSchedule &s, const PagedWalk &w,
+                                                const PagedPiece &p, int half, int half_tokens) {
+    HalfTiles t;
+    const int a = half * half_tokens, z = min(a + half_tokens, p.ntok);
+    t.exists = a < p.ntok;
+    t.first = w.r.base + p.tok0 + a;
+    t.last = w.r.base + p.tok0 + z - 1;
+    const int lo = s.window > 0 ? max(t.first - s.window + 1, 0) / kTilePositions : 0;
+    const int hi = t.last >= 0 ? t.last / kTilePositions + 1 : 0;
+    t.from = max(p.tile0 + p.first, lo);
+    t.upto = t.exists ? min(p.tile0 + p.last, hi) : t.from;
+    if (t.upto < t.from) t.upto = t.from;
+    return t;
+}
+
+template <bool kInt8>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap km,
+                   const __grid_constant__ CUtensorMap vm, const TilesArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    using Smem = TilesSmem<kInt8>;
+    constexpr uint32_t kOps = Smem::kOps, kRaws = Smem::kRaws;
+    Smem &sm = *reinterpret_cast<Smem *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const PagedSchedule &s = a.s;
+    volatile int *abort = &sm.abort_flag;
+    auto bar = [](uint64_t &b) { return smem_u32(&b); };
+    if (tid == 0) {
+        for (uint32_t i = 0; i < kOps; ++i) {
+            mbar_init(bar(sm.op_full[i]), kInt8 ? 128 : 1);
+            mbar_init(bar(sm.op_empty[i]), 1);
+        }
+        for (uint32_t i = 0; i < kRaws; ++i) {
+            mbar_init(bar(sm.raw_full[i]), 1);
+            mbar_init(bar(sm.raw_empty[i]), 128);
+        }
+        for (int i = 0; i < kInfo; ++i) mbar_init(bar(sm.info_full[i]), kInt8 ? 128 : 1);
+        for (int h = 0; h < 2; ++h) {
+            mbar_init(bar(sm.q_land[h]), 1);
+            mbar_init(bar(sm.q_full[h]), kInt8 ? 128 : 1);
+            mbar_init(bar(sm.q_empty[h]), 1 + kHalfRows);
+            mbar_init(bar(sm.s_full[h]), 1);
+            mbar_init(bar(sm.p_full[h]), kHalfRows);
+            mbar_init(bar(sm.o_done[h]), 1);
+            mbar_init(bar(sm.o_free[h]), kHalfRows);
+        }
+        mbar_init(bar(sm.fix), 1);
+        mbar_init(bar(sm.drain), 1);
+        sm.abort_flag = 0;
+        fence_mbarrier_init();
+    }
+    // rows of q past a half's whole tokens are never written: zeros, so that
+    // what is computed for them stays finite
+    for (int i = tid; i < 2 * kOperandBytes / 16; i += kThreads)
+        reinterpret_cast<uint4 *>(sm.q)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    if (warp == 8) {
+        tmem_alloc(smem_u32(&sm.tmem), 512);
+        tmem_relinquish();
+    }
+    griddep_launch_dependents();
+    griddep_wait();
+    const PagedShare sh = paged_share<kThreads>(s, blockIdx.x, gridDim.x);   // (synchronises)
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+    PagedWalk w;
+    w.start(s, sh);
+    const bool mine = static_cast<int>(blockIdx.x) < sh.ctas;
+    uint32_t it = 0;        // tiles of the pieces before this one
+    uint32_t qn[2] = {0, 0};   // pieces with the half before this one
+
+    if (warp < 8) {
+        // ------------------------------------------------------------ softmax
+        setmaxnreg_inc<kSoftmaxRegs>();
+        const int h = warp >> 2;
+        const int row = tid & (kHalfRows - 1);
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // lane 32 (warp % 4)
+        const uint32_t ts = tmem + lanes + h * 128, to = tmem + lanes + 256 + h * 128;
+        uint32_t sn = 0, on = 0;    // active tiles, pieces with any
+        bool ok = true;
+        for (; mine && ok && !w.done(s, sh.end); w.next(s)) {
+            const PagedPiece p = paged_piece(s, w, sh.begin, sh.end);
+            if (p.first == p.last && !p.whole) continue;
+            const bool work = p.last > p.first;
+            const HalfTiles t = half_tiles(s, w, p, h, a.half_tokens);
+            const int tok = row / a.o.G;
+            const bool mine_row = t.exists && tok < a.half_tokens && h * a.half_tokens + tok < p.ntok;
+            const int pos = t.first + tok;
+            float m = -INFINITY, l = 0.0f;
+            float c = a.scale_log2;
+            if (work && t.exists) {
+                ok = mbar_wait(bar(sm.q_full[h]), qn[h] & 1, abort, a.err, ROLE_EPILOGUE, 1,
+                               kWaitLimitNs, KID_ATTN);
+                if constexpr (kInt8) c *= sm.qinv[h][row];
+                mbar_arrive(bar(sm.q_empty[h]));
+                ++qn[h];
+            }
+            bool first = true;
+            for (int x = t.from; work && x < t.upto; ++x, ++sn) {
+                const uint32_t ti = it + static_cast<uint32_t>(x - p.tile0 - p.first);
+                const int info = ti % kInfo;
+                if (ok)
+                    // (in this order: a half that passes over tiles would not
+                    // know which of two phases an earlier info slot is in)
+                    ok = mbar_wait(bar(sm.s_full[h]), sn & 1, abort, a.err, ROLE_EPILOGUE, 2,
+                                   kWaitLimitNs, KID_ATTN) &&
+                         mbar_wait(bar(sm.info_full[info]), (ti / kInfo) & 1, abort, a.err,
+                                   ROLE_EPILOGUE, 3, kWaitLimitNs, KID_ATTN);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                __syncwarp();
+                tc_fence_after();
+                uint32_t r[128];
+                tmem_ld_128cols_sync(ts, r);
+                const int c0 = x * kTilePositions;
+                // INT8: t_j = s_j (k scale_j) c + log2 vs_j
+                if constexpr (kInt8) {
+                    const float4 *k4 = reinterpret_cast<const float4 *>(sm.ks[info]);
+                    const float4 *l4 = reinterpret_cast<const float4 *>(sm.lv[info]);
+                    const unsigned long long c2 = f2_bits(c, c);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float4 kk = k4[i], ll = l4[i];
+                        float x0, x1, x2, x3;
+                        f2_split(f2_fma(f2_mul(f2_bits(__uint_as_float(r[4 * i]),
+                                                       __uint_as_float(r[4 * i + 1])),
+                                               f2_bits(kk.x, kk.y)),
+                                        c2, f2_bits(ll.x, ll.y)),
+                                 x0, x1);
+                        f2_split(f2_fma(f2_mul(f2_bits(__uint_as_float(r[4 * i + 2]),
+                                                       __uint_as_float(r[4 * i + 3])),
+                                               f2_bits(kk.z, kk.w)),
+                                        c2, f2_bits(ll.z, ll.w)),
+                                 x2, x3);
+                        r[4 * i] = __float_as_uint(x0);
+                        r[4 * i + 1] = __float_as_uint(x1);
+                        r[4 * i + 2] = __float_as_uint(x2);
+                        r[4 * i + 3] = __float_as_uint(x3);
+                    }
+                }
+                const bool causal = c0 + kTilePositions - 1 > t.first;
+                const bool low = s.window > 0 && c0 <= t.last - s.window;
+                if (causal || low) {
+                    const int hi = pos - c0, lo = s.window > 0 ? pos - s.window + 1 - c0 : 0;
+#pragma unroll
+                    for (int j = 0; j < 128; ++j)
+                        if (j > hi || j < lo) r[j] = 0xFF800000u;
+                }
+                if constexpr (!kInt8) {
+                    const TileMask mk = sm.mask[info];
+                    if ((mk.w[0] & mk.w[1] & mk.w[2] & mk.w[3]) != 0xFFFFFFFFu) {
+#pragma unroll
+                        for (int j = 0; j < 128; ++j)
+                            if (!((mk.w[j >> 5] >> (j & 31)) & 1u)) r[j] = 0xFF800000u;
+                    }
+                }
+                float mx[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mx[j] = __uint_as_float(r[j]);
+#pragma unroll
+                for (int j = 4; j < 128; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(r[j]));
+                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                if constexpr (!kInt8) top *= c;   // (c > 0)
+                // the reference moves when the maximum passes it by the slack
+                float alpha = 1.0f;
+                if (top > m + kSlack || (m == -INFINITY && top > m)) {
+                    alpha = ex2(m - top);
+                    m = top;
+                    l *= alpha;
+                }
+                if (__any_sync(0xFFFFFFFFu, alpha != 1.0f) && !first) {
+                    // (the products before this tile's scores are done with O)
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t o[32];
+                        tmem_ld_32cols_sync(to + q * 32, o);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                        tmem_st_32cols(to + q * 32, o);
+                    }
+                }
+                first = false;
+                const float mu = m == -INFINITY ? 0.0f : m;   // a row that has seen nothing
+                const unsigned long long m2 = f2_bits(-mu, -mu), c2 = f2_bits(c, c);
+                unsigned long long l2[2] = {f2_bits(0.0f, 0.0f), f2_bits(0.0f, 0.0f)};
+                const float4 *i4 = reinterpret_cast<const float4 *>(sm.iv[kInt8 ? info : 0]);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int j = q * 64 + 4 * i;
+                        float y[4];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const unsigned long long v =
+                                f2_bits(__uint_as_float(r[j + 2 * e]), __uint_as_float(r[j + 2 * e + 1]));
+                            f2_split(kInt8 ? f2_add(v, m2) : f2_fma(v, c2, m2), y[2 * e], y[2 * e + 1]);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) y[e] = ex2(y[e]);
+                        if constexpr (kInt8) {
+                            const float4 iv = i4[q * 16 + i];
+                            l2[0] = f2_fma(f2_bits(y[0], y[1]), f2_bits(iv.x, iv.y), l2[0]);
+                            l2[1] = f2_fma(f2_bits(y[2], y[3]), f2_bits(iv.z, iv.w), l2[1]);
+                            pk[2 * i] = pack_f16x2(y[0], y[1]);
+                            pk[2 * i + 1] = pack_f16x2(y[2], y[3]);
+                        } else {
+                            l2[0] = f2_add(l2[0], f2_bits(y[0], y[1]));
+                            l2[1] = f2_add(l2[1], f2_bits(y[2], y[3]));
+                            pk[2 * i] = pack_bf16x2(y[0], y[1]);
+                            pk[2 * i + 1] = pack_bf16x2(y[2], y[3]);
+                        }
+                    }
+                    tmem_st_32cols(ts + q * 32, pk);
+                }
+                float la, lb, lc, ld;
+                f2_split(l2[0], la, lb);
+                f2_split(l2[1], lc, ld);
+                l += (la + lb) + (lc + ld);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(bar(sm.p_full[h]));
+            }
+            if (work) it += static_cast<uint32_t>(p.last - p.first);
+            // ---- the item's (or the share's) result of this row
+            const bool any = work && t.upto > t.from;
+            if (any) {
+                if (ok)
+                    ok = mbar_wait(bar(sm.o_done[h]), on & 1, abort, a.err, ROLE_EPILOGUE, 4,
+                                   kWaitLimitNs, KID_ATTN);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                ++on;
+            }
+            if (!ok) break;
+            tc_fence_after();
+            if (t.exists) {
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                const int irow = h * a.half_tokens * a.o.G + row;   // the item's row
+                float *part = slot_of(a.ws, kPagedTileRows, blockIdx.x, p.slot);
+                const int64_t orow =
+                    (static_cast<int64_t>(w.r.t0) + p.tok0 + h * a.half_tokens + tok) * a.o.Hq +
+                    static_cast<int64_t>(w.h) * a.o.G + (row - tok * a.o.G);
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t o[32];
+                    if (any) {
+                        tmem_ld_32cols_sync(to + q * 32, o);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = 0u;
+                    }
+                    if (mine_row) {
+                        const float f = p.whole ? inv : 1.0f;
+                        if (!p.whole || a.o.fp32) {
+                            float4 *dst = reinterpret_cast<float4 *>(
+                                (p.whole ? static_cast<float *>(a.o.out) + orow * kHeadDim
+                                         : part + static_cast<int64_t>(irow) * kHeadDim) +
+                                q * 32);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                dst[j] = make_float4(__uint_as_float(o[4 * j]) * f,
+                                                     __uint_as_float(o[4 * j + 1]) * f,
+                                                     __uint_as_float(o[4 * j + 2]) * f,
+                                                     __uint_as_float(o[4 * j + 3]) * f);
+                        } else {
+                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o.out) +
+                                                                   orow * kHeadDim + q * 32);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                uint32_t u[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    u[e] = pack_bf16x2(__uint_as_float(o[8 * j + 2 * e]) * f,
+                                                       __uint_as_float(o[8 * j + 2 * e + 1]) * f);
+                                dst[j] = make_uint4(u[0], u[1], u[2], u[3]);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (!p.whole && mine_row) {
+                    part[kPagedTileRows * kHeadDim + irow] = m * kLn2;
+                    part[kPagedTileRows * (kHeadDim + 1) + irow] = l;
+                }
+                if (any) {
+                    tc_fence_before();
+                    mbar_arrive(bar(sm.o_free[h]));
+                }
+            }
+        }
+    } else if (warp < 12) {
+        setmaxnreg_dec<kOtherRegs>();
+        if (warp == 8 && lane == 0 && mine) {
+            // ------------------------------------------------------ the products
+            const uint32_t idesc = kInt8 ? idesc_f16_f32(128, 128) : idesc_bf16_f32(128, 128);
+            uint32_t pn[2] = {0, 0}, on[2] = {0, 0};
+            bool ok = true;
+            for (; ok && !w.done(s, sh.end); w.next(s)) {
+                const PagedPiece p = paged_piece(s, w, sh.begin, sh.end);
+                if (p.last <= p.first) continue;
+                HalfTiles t[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    t[h] = half_tiles(s, w, p, h, a.half_tokens);
+                    if (!t[h].exists) continue;
+                    if (ok)
+                        ok = mbar_wait(bar(sm.q_full[h]), qn[h] & 1, abort, a.err, ROLE_MMA, 1,
+                                       kWaitLimitNs, KID_ATTN);
+                    ++qn[h];
+                    if (t[h].upto == t[h].from) mma_commit(bar(sm.q_empty[h]));
+                }
+                const int cb = p.tile0 + p.first, ce = p.tile0 + p.last;
+                auto wait_op = [&](uint32_t u, unsigned site) {
+                    if (ok)
+                        ok = mbar_wait(bar(sm.op_full[u % kOps]), (u / kOps) & 1, abort, a.err,
+                                       ROLE_MMA, site, kWaitLimitNs, KID_ATTN);
+                    tc_fence_after();
+                };
+                auto scores = [&](int h, uint32_t u, int x) {
+                    const uint32_t q = smem_u32(sm.q[h]), k = smem_u32(sm.op[u % kOps]);
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk) {
+                        const uint32_t off = (kk >> 2) * (kOperandBytes / 2) + (kk & 3) * 32;
+                        mma_f16_ss(tmem + h * 128, smem_desc_sw128(q + off), smem_desc_sw128(k + off),
+                                   idesc, kk > 0 ? 1u : 0u);
+                    }
+                    mma_commit(bar(sm.s_full[h]));
+                    if (x == t[h].upto - 1) mma_commit(bar(sm.q_empty[h]));
+                };
+                wait_op(2 * it, 2);
+                if (!ok) break;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (t[h].from <= cb && cb < t[h].upto) scores(h, 2 * it, cb);
+                mma_commit(bar(sm.op_empty[(2 * it) % kOps]));
+                for (int x = cb; x < ce && ok; ++x, ++it) {
+                    const uint32_t uv = 2 * it + 1, uk = 2 * it + 2;
+                    wait_op(uv, 3);
+                    if (!ok) break;
+                    bool have_k = false;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (ok && t[h].from <= x && x < t[h].upto) {
+                            ok = mbar_wait(bar(sm.p_full[h]), pn[h] & 1, abort, a.err, ROLE_MMA, 4,
+                                           kWaitLimitNs, KID_ATTN);
+                            if (ok && x == t[h].from && on[h] > 0)
+                                ok = mbar_wait(bar(sm.o_free[h]), (on[h] - 1) & 1, abort, a.err,
+                                               ROLE_MMA, 5, kWaitLimitNs, KID_ATTN);
+                            if (!ok) break;
+                            ++pn[h];
+                            tc_fence_after();
+                            const uint32_t v = smem_u32(sm.op[uv % kOps]);
+#pragma unroll
+                            for (int kk = 0; kk < 8; ++kk)
+                                mma_f16_tmemA(tmem + 256 + h * 128, tmem + h * 128 + kk * 8,
+                                              smem_desc_nmajor(v + kk * 2048), idesc | kBNMajor,
+                                              kk > 0 || x > t[h].from ? 1u : 0u);
+                            if (x == t[h].upto - 1) {
+                                mma_commit(bar(sm.o_done[h]));
+                                ++on[h];
+                            }
+                        }
+                        if (x + 1 < ce && t[h].from <= x + 1 && x + 1 < t[h].upto) {
+                            if (!have_k) wait_op(uk, 6);
+                            if (!ok) break;
+                            have_k = true;
+                            scores(h, uk, x + 1);
+                        }
+                    }
+                    if (!ok) break;
+                    mma_commit(bar(sm.op_empty[uv % kOps]));
+                    if (x + 1 < ce) {
+                        if (!have_k) wait_op(uk, 7);
+                        mma_commit(bar(sm.op_empty[uk % kOps]));
+                    }
+                }
+            }
+            // nothing may be in flight when tensor memory is freed and the CTA ends
+            mma_commit(bar(sm.drain));
+            int never = 0;
+            mbar_wait(bar(sm.drain), 0, &never, a.err, ROLE_MMA, 8, kWaitLimitNs, KID_ATTN);
+        } else if (warp == 9 && mine) {
+            // ---------------------------------------------------------- the loads
+            bool ok = true;
+            uint32_t u = 0, fixes = 0;   // operand tiles, V tiles made zero in places
+            for (; ok && !w.done(s, sh.end); w.next(s)) {
+                const PagedPiece p = paged_piece(s, w, sh.begin, sh.end);
+                if (p.last <= p.first) continue;
+                int lo, hi;
+                request_span(s, w.r, lo, hi);
+                for (int x = p.first; x < p.last && ok; ++x, ++it) {
+                    const TileBoxes tb = find_boxes(a.c, w.b, w.h, p.tile0 + x, lo, hi, a.err);
+                    const int info = it % kInfo;
+                    const bool full = (tb.mask.w[0] & tb.mask.w[1] & tb.mask.w[2] & tb.mask.w[3]) ==
+                                      0xFFFFFFFFu;
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv, ++u) {
+                        constexpr uint32_t kSlots = kInt8 ? kRaws : kOps;
+                        const uint32_t sl = u % kSlots;
+                        uint64_t &full_bar = kInt8 ? sm.raw_full[sl] : sm.op_full[sl];
+                        uint64_t &empty_bar = kInt8 ? sm.raw_empty[sl] : sm.op_empty[sl];
+                        if (ok && u >= kSlots)
+                            ok = mbar_wait(bar(empty_bar), (u / kSlots - 1) & 1, abort, a.err,
+                                           ROLE_PRODUCER, 1, kWaitLimitNs, KID_ATTN);
+                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        if (!ok) break;
+                        const uint32_t dst = kInt8 ? smem_u32(sm.raw[sl]) : smem_u32(sm.op[sl]);
+                        // A V tile with masked positions is made zero there
+                        // (BF16: whatever lies in them, times a weight of zero,
+                        // need not be zero) before the products may read it.
+                        const bool mend = !kInt8 && kv == 1 && !full;
+                        const uint32_t b = mend ? bar(sm.fix) : bar(full_bar);
+                        if (lane == 0) {
+                            if (kv == 0) sm.mask[info] = tb.mask;
+                            mbar_arrive_expect_tx(b, tile_bytes<kInt8>(a.c, tb) +
+                                                         (kInt8 && kv == 0 ? 2 * scale_bytes(a.c, tb) : 0));
+                            if (!kInt8 && kv == 0) mbar_arrive(bar(sm.info_full[info]));
+                        }
+                        __syncwarp();
+                        copy_boxes<kInt8>(a.c, tb, kv == 0 ? &km : &vm, dst, b);
+                        if constexpr (kInt8) {
+                            if (kv == 0) {
+                                copy_scales(a.c, tb, a.c.ks, smem_u32(sm.rks[info]), b);
+                                copy_scales(a.c, tb, a.c.vs, smem_u32(sm.rvs[info]), b);
+                            }
+                        }
+                        if (mend) {
+                            ok = mbar_wait(b, fixes & 1, abort, a.err, ROLE_PRODUCER, 2, kWaitLimitNs,
+                                           KID_ATTN);
+                            ++fixes;
+                            for (int i = lane; i < kOperandBytes / 16; i += 32) {
+                                const int r = (i >> 3) & 127;
+                                if (!((tb.mask.w[r >> 5] >> (r & 31)) & 1u))
+                                    reinterpret_cast<uint4 *>(sm.op[sl])[i] = make_uint4(0, 0, 0, 0);
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(bar(full_bar));
+                        }
+                        if (kv == 0 && x == p.first) {
+                            // the item's q, once the item before is done with its own
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                if (h * a.half_tokens >= p.ntok) continue;
+                                if (ok && qn[h] > 0)
+                                    ok = mbar_wait(bar(sm.q_empty[h]), (qn[h] - 1) & 1, abort, a.err,
+                                                   ROLE_PRODUCER, 3, kWaitLimitNs, KID_ATTN);
+                                ok = __all_sync(0xFFFFFFFFu, ok);
+                                if (!ok) break;
+                                ++qn[h];
+                                if (lane == 0) {
+                                    const uint32_t qb = bar(kInt8 ? sm.q_land[h] : sm.q_full[h]);
+                                    mbar_arrive_expect_tx(qb, a.half_tokens * a.o.G * kHeadDim * 2);
+#pragma unroll
+                                    for (int d = 0; d < 2; ++d)
+                                        tma_load_3d(smem_u32(sm.q[h]) + d * (kOperandBytes / 2), &qm,
+                                                    d * 64, w.h * a.o.G,
+                                                    w.r.t0 + p.tok0 + h * a.half_tokens, qb);
+                                }
+                                __syncwarp();
+                            }
+                        }
+                    }
+                }
+            }
+            if (!ok) {   // nothing may be in flight when the CTA ends
+                int never = 0;
+                constexpr uint32_t kSlots = kInt8 ? kRaws : kOps;
+                for (uint32_t x = u > kSlots ? u - kSlots : 0; x < u; ++x)
+                    mbar_wait(bar(kInt8 ? sm.raw_full[x % kSlots] : sm.op_full[x % kSlots]),
+                              (x / kSlots) & 1, &never, a.err, ROLE_PRODUCER, 4, kWaitLimitNs, KID_ATTN);
+                for (int h = 0; h < 2; ++h)
+                    if (qn[h] > 0)
+                        mbar_wait(bar(kInt8 ? sm.q_land[h] : sm.q_full[h]), (qn[h] - 1) & 1, &never,
+                                  a.err, ROLE_PRODUCER, 5, kWaitLimitNs, KID_ATTN);
+            }
+        }
+    } else {
+        setmaxnreg_dec<kOtherRegs>();
+        if constexpr (kInt8) {
+            // ---------------------------------------------------- INT8 to fp16
+            const int ct = tid - 384;               // 0 .. 127
+            const int cw = ct >> 5;
+            bool ok = true;
+            uint32_t u = 0;
+            for (; mine && ok && !w.done(s, sh.end); w.next(s)) {
+                const PagedPiece p = paged_piece(s, w, sh.begin, sh.end);
+                if (p.last <= p.first) continue;
+                for (int x = p.first; x < p.last && ok; ++x, ++it) {
+                    const int info = it % kInfo;
+                    for (int kv = 0; kv < 2; ++kv, ++u) {
+                        const uint32_t rs = u % kRaws, os = u % kOps;
+                        ok = ok && mbar_wait(bar(sm.raw_full[rs]), (u / kRaws) & 1, abort, a.err,
+                                             ROLE_CONVERT, 1, kWaitLimitNs, KID_ATTN);
+                        if (ok && u >= kOps)
+                            ok = mbar_wait(bar(sm.op_empty[os]), (u / kOps - 1) & 1, abort, a.err,
+                                           ROLE_CONVERT, 2, kWaitLimitNs, KID_ATTN);
+                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        if (!ok) break;
+                        if (kv == 0) {
+                            // what the softmax takes of the scales, one position per thread
+                            const bool live = (sm.mask[info].w[ct >> 5] >> (ct & 31)) & 1u;
+                            const float v = fmaxf(sm.rvs[info][ct], 0x1p-100f);
+                            const float vn = sm.rvs[info][ct] == sm.rvs[info][ct] ? v : sm.rvs[info][ct];
+                            sm.ks[info][ct] = live ? sm.rks[info][ct] : 0.0f;
+                            sm.lv[info][ct] = live ? log2f(vn) : -INFINITY;
+                            sm.iv[info][ct] = live ? 1.0f / vn : 0.0f;
+                            mbar_arrive(bar(sm.info_full[info]));
+                        }
+                        // 16 codes to 32 bytes at a time. Eight lanes take pieces 0-3
+                        // (4-7) of rows r and r ^ 5: reads and writes through the
+                        // swizzle then fall in distinct banks.
+                        const uint8_t *src = sm.raw[rs];
+                        uint8_t *dst = sm.op[os];
+                        const int pc = (lane & 3) + ((lane >> 3) & 1) * 4;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int pi = (i & 1) * 2 + (lane >> 4);
+                            const int r = cw * 32 + (i >> 1) * 8 + ((lane & 4) ? pi ^ 5 : pi);
+                            const uint4 y = *reinterpret_cast<const uint4 *>(
+                                src + r * 128 + ((pc ^ (r & 7)) << 4));
+                            uint4 e, f;
+                            i8x4_to_f16x4(y.x, e.x, e.y);
+                            i8x4_to_f16x4(y.y, e.z, e.w);
+                            i8x4_to_f16x4(y.z, f.x, f.y);
+                            i8x4_to_f16x4(y.w, f.z, f.w);
+                            uint8_t *d = dst + (pc >> 2) * (kOperandBytes / 2) + r * 128;
+                            const int dp = (pc & 3) * 2;
+                            *reinterpret_cast<uint4 *>(d + ((dp ^ (r & 7)) << 4)) = e;
+                            *reinterpret_cast<uint4 *>(d + (((dp + 1) ^ (r & 7)) << 4)) = f;
+                        }
+                        fence_proxy_async_smem();
+                        mbar_arrive(bar(sm.op_full[os]));
+                        mbar_arrive(bar(sm.raw_empty[rs]));
+                        if (kv == 0 && x == p.first) {
+                            // the item's q to fp16, one row per thread, each scaled so that
+                            // its largest value lies in [2^14, 2^15)
+                            for (int h = 0; h < 2; ++h) {
+                                if (h * a.half_tokens >= p.ntok) continue;
+                                ok = ok && mbar_wait(bar(sm.q_land[h]), qn[h] & 1, abort, a.err,
+                                                     ROLE_CONVERT, 3, kWaitLimitNs, KID_ATTN);
+                                ++qn[h];
+                                if (!ok) break;
+                                uint32_t mq = 0;
+#pragma unroll 4
+                                for (int j = 0; j < 16; ++j) {
+                                    const uint4 y = *reinterpret_cast<const uint4 *>(
+                                        sm.q[h] + (j >> 3) * (kOperandBytes / 2) + ct * 128 +
+                                        (((j & 7) ^ (ct & 7)) << 4));
+                                    mq = max(mq, amax_bits8(y));
+                                }
+                                const int be = static_cast<int>(mq >> 7);
+                                const int se = be == 0 ? 0 : max(-100, min(100, 14 - (be - 127)));
+                                const float qs = __uint_as_float(static_cast<uint32_t>(se + 127) << 23);
+                                sm.qinv[h][ct] = __uint_as_float(static_cast<uint32_t>(127 - se) << 23);
+#pragma unroll 4
+                                for (int j = 0; j < 16; ++j) {
+                                    uint4 *at = reinterpret_cast<uint4 *>(
+                                        sm.q[h] + (j >> 3) * (kOperandBytes / 2) + ct * 128 +
+                                        (((j & 7) ^ (ct & 7)) << 4));
+                                    uint4 y = *at;
+                                    uint32_t *yw = reinterpret_cast<uint32_t *>(&y);
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e)
+                                        yw[e] = pack_f16x2(__uint_as_float(yw[e] << 16) * qs,
+                                                           __uint_as_float(yw[e] & 0xFFFF0000u) * qs);
+                                    *at = y;
+                                }
+                                fence_proxy_async_smem();
+                                mbar_arrive(bar(sm.q_full[h]));
+                            }
+                        }
+                    }
+                }
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+// q as [T, Hq, 128]: a box is 64 dimensions x the G heads of a kv head x the
+// whole tokens of a half.
+bool encode_q(CUtensorMap *map, const PagedAttnProblem &p, int half_tokens) {
+    auto fn = tensor_map_encode_fn();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(p.Hq), static_cast<cuuint64_t>(p.T)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(p.qh) * 2, static_cast<cuuint64_t>(p.qt) * 2};
+    cuuint32_t bx[3] = {64, static_cast<cuuint32_t>(p.Hq / p.Hkv),
+                        static_cast<cuuint32_t>(half_tokens)};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t *>(p.q), dims, strides,
+              bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kInt8>
+cudaError_t launch_kind(const PagedAttnProblem &p, const PagedSetup &u, int ctas,
+                        unsigned long long *err, cudaStream_t stream) {
+    auto kernel = paged_tiles_kernel<kInt8>;
+    const size_t smem = sizeof(TilesSmem<kInt8>) + 1024;
+    static_assert(sizeof(TilesSmem<kInt8>) + 1024 <= 227 * 1024, "shared memory");
+    static int attr_done[64] = {0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!attr_done[dev]) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+        attr_done[dev] = 1;
+    }
+    TilesArgs a;
+    a.s = u.s;
+    a.c = u.c;
+    a.o = u.o;
+    a.half_tokens = kHalfRows / u.o.G;
+    a.scale_log2 = p.scale * kLog2e;
+    a.ws = static_cast<float *>(p.workspace);
+    a.err = err;
+    CUtensorMap qm, km, vm;
+    if (!encode_q(&qm, p, a.half_tokens) || !paged_encode_cache(&km, p.kc, kInt8, p) ||
+        !paged_encode_cache(&vm, p.vc, kInt8, p))
+        return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, qm, km, vm, a);
+    if (e != cudaSuccess) return e;
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_tiles(const PagedAttnProblem &p, const PagedSetup &u, int ctas,
+                               unsigned long long *err, cudaStream_t stream) {
+    return p.ks != nullptr ? launch_kind<true>(p, u, ctas, err, stream)
+                           : launch_kind<false>(p, u, ctas, err, stream);
+}
+
+}  // namespace w8a8
