@@ -15,6 +15,7 @@ paged_kv_plan (block tables and slots), paged_kv_write, attention_paged.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -141,9 +142,19 @@ def _check(status: int, what: str) -> None:
         raise W8A8Error(status, what)
 
 
+def _current_raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# The handle of the current stream without a Stream object around it (3 us of a
+# decode-sized call on the host), where torch has that.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_raw_stream)
+
+
 def _stream(stream: Optional[torch.cuda.Stream]) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is None:
+        return _current_raw_stream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -174,13 +185,16 @@ def _require_workspace(ws: torch.Tensor, device: torch.device) -> None:
         raise ValueError(f"workspace: expected a contiguous uint8 tensor on {device}")
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on_device(device: torch.device, stream: Optional[torch.cuda.Stream]):
     """Makes the operands' device current for the call (the library resolves
     per-device state, such as its built-in scratch, on the current device);
     a stream of another device is refused."""
     if stream is not None and stream.device != device:
         raise ValueError(f"stream belongs to {stream.device}, the operands to {device}")
-    return torch.cuda.device(device)
+    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 def _empty(shape, dtype: torch.dtype, device: torch.device,
@@ -189,6 +203,8 @@ def _empty(shape, dtype: torch.dtype, device: torch.device,
     runs on: the allocator may hand it out again only in that stream's order."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
+    if stream.device != device:
+        raise ValueError(f"stream belongs to {stream.device}, the operands to {device}")
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
