@@ -94,27 +94,39 @@ struct TilesSmem {
     volatile int abort_flag;
 };
 
-// D[tmem] (+)= A[smem] * B[smem], kind::f16, cta_group::1.
-__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                           uint32_t accumulate) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
+// Shared-memory operand descriptors, all with the 128-byte swizzle and 8-row
+// groups 1024 bytes apart: the upper word is one constant, the lower word the
+// address and the leading offset, in units of 16 bytes. One thread issues every
+// product, so what it computes per instruction counts: with whole descriptors
+// built from addresses an instruction took 140 cycles to issue, against the 64
+// that the tensor core needs for it.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_kmajor(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+// N-major: rows of k (128 bytes: 64 values of n); the next 64 values of n lie
+// half an operand further (leading offset).
+__device__ __forceinline__ uint32_t desc_nmajor(uint32_t saddr) {
+    return (saddr >> 4) | (static_cast<uint32_t>(kOperandBytes / 2 / 16) << 16);
 }
 
-// Descriptor of an N-major operand tile with the 128-byte swizzle: rows of k
-// (128 bytes: 64 values of n), 8-row groups 1024 bytes apart (stride offset),
-// the next 64 values of n 16 KB further (leading offset).
-__device__ __forceinline__ uint64_t smem_desc_nmajor(uint32_t saddr) {
-    uint64_t d = 0;
-    d |= static_cast<uint64_t>((saddr & 0x3FFFF) >> 4);
-    d |= static_cast<uint64_t>((kOperandBytes / 2) >> 4) << 16;
-    d |= static_cast<uint64_t>(1024 >> 4) << 32;
-    d |= static_cast<uint64_t>(1) << 46;
-    d |= static_cast<uint64_t>(2) << 61;
-    return d;
+// D[tmem] (+)= A * B, kind::f16, cta_group::1; A from shared memory or from
+// tensor memory.
+template <bool kAccumulate>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n"
+        " mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "n"(kAccumulate ? 1 : 0), "n"(kDescHi)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.b32 p, %4, 0;\n"
+        " mov.b64 db, {%2, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHi)
+        : "memory");
 }
 constexpr uint32_t kBNMajor = 1u << 16;   // instruction descriptor: B is N-major
 
@@ -148,6 +160,13 @@ __device__ __forceinline__ void tmem_st_32cols(uint32_t t, const uint32_t (&r)[3
             W8A8_I16(r, 0),
         W8A8_I16(r, 16), "r"(t)
         : "memory");
+}
+
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -467,93 +486,112 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
         }
     } else if (warp < 12) {
         setmaxnreg_dec<kOtherRegs>();
-        if (warp == 8 && lane == 0 && mine) {
+        if (warp == 8 && mine) {
             // ------------------------------------------------------ the products
-            const uint32_t idesc = kInt8 ? idesc_f16_f32(128, 128) : idesc_bf16_f32(128, 128);
+            // The whole warp walks, waits and counts, on values made uniform
+            // (u()), and one elected lane issues: the products' operands then
+            // stay in uniform registers.
+            constexpr uint32_t idesc = kInt8 ? idesc_f16_f32(128, 128) : idesc_bf16_f32(128, 128);
+            auto u = [](auto v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
+            const uint32_t q0 = u(desc_kmajor(smem_u32(sm.q))), k0 = u(desc_kmajor(smem_u32(sm.op)));
+            const uint32_t v0 = u(desc_nmajor(smem_u32(sm.op)));
+            const uint32_t tm = u(tmem);
+            const bool leader = elect_one();
             uint32_t pn[2] = {0, 0}, on[2] = {0, 0};
+            uint32_t sk = 0, ph = 0;     // slot and phase of the next operand tile
             bool ok = true;
-            for (; ok && !w.done(s, sh.end); w.next(s)) {
+            auto wait = [&](uint64_t &b, uint32_t phase, unsigned site) {
+                ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(bar(b), phase & 1, abort, a.err, ROLE_MMA,
+                                                             site, kWaitLimitNs, KID_ATTN));
+                tc_fence_after();
+            };
+            for (; ok && u(!w.done(s, sh.end)); w.next(s)) {
                 const PagedPiece p = paged_piece(s, w, sh.begin, sh.end);
-                if (p.last <= p.first) continue;
-                HalfTiles t[2];
+                const int cb = u(p.tile0 + p.first), ce = u(p.tile0 + p.last);
+                if (ce <= cb) continue;
+                int from[2], upto[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    t[h] = half_tiles(s, w, p, h, a.half_tokens);
-                    if (!t[h].exists) continue;
-                    if (ok)
-                        ok = mbar_wait(bar(sm.q_full[h]), qn[h] & 1, abort, a.err, ROLE_MMA, 1,
-                                       kWaitLimitNs, KID_ATTN);
-                    ++qn[h];
-                    if (t[h].upto == t[h].from) mma_commit(bar(sm.q_empty[h]));
+                    const HalfTiles t = half_tiles(s, w, p, h, a.half_tokens);
+                    from[h] = u(t.from);
+                    upto[h] = u(t.upto);
+                    if (!u(t.exists)) continue;
+                    wait(sm.q_full[h], qn[h]++, 1);
+                    if (upto[h] == from[h] && leader) mma_commit(bar(sm.q_empty[h]));
                 }
-                const int cb = p.tile0 + p.first, ce = p.tile0 + p.last;
-                auto wait_op = [&](uint32_t u, unsigned site) {
-                    if (ok)
-                        ok = mbar_wait(bar(sm.op_full[u % kOps]), (u / kOps) & 1, abort, a.err,
-                                       ROLE_MMA, site, kWaitLimitNs, KID_ATTN);
-                    tc_fence_after();
-                };
-                auto scores = [&](int h, uint32_t u, int x) {
-                    const uint32_t q = smem_u32(sm.q[h]), k = smem_u32(sm.op[u % kOps]);
+                if (!ok) break;
+                auto scores = [&](int h, uint32_t slot, int x) {
+                    const uint32_t q = q0 + h * (kOperandBytes / 16);
+                    const uint32_t k = k0 + slot * (kOperandBytes / 16);
+                    if (leader) {
+                        mma_ss<false>(tm + h * 128, q, k, idesc);
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) {
-                        const uint32_t off = (kk >> 2) * (kOperandBytes / 2) + (kk & 3) * 32;
-                        mma_f16_ss(tmem + h * 128, smem_desc_sw128(q + off), smem_desc_sw128(k + off),
-                                   idesc, kk > 0 ? 1u : 0u);
+                        for (int kk = 1; kk < 8; ++kk) {
+                            const uint32_t off = (kk >> 2) * (kOperandBytes / 32) + (kk & 3) * 2;
+                            mma_ss<true>(tm + h * 128, q + off, k + off, idesc);
+                        }
+                        mma_commit(bar(sm.s_full[h]));
+                        if (x == upto[h] - 1) mma_commit(bar(sm.q_empty[h]));
                     }
-                    mma_commit(bar(sm.s_full[h]));
-                    if (x == t[h].upto - 1) mma_commit(bar(sm.q_empty[h]));
+                    __syncwarp();
                 };
-                wait_op(2 * it, 2);
+                auto advance = [&]() {
+                    if (++sk == kOps) {
+                        sk = 0;
+                        ph ^= 1;
+                    }
+                };
+                wait(sm.op_full[sk], ph, 2);
                 if (!ok) break;
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    if (t[h].from <= cb && cb < t[h].upto) scores(h, 2 * it, cb);
-                mma_commit(bar(sm.op_empty[(2 * it) % kOps]));
-                for (int x = cb; x < ce && ok; ++x, ++it) {
-                    const uint32_t uv = 2 * it + 1, uk = 2 * it + 2;
-                    wait_op(uv, 3);
+                    if (from[h] <= cb && cb < upto[h]) scores(h, sk, cb);
+                if (leader) mma_commit(bar(sm.op_empty[sk]));
+                advance();
+                for (int x = cb; x < ce; ++x) {
+                    const uint32_t sv = sk;
+                    wait(sm.op_full[sk], ph, 3);
                     if (!ok) break;
+                    advance();
                     bool have_k = false;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        if (ok && t[h].from <= x && x < t[h].upto) {
-                            ok = mbar_wait(bar(sm.p_full[h]), pn[h] & 1, abort, a.err, ROLE_MMA, 4,
-                                           kWaitLimitNs, KID_ATTN);
-                            if (ok && x == t[h].from && on[h] > 0)
-                                ok = mbar_wait(bar(sm.o_free[h]), (on[h] - 1) & 1, abort, a.err,
-                                               ROLE_MMA, 5, kWaitLimitNs, KID_ATTN);
+                        if (from[h] <= x && x < upto[h]) {
+                            wait(sm.p_full[h], pn[h]++, 4);
+                            if (ok && x == from[h] && on[h] > 0) wait(sm.o_free[h], on[h] - 1, 5);
                             if (!ok) break;
-                            ++pn[h];
-                            tc_fence_after();
-                            const uint32_t v = smem_u32(sm.op[uv % kOps]);
+                            const uint32_t v = v0 + sv * (kOperandBytes / 16);
+                            if (leader) {
+                                mma_ts(tm + 256 + h * 128, tm + h * 128, v, idesc | kBNMajor,
+                                       x > from[h] ? 1u : 0u);
 #pragma unroll
-                            for (int kk = 0; kk < 8; ++kk)
-                                mma_f16_tmemA(tmem + 256 + h * 128, tmem + h * 128 + kk * 8,
-                                              smem_desc_nmajor(v + kk * 2048), idesc | kBNMajor,
-                                              kk > 0 || x > t[h].from ? 1u : 0u);
-                            if (x == t[h].upto - 1) {
-                                mma_commit(bar(sm.o_done[h]));
-                                ++on[h];
+                                for (int kk = 1; kk < 8; ++kk)
+                                    mma_ts(tm + 256 + h * 128, tm + h * 128 + kk * 8, v + kk * 128,
+                                           idesc | kBNMajor, 1u);
+                                if (x == upto[h] - 1) mma_commit(bar(sm.o_done[h]));
                             }
+                            __syncwarp();
+                            if (x == upto[h] - 1) ++on[h];
                         }
-                        if (x + 1 < ce && t[h].from <= x + 1 && x + 1 < t[h].upto) {
-                            if (!have_k) wait_op(uk, 6);
+                        if (x + 1 < ce && from[h] <= x + 1 && x + 1 < upto[h]) {
+                            if (!have_k) wait(sm.op_full[sk], ph, 6);
                             if (!ok) break;
                             have_k = true;
-                            scores(h, uk, x + 1);
+                            scores(h, sk, x + 1);
                         }
                     }
                     if (!ok) break;
-                    mma_commit(bar(sm.op_empty[uv % kOps]));
+                    if (leader) mma_commit(bar(sm.op_empty[sv]));
                     if (x + 1 < ce) {
-                        if (!have_k) wait_op(uk, 7);
-                        mma_commit(bar(sm.op_empty[uk % kOps]));
+                        if (!have_k) wait(sm.op_full[sk], ph, 7);
+                        if (leader) mma_commit(bar(sm.op_empty[sk]));
+                        advance();
                     }
                 }
             }
             // nothing may be in flight when tensor memory is freed and the CTA ends
-            mma_commit(bar(sm.drain));
+            if (leader) mma_commit(bar(sm.drain));
+            __syncwarp();
             int never = 0;
             mbar_wait(bar(sm.drain), 0, &never, a.err, ROLE_MMA, 8, kWaitLimitNs, KID_ATTN);
         } else if (warp == 9 && mine) {
