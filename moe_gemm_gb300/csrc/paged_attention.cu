@@ -236,7 +236,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant_
                 const int r = 8 * nt + 2 * t + j;
                 const int pos = w.r.base + p.tok0 + r / a.o.G;
                 upto[nt][j] = r < rows ? pos + 1 : 0;
-                from[nt][j] = s.window > 0 ? pos - s.window + 1 : 0;
+                from[nt][j] = s.window > 0 ? max(pos, 0) - s.window + 1 : 0;
             }
         // tiles that every row sees whole need no mask
         const int pos_first = w.r.base + p.tok0, pos_last = pos_first + p.ntok - 1;

@@ -119,7 +119,7 @@ __device__ __forceinline__ uint32_t scale_bytes(const PagedCache &c, const TileB
 // outside them is read.
 __device__ __forceinline__ void request_span(const PagedSchedule &s, const PagedRequest &r, int &lo,
                                              int &hi) {
-    lo = s.window > 0 ? max(r.base - s.window + 1, 0) : 0;
+    lo = s.window > 0 ? max(max(r.base, 0) - s.window + 1, 0) : 0;
     hi = r.kv;
 }
 

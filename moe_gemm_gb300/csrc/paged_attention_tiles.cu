@@ -14,23 +14,29 @@
 //
 // Tensor memory: S0, S1, O0, O1 of 128 columns each (all 512).
 //
-// The reference that the running maximum gives the exponentials moves only
-// when a tile's maximum passes it by more than 8 (in log2): weights are then up
-// to 2^8 instead of 1, which costs no accuracy, and O is rescaled a few times
-// per item instead of at every tile. Sums and statistics are FP32.
+// The reference m of the exponentials p_j = 2^(t_j - m) (t: scores in log2 units)
+// is a maximum that was seen, not the running one: it stays while the tile's
+// sums show that no weight passes 2^8, so most tiles take no maximum at all, and
+// O is rescaled a few times per item instead of at every tile. Weights above 1
+// cost no accuracy. Sums and statistics are FP32.
 //
 // BF16 pages: P is rounded to BF16 for the product (half a step 2^-8 of each
 // weight; V is BF16, and both operands have one type).
 // INT8 pages: a converter warpgroup widens the codes to fp16 (exact) into
 // shared memory. Scores are S * (k scale); a weight carries its v scale,
-//   P_j = 2^(s_j + log2 vs_j - m), m the running maximum of s_j + log2 vs_j,
-// so P is at most 2^8 whatever the scales' range, and is rounded to fp16 (half a step
-// 2^-11); the denominator adds P_j / vs_j. q goes to fp16 too, each row scaled
-// by a power of two that the scores take back exactly. Scales below 2^-100
-// count as 2^-100.
+// P_j = p_j * vs_j * 2^-e, rounded to fp16 (half a step 2^-11). e follows the
+// largest v scale of the tiles so far (P stays below 2^12, and what falls below
+// fp16's normal range is under 2^-25 of the largest), and O is in units of 2^e.
+// q goes to fp16 too, scaled by one power of two per item, which the k scales
+// take back exactly.
 //
-// Warps: 0-3 and 4-7 softmax of the halves, 8 issues the products, 9 loads,
-// 12-15 convert (INT8).
+// The softmax warps read S in the layout of 16 x 256 bits: a thread has 4 rows
+// and 2 of every 8 columns, so the per-column scales are read from shared memory
+// once for 4 rows (a row per thread reads them for one: the reads alone then
+// took longer than the products).
+//
+// Warps: 0-3 and 4-7 softmax of the halves, 8 and 10 issue the halves'
+// products, 9 loads, 12-15 convert (INT8).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -54,7 +60,7 @@ constexpr int kHalfRows = 128;
 constexpr int kInfo = 4;             // tiles whose mask and scales are kept
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 8.0f;       // log2 by which weights may pass 1
+constexpr float kMaxWeight = 256.0f; // sums of a tile's weights that move the reference
 constexpr int kOperandBytes = 128 * 128 * 2;
 // Registers of a softmax thread and of the others: 2 x 128 x 192 + 2 x 128 x
 // 64 = the 512 x 128 that the block is launched with.
@@ -80,16 +86,18 @@ struct TilesSmem {
     uint8_t op[kOps][kOperandBytes];
     uint8_t raw[kInt8 ? kRaws : 1][kInt8 ? kOperandBytes / 2 : 16];
     float rks[kInfo][kInt8 ? 128 : 4], rvs[kInfo][kInt8 ? 128 : 4];   // scales as stored
-    float ks[kInfo][kInt8 ? 128 : 4];    // k scale
-    float lv[kInfo][kInt8 ? 128 : 4];    // log2 of the v scale, -inf: masked for every query
-    float iv[kInfo][kInt8 ? 128 : 4];    // 1 / v scale
-    float qinv[2][kHalfRows];
+    // of two columns: what a score is multiplied by (to log2 units), then what
+    // its weight is; both 0 where the position is masked for every query
+    float4 col[kInfo][kInt8 ? 64 : 1];
+    float unit[kInfo];                   // 2^e
+    float vmax[2][4];
+    uint32_t qmax[4];
     TileMask mask[kInfo];
     uint64_t op_full[kOps], op_empty[kOps], raw_full[kRaws], raw_empty[kRaws];
     uint64_t info_full[kInfo];
     uint64_t q_land[2], q_full[2], q_empty[2];
     uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
-    uint64_t fix, drain;
+    uint64_t fix, drain[2];
     uint32_t tmem;
     volatile int abort_flag;
 };
@@ -130,33 +138,60 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
 }
 constexpr uint32_t kBNMajor = 1u << 16;   // instruction descriptor: B is N-major
 
-#define W8A8_R16(r, o)                                                                          \
-    "=r"(r[o + 0]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]),             \
-        "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7]), "=r"(r[o + 8]), "=r"(r[o + 9]),         \
-        "=r"(r[o + 10]), "=r"(r[o + 11]), "=r"(r[o + 12]), "=r"(r[o + 13]), "=r"(r[o + 14]),    \
-        "=r"(r[o + 15])
+#define W8A8_O16(r)                                                                            \
+    "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),         \
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),              \
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+#define W8A8_IO16(r)                                                                           \
+    "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),         \
+        "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),              \
+        "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
 #define W8A8_I16(r, o)                                                                          \
     "r"(r[o + 0]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), "r"(r[o + 5]),   \
         "r"(r[o + 6]), "r"(r[o + 7]), "r"(r[o + 8]), "r"(r[o + 9]), "r"(r[o + 10]),             \
         "r"(r[o + 11]), "r"(r[o + 12]), "r"(r[o + 13]), "r"(r[o + 14]), "r"(r[o + 15])
 
-// 128 columns of the thread's lane, with the wait for them.
-__device__ __forceinline__ void tmem_ld_128cols_sync(uint32_t t, uint32_t (&r)[128]) {
+constexpr uint32_t kLane16 = 16u << 16;   // tensor-memory address of lane 16
+
+// 32 columns of the warp's 32 lanes as two blocks of 16 lanes: lane l of the warp
+// gets, of the lanes l / 4 (registers 4 i, 4 i + 1) and l / 4 + 8 (4 i + 2, 4 i +
+// 3) of each block, columns 8 i + 2 (l % 4) and the one after it. Asynchronous:
+// valid after tmem_wait_tile on the same registers.
+__device__ __forceinline__ void tmem_ld_tile(uint32_t t, uint32_t (&a)[16], uint32_t (&b)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%128];\n"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%129];\n"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95}, [%130];\n"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%131];\n"
-        "tcgen05.wait::ld.sync.aligned;"
-        : W8A8_R16(r, 0), W8A8_R16(r, 16), W8A8_R16(r, 32), W8A8_R16(r, 48), W8A8_R16(r, 64),
-          W8A8_R16(r, 80), W8A8_R16(r, 96), W8A8_R16(r, 112)
-        : "r"(t), "r"(t + 32), "r"(t + 64), "r"(t + 96)
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : W8A8_O16(a)
+        : "r"(t)
+        : "memory");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : W8A8_O16(b)
+        : "r"(t + kLane16)
         : "memory");
 }
-
-__device__ __forceinline__ void tmem_st_32cols(uint32_t t, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_wait_tile(uint32_t (&a)[16], uint32_t (&b)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : W8A8_IO16(a), W8A8_IO16(b) : : "memory");
+}
+__device__ __forceinline__ void tmem_st_tile(uint32_t t, const uint32_t (&a)[16],
+                                             const uint32_t (&b)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%16], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::W8A8_I16(a, 0),
+        "r"(t)
+        : "memory");
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%16], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::W8A8_I16(b, 0),
+        "r"(t + kLane16)
+        : "memory");
+}
+// 64 columns of 16 lanes from 16-bit pairs: register 2 i + j is column 4 i + l % 4
+// of lane l / 4 + 8 j.
+__device__ __forceinline__ void tmem_st_p(uint32_t t, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x16.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::
             W8A8_I16(r, 0),
         W8A8_I16(r, 16), "r"(t)
         : "memory");
@@ -181,6 +216,147 @@ __device__ __forceinline__ unsigned long long f2_fma(unsigned long long a, unsig
     return r;
 }
 
+// What hides keys from a thread's rows: of row k, the columns 8 i + 2 (l % 4) + e
+// with 8 i + e in [lo[k], hi[k]] are seen, and those whose bit in the tile's mask
+// (shifted by 2 (l % 4)) is set.
+struct RowMask {
+    int lo[4], hi[4];
+    uint32_t w[4];
+};
+
+__device__ __forceinline__ bool hidden(const RowMask &m, int k, int c) {
+    return c > m.hi[k] || c < m.lo[k] || !((m.w[c >> 5] >> (c & 31)) & 1u);
+}
+
+// The mask as values that only the masked form of a loop can use: the compiler
+// otherwise works out all of a tile's comparisons ahead of the choice between the
+// forms, for tiles without a mask too (measured: twice the time of a long chunk).
+__device__ __forceinline__ RowMask here(RowMask m) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        asm volatile("" : "+r"(m.lo[k]), "+r"(m.hi[k]), "+r"(m.w[k]));
+    return m;
+}
+
+// One tile's weights of a thread's 4 rows (row k: lanes l / 4 + 8 (k & 1) of
+// block k >> 1) against the references -nm, as P's register image, and their
+// sums by row.
+template <bool kInt8, bool kMasked>
+__device__ __forceinline__ void weigh(uint32_t ts, const float4 *col, float c,
+                                      const float (&nm)[4], const RowMask &mask,
+                                      uint32_t (&pk)[2][32], float (&sum)[4]) {
+    RowMask mk;
+    if constexpr (kMasked) mk = here(mask);
+    unsigned long long l2[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) l2[k] = f2_bits(0.0f, 0.0f);
+    uint32_t r[2][2][16];
+    tmem_ld_tile(ts, r[0][0], r[0][1]);
+#pragma unroll
+    for (int cc = 0; cc < 4; ++cc) {
+        const int cur = cc & 1;
+        tmem_wait_tile(r[cur][0], r[cur][1]);
+        if (cc < 3) tmem_ld_tile(ts + (cc + 1) * 32, r[cur ^ 1][0], r[cur ^ 1][1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float4 f = make_float4(c, c, 1.0f, 1.0f);
+            if constexpr (kInt8) f = col[(cc * 4 + i) * 4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t(&x)[16] = r[cur][k >> 1];
+                const int o = 4 * i + 2 * (k & 1);
+                float p0, p1;
+                f2_split(f2_fma(f2_bits(__uint_as_float(x[o]), __uint_as_float(x[o + 1])),
+                                f2_bits(f.x, f.y), f2_bits(nm[k], nm[k])),
+                         p0, p1);
+                if constexpr (kMasked) {
+                    const int cl = cc * 32 + i * 8;
+                    if (hidden(mk, k, cl)) p0 = -INFINITY;
+                    if (hidden(mk, k, cl + 1)) p1 = -INFINITY;
+                }
+                p0 = ex2(p0);
+                p1 = ex2(p1);
+                unsigned long long p2 = f2_bits(p0, p1);
+                l2[k] = f2_add(l2[k], p2);
+                uint32_t &out = pk[k >> 1][(cc * 4 + i) * 2 + (k & 1)];
+                if constexpr (kInt8) {
+                    f2_split(f2_mul(p2, f2_bits(f.z, f.w)), p0, p1);
+                    out = pack_f16x2(p0, p1);
+                } else {
+                    out = pack_bf16x2(p0, p1);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float a, b;
+        f2_split(l2[k], a, b);
+        sum[k] = a + b;
+    }
+}
+
+// The largest score of each of a thread's rows in a tile (log2 units; the same
+// in the 4 lanes that share the rows).
+template <bool kInt8, bool kMasked>
+__device__ __forceinline__ void row_max(uint32_t ts, const float4 *col, float c, const RowMask &mask,
+                                        float (&top)[4]) {
+    RowMask mk;
+    if constexpr (kMasked) mk = here(mask);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top[k] = -INFINITY;
+#pragma unroll
+    for (int cc = 0; cc < 4; ++cc) {
+        uint32_t r[2][16];
+        tmem_ld_tile(ts + cc * 32, r[0], r[1]);
+        tmem_wait_tile(r[0], r[1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float4 f = make_float4(c, c, 1.0f, 1.0f);
+            if constexpr (kInt8) f = col[(cc * 4 + i) * 4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int o = 4 * i + 2 * (k & 1);
+                float p0 = __uint_as_float(r[k >> 1][o]) * f.x;
+                float p1 = __uint_as_float(r[k >> 1][o + 1]) * f.y;
+                if constexpr (kMasked) {
+                    const int cl = cc * 32 + i * 8;
+                    if (hidden(mk, k, cl)) p0 = -INFINITY;
+                    if (hidden(mk, k, cl + 1)) p1 = -INFINITY;
+                }
+                top[k] = fmaxf(top[k], fmaxf(p0, p1));
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        top[k] = fmaxf(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], 1));
+        top[k] = fmaxf(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], 2));
+    }
+}
+
+// O (in tensor memory) times a factor per row.
+__device__ __forceinline__ void scale_rows(uint32_t to, const float (&f)[4]) {
+#pragma unroll 1
+    for (int cc = 0; cc < 4; ++cc) {
+        uint32_t r[2][16];
+        tmem_ld_tile(to + cc * 32, r[0], r[1]);
+        tmem_wait_tile(r[0], r[1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                r[h][j] = __float_as_uint(__uint_as_float(r[h][j]) * f[2 * h + ((j >> 1) & 1)]);
+        tmem_st_tile(to + cc * 32, r[0], r[1]);
+    }
+}
+
+// 16-byte piece j of row r of q in shared memory.
+__device__ __forceinline__ uint4 *q_piece(uint8_t *q, int r, int j) {
+    return reinterpret_cast<uint4 *>(q + (j >> 3) * (kOperandBytes / 2) + r * 128 +
+                                     (((j & 7) ^ (r & 7)) << 4));
+}
+
 // The tiles that a half of an item sees within a piece: [from, upto), in tiles
 // of the request.
 struct HalfTiles {
@@ -196,7 +372,7 @@ __device__ __forceinline__ HalfTiles half_tiles(const PagedSchedule &s, const Pa
     t.exists = a < p.ntok;
     t.first = w.r.base + p.tok0 + a;
     t.last = w.r.base + p.tok0 + z - 1;
-    const int lo = s.window > 0 ? max(t.first - s.window + 1, 0) / kTilePositions : 0;
+    const int lo = s.window > 0 ? max(max(t.first, 0) - s.window + 1, 0) / kTilePositions : 0;
     const int hi = t.last >= 0 ? t.last / kTilePositions + 1 : 0;
     t.from = max(p.tile0 + p.first, lo);
     t.upto = t.exists ? min(p.tile0 + p.last, hi) : t.from;
@@ -220,7 +396,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
     if (tid == 0) {
         for (uint32_t i = 0; i < kOps; ++i) {
             mbar_init(bar(sm.op_full[i]), kInt8 ? 128 : 1);
-            mbar_init(bar(sm.op_empty[i]), 1);
+            mbar_init(bar(sm.op_empty[i]), 2);   // one arrival per half
         }
         for (uint32_t i = 0; i < kRaws; ++i) {
             mbar_init(bar(sm.raw_full[i]), 1);
@@ -237,7 +413,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
             mbar_init(bar(sm.o_free[h]), kHalfRows);
         }
         mbar_init(bar(sm.fix), 1);
-        mbar_init(bar(sm.drain), 1);
+        mbar_init(bar(sm.drain[0]), 1);
+        mbar_init(bar(sm.drain[1]), 1);
         sm.abort_flag = 0;
         fence_mbarrier_init();
     }
@@ -267,7 +444,9 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
         // ------------------------------------------------------------ softmax
         setmaxnreg_inc<kSoftmaxRegs>();
         const int h = warp >> 2;
-        const int row = tid & (kHalfRows - 1);
+        const int row = tid & (kHalfRows - 1);       // the epilogue's row
+        const int tok = row / a.o.G;
+        const int quad = lane & 3, r4 = (warp & 3) * 32 + (lane >> 2);
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // lane 32 (warp % 4)
         const uint32_t ts = tmem + lanes + h * 128, to = tmem + lanes + 256 + h * 128;
         uint32_t sn = 0, on = 0;    // active tiles, pieces with any
@@ -277,18 +456,22 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
             if (p.first == p.last && !p.whole) continue;
             const bool work = p.last > p.first;
             const HalfTiles t = half_tiles(s, w, p, h, a.half_tokens);
-            const int tok = row / a.o.G;
-            const bool mine_row = t.exists && tok < a.half_tokens && h * a.half_tokens + tok < p.ntok;
-            const int pos = t.first + tok;
-            float m = -INFINITY, l = 0.0f;
-            float c = a.scale_log2;
             if (work && t.exists) {
                 ok = mbar_wait(bar(sm.q_full[h]), qn[h] & 1, abort, a.err, ROLE_EPILOGUE, 1,
                                kWaitLimitNs, KID_ATTN);
-                if constexpr (kInt8) c *= sm.qinv[h][row];
                 mbar_arrive(bar(sm.q_empty[h]));
                 ++qn[h];
             }
+            // the thread's rows: r4 + 8 k
+            float m[4], l[4];
+            int pos[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                m[k] = -INFINITY;
+                l[k] = 0.0f;
+                pos[k] = t.first + (r4 + 8 * k) / a.o.G;
+            }
+            float unit = 0.0f;
             bool first = true;
             for (int x = t.from; work && x < t.upto; ++x, ++sn) {
                 const uint32_t ti = it + static_cast<uint32_t>(x - p.tile0 - p.first);
@@ -302,117 +485,73 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                                    ROLE_EPILOGUE, 3, kWaitLimitNs, KID_ATTN);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
-                __syncwarp();
                 tc_fence_after();
-                uint32_t r[128];
-                tmem_ld_128cols_sync(ts, r);
                 const int c0 = x * kTilePositions;
-                // INT8: t_j = s_j (k scale_j) c + log2 vs_j
+                RowMask mk;
+                {
+                    const TileMask tm = sm.mask[info];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        mk.w[k] = tm.w[k];
+                        mk.hi[k] = pos[k] - c0 - 2 * quad;
+                        mk.lo[k] = s.window > 0 ? mk.hi[k] - s.window + 1 : -kTilePositions;
+                    }
+                }
+                const bool masked = c0 + kTilePositions - 1 > t.first ||
+                                    (s.window > 0 && c0 <= t.last - s.window) ||
+                                    (mk.w[0] & mk.w[1] & mk.w[2] & mk.w[3]) != 0xFFFFFFFFu;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mk.w[k] >>= 2 * quad;
+                const float4 *col = kInt8 ? &sm.col[info][quad] : nullptr;
+                bool move = m[0] == -INFINITY || m[1] == -INFINITY || m[2] == -INFINITY ||
+                            m[3] == -INFINITY;
+                float turn = 1.0f;          // change of O's unit
                 if constexpr (kInt8) {
-                    const float4 *k4 = reinterpret_cast<const float4 *>(sm.ks[info]);
-                    const float4 *l4 = reinterpret_cast<const float4 *>(sm.lv[info]);
-                    const unsigned long long c2 = f2_bits(c, c);
+                    const float un = sm.unit[info];
+                    if (un != unit && !first) turn = unit / un;
+                    unit = un;
+                }
+                uint32_t pk[2][32];
+                float sum[4];
+                for (bool again = false;; again = true) {
+                    if (__any_sync(0xFFFFFFFFu, move)) {
+                        // new references: the tile's maxima
+                        float top[4], f[4];
+                        if (masked) row_max<kInt8, true>(ts, col, a.scale_log2, mk, top);
+                        else row_max<kInt8, false>(ts, col, a.scale_log2, mk, top);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float4 kk = k4[i], ll = l4[i];
-                        float x0, x1, x2, x3;
-                        f2_split(f2_fma(f2_mul(f2_bits(__uint_as_float(r[4 * i]),
-                                                       __uint_as_float(r[4 * i + 1])),
-                                               f2_bits(kk.x, kk.y)),
-                                        c2, f2_bits(ll.x, ll.y)),
-                                 x0, x1);
-                        f2_split(f2_fma(f2_mul(f2_bits(__uint_as_float(r[4 * i + 2]),
-                                                       __uint_as_float(r[4 * i + 3])),
-                                               f2_bits(kk.z, kk.w)),
-                                        c2, f2_bits(ll.z, ll.w)),
-                                 x2, x3);
-                        r[4 * i] = __float_as_uint(x0);
-                        r[4 * i + 1] = __float_as_uint(x1);
-                        r[4 * i + 2] = __float_as_uint(x2);
-                        r[4 * i + 3] = __float_as_uint(x3);
+                        for (int k = 0; k < 4; ++k) {
+                            f[k] = turn;
+                            if (top[k] > m[k]) {
+                                const float alpha = ex2(m[k] - top[k]);
+                                f[k] *= alpha;
+                                l[k] *= alpha;
+                                m[k] = top[k];
+                            }
+                        }
+                        // (the products before this tile's scores are done with O)
+                        if (!first) scale_rows(to, f);
+                        turn = 1.0f;
+                        again = true;
                     }
+                    float nm[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) nm[k] = m[k] == -INFINITY ? 0.0f : -m[k];
+                    if (masked) weigh<kInt8, true>(ts, col, a.scale_log2, nm, mk, pk, sum);
+                    else weigh<kInt8, false>(ts, col, a.scale_log2, nm, mk, pk, sum);
+                    if (again) break;
+                    move = !(fmaxf(fmaxf(sum[0], sum[1]), fmaxf(sum[2], sum[3])) <= kMaxWeight);
+                    if (!__any_sync(0xFFFFFFFFu, move)) break;
                 }
-                const bool causal = c0 + kTilePositions - 1 > t.first;
-                const bool low = s.window > 0 && c0 <= t.last - s.window;
-                if (causal || low) {
-                    const int hi = pos - c0, lo = s.window > 0 ? pos - s.window + 1 - c0 : 0;
-#pragma unroll
-                    for (int j = 0; j < 128; ++j)
-                        if (j > hi || j < lo) r[j] = 0xFF800000u;
-                }
-                if constexpr (!kInt8) {
-                    const TileMask mk = sm.mask[info];
-                    if ((mk.w[0] & mk.w[1] & mk.w[2] & mk.w[3]) != 0xFFFFFFFFu) {
-#pragma unroll
-                        for (int j = 0; j < 128; ++j)
-                            if (!((mk.w[j >> 5] >> (j & 31)) & 1u)) r[j] = 0xFF800000u;
-                    }
-                }
-                float mx[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) mx[j] = __uint_as_float(r[j]);
-#pragma unroll
-                for (int j = 4; j < 128; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(r[j]));
-                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                if constexpr (!kInt8) top *= c;   // (c > 0)
-                // the reference moves when the maximum passes it by the slack
-                float alpha = 1.0f;
-                if (top > m + kSlack || (m == -INFINITY && top > m)) {
-                    alpha = ex2(m - top);
-                    m = top;
-                    l *= alpha;
-                }
-                if (__any_sync(0xFFFFFFFFu, alpha != 1.0f) && !first) {
-                    // (the products before this tile's scores are done with O)
-#pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t o[32];
-                        tmem_ld_32cols_sync(to + q * 32, o);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-                        tmem_st_32cols(to + q * 32, o);
-                    }
+                if (turn != 1.0f) {
+                    const float f[4] = {turn, turn, turn, turn};
+                    scale_rows(to, f);
                 }
                 first = false;
-                const float mu = m == -INFINITY ? 0.0f : m;   // a row that has seen nothing
-                const unsigned long long m2 = f2_bits(-mu, -mu), c2 = f2_bits(c, c);
-                unsigned long long l2[2] = {f2_bits(0.0f, 0.0f), f2_bits(0.0f, 0.0f)};
-                const float4 *i4 = reinterpret_cast<const float4 *>(sm.iv[kInt8 ? info : 0]);
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t pk[32];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int j = q * 64 + 4 * i;
-                        float y[4];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const unsigned long long v =
-                                f2_bits(__uint_as_float(r[j + 2 * e]), __uint_as_float(r[j + 2 * e + 1]));
-                            f2_split(kInt8 ? f2_add(v, m2) : f2_fma(v, c2, m2), y[2 * e], y[2 * e + 1]);
-                        }
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) y[e] = ex2(y[e]);
-                        if constexpr (kInt8) {
-                            const float4 iv = i4[q * 16 + i];
-                            l2[0] = f2_fma(f2_bits(y[0], y[1]), f2_bits(iv.x, iv.y), l2[0]);
-                            l2[1] = f2_fma(f2_bits(y[2], y[3]), f2_bits(iv.z, iv.w), l2[1]);
-                            pk[2 * i] = pack_f16x2(y[0], y[1]);
-                            pk[2 * i + 1] = pack_f16x2(y[2], y[3]);
-                        } else {
-                            l2[0] = f2_add(l2[0], f2_bits(y[0], y[1]));
-                            l2[1] = f2_add(l2[1], f2_bits(y[2], y[3]));
-                            pk[2 * i] = pack_bf16x2(y[0], y[1]);
-                            pk[2 * i + 1] = pack_bf16x2(y[2], y[3]);
-                        }
-                    }
-                    tmem_st_32cols(ts + q * 32, pk);
-                }
-                float la, lb, lc, ld;
-                f2_split(l2[0], la, lb);
-                f2_split(l2[1], lc, ld);
-                l += (la + lb) + (lc + ld);
+                for (int k = 0; k < 4; ++k) l[k] += sum[k];
+                tmem_st_p(ts, pk[0]);
+                tmem_st_p(ts + kLane16, pk[1]);
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(bar(sm.p_full[h]));
@@ -430,7 +569,22 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
             if (!ok) break;
             tc_fence_after();
             if (t.exists) {
-                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                // from the lanes that share rows to the lane that stores one: lane i's
+                // row is row k = i / 8 of lanes 4 (i % 8) ..
+                float rl = 0.0f, rm = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    l[k] += __shfl_xor_sync(0xFFFFFFFFu, l[k], 1);
+                    l[k] += __shfl_xor_sync(0xFFFFFFFFu, l[k], 2);
+                    const float lk = __shfl_sync(0xFFFFFFFFu, l[k], (lane & 7) * 4);
+                    const float mk = __shfl_sync(0xFFFFFFFFu, m[k], (lane & 7) * 4);
+                    if (lane >> 3 == k) {
+                        rl = lk;
+                        rm = mk;
+                    }
+                }
+                const float f = (p.whole ? (rl == 0.0f ? 0.0f : 1.0f / rl) : 1.0f) * (kInt8 ? unit : 1.0f);
+                const bool mine_row = tok < a.half_tokens && h * a.half_tokens + tok < p.ntok;
                 const int irow = h * a.half_tokens * a.o.G + row;   // the item's row
                 float *part = slot_of(a.ws, kPagedTileRows, blockIdx.x, p.slot);
                 const int64_t orow =
@@ -446,7 +600,6 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                         for (int j = 0; j < 32; ++j) o[j] = 0u;
                     }
                     if (mine_row) {
-                        const float f = p.whole ? inv : 1.0f;
                         if (!p.whole || a.o.fp32) {
                             float4 *dst = reinterpret_cast<float4 *>(
                                 (p.whole ? static_cast<float *>(a.o.out) + orow * kHeadDim
@@ -475,8 +628,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                     __syncwarp();
                 }
                 if (!p.whole && mine_row) {
-                    part[kPagedTileRows * kHeadDim + irow] = m * kLn2;
-                    part[kPagedTileRows * (kHeadDim + 1) + irow] = l;
+                    part[kPagedTileRows * kHeadDim + irow] = rm * kLn2;
+                    part[kPagedTileRows * (kHeadDim + 1) + irow] = rl;
                 }
                 if (any) {
                     tc_fence_before();
@@ -486,18 +639,20 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
         }
     } else if (warp < 12) {
         setmaxnreg_dec<kOtherRegs>();
-        if (warp == 8 && mine) {
-            // ------------------------------------------------------ the products
+        if ((warp == 8 || warp == 10) && mine) {
+            // ------------------------------------------ the products of one half
             // The whole warp walks, waits and counts, on values made uniform
             // (u()), and one elected lane issues: the products' operands then
-            // stay in uniform registers.
+            // stay in uniform registers. A warp per half, so that neither's
+            // waits hold up the other's products.
             constexpr uint32_t idesc = kInt8 ? idesc_f16_f32(128, 128) : idesc_bf16_f32(128, 128);
             auto u = [](auto v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
-            const uint32_t q0 = u(desc_kmajor(smem_u32(sm.q))), k0 = u(desc_kmajor(smem_u32(sm.op)));
-            const uint32_t v0 = u(desc_nmajor(smem_u32(sm.op)));
-            const uint32_t tm = u(tmem);
+            const int h = warp == 8 ? 0 : 1;
+            const uint32_t q0 = u(desc_kmajor(smem_u32(sm.q[h])));
+            const uint32_t k0 = u(desc_kmajor(smem_u32(sm.op))), v0 = u(desc_nmajor(smem_u32(sm.op)));
+            const uint32_t tsc = u(tmem) + h * 128, to = u(tmem) + 256 + h * 128;
             const bool leader = elect_one();
-            uint32_t pn[2] = {0, 0}, on[2] = {0, 0};
+            uint32_t pn = 0, on = 0, nq = 0;
             uint32_t sk = 0, ph = 0;     // slot and phase of the next operand tile
             bool ok = true;
             auto wait = [&](uint64_t &b, uint32_t phase, unsigned site) {
@@ -505,95 +660,80 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                                                              site, kWaitLimitNs, KID_ATTN));
                 tc_fence_after();
             };
+            auto advance = [&]() {
+                if (++sk == kOps) {
+                    sk = 0;
+                    ph ^= 1;
+                }
+            };
             for (; ok && u(!w.done(s, sh.end)); w.next(s)) {
                 const PagedPiece p = paged_piece(s, w, sh.begin, sh.end);
                 const int cb = u(p.tile0 + p.first), ce = u(p.tile0 + p.last);
                 if (ce <= cb) continue;
-                int from[2], upto[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const HalfTiles t = half_tiles(s, w, p, h, a.half_tokens);
-                    from[h] = u(t.from);
-                    upto[h] = u(t.upto);
-                    if (!u(t.exists)) continue;
-                    wait(sm.q_full[h], qn[h]++, 1);
-                    if (upto[h] == from[h] && leader) mma_commit(bar(sm.q_empty[h]));
+                const HalfTiles t = half_tiles(s, w, p, h, a.half_tokens);
+                const int from = u(t.from), upto = u(t.upto);
+                if (u(t.exists)) {
+                    wait(sm.q_full[h], nq++, 1);
+                    if (upto == from && leader) mma_commit(bar(sm.q_empty[h]));
                 }
-                if (!ok) break;
-                auto scores = [&](int h, uint32_t slot, int x) {
-                    const uint32_t q = q0 + h * (kOperandBytes / 16);
-                    const uint32_t k = k0 + slot * (kOperandBytes / 16);
+                auto scores = [&](int x) {
+                    const uint32_t k = k0 + sk * (kOperandBytes / 16);
                     if (leader) {
-                        mma_ss<false>(tm + h * 128, q, k, idesc);
+                        mma_ss<false>(tsc, q0, k, idesc);
 #pragma unroll
                         for (int kk = 1; kk < 8; ++kk) {
                             const uint32_t off = (kk >> 2) * (kOperandBytes / 32) + (kk & 3) * 2;
-                            mma_ss<true>(tm + h * 128, q + off, k + off, idesc);
+                            mma_ss<true>(tsc, q0 + off, k + off, idesc);
                         }
                         mma_commit(bar(sm.s_full[h]));
-                        if (x == upto[h] - 1) mma_commit(bar(sm.q_empty[h]));
+                        if (x == upto - 1) mma_commit(bar(sm.q_empty[h]));
                     }
                     __syncwarp();
                 };
-                auto advance = [&]() {
-                    if (++sk == kOps) {
-                        sk = 0;
-                        ph ^= 1;
-                    }
-                };
+                // operand tiles come as K, V of each tile; the scores of tile
+                // x + 1 follow the output product of tile x
                 wait(sm.op_full[sk], ph, 2);
                 if (!ok) break;
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (from[h] <= cb && cb < upto[h]) scores(h, sk, cb);
+                if (from <= cb && cb < upto) scores(cb);
                 if (leader) mma_commit(bar(sm.op_empty[sk]));
                 advance();
                 for (int x = cb; x < ce; ++x) {
-                    const uint32_t sv = sk;
                     wait(sm.op_full[sk], ph, 3);
+                    if (from <= x && x < upto) {
+                        wait(sm.p_full[h], pn++, 4);
+                        if (x == from && on > 0) wait(sm.o_free[h], on - 1, 5);
+                        if (!ok) break;
+                        const uint32_t v = v0 + sk * (kOperandBytes / 16);
+                        if (leader) {
+                            mma_ts(to, tsc, v, idesc | kBNMajor, x > from ? 1u : 0u);
+#pragma unroll
+                            for (int kk = 1; kk < 8; ++kk)
+                                mma_ts(to, tsc + kk * 8, v + kk * 128, idesc | kBNMajor, 1u);
+                            if (x == upto - 1) mma_commit(bar(sm.o_done[h]));
+                        }
+                        __syncwarp();
+                        if (x == upto - 1) ++on;
+                    }
                     if (!ok) break;
+                    const uint32_t sv = sk;
                     advance();
-                    bool have_k = false;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (from[h] <= x && x < upto[h]) {
-                            wait(sm.p_full[h], pn[h]++, 4);
-                            if (ok && x == from[h] && on[h] > 0) wait(sm.o_free[h], on[h] - 1, 5);
-                            if (!ok) break;
-                            const uint32_t v = v0 + sv * (kOperandBytes / 16);
-                            if (leader) {
-                                mma_ts(tm + 256 + h * 128, tm + h * 128, v, idesc | kBNMajor,
-                                       x > from[h] ? 1u : 0u);
-#pragma unroll
-                                for (int kk = 1; kk < 8; ++kk)
-                                    mma_ts(tm + 256 + h * 128, tm + h * 128 + kk * 8, v + kk * 128,
-                                           idesc | kBNMajor, 1u);
-                                if (x == upto[h] - 1) mma_commit(bar(sm.o_done[h]));
-                            }
-                            __syncwarp();
-                            if (x == upto[h] - 1) ++on[h];
-                        }
-                        if (x + 1 < ce && from[h] <= x + 1 && x + 1 < upto[h]) {
-                            if (!have_k) wait(sm.op_full[sk], ph, 6);
-                            if (!ok) break;
-                            have_k = true;
-                            scores(h, sk, x + 1);
-                        }
-                    }
-                    if (!ok) break;
-                    if (leader) mma_commit(bar(sm.op_empty[sv]));
                     if (x + 1 < ce) {
-                        if (!have_k) wait(sm.op_full[sk], ph, 7);
-                        if (leader) mma_commit(bar(sm.op_empty[sk]));
-                        advance();
+                        wait(sm.op_full[sk], ph, 6);
+                        if (!ok) break;
+                        if (from <= x + 1 && x + 1 < upto) scores(x + 1);
                     }
+                    if (leader) {
+                        mma_commit(bar(sm.op_empty[sv]));
+                        if (x + 1 < ce) mma_commit(bar(sm.op_empty[sk]));
+                    }
+                    if (x + 1 < ce) advance();
                 }
             }
             // nothing may be in flight when tensor memory is freed and the CTA ends
-            if (leader) mma_commit(bar(sm.drain));
+            if (leader) mma_commit(bar(sm.drain[h]));
             __syncwarp();
             int never = 0;
-            mbar_wait(bar(sm.drain), 0, &never, a.err, ROLE_MMA, 8, kWaitLimitNs, KID_ATTN);
+            mbar_wait(bar(sm.drain[h]), 0, &never, a.err, ROLE_MMA, 8, kWaitLimitNs, KID_ATTN);
         } else if (warp == 9 && mine) {
             // ---------------------------------------------------------- the loads
             bool ok = true;
@@ -701,6 +841,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
             for (; mine && ok && !w.done(s, sh.end); w.next(s)) {
                 const PagedPiece p = paged_piece(s, w, sh.begin, sh.end);
                 if (p.last <= p.first) continue;
+                int e = -100;                       // O's unit is 2^e
+                float unscale = 0.0f;               // of q's scaling, and to log2 units
                 for (int x = p.first; x < p.last && ok; ++x, ++it) {
                     const int info = it % kInfo;
                     for (int kv = 0; kv < 2; ++kv, ++u) {
@@ -710,18 +852,9 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                         if (ok && u >= kOps)
                             ok = mbar_wait(bar(sm.op_empty[os]), (u / kOps - 1) & 1, abort, a.err,
                                            ROLE_CONVERT, 2, kWaitLimitNs, KID_ATTN);
-                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        // (the four warps go on, or stop, together: they meet below)
+                        ok = !named_barrier_or(1, 128, !ok);
                         if (!ok) break;
-                        if (kv == 0) {
-                            // what the softmax takes of the scales, one position per thread
-                            const bool live = (sm.mask[info].w[ct >> 5] >> (ct & 31)) & 1u;
-                            const float v = fmaxf(sm.rvs[info][ct], 0x1p-100f);
-                            const float vn = sm.rvs[info][ct] == sm.rvs[info][ct] ? v : sm.rvs[info][ct];
-                            sm.ks[info][ct] = live ? sm.rks[info][ct] : 0.0f;
-                            sm.lv[info][ct] = live ? log2f(vn) : -INFINITY;
-                            sm.iv[info][ct] = live ? 1.0f / vn : 0.0f;
-                            mbar_arrive(bar(sm.info_full[info]));
-                        }
                         // 16 codes to 32 bytes at a time. Eight lanes take pieces 0-3
                         // (4-7) of rows r and r ^ 5: reads and writes through the
                         // swizzle then fall in distinct banks.
@@ -734,57 +867,78 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                             const int r = cw * 32 + (i >> 1) * 8 + ((lane & 4) ? pi ^ 5 : pi);
                             const uint4 y = *reinterpret_cast<const uint4 *>(
                                 src + r * 128 + ((pc ^ (r & 7)) << 4));
-                            uint4 e, f;
-                            i8x4_to_f16x4(y.x, e.x, e.y);
-                            i8x4_to_f16x4(y.y, e.z, e.w);
+                            uint4 g, f;
+                            i8x4_to_f16x4(y.x, g.x, g.y);
+                            i8x4_to_f16x4(y.y, g.z, g.w);
                             i8x4_to_f16x4(y.z, f.x, f.y);
                             i8x4_to_f16x4(y.w, f.z, f.w);
                             uint8_t *d = dst + (pc >> 2) * (kOperandBytes / 2) + r * 128;
                             const int dp = (pc & 3) * 2;
-                            *reinterpret_cast<uint4 *>(d + ((dp ^ (r & 7)) << 4)) = e;
+                            *reinterpret_cast<uint4 *>(d + ((dp ^ (r & 7)) << 4)) = g;
                             *reinterpret_cast<uint4 *>(d + (((dp + 1) ^ (r & 7)) << 4)) = f;
                         }
                         fence_proxy_async_smem();
                         mbar_arrive(bar(sm.op_full[os]));
-                        mbar_arrive(bar(sm.raw_empty[rs]));
-                        if (kv == 0 && x == p.first) {
-                            // the item's q to fp16, one row per thread, each scaled so that
-                            // its largest value lies in [2^14, 2^15)
-                            for (int h = 0; h < 2; ++h) {
-                                if (h * a.half_tokens >= p.ntok) continue;
+                        if (kv == 1) {
+                            mbar_arrive(bar(sm.raw_empty[rs]));
+                            continue;
+                        }
+                        if (x == p.first) {
+                            // the item's q to fp16, a row of each half per thread, scaled
+                            // so that the largest value lies in [2^14, 2^15)
+                            const int halves = a.half_tokens < p.ntok ? 2 : 1;
+                            uint32_t mq = 0;
+                            for (int h = 0; h < halves; ++h) {
                                 ok = ok && mbar_wait(bar(sm.q_land[h]), qn[h] & 1, abort, a.err,
                                                      ROLE_CONVERT, 3, kWaitLimitNs, KID_ATTN);
                                 ++qn[h];
-                                if (!ok) break;
-                                uint32_t mq = 0;
+#pragma unroll 4
+                                for (int j = 0; j < 16; ++j)
+                                    mq = max(mq, amax_bits8(*q_piece(sm.q[h], ct, j)));
+                            }
+                            mq = __reduce_max_sync(0xFFFFFFFFu, mq);
+                            if (lane == 0) sm.qmax[cw] = mq;
+                            ok = !named_barrier_or(1, 128, !ok);
+                            if (!ok) break;
+                            mq = max(max(sm.qmax[0], sm.qmax[1]), max(sm.qmax[2], sm.qmax[3]));
+                            const int be = static_cast<int>(mq >> 7);
+                            const int se = be == 0 ? 0 : max(-100, min(100, 14 - (be - 127)));
+                            const float qs = __uint_as_float(static_cast<uint32_t>(se + 127) << 23);
+                            unscale = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - se) << 23);
+                            for (int h = 0; h < halves; ++h) {
 #pragma unroll 4
                                 for (int j = 0; j < 16; ++j) {
-                                    const uint4 y = *reinterpret_cast<const uint4 *>(
-                                        sm.q[h] + (j >> 3) * (kOperandBytes / 2) + ct * 128 +
-                                        (((j & 7) ^ (ct & 7)) << 4));
-                                    mq = max(mq, amax_bits8(y));
-                                }
-                                const int be = static_cast<int>(mq >> 7);
-                                const int se = be == 0 ? 0 : max(-100, min(100, 14 - (be - 127)));
-                                const float qs = __uint_as_float(static_cast<uint32_t>(se + 127) << 23);
-                                sm.qinv[h][ct] = __uint_as_float(static_cast<uint32_t>(127 - se) << 23);
-#pragma unroll 4
-                                for (int j = 0; j < 16; ++j) {
-                                    uint4 *at = reinterpret_cast<uint4 *>(
-                                        sm.q[h] + (j >> 3) * (kOperandBytes / 2) + ct * 128 +
-                                        (((j & 7) ^ (ct & 7)) << 4));
-                                    uint4 y = *at;
-                                    uint32_t *yw = reinterpret_cast<uint32_t *>(&y);
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e)
-                                        yw[e] = pack_f16x2(__uint_as_float(yw[e] << 16) * qs,
-                                                           __uint_as_float(yw[e] & 0xFFFF0000u) * qs);
-                                    *at = y;
+                                    uint4 y = *q_piece(sm.q[h], ct, j);
+                                    y.x = pack_f16x2(__uint_as_float(y.x << 16) * qs, __uint_as_float(y.x & 0xFFFF0000u) * qs);
+                                    y.y = pack_f16x2(__uint_as_float(y.y << 16) * qs, __uint_as_float(y.y & 0xFFFF0000u) * qs);
+                                    y.z = pack_f16x2(__uint_as_float(y.z << 16) * qs, __uint_as_float(y.z & 0xFFFF0000u) * qs);
+                                    y.w = pack_f16x2(__uint_as_float(y.w << 16) * qs, __uint_as_float(y.w & 0xFFFF0000u) * qs);
+                                    *q_piece(sm.q[h], ct, j) = y;
                                 }
                                 fence_proxy_async_smem();
                                 mbar_arrive(bar(sm.q_full[h]));
                             }
                         }
+                        // what the softmax takes of the scales, one position per thread
+                        const bool live = (sm.mask[info].w[cw] >> lane) & 1u;
+                        const float rk = live ? sm.rks[info][ct] : 0.0f;
+                        const float rv = live ? sm.rvs[info][ct] : 0.0f;
+                        mbar_arrive(bar(sm.raw_empty[rs]));
+                        const uint32_t wm = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(rv)));
+                        if (lane == 0) sm.vmax[it & 1][cw] = __uint_as_float(wm);
+                        named_barrier_sync(1, 128);
+                        const float top = fmaxf(fmaxf(sm.vmax[it & 1][0], sm.vmax[it & 1][1]),
+                                                fmaxf(sm.vmax[it & 1][2], sm.vmax[it & 1][3]));
+                        // a new unit when the largest weight would pass 16 of it
+                        const int te = max(-100, min(100, static_cast<int>(__float_as_uint(top) >> 23) - 127));
+                        if (te >= e + 4) e = te;
+                        const float un = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+                        const float ui = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                        float *c4 = reinterpret_cast<float *>(&sm.col[info][ct >> 1]) + (ct & 1);
+                        c4[0] = rk * unscale;
+                        c4[2] = rv * ui;
+                        if (ct == 0) sm.unit[info] = un;
+                        mbar_arrive(bar(sm.info_full[info]));
                     }
                 }
             }

@@ -192,7 +192,7 @@ __device__ __forceinline__ PagedPiece paged_piece(const PagedSchedule &s, const 
     p.tok0 = w.i * s.tile_tokens;
     p.ntok = min(w.r.n - p.tok0, s.tile_tokens);
     const int hi = max(w.r.base + p.tok0 + p.ntok, 0);
-    const int lo = s.window > 0 ? max(w.r.base + p.tok0 - s.window + 1, 0) : 0;
+    const int lo = s.window > 0 ? max(max(w.r.base + p.tok0, 0) - s.window + 1, 0) : 0;
     p.tile0 = lo / kTilePositions;
     p.ntiles = hi > lo ? (hi + kTilePositions - 1) / kTilePositions - p.tile0 : 0;
     const long long x0 = max(begin - w.at, 0ll), x1 = min(end - w.at, w.cost);
