@@ -99,6 +99,7 @@ struct TilesSmem {
     uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
     uint64_t fix, drain[2];
     uint32_t tmem;
+    unsigned pipe;                       // held by the warp whose products go out
     volatile int abort_flag;
 };
 
@@ -335,6 +336,23 @@ __device__ __forceinline__ void row_max(uint32_t ts, const float4 *col, float c,
     }
 }
 
+// 4 x 4 transpose over the four lanes of a quad: lane q's v[i] becomes lane i's
+// v[q].
+__device__ __forceinline__ void quad_transpose(uint32_t (&v)[4], int quad) {
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+        const bool up = (quad & o) != 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & o) continue;
+            const uint32_t give = up ? v[i] : v[i | o];
+            const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, give, o);
+            if (up) v[i] = got;
+            else v[i | o] = got;
+        }
+    }
+}
+
 // O (in tensor memory) times a factor per row.
 __device__ __forceinline__ void scale_rows(uint32_t to, const float (&f)[4]) {
 #pragma unroll 1
@@ -416,6 +434,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
         mbar_init(bar(sm.drain[0]), 1);
         mbar_init(bar(sm.drain[1]), 1);
         sm.abort_flag = 0;
+        sm.pipe = 0;
         fence_mbarrier_init();
     }
     // rows of q past a half's whole tokens are never written: zeros, so that
@@ -444,8 +463,6 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
         // ------------------------------------------------------------ softmax
         setmaxnreg_inc<kSoftmaxRegs>();
         const int h = warp >> 2;
-        const int row = tid & (kHalfRows - 1);       // the epilogue's row
-        const int tok = row / a.o.G;
         const int quad = lane & 3, r4 = (warp & 3) * 32 + (lane >> 2);
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // lane 32 (warp % 4)
         const uint32_t ts = tmem + lanes + h * 128, to = tmem + lanes + 256 + h * 128;
@@ -569,67 +586,64 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
             if (!ok) break;
             tc_fence_after();
             if (t.exists) {
-                // from the lanes that share rows to the lane that stores one: lane i's
-                // row is row k = i / 8 of lanes 4 (i % 8) ..
-                float rl = 0.0f, rm = 0.0f;
+                float f[4];
+                int64_t at[4];      // of the rows: where they go, < 0: nowhere
+                float *part = slot_of(a.ws, kPagedTileRows, blockIdx.x, p.slot);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     l[k] += __shfl_xor_sync(0xFFFFFFFFu, l[k], 1);
                     l[k] += __shfl_xor_sync(0xFFFFFFFFu, l[k], 2);
-                    const float lk = __shfl_sync(0xFFFFFFFFu, l[k], (lane & 7) * 4);
-                    const float mk = __shfl_sync(0xFFFFFFFFu, m[k], (lane & 7) * 4);
-                    if (lane >> 3 == k) {
-                        rl = lk;
-                        rm = mk;
-                    }
-                }
-                const float f = (p.whole ? (rl == 0.0f ? 0.0f : 1.0f / rl) : 1.0f) * (kInt8 ? unit : 1.0f);
-                const bool mine_row = tok < a.half_tokens && h * a.half_tokens + tok < p.ntok;
-                const int irow = h * a.half_tokens * a.o.G + row;   // the item's row
-                float *part = slot_of(a.ws, kPagedTileRows, blockIdx.x, p.slot);
-                const int64_t orow =
-                    (static_cast<int64_t>(w.r.t0) + p.tok0 + h * a.half_tokens + tok) * a.o.Hq +
-                    static_cast<int64_t>(w.h) * a.o.G + (row - tok * a.o.G);
-#pragma unroll 1
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t o[32];
-                    if (any) {
-                        tmem_ld_32cols_sync(to + q * 32, o);
+                    const int row = r4 + 8 * k, tok = row / a.o.G;
+                    const int irow = h * a.half_tokens * a.o.G + row;   // the item's row
+                    f[k] = kInt8 ? unit : 1.0f;
+                    at[k] = -1;
+                    if (tok >= a.half_tokens || h * a.half_tokens + tok >= p.ntok) continue;
+                    if (p.whole) {
+                        f[k] *= l[k] == 0.0f ? 0.0f : 1.0f / l[k];
+                        at[k] = ((static_cast<int64_t>(w.r.t0) + p.tok0 + h * a.half_tokens + tok) * a.o.Hq +
+                                 static_cast<int64_t>(w.h) * a.o.G + (row - tok * a.o.G)) * kHeadDim;
                     } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = 0u;
-                    }
-                    if (mine_row) {
-                        if (!p.whole || a.o.fp32) {
-                            float4 *dst = reinterpret_cast<float4 *>(
-                                (p.whole ? static_cast<float *>(a.o.out) + orow * kHeadDim
-                                         : part + static_cast<int64_t>(irow) * kHeadDim) +
-                                q * 32);
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                dst[j] = make_float4(__uint_as_float(o[4 * j]) * f,
-                                                     __uint_as_float(o[4 * j + 1]) * f,
-                                                     __uint_as_float(o[4 * j + 2]) * f,
-                                                     __uint_as_float(o[4 * j + 3]) * f);
-                        } else {
-                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o.out) +
-                                                                   orow * kHeadDim + q * 32);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                uint32_t u[4];
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    u[e] = pack_bf16x2(__uint_as_float(o[8 * j + 2 * e]) * f,
-                                                       __uint_as_float(o[8 * j + 2 * e + 1]) * f);
-                                dst[j] = make_uint4(u[0], u[1], u[2], u[3]);
-                            }
+                        at[k] = static_cast<int64_t>(irow) * kHeadDim;
+                        if (quad == 0) {
+                            part[kPagedTileRows * kHeadDim + irow] = m[k] * kLn2;
+                            part[kPagedTileRows * (kHeadDim + 1) + irow] = l[k];
                         }
                     }
-                    __syncwarp();
                 }
-                if (!p.whole && mine_row) {
-                    part[kPagedTileRows * kHeadDim + irow] = rm * kLn2;
-                    part[kPagedTileRows * (kHeadDim + 1) + irow] = rl;
+                const bool wide = !p.whole || a.o.fp32;
+                float *base = p.whole ? static_cast<float *>(a.o.out) : part;
+#pragma unroll 1
+                for (int cc = 0; cc < 4; ++cc) {
+                    uint32_t r[2][16];
+                    if (any) {
+                        tmem_ld_tile(to + cc * 32, r[0], r[1]);
+                        tmem_wait_tile(r[0], r[1]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) r[0][j] = r[1][j] = 0u;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t v[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float x0 = __uint_as_float(r[k >> 1][4 * i + 2 * (k & 1)]) * f[k];
+                            const float x1 = __uint_as_float(r[k >> 1][4 * i + 2 * (k & 1) + 1]) * f[k];
+                            if (wide) {
+                                if (at[k] >= 0)
+                                    *reinterpret_cast<float2 *>(base + at[k] + cc * 32 + i * 8 + 2 * quad) =
+                                        make_float2(x0, x1);
+                            }
+                            v[i] = pack_bf16x2(x0, x1);
+                        }
+                        // the four lanes of a row change columns 8 i + 2 q of each i
+                        // for the 8 columns of i = q: 16 bytes to store
+                        quad_transpose(v, quad);
+                        if (!wide && at[k] >= 0)
+                            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o.out) + at[k] + cc * 32 +
+                                                       quad * 8) = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
+                    __syncwarp();
                 }
                 if (any) {
                     tc_fence_before();
@@ -659,6 +673,28 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                 ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(bar(b), phase & 1, abort, a.err, ROLE_MMA,
                                                              site, kWaitLimitNs, KID_ATTN));
                 tc_fence_after();
+            };
+            // The two halves' products go out one group (output product, then the
+            // next scores) at a time: mixed, both groups would take as long as
+            // the two together, and both halves' softmax would run at once.
+            auto hold = [&]() {
+                if (leader && ok) {
+                    const unsigned long long t0 = globaltimer_ns();
+                    for (uint32_t i = 1; atomicCAS_block(&sm.pipe, 0u, 1u) != 0u; ++i) {
+                        if ((i & 255u) != 0) continue;
+                        if (*abort || globaltimer_ns() - t0 > kWaitLimitNs) {
+                            *abort = 1;
+                            record_device_error(a.err, KID_ATTN, ROLE_MMA, 9);
+                            ok = false;
+                            break;
+                        }
+                    }
+                }
+                ok = __all_sync(0xFFFFFFFFu, ok);
+            };
+            auto let_go = [&]() {
+                if (leader) atomicExch_block(&sm.pipe, 0u);
+                __syncwarp();
             };
             auto advance = [&]() {
                 if (++sk == kOps) {
@@ -699,9 +735,12 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                 advance();
                 for (int x = cb; x < ce; ++x) {
                     wait(sm.op_full[sk], ph, 3);
+                    const uint32_t sn = sk + 1 == kOps ? 0 : sk + 1;
+                    if (x + 1 < ce) wait(sm.op_full[sn], sn == 0 ? ph ^ 1 : ph, 6);
                     if (from <= x && x < upto) {
                         wait(sm.p_full[h], pn++, 4);
                         if (x == from && on > 0) wait(sm.o_free[h], on - 1, 5);
+                        hold();
                         if (!ok) break;
                         const uint32_t v = v0 + sk * (kOperandBytes / 16);
                         if (leader) {
@@ -717,11 +756,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                     if (!ok) break;
                     const uint32_t sv = sk;
                     advance();
-                    if (x + 1 < ce) {
-                        wait(sm.op_full[sk], ph, 6);
-                        if (!ok) break;
-                        if (from <= x + 1 && x + 1 < upto) scores(x + 1);
-                    }
+                    if (from <= x + 1 && x + 1 < upto && x + 1 < ce) scores(x + 1);
+                    if (from <= x && x < upto) let_go();
                     if (leader) {
                         mma_commit(bar(sm.op_empty[sv]));
                         if (x + 1 < ce) mma_commit(bar(sm.op_empty[sk]));
