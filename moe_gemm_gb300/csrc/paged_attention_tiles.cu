@@ -62,9 +62,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kMaxWeight = 256.0f; // sums of a tile's weights that move the reference
 constexpr int kOperandBytes = 128 * 128 * 2;
-// Registers of a softmax thread and of the others: 2 x 128 x 192 + 2 x 128 x
-// 64 = the 512 x 128 that the block is launched with.
-constexpr int kSoftmaxRegs = 192, kOtherRegs = 64;
+// Registers of a softmax thread and of the others: 2 x 128 x 168 + 2 x 128 x
+// 88 = the 512 x 128 that the block is launched with.
+constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;
 
 struct TilesArgs {
     PagedSchedule s;
@@ -90,14 +90,13 @@ struct TilesSmem {
     // its weight is; both 0 where the position is masked for every query
     float4 col[kInfo][kInt8 ? 64 : 1];
     float unit[kInfo];                   // 2^e
-    float vmax[2][4];
     uint32_t qmax[4];
     TileMask mask[kInfo];
     uint64_t op_full[kOps], op_empty[kOps], raw_full[kRaws], raw_empty[kRaws];
     uint64_t info_full[kInfo];
     uint64_t q_land[2], q_full[2], q_empty[2];
     uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
-    uint64_t fix, drain[2];
+    uint64_t q_max, fix, drain[2];
     uint32_t tmem;
     unsigned pipe;                       // held by the warp whose products go out
     volatile int abort_flag;
@@ -251,20 +250,18 @@ __device__ __forceinline__ void weigh(uint32_t ts, const float4 *col, float c,
     unsigned long long l2[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) l2[k] = f2_bits(0.0f, 0.0f);
-    uint32_t r[2][2][16];
-    tmem_ld_tile(ts, r[0][0], r[0][1]);
 #pragma unroll
     for (int cc = 0; cc < 4; ++cc) {
-        const int cur = cc & 1;
-        tmem_wait_tile(r[cur][0], r[cur][1]);
-        if (cc < 3) tmem_ld_tile(ts + (cc + 1) * 32, r[cur ^ 1][0], r[cur ^ 1][1]);
+        uint32_t r[2][16];
+        tmem_ld_tile(ts + cc * 32, r[0], r[1]);
+        tmem_wait_tile(r[0], r[1]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float4 f = make_float4(c, c, 1.0f, 1.0f);
             if constexpr (kInt8) f = col[(cc * 4 + i) * 4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const uint32_t(&x)[16] = r[cur][k >> 1];
+                const uint32_t(&x)[16] = r[k >> 1];
                 const int o = 4 * i + 2 * (k & 1);
                 float p0, p1;
                 f2_split(f2_fma(f2_bits(__uint_as_float(x[o]), __uint_as_float(x[o + 1])),
@@ -430,6 +427,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
             mbar_init(bar(sm.o_done[h]), 1);
             mbar_init(bar(sm.o_free[h]), kHalfRows);
         }
+        mbar_init(bar(sm.q_max), 128);
         mbar_init(bar(sm.fix), 1);
         mbar_init(bar(sm.drain[0]), 1);
         mbar_init(bar(sm.drain[1]), 1);
@@ -779,8 +777,9 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                 if (p.last <= p.first) continue;
                 int lo, hi;
                 request_span(s, w.r, lo, hi);
+                TileBoxes next = find_boxes(a.c, w.b, w.h, p.tile0 + p.first, lo, hi, a.err);
                 for (int x = p.first; x < p.last && ok; ++x, ++it) {
-                    const TileBoxes tb = find_boxes(a.c, w.b, w.h, p.tile0 + x, lo, hi, a.err);
+                    const TileBoxes tb = next;
                     const int info = it % kInfo;
                     const bool full = (tb.mask.w[0] & tb.mask.w[1] & tb.mask.w[2] & tb.mask.w[3]) ==
                                       0xFFFFFFFFu;
@@ -815,6 +814,9 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                                 copy_scales(a.c, tb, a.c.vs, smem_u32(sm.rvs[info]), b);
                             }
                         }
+                        // (the table's entries for the next tile come while V waits)
+                        if (kv == 0 && x + 1 < p.last)
+                            next = find_boxes(a.c, w.b, w.h, p.tile0 + x + 1, lo, hi, a.err);
                         if (mend) {
                             ok = mbar_wait(b, fixes & 1, abort, a.err, ROLE_PRODUCER, 2, kWaitLimitNs,
                                            KID_ATTN);
@@ -873,7 +875,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
             const int ct = tid - 384;               // 0 .. 127
             const int cw = ct >> 5;
             bool ok = true;
-            uint32_t u = 0;
+            uint32_t u = 0, items = 0;
             for (; mine && ok && !w.done(s, sh.end); w.next(s)) {
                 const PagedPiece p = paged_piece(s, w, sh.begin, sh.end);
                 if (p.last <= p.first) continue;
@@ -888,8 +890,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                         if (ok && u >= kOps)
                             ok = mbar_wait(bar(sm.op_empty[os]), (u / kOps - 1) & 1, abort, a.err,
                                            ROLE_CONVERT, 2, kWaitLimitNs, KID_ATTN);
-                        // (the four warps go on, or stop, together: they meet below)
-                        ok = !named_barrier_or(1, 128, !ok);
+                        ok = __all_sync(0xFFFFFFFFu, ok);
                         if (!ok) break;
                         // 16 codes to 32 bytes at a time. Eight lanes take pieces 0-3
                         // (4-7) of rows r and r ^ 5: reads and writes through the
@@ -898,20 +899,28 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                         uint8_t *dst = sm.op[os];
                         const int pc = (lane & 3) + ((lane >> 3) & 1) * 4;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int pi = (i & 1) * 2 + (lane >> 4);
-                            const int r = cw * 32 + (i >> 1) * 8 + ((lane & 4) ? pi ^ 5 : pi);
-                            const uint4 y = *reinterpret_cast<const uint4 *>(
-                                src + r * 128 + ((pc ^ (r & 7)) << 4));
-                            uint4 g, f;
-                            i8x4_to_f16x4(y.x, g.x, g.y);
-                            i8x4_to_f16x4(y.y, g.z, g.w);
-                            i8x4_to_f16x4(y.z, f.x, f.y);
-                            i8x4_to_f16x4(y.w, f.z, f.w);
-                            uint8_t *d = dst + (pc >> 2) * (kOperandBytes / 2) + r * 128;
-                            const int dp = (pc & 3) * 2;
-                            *reinterpret_cast<uint4 *>(d + ((dp ^ (r & 7)) << 4)) = g;
-                            *reinterpret_cast<uint4 *>(d + (((dp + 1) ^ (r & 7)) << 4)) = f;
+                        for (int j = 0; j < 2; ++j) {
+                            uint4 y[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int pi = (i & 1) * 2 + (lane >> 4);
+                                const int r = cw * 32 + (2 * j + (i >> 1)) * 8 + ((lane & 4) ? pi ^ 5 : pi);
+                                y[i] = *reinterpret_cast<const uint4 *>(src + r * 128 + ((pc ^ (r & 7)) << 4));
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int pi = (i & 1) * 2 + (lane >> 4);
+                                const int r = cw * 32 + (2 * j + (i >> 1)) * 8 + ((lane & 4) ? pi ^ 5 : pi);
+                                uint4 g, f;
+                                i8x4_to_f16x4(y[i].x, g.x, g.y);
+                                i8x4_to_f16x4(y[i].y, g.z, g.w);
+                                i8x4_to_f16x4(y[i].z, f.x, f.y);
+                                i8x4_to_f16x4(y[i].w, f.z, f.w);
+                                uint8_t *d = dst + (pc >> 2) * (kOperandBytes / 2) + r * 128;
+                                const int dp = (pc & 3) * 2;
+                                *reinterpret_cast<uint4 *>(d + ((dp ^ (r & 7)) << 4)) = g;
+                                *reinterpret_cast<uint4 *>(d + (((dp + 1) ^ (r & 7)) << 4)) = f;
+                            }
                         }
                         fence_proxy_async_smem();
                         mbar_arrive(bar(sm.op_full[os]));
@@ -934,7 +943,12 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                             }
                             mq = __reduce_max_sync(0xFFFFFFFFu, mq);
                             if (lane == 0) sm.qmax[cw] = mq;
-                            ok = !named_barrier_or(1, 128, !ok);
+                            __syncwarp();
+                            mbar_arrive(bar(sm.q_max));
+                            ok = ok && mbar_wait(bar(sm.q_max), items & 1, abort, a.err, ROLE_CONVERT,
+                                                 4, kWaitLimitNs, KID_ATTN);
+                            ++items;
+                            ok = __all_sync(0xFFFFFFFFu, ok);
                             if (!ok) break;
                             mq = max(max(sm.qmax[0], sm.qmax[1]), max(sm.qmax[2], sm.qmax[3]));
                             const int be = static_cast<int>(mq >> 7);
@@ -955,18 +969,21 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                                 mbar_arrive(bar(sm.q_full[h]));
                             }
                         }
-                        // what the softmax takes of the scales, one position per thread
+                        // what the softmax takes of the scales, one position per thread;
+                        // the tile's largest v scale, by every warp for itself
+                        const TileMask tm = sm.mask[info];
+                        uint32_t wm = 0;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if ((tm.w[i] >> lane) & 1u)
+                                wm = max(wm, __float_as_uint(fabsf(sm.rvs[info][32 * i + lane])));
+                        wm = __reduce_max_sync(0xFFFFFFFFu, wm);
                         const bool live = (sm.mask[info].w[cw] >> lane) & 1u;
                         const float rk = live ? sm.rks[info][ct] : 0.0f;
                         const float rv = live ? sm.rvs[info][ct] : 0.0f;
                         mbar_arrive(bar(sm.raw_empty[rs]));
-                        const uint32_t wm = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(rv)));
-                        if (lane == 0) sm.vmax[it & 1][cw] = __uint_as_float(wm);
-                        named_barrier_sync(1, 128);
-                        const float top = fmaxf(fmaxf(sm.vmax[it & 1][0], sm.vmax[it & 1][1]),
-                                                fmaxf(sm.vmax[it & 1][2], sm.vmax[it & 1][3]));
                         // a new unit when the largest weight would pass 16 of it
-                        const int te = max(-100, min(100, static_cast<int>(__float_as_uint(top) >> 23) - 127));
+                        const int te = max(-100, min(100, static_cast<int>(wm >> 23) - 127));
                         if (te >= e + 4) e = te;
                         const float un = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
                         const float ui = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
