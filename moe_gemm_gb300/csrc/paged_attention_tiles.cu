@@ -303,8 +303,10 @@ __device__ __forceinline__ void row_max(uint32_t ts, const float4 *col, float c,
     if constexpr (kMasked) mk = here(mask);
 #pragma unroll
     for (int k = 0; k < 4; ++k) top[k] = -INFINITY;
-#pragma unroll
+#pragma unroll 1
     for (int cc = 0; cc < 4; ++cc) {
+        uint32_t w = 0;
+        if constexpr (kMasked) w = cc == 0 ? mk.w[0] : cc == 1 ? mk.w[1] : cc == 2 ? mk.w[2] : mk.w[3];
         uint32_t r[2][16];
         tmem_ld_tile(ts + cc * 32, r[0], r[1]);
         tmem_wait_tile(r[0], r[1]);
@@ -318,9 +320,10 @@ __device__ __forceinline__ void row_max(uint32_t ts, const float4 *col, float c,
                 float p0 = __uint_as_float(r[k >> 1][o]) * f.x;
                 float p1 = __uint_as_float(r[k >> 1][o + 1]) * f.y;
                 if constexpr (kMasked) {
-                    const int cl = cc * 32 + i * 8;
-                    if (hidden(mk, k, cl)) p0 = -INFINITY;
-                    if (hidden(mk, k, cl + 1)) p1 = -INFINITY;
+                    const int cl = i * 8;
+                    const int hi = mk.hi[k] - cc * 32, lo = mk.lo[k] - cc * 32;
+                    if (cl > hi || cl < lo || !((w >> cl) & 1u)) p0 = -INFINITY;
+                    if (cl + 1 > hi || cl + 1 < lo || !((w >> (cl + 1)) & 1u)) p1 = -INFINITY;
                 }
                 top[k] = fmaxf(top[k], fmaxf(p0, p1));
             }
@@ -462,6 +465,9 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
         setmaxnreg_inc<kSoftmaxRegs>();
         const int h = warp >> 2;
         const int quad = lane & 3, r4 = (warp & 3) * 32 + (lane >> 2);
+        int tok4[4];        // the tokens, within the half, of the thread's rows r4 + 8 k
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tok4[k] = (r4 + 8 * k) / a.o.G;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // lane 32 (warp % 4)
         const uint32_t ts = tmem + lanes + h * 128, to = tmem + lanes + 256 + h * 128;
         uint32_t sn = 0, on = 0;    // active tiles, pieces with any
@@ -477,14 +483,13 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                 mbar_arrive(bar(sm.q_empty[h]));
                 ++qn[h];
             }
-            // the thread's rows: r4 + 8 k
             float m[4], l[4];
             int pos[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 m[k] = -INFINITY;
                 l[k] = 0.0f;
-                pos[k] = t.first + (r4 + 8 * k) / a.o.G;
+                pos[k] = t.first + tok4[k];
             }
             float unit = 0.0f;
             bool first = true;
@@ -591,7 +596,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                 for (int k = 0; k < 4; ++k) {
                     l[k] += __shfl_xor_sync(0xFFFFFFFFu, l[k], 1);
                     l[k] += __shfl_xor_sync(0xFFFFFFFFu, l[k], 2);
-                    const int row = r4 + 8 * k, tok = row / a.o.G;
+                    const int row = r4 + 8 * k, tok = tok4[k];
                     const int irow = h * a.half_tokens * a.o.G + row;   // the item's row
                     f[k] = kInt8 ? unit : 1.0f;
                     at[k] = -1;
