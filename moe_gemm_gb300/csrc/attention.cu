@@ -310,7 +310,8 @@ attn_decode_kernel(const uint16_t *__restrict__ q, const void *__restrict__ kc,
         cp_async_commit();
         const int n = rows_of(cc);
         attend_chunk<NT, kInt8>(
-            st, r, qf, [n](int row, int, int) { return row < n; }, scale, qinv, pw, gid, t);
+            st, r, qf, [n](int row, int, int) { return row < n; }, [](ChunkRegs<kInt8> &) {}, scale, qinv, pw,
+            gid, t);
     }
     cp_async_wait_group<0>();
     __syncthreads();   // the stages are free for the merge below

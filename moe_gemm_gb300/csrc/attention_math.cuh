@@ -98,11 +98,14 @@ struct WarpState {
 // One chunk into the warp's running state (online softmax: the state is
 // rescaled by exp(m_old - m_new) when a larger score arrives). valid(row, nt,
 // j) tells whether query row 8 nt + 2 t + j sees the chunk's position `row`;
-// the V scales of positions that no query sees are zero.
-template <int NT, bool kInt8, typename Valid>
-__device__ __forceinline__ void attend_chunk(WarpState<NT> &st, const ChunkRegs<kInt8> &r,
+// the V scales of positions that no query sees are zero. values(r) is called once
+// the scores are done and may fill in V's part of r (which then need not be held
+// beside K's).
+template <int NT, bool kInt8, typename Valid, typename Values>
+__device__ __forceinline__ void attend_chunk(WarpState<NT> &st, ChunkRegs<kInt8> &r,
                                              const uint32_t (&qf)[NT][16], Valid valid,
-                                             float scale, float qinv, int pw, int gid, int t) {
+                                             Values values, float scale, float qinv, int pw, int gid,
+                                             int t) {
     // ---- scores: k-step kb covers dims 32 t + 4 kb + {0..3} of each lane
     float sacc[2][NT][4];
 #pragma unroll
@@ -169,6 +172,7 @@ __device__ __forceinline__ void attend_chunk(WarpState<NT> &st, const ChunkRegs<
             st.m[nt][j] = m_new;
             st.l[nt][j] *= alpha[nt][j];
         }
+    values(r);
     // the warp's largest V scale of the chunk sets the power of two that keeps
     // P' in fp16's normal range (INT8 cache); rows of other lanes t are the same
     int se = st.se;

@@ -34,8 +34,7 @@ namespace {
 constexpr int kMaxCtas = 512;        // of the rows kernel
 constexpr int kRowsMax = 16;         // query rows of an item, rows kernel
 constexpr int kRowWarps = 4;         // 32 positions of a tile each
-constexpr int kRowThreads = (kRowWarps + 1) * 32;   // and a warp that loads
-constexpr int kRowStages = 2;
+constexpr int kRowThreads = kRowWarps * 32;
 constexpr float kNegInf = -INFINITY;
 
 // The kernel of a call, by the query rows that a request and kv head have on
@@ -56,53 +55,64 @@ struct RowsArgs {
     unsigned long long *err;
 };
 
+// Tiles that a warp keeps in flight. INT8: 2, so that three CTAs fit an SM.
+template <bool kInt8>
+constexpr int kRowStages = kInt8 ? 2 : 3;
+
 template <int NT, bool kInt8>
 struct RowsSmem {
-    struct Stage {
-        uint4 k[Tile<kInt8>::kBytes / 16];
-        uint4 v[Tile<kInt8>::kBytes / 16];
-    };
-    Stage stage[kRowStages];                        // 1024-byte aligned
-    float ks[kRowStages][kTilePositions], vs[kRowStages][kTilePositions];
-    TileMask mask[kRowStages];
-    float merge[2][8 * NT * 4][32];                 // two warps' outputs, as fragments
+    static constexpr int kSlice = Tile<kInt8>::kBytes / kRowWarps;   // K, or V, of 32 positions
+    static constexpr int kStages = kRowStages<kInt8>;
+    uint4 k[kRowWarps][kStages][kSlice / 16];       // 1024-byte aligned
+    uint4 v[kRowWarps][kStages][kSlice / 16];
+    float ks[kRowWarps][kStages][32], vs[kRowWarps][kStages][32];
+    uint32_t mask[kRowWarps][kStages];              // which positions hold keys
+    float merge[8 * NT * 4][32];                    // a warp's output, as fragments
     float red_m[kRowWarps][8 * NT], red_l[kRowWarps][8 * NT];
-    uint64_t full[kRowStages], empty[kRowStages];
+    uint64_t kfull[kRowWarps][kStages], vfull[kRowWarps][kStages];
     volatile int abort_flag;
 };
 
-// A lane's fragments of a landed tile (attention_math.cuh: ChunkRegs).
+// A lane's fragments of 32 landed positions (attention_math.cuh: ChunkRegs);
+// bit i of the mask: position i is a key.
+__device__ __forceinline__ int slice_at(int row, int piece) {
+    return ((piece >> 3) * 32 + row) * 8 + ((piece & 7) ^ (row & 7));
+}
+
 template <bool kInt8>
-__device__ __forceinline__ void tile_frags(ChunkRegs<kInt8> &r, const uint4 *k, const uint4 *v,
-                                           const float *ks, const float *vs, const TileMask &mask,
-                                           bool full, int pw, int gid, int t) {
+__device__ __forceinline__ void key_frags(ChunkRegs<kInt8> &r, const uint4 *k, const float *ks,
+                                          int gid, int t) {
     using R = ChunkRegs<kInt8>;
-    auto at = [](int row, int piece) {
-        const int half = piece >> 3;
-        return (half * kTilePositions + row) * 8 + ((piece & 7) ^ (row & 7));
-    };
-    auto ok = [&](int row) { return full || ((mask.w[row >> 5] >> (row & 31)) & 1u); };
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            const int row = 16 * mt + gid + 8 * hf;
+#pragma unroll
+            for (int x = 0; x < R::KV; ++x) r.k[mt][hf][x] = k[slice_at(row, t * R::KV + x)];
+            r.ks[mt][hf] = kInt8 ? ks[row] : 1.0f;
+        }
+}
+
+template <bool kInt8>
+__device__ __forceinline__ void value_frags(ChunkRegs<kInt8> &r, const uint4 *v, const float *vs,
+                                            uint32_t mask, int gid, int t) {
+    using R = ChunkRegs<kInt8>;
+    auto ok = [&](int row) { return (mask >> row) & 1u; };
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-            const int row = pw + 16 * mt + gid + 8 * hf;
-#pragma unroll
-            for (int x = 0; x < R::KV; ++x) r.k[mt][hf][x] = k[at(row, t * R::KV + x)];
-            if constexpr (kInt8) {
-                r.ks[mt][hf] = ks[row];
-                r.vs[mt][hf] = ok(row) ? vs[row] : 0.0f;
-            } else {
-                r.ks[mt][hf] = 1.0f;
-                r.vs[mt][hf] = ok(row) ? 1.0f : 0.0f;
-            }
+            const int row = 16 * mt + gid + 8 * hf;
+            const float s = kInt8 ? vs[row] : 1.0f;
+            r.vs[mt][hf] = ok(row) ? s : 0.0f;
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int row = pw + 16 * mt + 2 * t + (j < 2 ? j : j + 6);
+            const int row = 16 * mt + 2 * t + (j < 2 ? j : j + 6);
 #pragma unroll
             for (int x = 0; x < R::VV; ++x) {
-                r.v[mt][j][x] = v[at(row, gid * R::VV + x)];
+                r.v[mt][j][x] = v[slice_at(row, gid * R::VV + x)];
                 // what lies in a masked BF16 position may be no number at all
                 if (!kInt8 && !ok(row)) r.v[mt][j][x] = make_uint4(0, 0, 0, 0);
             }
@@ -110,136 +120,123 @@ __device__ __forceinline__ void tile_frags(ChunkRegs<kInt8> &r, const uint4 *k, 
     }
 }
 
-// A persistent CTA: four warps of 32 positions of a tile each, and one that
-// keeps tiles in flight. Query row r of an item is query head r % G of its new
-// token r / G. Arithmetic as in the contiguous-cache kernel (attention.cu):
-// scores and outputs by mma.sync with FP32 sums, the probabilities split into
-// two fp16 (three bf16) parts, running maximum and sum per warp, joined when
-// the item ends.
+// A persistent CTA of four warps. Warp w takes positions [32 w, 32 w + 32) of
+// each of its items' tiles, and loads them for itself: one to four TMA boxes of
+// K and of V and the scales, kRowStages tiles ahead, so that warps wait for one
+// another only when an item ends (a fifth warp that loaded for all held the
+// registers of one to two CTAs per SM: a decode step of 32 requests at 4096
+// positions took 62 us against this form's 50). Query row r of an item is query
+// head r % G of its new token r / G. Arithmetic as in the contiguous-cache
+// kernel (attention.cu): scores and outputs by mma.sync with FP32 sums, the
+// probabilities split into two fp16 (three bf16) parts, running maximum and sum
+// per warp.
 template <int NT, bool kInt8>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, kInt8 ? 2 : 1)
 paged_rows_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm,
                   const RowsArgs a) {
     extern __shared__ uint8_t smem_raw[];
     using Smem = RowsSmem<NT, kInt8>;
+    constexpr int kStages = Smem::kStages;
     Smem &sm = *reinterpret_cast<Smem *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int gid = lane >> 2, t = lane & 3;
     const PagedSchedule &s = a.s;
     if (tid == 0) {
-        for (int i = 0; i < kRowStages; ++i) {
-            mbar_init(smem_u32(&sm.full[i]), 1);
-            mbar_init(smem_u32(&sm.empty[i]), kRowWarps * 32);
-        }
+        for (int i = 0; i < kRowWarps; ++i)
+            for (int j = 0; j < kStages; ++j) {
+                mbar_init(smem_u32(&sm.kfull[i][j]), 1);
+                mbar_init(smem_u32(&sm.vfull[i][j]), 1);
+            }
         sm.abort_flag = 0;
         fence_mbarrier_init();
     }
     griddep_launch_dependents();
     griddep_wait();   // lengths, tables and the cache may come from the kernel before
     const PagedShare sh = paged_share<kRowThreads>(s, blockIdx.x, gridDim.x);   // (synchronises)
-    if (static_cast<int>(blockIdx.x) >= sh.ctas) return;
     PagedWalk w;
     w.start(s, sh);
-    uint32_t it = 0;   // tiles so far: stage it % kRowStages, phase it / kRowStages
+    if (tid == kRowThreads - 1)
+        paged_write_cut(s, sh, w, blockIdx.x, cuts_of(a.ws, kRowsMax, gridDim.x));
+    if (static_cast<int>(blockIdx.x) >= sh.ctas || w.done(s, sh.end)) return;
+    uint32_t it = 0, issued = 0;   // tiles so far: stage it % kStages, phase it / kStages
     bool ok = true;
+    const int box_shift = __ffs(a.c.box) - 1;
 
-    if (warp == kRowWarps) {
-        for (; !w.done(s, sh.end); w.next(s)) {
-            const PagedPiece p = paged_piece(s, w, sh.begin, sh.end);
-            int lo, hi;
-            request_span(s, w.r, lo, hi);
-            for (int x = p.first; x < p.last; ++x, ++it) {
-                const int st = it % kRowStages;
-                if (ok && it >= kRowStages)
-                    ok = mbar_wait(smem_u32(&sm.empty[st]), (it / kRowStages - 1) & 1, &sm.abort_flag,
-                                   a.err, ROLE_PRODUCER, 1, kWaitLimitNs, KID_ATTN);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
-                const TileBoxes tb = find_boxes(a.c, w.b, w.h, p.tile0 + x, lo, hi, a.err);
-                const uint32_t bar = smem_u32(&sm.full[st]);
-                if (lane == 0) {
-                    sm.mask[st] = tb.mask;
-                    mbar_arrive_expect_tx(bar, 2 * tile_bytes<kInt8>(a.c, tb) +
-                                                   (kInt8 ? 2 * scale_bytes(a.c, tb) : 0));
-                }
-                __syncwarp();
-                copy_boxes<kInt8>(a.c, tb, &km, smem_u32(sm.stage[st].k), bar);
-                copy_boxes<kInt8>(a.c, tb, &vm, smem_u32(sm.stage[st].v), bar);
-                if constexpr (kInt8) {
-                    copy_scales(a.c, tb, a.c.ks, smem_u32(sm.ks[st]), bar);
-                    copy_scales(a.c, tb, a.c.vs, smem_u32(sm.vs[st]), bar);
-                }
-            }
-            if (!ok) break;
+    // The block-table entry of the lane's box of the warp's part of tile x (of the
+    // request's tiles), -2 when the box holds no key. Asked for one tile ahead of
+    // the copies: the answer takes as long as a tile.
+    auto lookup = [&](const PagedWalk &w, int x) -> int {
+        int lo, hi;
+        request_span(s, w.r, lo, hi);
+        const int pos = x * kTilePositions + 32 * warp + (lane << box_shift);
+        if ((lane << box_shift) >= 32 || pos >= hi || pos + a.c.box <= lo) return -2;
+        return __ldg(a.c.table + static_cast<int64_t>(w.b) * a.c.W + pos / a.c.page);
+    };
+    // Where the lane's box lies in the cache (-1: not loaded), from its entry.
+    auto place = [&](const PagedWalk &w, int x, int id) -> int {
+        if (id == -2) return -1;
+        if (id < 0 || id >= a.c.P) {
+            record_device_error(a.err, KID_ATTN, ROLE_PRODUCER, 9);
+            return -1;
         }
-        // nothing may be in flight when the CTA ends
-        if (!ok)
-            for (uint32_t x = it > kRowStages ? it - kRowStages : 0; x < it; ++x)
-                mbar_wait(smem_u32(&sm.full[x % kRowStages]), (x / kRowStages) & 1, &sm.abort_flag,
-                          a.err, ROLE_PRODUCER, 2, kWaitLimitNs, KID_ATTN);
-        return;
-    }
+        const int pos = x * kTilePositions + 32 * warp + (lane << box_shift);
+        return (id * a.c.Hkv + w.h) * a.c.page + pos % a.c.page;   // (rows of the cache: below 2^31)
+    };
+    // Starts the copies of K, or of V, of the boxes at `row` into stage n % kStages
+    // (whose last reader, this warp, is done with it).
+    auto copy = [&](bool v, int row, uint32_t n) {
+        const int sg = n % kStages;
+        const uint32_t bar = smem_u32(v ? &sm.vfull[warp][sg] : &sm.kfull[warp][sg]);
+        const unsigned used = __ballot_sync(0xFFFFFFFFu, row >= 0);
+        if (lane == 0)
+            mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(used) << box_shift) *
+                                           (kInt8 ? 128 + 4 : 2 * 128));
+        __syncwarp();
+        if (row < 0) return;
+        const uint32_t dst = smem_u32(v ? sm.v[warp][sg] : sm.k[warp][sg]) +
+                             static_cast<uint32_t>(lane << box_shift) * 128;
+#pragma unroll
+        for (int half = 0; half < Tile<kInt8>::kHalves; ++half)
+            tma_load_2d(dst + half * 4096, v ? &vm : &km, half * 64, row, bar);
+        if constexpr (kInt8)
+            bulk_g2s(smem_u32(v ? &sm.vs[warp][sg][lane << box_shift] : &sm.ks[warp][sg][lane << box_shift]),
+                     (v ? a.c.vs : a.c.ks) + row, a.c.box * 4, bar);
+    };
+    // Which of the 32 positions hold keys, given where the boxes lie.
+    auto keys = [&](const PagedWalk &w, int x, int row) -> uint32_t {
+        int lo, hi;
+        request_span(s, w.r, lo, hi);
+        const unsigned used = __ballot_sync(0xFFFFFFFFu, row >= 0);
+        const int pos = x * kTilePositions + 32 * warp + lane;
+        return __ballot_sync(0xFFFFFFFFu,
+                             ((used >> (lane >> box_shift)) & 1u) && pos >= lo && pos < hi);
+    };
+    int ahead = -2;
+    auto begin = [&](const PagedWalk &w, const PagedPiece &p) {
+        int id[kStages];
+#pragma unroll
+        for (int j = 0; j < kStages; ++j)
+            id[j] = p.first + j < p.last ? lookup(w, p.tile0 + p.first + j) : -2;
+        if (p.first + kStages < p.last) ahead = lookup(w, p.tile0 + p.first + kStages);
+#pragma unroll
+        for (int j = 0; j < kStages; ++j) {
+            if (p.first + j >= p.last) continue;
+            const int x = p.tile0 + p.first + j, row = place(w, x, id[j]);
+            copy(false, row, it + j);
+            copy(true, row, it + j);
+            const uint32_t mask = keys(w, x, row);
+            if (lane == 0) sm.mask[warp][(it + j) % kStages] = mask;
+        }
+        issued = it + min(kStages, p.last - p.first);
+        __syncwarp();
+    };
+    PagedPiece p = paged_piece(s, w, sh.begin, sh.end);
+    begin(w, p);
 
-    const int pw = warp * 32;
-    for (; !w.done(s, sh.end); w.next(s)) {
-        const PagedPiece p = paged_piece(s, w, sh.begin, sh.end);
-        if (p.first == p.last && !p.whole) continue;
+    while (true) {
         const int rows = p.ntok * a.o.G;
-        // q rows 8 nt + gid, dims [32 t, 32 t + 32), as bf16 pairs
-        uint32_t qf[NT][16];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int r = 8 * nt + gid;
-            const bool use = r < rows;
-            const int tok = use ? r / a.o.G : 0, g = use ? r % a.o.G : 0;
-            const uint4 *src = reinterpret_cast<const uint4 *>(
-                a.q + (static_cast<int64_t>(w.r.t0) + p.tok0 + tok) * a.qt +
-                (static_cast<int64_t>(w.h) * a.o.G + g) * a.qh + 32 * t);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const uint4 y = use ? __ldg(src + x) : make_uint4(0, 0, 0, 0);
-                qf[nt][4 * x + 0] = y.x;
-                qf[nt][4 * x + 1] = y.y;
-                qf[nt][4 * x + 2] = y.z;
-                qf[nt][4 * x + 3] = y.w;
-            }
-        }
-        // INT8: q in fp16, scaled by the power of two that puts the item's
-        // largest |q| in [2^14, 2^15); the scores are scaled back exactly
-        float qinv = 1.0f;
-        if constexpr (kInt8) {
-            uint32_t mq = 0;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int x = 0; x < 16; ++x) mq = __vmaxu2(mq, qf[nt][x] & 0x7FFF7FFFu);
-            mq = max(mq & 0xFFFFu, mq >> 16);
-            mq = __reduce_max_sync(0xFFFFFFFFu, mq);
-            const int bexp = static_cast<int>((mq >> 7) & 0xFFu);
-            const int se = bexp == 0 ? 0 : max(-100, min(100, 14 - (bexp - 127)));
-            const float qs = __uint_as_float(static_cast<uint32_t>(se + 127) << 23);
-            qinv = __uint_as_float(static_cast<uint32_t>(127 - se) << 23);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int x = 0; x < 16; ++x)
-                    qf[nt][x] = pack_f16x2(__uint_as_float(qf[nt][x] << 16) * qs,
-                                           __uint_as_float(qf[nt][x] & 0xFFFF0000u) * qs);
-        }
-        // the positions that this lane's score columns see: [from, upto)
-        int from[NT][2], upto[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int r = 8 * nt + 2 * t + j;
-                const int pos = w.r.base + p.tok0 + r / a.o.G;
-                upto[nt][j] = r < rows ? pos + 1 : 0;
-                from[nt][j] = s.window > 0 ? max(pos, 0) - s.window + 1 : 0;
-            }
-        // tiles that every row sees whole need no mask
-        const int pos_first = w.r.base + p.tok0, pos_last = pos_first + p.ntok - 1;
+        const bool idle = p.first == p.last && !p.whole;
         WarpState<NT> st;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -255,39 +252,141 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant_
 #pragma unroll
                 for (int k = 0; k < 4; ++k) st.o[i][nt][k] = 0.0f;
         st.se = 0;
-
-        for (int x = p.first; x < p.last; ++x, ++it) {
-            const int sg = it % kRowStages;
-            if (ok)
-                ok = mbar_wait(smem_u32(&sm.full[sg]), (it / kRowStages) & 1, &sm.abort_flag, a.err,
-                               ROLE_EPILOGUE, 3, kWaitLimitNs, KID_ATTN);
-            __syncwarp();
-            const TileMask m = sm.mask[sg];
-            const bool full = (m.w[0] & m.w[1] & m.w[2] & m.w[3]) == 0xFFFFFFFFu;
-            ChunkRegs<kInt8> r;
-            tile_frags<kInt8>(r, sm.stage[sg].k, sm.stage[sg].v, sm.ks[sg], sm.vs[sg], m, full, pw,
-                              gid, t);
-            mbar_arrive(smem_u32(&sm.empty[sg]));
-            const int c0 = (p.tile0 + x) * kTilePositions;
-            const bool plain = full && c0 + kTilePositions - 1 <= pos_first &&
-                               (s.window == 0 || c0 > pos_last - s.window);
-            if (plain) {
-                attend_chunk<NT, kInt8>(
-                    st, r, qf, [](int, int, int) { return true; }, a.scale, qinv, pw, gid, t);
-            } else {
-                const uint32_t mw = m.w[warp];   // this warp's 32 positions
-                attend_chunk<NT, kInt8>(
-                    st, r, qf,
-                    [&](int row, int nt, int j) {
-                        return ((mw >> (row - pw)) & 1u) && c0 + row < upto[nt][j] &&
-                               c0 + row >= from[nt][j];
-                    },
-                    a.scale, qinv, pw, gid, t);
+        if (p.first < p.last) {
+            // q rows 8 nt + gid, dims [32 t, 32 t + 32), as bf16 pairs
+            uint32_t qf[NT][16];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int r = 8 * nt + gid;
+                const bool use = r < rows;
+                const int tok = use ? r / a.o.G : 0, g = use ? r % a.o.G : 0;
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                    a.q + (static_cast<int64_t>(w.r.t0) + p.tok0 + tok) * a.qt +
+                    (static_cast<int64_t>(w.h) * a.o.G + g) * a.qh + 32 * t);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const uint4 y = use ? __ldg(src + x) : make_uint4(0, 0, 0, 0);
+                    qf[nt][4 * x + 0] = y.x;
+                    qf[nt][4 * x + 1] = y.y;
+                    qf[nt][4 * x + 2] = y.z;
+                    qf[nt][4 * x + 3] = y.w;
+                }
             }
+            // INT8: q in fp16, scaled by the power of two that puts the item's
+            // largest |q| in [2^14, 2^15); the scores are scaled back exactly
+            float qinv = 1.0f;
+            if constexpr (kInt8) {
+                uint32_t mq = 0;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) mq = __vmaxu2(mq, qf[nt][x] & 0x7FFF7FFFu);
+                mq = max(mq & 0xFFFFu, mq >> 16);
+                mq = __reduce_max_sync(0xFFFFFFFFu, mq);
+                const int bexp = static_cast<int>((mq >> 7) & 0xFFu);
+                const int se = bexp == 0 ? 0 : max(-100, min(100, 14 - (bexp - 127)));
+                const float qs = __uint_as_float(static_cast<uint32_t>(se + 127) << 23);
+                qinv = __uint_as_float(static_cast<uint32_t>(127 - se) << 23);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 16; ++x)
+                        qf[nt][x] = pack_f16x2(__uint_as_float(qf[nt][x] << 16) * qs,
+                                               __uint_as_float(qf[nt][x] & 0xFFFF0000u) * qs);
+            }
+            // the positions that this lane's score columns see: [from, upto)
+            int from[NT][2], upto[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int r = 8 * nt + 2 * t + j;
+                    const int pos = w.r.base + p.tok0 + r / a.o.G;
+                    upto[nt][j] = r < rows ? pos + 1 : 0;
+                    from[nt][j] = s.window > 0 ? max(pos, 0) - s.window + 1 : 0;
+                }
+            // tiles that every row sees whole need no mask
+            const int pos_first = w.r.base + p.tok0, pos_last = pos_first + p.ntok - 1;
+            // (not unrolled over the stages: the two forms of the body fill the
+            // instruction cache as it is, and three copies ran at half the speed)
+#pragma unroll 1
+            for (int x = p.first; x < p.last; ++x) {
+                const int sg = it % kStages;
+                auto landed = [&](uint64_t &bar, unsigned site) {
+                    if (ok)
+                        ok = mbar_wait(smem_u32(&bar), (it / kStages) & 1, &sm.abort_flag, a.err,
+                                       ROLE_EPILOGUE, site, kWaitLimitNs, KID_ATTN);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                };
+                landed(sm.kfull[warp][sg], 3);
+                const uint32_t mw = sm.mask[warp][sg];
+                ChunkRegs<kInt8> r;
+                key_frags<kInt8>(r, sm.k[warp][sg], sm.ks[warp][sg], gid, t);
+                __syncwarp();   // every lane has its fragments: K's stage is free
+                const bool more = ok && x + kStages < p.last;
+                const int next = p.tile0 + x + kStages;
+                int row = -1;
+                uint32_t mask = 0;
+                if (more) {
+                    row = place(w, next, ahead);
+                    if (x + kStages + 1 < p.last) ahead = lookup(w, next + 1);
+                    mask = keys(w, next, row);
+                    copy(false, row, it + kStages);
+                }
+                auto values = [&](ChunkRegs<kInt8> &r) {
+                    landed(sm.vfull[warp][sg], 4);
+                    value_frags<kInt8>(r, sm.v[warp][sg], sm.vs[warp][sg], mw, gid, t);
+                    __syncwarp();
+                    if (more) {
+                        copy(true, row, it + kStages);
+                        if (lane == 0) sm.mask[warp][sg] = mask;
+                        issued = it + kStages + 1;
+                    }
+                };
+                const int c0 = (p.tile0 + x) * kTilePositions + 32 * warp;
+                const bool plain = mw == 0xFFFFFFFFu && c0 + 31 <= pos_first &&
+                                   (s.window == 0 || c0 > pos_last - s.window);
+                if (plain) {
+                    attend_chunk<NT, kInt8>(
+                        st, r, qf, [](int, int, int) { return true; }, values, a.scale, qinv, 0, gid, t);
+                } else {
+                    attend_chunk<NT, kInt8>(
+                        st, r, qf,
+                        [&](int row, int nt, int e) {
+                            return ((mw >> row) & 1u) && c0 + row < upto[nt][e] &&
+                                   c0 + row >= from[nt][e];
+                        },
+                        values, a.scale, qinv, 0, gid, t);
+                }
+                ++it;
+                if (!ok && issued > it) {   // what is in flight lands before the CTA ends
+                    int never = 0;
+                    for (uint32_t n = it; n < issued; ++n) {
+                        mbar_wait(smem_u32(&sm.kfull[warp][n % kStages]), (n / kStages) & 1, &never,
+                                  a.err, ROLE_PRODUCER, 2, kWaitLimitNs, KID_ATTN);
+                        mbar_wait(smem_u32(&sm.vfull[warp][n % kStages]), (n / kStages) & 1, &never,
+                                  a.err, ROLE_PRODUCER, 2, kWaitLimitNs, KID_ATTN);
+                    }
+                    issued = it;
+                }
+            }
+        }
+        // the next item's first tiles are on their way while this one ends
+        const PagedWalk cw = w;
+        const PagedPiece cp = p;
+        w.next(s);
+        const bool last = w.done(s, sh.end);
+        if (!last) {
+            p = paged_piece(s, w, sh.begin, sh.end);
+            if (ok) begin(w, p);
+        }
+        if (idle) {
+            if (last) break;
+            continue;
         }
 
         // ---- join the four warps: every warp's state weighted by
-        // e^(its max - the item's max); warps 2, 3 into 0, 1, then 1 into 0
+        // e^(its max - the item's max)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -300,7 +399,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant_
                     sm.red_l[warp][8 * nt + 2 * t + j] = l;
                 }
             }
-        named_barrier_sync(1, kRowWarps * 32);
+        named_barrier_sync(1, kRowThreads);
         const float unit = __uint_as_float(static_cast<uint32_t>(127 - st.se) << 23);   // 2^-se
         float mx[NT][2], l[NT][2];
 #pragma unroll
@@ -324,77 +423,79 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant_
                     st.o[i][nt][j + 2] *= f;
                 }
             }
-#pragma unroll
-        for (int step = 2; step > 0; step >>= 1) {
-            if (warp >= step && warp < 2 * step) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            sm.merge[warp - step][(i * NT + nt) * 4 + k][lane] = st.o[i][nt][k];
-            }
-            named_barrier_sync(1, kRowWarps * 32);
-            if (warp < step) {
+#pragma unroll 1
+        for (int giver = 1; giver < kRowWarps; ++giver) {
+            if (warp == giver) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            st.o[i][nt][k] += sm.merge[warp][(i * NT + nt) * 4 + k][lane];
+                            sm.merge[(i * NT + nt) * 4 + k][lane] = st.o[i][nt][k];
             }
-            named_barrier_sync(1, kRowWarps * 32);
+            named_barrier_sync(1, kRowThreads);
+            if (warp == 0) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            st.o[i][nt][k] += sm.merge[(i * NT + nt) * 4 + k][lane];
+            }
+            named_barrier_sync(1, kRowThreads);
         }
-        if (warp != 0 || !ok) continue;
-        // lane (gid, t) has dims [16 gid, 16 gid + 16) of rows 8 nt + 2 t + j:
-        // fragment i, elements j and j + 2 are dims 2 i and 2 i + 1 of them
-        float *part = slot_of(a.ws, kRowsMax, blockIdx.x, p.slot);
+        if (warp == 0 && ok) {
+            // lane (gid, t) has dims [16 gid, 16 gid + 16) of rows 8 nt + 2 t + j:
+            // fragment i, elements j and j + 2 are dims 2 i and 2 i + 1 of them
+            float *part = slot_of(a.ws, kRowsMax, blockIdx.x, cp.slot);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int r = 8 * nt + 2 * t + j;
-                if (r >= rows) continue;
-                float v[16];
+                for (int j = 0; j < 2; ++j) {
+                    const int r = 8 * nt + 2 * t + j;
+                    if (r >= rows) continue;
+                    float v[16];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    v[2 * i] = st.o[i][nt][j];
-                    v[2 * i + 1] = st.o[i][nt][j + 2];
-                }
-                if (!p.whole) {
-                    float4 *dst = reinterpret_cast<float4 *>(part + r * kHeadDim + 16 * gid);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                    if (gid == 0) {
-                        part[kRowsMax * kHeadDim + r] = mx[nt][j];
-                        part[kRowsMax * (kHeadDim + 1) + r] = l[nt][j];
+                    for (int i = 0; i < 8; ++i) {
+                        v[2 * i] = st.o[i][nt][j];
+                        v[2 * i + 1] = st.o[i][nt][j + 2];
                     }
-                    continue;
+                    if (!cp.whole) {
+                        float4 *dst = reinterpret_cast<float4 *>(part + r * kHeadDim + 16 * gid);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                        if (gid == 0) {
+                            part[kRowsMax * kHeadDim + r] = mx[nt][j];
+                            part[kRowsMax * (kHeadDim + 1) + r] = l[nt][j];
+                        }
+                        continue;
+                    }
+                    const int64_t orow = out_row(a.o, cw.r, cw.h, cp.tok0, r);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)   // (a row that sees nothing: zeros)
+                        v[i] = l[nt][j] == 0.0f ? 0.0f : v[i] / l[nt][j];
+                    if (a.o.fp32) {
+                        float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.o.out) +
+                                                                 orow * kHeadDim + 16 * gid);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    } else {
+                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o.out) +
+                                                               orow * kHeadDim + 16 * gid);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            dst[i] = make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]),
+                                                pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                                                pack_bf16x2(v[8 * i + 4], v[8 * i + 5]),
+                                                pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+                    }
                 }
-                const int64_t orow = out_row(a.o, w.r, w.h, p.tok0, r);
-#pragma unroll
-                for (int i = 0; i < 16; ++i)   // (a row that sees nothing: zeros)
-                    v[i] = l[nt][j] == 0.0f ? 0.0f : v[i] / l[nt][j];
-                if (a.o.fp32) {
-                    float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.o.out) +
-                                                             orow * kHeadDim + 16 * gid);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                } else {
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o.out) +
-                                                           orow * kHeadDim + 16 * gid);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        dst[i] = make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]),
-                                            pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
-                                            pack_bf16x2(v[8 * i + 4], v[8 * i + 5]),
-                                            pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
-                }
-            }
+        }
+        if (last) break;
     }
 }
 
@@ -402,27 +503,30 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant_
 constexpr int kCombineThreads = 128;
 
 struct CombineArgs {
-    PagedSchedule s;
+    const int32_t *cu;
+    int B, T;
     PagedOut o;
-    const float *ws;
+    float *ws;
     int rows;               // rows of a slot
-    int max_ctas;           // the attention kernel's grid
+    int ctas;               // the attention kernel's grid
 };
 
-// Block (c, y): when the border before CTA c is the first one inside an item,
-// joins the item's shares for rows 4 y + warp, + 4 gridDim.y, ... The other
-// blocks find that out and end. Blocks also write zeros to rows of tokens that
-// belong to no request.
+// Block (c, y): when the border before CTA c is the first one inside an item
+// (its cut says so), joins the item's shares for rows 4 y + warp, + 4 gridDim.y,
+// ... Lane j works out share j and holds its maximum and sum, so a row costs one
+// round of loads for those and one for the shares' outputs. Blocks also write
+// zeros to rows of tokens that belong to no request.
 __global__ void __launch_bounds__(kCombineThreads)
 paged_combine_kernel(const CombineArgs a) {
     griddep_launch_dependents();
     griddep_wait();
-    const PagedSchedule &s = a.s;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = blockIdx.x;
+    const PagedCut cut = cuts_of(a.ws, a.rows, a.ctas)[c];
     {
-        const int64_t first = min(max(s.cu[0], 0), s.T), last = min(max(s.cu[s.B], 0), s.T);
+        const int64_t first = min(max(a.cu[0], 0), a.T), last = min(max(a.cu[a.B], 0), a.T);
         const int64_t per = static_cast<int64_t>(a.o.Hq) * kHeadDim * (a.o.fp32 ? 4 : 2) / 16;
-        const int64_t n = (first + s.T - last) * per;
+        const int64_t n = (first + a.T - last) * per;
         uint4 *out = static_cast<uint4 *>(a.o.out);
         const int64_t stride = static_cast<int64_t>(gridDim.x) * gridDim.y * kCombineThreads;
         for (int64_t i = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * kCombineThreads +
@@ -430,45 +534,76 @@ paged_combine_kernel(const CombineArgs a) {
              i < n; i += stride)
             out[i < first * per ? i : i - first * per + last * per] = make_uint4(0, 0, 0, 0);
     }
-    const int c = blockIdx.x + 1;   // (the first CTA's border cuts nothing)
-    const PagedShare sh = paged_share<kCombineThreads>(s, c, a.max_ctas);
-    if (c >= sh.ctas || sh.b >= s.B) return;
-    PagedWalk w;
-    w.start(s, sh);
-    if (w.at >= sh.begin) return;                                  // between two items
-    if (paged_border(sh.total, sh.ctas, c - 1) > w.at) return;     // an earlier border cut it first
-    // the last CTA that has a share of the item
-    int end = c;
-    while (end + 1 < sh.ctas && paged_border(sh.total, sh.ctas, end + 1) < w.at + w.cost) ++end;
-    const PagedPiece first = paged_piece(s, w, paged_border(sh.total, sh.ctas, c - 1), sh.begin);
-    if (first.ntiles == 0) return;                                 // its zeros are written
-    const int rows = first.ntok * a.o.G;
-    for (int r = blockIdx.y * (kCombineThreads / 32) + warp; r < rows;
-         r += gridDim.y * (kCombineThreads / 32)) {
+    if (cut.ntiles <= 0) return;
+    PagedRequest r;
+    r.t0 = cut.t0;
+    const int rows = cut.ntok * a.o.G;
+    for (int row = blockIdx.y * (kCombineThreads / 32) + warp; row < rows;
+         row += gridDim.y * (kCombineThreads / 32)) {
         float m = kNegInf, l = 0.0f;
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        bool whole = false;
-        for (int k = c - 1; k <= end && !whole; ++k) {
-            const PagedPiece p = paged_piece(s, w, paged_border(sh.total, sh.ctas, k),
-                                             paged_border(sh.total, sh.ctas, k + 1));
-            whole = p.whole;
-            if (p.first == p.last) continue;
-            const float *part =
-                a.ws + (static_cast<int64_t>(k) * 2 + p.slot) * a.rows * (kHeadDim + 2);
-            const float pm = part[a.rows * kHeadDim + r], pl = part[a.rows * (kHeadDim + 1) + r];
-            const float4 v = reinterpret_cast<const float4 *>(part + r * kHeadDim)[lane];
-            const float mn = fmaxf(m, pm);
+        // 32 CTAs at a time, from the one that the border ends
+        for (int k0 = c - 1; k0 < cut.ctas; k0 += 32) {
+            const int k = k0 + lane;
+            const long long from = paged_border(cut.total, cut.ctas, min(k, cut.ctas));
+            const long long upto = paged_border(cut.total, cut.ctas, min(k + 1, cut.ctas));
+            const bool in = k < cut.ctas && from < cut.at + cut.cost;
+            PagedPiece p;
+            p.ntiles = cut.ntiles;
+            p.first = p.last = 0;
+            p.whole = false;
+            if (in) paged_part(p, cut.at, cut.cost, from, upto);
+            if (__any_sync(0xFFFFFFFFu, p.whole)) return;   // one CTA has all its tiles: it wrote it
+            const bool has = p.last > p.first;
+            const float *part = a.ws + (static_cast<int64_t>(k) * 2 + p.slot) * a.rows * (kHeadDim + 2);
+            float pm = kNegInf, pl = 0.0f;
+            if (has) {
+                pm = part[a.rows * kHeadDim + row];
+                pl = part[a.rows * (kHeadDim + 1) + row];
+            }
+            float mn = pm;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, o));
+            mn = fmaxf(mn, m);
             const float mu = mn == kNegInf ? 0.0f : mn;
-            const float fo = expf(m - mu), fn = expf(pm - mu);
+            const float fo = expf(m - mu), fn = has ? expf(pm - mu) : 0.0f;
             m = mn;
-            l = l * fo + pl * fn;
-            acc.x = acc.x * fo + v.x * fn;
-            acc.y = acc.y * fo + v.y * fn;
-            acc.z = acc.z * fo + v.z * fn;
-            acc.w = acc.w * fo + v.w * fn;
+            float ls = pl * fn;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xFFFFFFFFu, ls, o);
+            l = l * fo + ls;
+            acc.x *= fo;
+            acc.y *= fo;
+            acc.z *= fo;
+            acc.w *= fo;
+            unsigned todo = __ballot_sync(0xFFFFFFFFu, has);
+            while (todo != 0) {      // four shares' outputs at a time
+                float4 v[4];
+                float f[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = todo != 0 ? __ffs(todo) - 1 : 0;
+                    const int slot = __shfl_sync(0xFFFFFFFFu, p.slot, j);
+                    f[e] = __shfl_sync(0xFFFFFFFFu, fn, j);
+                    if (todo == 0) f[e] = 0.0f;
+                    v[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (todo != 0)
+                        v[e] = reinterpret_cast<const float4 *>(
+                            a.ws + (static_cast<int64_t>(k0 + j) * 2 + slot) * a.rows * (kHeadDim + 2) +
+                            row * kHeadDim)[lane];
+                    todo &= todo - 1;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    acc.x = fmaf(v[e].x, f[e], acc.x);
+                    acc.y = fmaf(v[e].y, f[e], acc.y);
+                    acc.z = fmaf(v[e].z, f[e], acc.z);
+                    acc.w = fmaf(v[e].w, f[e], acc.w);
+                }
+            }
+            if (__any_sync(0xFFFFFFFFu, !in)) break;
         }
-        if (whole) return;                                         // one CTA wrote the item
-        const int64_t orow = out_row(a.o, w.r, w.h, first.tok0, r);
+        const int64_t orow = out_row(a.o, r, cut.h, cut.tok0, row);
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (l != 0.0f) v = make_float4(acc.x / l, acc.y / l, acc.z / l, acc.w / l);
         if (a.o.fp32)
@@ -500,16 +635,20 @@ cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, int threads, size_t
 
 int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 
-cudaError_t launch_combine(const PagedSchedule &s, const PagedOut &o, const float *ws, int rows,
-                           int max_ctas, cudaStream_t stream) {
+// A warp of the rows kernel copies its 32 positions in boxes of this many.
+int rows_box(const PagedAttnProblem &p) { return gcd(static_cast<int>(p.page), 32); }
+
+cudaError_t launch_combine(const PagedSetup &u, float *ws, int rows, int ctas, cudaStream_t stream) {
     CombineArgs a;
-    a.s = s;
-    a.o = o;
+    a.cu = u.s.cu;
+    a.B = u.s.B;
+    a.T = u.s.T;
+    a.o = u.o;
     a.ws = ws;
     a.rows = rows;
-    a.max_ctas = max_ctas;
+    a.ctas = ctas;
     const unsigned y = rows <= 16 ? 2 : 8;
-    return launch_pdl(paged_combine_kernel, dim3(max_ctas, y), kCombineThreads, 0, stream, a);
+    return launch_pdl(paged_combine_kernel, dim3(ctas, y), kCombineThreads, 0, stream, a);
 }
 
 template <int NT, bool kInt8>
@@ -534,7 +673,8 @@ cudaError_t launch_rows(const PagedAttnProblem &p, const CUtensorMap &km, const 
     int ctas = per_sm[dev] * num_sms;
     if (ctas > kMaxCtas) ctas = kMaxCtas;
     RowsArgs a;
-    const PagedSetup u = paged_setup(p, 8 * NT);
+    PagedSetup u = paged_setup(p, 8 * NT);
+    u.c.box = rows_box(p);
     a.s = u.s;
     a.c = u.c;
     a.o = u.o;
@@ -546,7 +686,7 @@ cudaError_t launch_rows(const PagedAttnProblem &p, const CUtensorMap &km, const 
     a.err = err;
     e = launch_pdl(kernel, dim3(ctas), kRowThreads, smem, stream, km, vm, a);
     if (e != cudaSuccess) return e;
-    return launch_combine(a.s, a.o, a.ws, kRowsMax, ctas, stream);
+    return launch_combine(u, a.ws, kRowsMax, ctas, stream);
 }
 
 }  // namespace
@@ -581,13 +721,13 @@ PagedSetup paged_setup(const PagedAttnProblem &p, int rows) {
     return u;
 }
 
-bool paged_encode_cache(CUtensorMap *map, const void *ptr, bool int8, const PagedAttnProblem &p) {
+bool paged_encode_cache(CUtensorMap *map, const void *ptr, bool int8, const PagedAttnProblem &p,
+                        int box) {
     auto fn = tensor_map_encode_fn();
     if (fn == nullptr) return false;
     cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(p.P * p.Hkv * p.page)};
     cuuint64_t strides[1] = {int8 ? 128u : 256u};
-    cuuint32_t bx[2] = {int8 ? 128u : 64u,
-                        static_cast<cuuint32_t>(gcd(static_cast<int>(p.page), kTilePositions))};
+    cuuint32_t bx[2] = {int8 ? 128u : 64u, static_cast<cuuint32_t>(box)};
     cuuint32_t estr[2] = {1, 1};
     return fn(map, int8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
               const_cast<void *>(ptr), dims, strides, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -597,10 +737,11 @@ bool paged_encode_cache(CUtensorMap *map, const void *ptr, bool int8, const Page
 
 size_t paged_attn_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hkv) {
     if (T <= 0 || B <= 0) return 0;
-    const size_t slots = uses_tiles(T, B, Hq / Hkv)
-                             ? static_cast<size_t>(kPagedTileCtas) * 2 * kPagedTileRows
-                             : static_cast<size_t>(kMaxCtas) * 2 * kRowsMax;
-    return slots * (kHeadDim + 2) * sizeof(float);
+    const size_t row = (kHeadDim + 2) * sizeof(float);
+    const size_t few = kMaxCtas * (2 * kRowsMax * row + sizeof(PagedCut));
+    // (calls for the tiles kernel may take the rows kernel, by q's strides)
+    const size_t many = kPagedTileCtas * (2 * kPagedTileRows * row + sizeof(PagedCut));
+    return uses_tiles(T, B, Hq / Hkv) && many > few ? many : few;
 }
 
 cudaError_t launch_paged_attention(const PagedAttnProblem &p, cudaStream_t stream) {
@@ -618,12 +759,12 @@ cudaError_t launch_paged_attention(const PagedAttnProblem &p, cudaStream_t strea
         const int ctas = info.num_sms < kPagedTileCtas ? info.num_sms : kPagedTileCtas;
         e = launch_paged_tiles(p, u, ctas, err, stream);
         if (e != cudaSuccess) return e;
-        return launch_combine(u.s, u.o, static_cast<float *>(p.workspace), kPagedTileRows, ctas,
-                              stream);
+        return launch_combine(u, static_cast<float *>(p.workspace), kPagedTileRows, ctas, stream);
     }
     const bool int8 = p.ks != nullptr;
     CUtensorMap km, vm;
-    if (!paged_encode_cache(&km, p.kc, int8, p) || !paged_encode_cache(&vm, p.vc, int8, p))
+    if (!paged_encode_cache(&km, p.kc, int8, p, rows_box(p)) ||
+        !paged_encode_cache(&vm, p.vc, int8, p, rows_box(p)))
         return cudaErrorInvalidValue;
     // An item takes whole tokens: 8 rows when the group fits and the call has
     // about one token per request, else 16.

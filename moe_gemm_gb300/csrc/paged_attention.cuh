@@ -129,6 +129,10 @@ __device__ __forceinline__ void request_span(const PagedSchedule &s, const Paged
 __device__ __forceinline__ float *slot_of(float *ws, int rows, int cta, int slot) {
     return ws + (static_cast<int64_t>(cta) * 2 + slot) * rows * (kHeadDim + 2);
 }
+// After the slots of `ctas` CTAs, the cuts.
+__host__ __device__ inline PagedCut *cuts_of(float *ws, int rows, int ctas) {
+    return reinterpret_cast<PagedCut *>(ws + static_cast<int64_t>(ctas) * 2 * rows * (kHeadDim + 2));
+}
 
 struct PagedOut {
     void *out;              // [T, Hq, 128]
@@ -150,8 +154,9 @@ struct PagedSetup {
 PagedSetup paged_setup(const PagedAttnProblem &p, int rows);
 
 // A tensor map over the cache as rows of 128 bytes or BF16 values, a box of
-// 128 bytes x PagedCache::box rows.
-bool paged_encode_cache(CUtensorMap *map, const void *ptr, bool int8, const PagedAttnProblem &p);
+// 128 bytes x `box` rows.
+bool paged_encode_cache(CUtensorMap *map, const void *ptr, bool int8, const PagedAttnProblem &p,
+                        int box);
 
 // The tiles kernel (paged_attention_tiles.cu): 256 query rows per item on the
 // tcgen05 tensor cores. Its workspace slots have kPagedTileRows rows and it

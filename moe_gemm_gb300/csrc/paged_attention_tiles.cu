@@ -456,6 +456,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
     const uint32_t tmem = sm.tmem;
     PagedWalk w;
     w.start(s, sh);
+    if (tid == kThreads - 1)
+        paged_write_cut(s, sh, w, blockIdx.x, cuts_of(a.ws, kPagedTileRows, gridDim.x));
     const bool mine = static_cast<int>(blockIdx.x) < sh.ctas;
     uint32_t it = 0;        // tiles of the pieces before this one
     uint32_t qn[2] = {0, 0};   // pieces with the half before this one
@@ -1051,8 +1053,8 @@ cudaError_t launch_kind(const PagedAttnProblem &p, const PagedSetup &u, int ctas
     a.ws = static_cast<float *>(p.workspace);
     a.err = err;
     CUtensorMap qm, km, vm;
-    if (!encode_q(&qm, p, a.half_tokens) || !paged_encode_cache(&km, p.kc, kInt8, p) ||
-        !paged_encode_cache(&vm, p.vc, kInt8, p))
+    if (!encode_q(&qm, p, a.half_tokens) || !paged_encode_cache(&km, p.kc, kInt8, p, u.c.box) ||
+        !paged_encode_cache(&vm, p.vc, kInt8, p, u.c.box))
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));

@@ -74,7 +74,7 @@ struct PagedShare {
 };
 
 __device__ __forceinline__ long long paged_border(long long total, int ctas, int c) {
-    return c >= ctas ? total : total / ctas * c + total % ctas * c / ctas;
+    return c >= ctas ? total : total * c / ctas;   // (total < 2^50, c < 2^10)
 }
 
 // The share of CTA `cta` (for the combine: the border where it begins). Every
@@ -177,6 +177,14 @@ struct PagedWalk {
     }
 };
 
+// What the combine kernel needs of an item that a border cuts: written, for the
+// first border inside the item, by the CTA that begins there.
+struct PagedCut {
+    long long total, at, cost;   // of the line, and the item's place on it
+    int ctas, ntiles;            // ntiles 0: this border is not the first inside an item
+    int t0, tok0, ntok, h;       // the item
+};
+
 // One CTA's part of an item.
 struct PagedPiece {
     int tok0, ntok;         // the item's new tokens within the request
@@ -185,6 +193,16 @@ struct PagedPiece {
     bool whole;             // no other CTA has a part of the item
     int slot;               // the CTA's workspace slot for it
 };
+
+// The part of an item of `ntiles` cache tiles that lies in [begin, end).
+__device__ __forceinline__ void paged_part(PagedPiece &p, long long at, long long cost,
+                                           long long begin, long long end) {
+    const long long x0 = max(begin - at, 0ll), x1 = min(end - at, cost);
+    p.first = x0 == 0 ? 0 : static_cast<int>(x0 * p.ntiles / cost);
+    p.last = x1 == cost ? p.ntiles : static_cast<int>(x1 * p.ntiles / cost);
+    p.whole = p.first == 0 && p.last == p.ntiles && (p.ntiles > 0 || x0 == 0);
+    p.slot = x0 > 0 ? 0 : 1;
+}
 
 __device__ __forceinline__ PagedPiece paged_piece(const PagedSchedule &s, const PagedWalk &w,
                                                   long long begin, long long end) {
@@ -195,12 +213,29 @@ __device__ __forceinline__ PagedPiece paged_piece(const PagedSchedule &s, const 
     const int lo = s.window > 0 ? max(max(w.r.base + p.tok0, 0) - s.window + 1, 0) : 0;
     p.tile0 = lo / kTilePositions;
     p.ntiles = hi > lo ? (hi + kTilePositions - 1) / kTilePositions - p.tile0 : 0;
-    const long long x0 = max(begin - w.at, 0ll), x1 = min(end - w.at, w.cost);
-    p.first = x0 == 0 ? 0 : static_cast<int>(x0 * p.ntiles / w.cost);
-    p.last = x1 == w.cost ? p.ntiles : static_cast<int>(x1 * p.ntiles / w.cost);
-    p.whole = p.first == 0 && p.last == p.ntiles && (p.ntiles > 0 || x0 == 0);
-    p.slot = x0 > 0 ? 0 : 1;
+    paged_part(p, w.at, w.cost, begin, end);
     return p;
+}
+
+// Called by one thread of every CTA of the attention kernel.
+__device__ __forceinline__ void paged_write_cut(const PagedSchedule &s, const PagedShare &sh,
+                                                const PagedWalk &w, int cta, PagedCut *cuts) {
+    PagedCut c;
+    c.ntiles = 0;
+    if (cta > 0 && cta < sh.ctas && w.b < s.B && w.at < sh.begin &&
+        paged_border(sh.total, sh.ctas, cta - 1) <= w.at) {
+        const PagedPiece p = paged_piece(s, w, sh.begin, sh.end);
+        c.total = sh.total;
+        c.at = w.at;
+        c.cost = w.cost;
+        c.ctas = sh.ctas;
+        c.ntiles = p.ntiles;
+        c.t0 = w.r.t0;
+        c.tok0 = p.tok0;
+        c.ntok = p.ntok;
+        c.h = w.h;
+    }
+    cuts[cta] = c;
 }
 
 }  // namespace w8a8
