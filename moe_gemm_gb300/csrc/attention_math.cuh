@@ -71,6 +71,12 @@ __device__ __forceinline__ uint32_t word_of(const uint4 &v, int i) {
     return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w));
 }
 
+__device__ __forceinline__ float ex2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // One chunk's operands in registers: K rows pw + 16 mt + gid (+ 8), dims
 // [32 t, 32 t + 32); V rows pw + 16 mt + 2 t + {0, 1, 8, 9}, dims [16 gid,
 // 16 gid + 16); the K and V scales of the K rows (zero past the sequence).
@@ -100,12 +106,17 @@ struct WarpState {
 // j) tells whether query row 8 nt + 2 t + j sees the chunk's position `row`;
 // the V scales of positions that no query sees are zero. values(r) is called once
 // the scores are done and may fill in V's part of r (which then need not be held
-// beside K's).
-template <int NT, bool kInt8, typename Valid, typename Values>
+// beside K's). kLog2: scale takes the scores to log2 units, and the exponentials
+// are powers of two by the hardware's approximation (2 ulp) instead of expf.
+template <int NT, bool kInt8, bool kLog2 = false, typename Valid, typename Values>
 __device__ __forceinline__ void attend_chunk(WarpState<NT> &st, ChunkRegs<kInt8> &r,
                                              const uint32_t (&qf)[NT][16], Valid valid,
                                              Values values, float scale, float qinv, int pw, int gid,
                                              int t) {
+    auto power = [](float v) {
+        if constexpr (kLog2) return ex2_approx(v);
+        else return expf(v);
+    };
     // ---- scores: k-step kb covers dims 32 t + 4 kb + {0..3} of each lane
     float sacc[2][NT][4];
 #pragma unroll
@@ -168,7 +179,7 @@ __device__ __forceinline__ void attend_chunk(WarpState<NT> &st, ChunkRegs<kInt8>
             for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
             const float m_new = fmaxf(st.m[nt][j], m);
             mu[nt][j] = m_new == -INFINITY ? 0.0f : m_new;   // no valid score yet
-            alpha[nt][j] = expf(st.m[nt][j] - mu[nt][j]);    // 0 while the state is empty
+            alpha[nt][j] = power(st.m[nt][j] - mu[nt][j]);    // 0 while the state is empty
             st.m[nt][j] = m_new;
             st.l[nt][j] *= alpha[nt][j];
         }
@@ -203,7 +214,7 @@ __device__ __forceinline__ void attend_chunk(WarpState<NT> &st, ChunkRegs<kInt8>
             float pp[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float pr = expf(sacc[mt][nt][i] - mu[nt][i & 1]);
+                const float pr = power(sacc[mt][nt][i] - mu[nt][i & 1]);
                 st.l[nt][i & 1] += pr;
                 pp[i] = (pr * r.vs[mt][i >> 1]) * pscale;
             }

@@ -50,7 +50,7 @@ struct RowsArgs {
     PagedOut o;
     const uint16_t *q;      // [T, Hq, 128], token stride qt, head stride qh
     int64_t qt, qh;
-    float scale;
+    float scale;            // to log2 units
     float *ws;
     unsigned long long *err;
 };
@@ -171,7 +171,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant_
         request_span(s, w.r, lo, hi);
         const int pos = x * kTilePositions + 32 * warp + (lane << box_shift);
         if ((lane << box_shift) >= 32 || pos >= hi || pos + a.c.box <= lo) return -2;
-        return __ldg(a.c.table + static_cast<int64_t>(w.b) * a.c.W + pos / a.c.page);
+        return __ldg(a.c.table + static_cast<int64_t>(w.b) * a.c.W + page_of(a.c, pos));
     };
     // Where the lane's box lies in the cache (-1: not loaded), from its entry.
     auto place = [&](const PagedWalk &w, int x, int id) -> int {
@@ -181,7 +181,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant_
             return -1;
         }
         const int pos = x * kTilePositions + 32 * warp + (lane << box_shift);
-        return (id * a.c.Hkv + w.h) * a.c.page + pos % a.c.page;   // (rows of the cache: below 2^31)
+        return (id * a.c.Hkv + w.h) * a.c.page + pos - page_of(a.c, pos) * a.c.page;   // (rows of the cache: below 2^31)
     };
     // Starts the copies of K, or of V, of the boxes at `row` into stage n % kStages
     // (whose last reader, this warp, is done with it).
@@ -347,10 +347,10 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant_
                 const bool plain = mw == 0xFFFFFFFFu && c0 + 31 <= pos_first &&
                                    (s.window == 0 || c0 > pos_last - s.window);
                 if (plain) {
-                    attend_chunk<NT, kInt8>(
+                    attend_chunk<NT, kInt8, true>(
                         st, r, qf, [](int, int, int) { return true; }, values, a.scale, qinv, 0, gid, t);
                 } else {
-                    attend_chunk<NT, kInt8>(
+                    attend_chunk<NT, kInt8, true>(
                         st, r, qf,
                         [&](int row, int nt, int e) {
                             return ((mw >> row) & 1u) && c0 + row < upto[nt][e] &&
@@ -415,8 +415,8 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant_
                 l[nt][j] = 0.0f;
 #pragma unroll
                 for (int x = 0; x < kRowWarps; ++x)
-                    l[nt][j] += sm.red_l[x][r] * expf(sm.red_m[x][r] - mu);
-                const float f = unit * expf(st.m[nt][j] - mu);
+                    l[nt][j] += sm.red_l[x][r] * ex2_approx(sm.red_m[x][r] - mu);
+                const float f = unit * ex2_approx(st.m[nt][j] - mu);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     st.o[i][nt][j] *= f;
@@ -566,7 +566,7 @@ paged_combine_kernel(const CombineArgs a) {
             for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, o));
             mn = fmaxf(mn, m);
             const float mu = mn == kNegInf ? 0.0f : mn;
-            const float fo = expf(m - mu), fn = has ? expf(pm - mu) : 0.0f;
+            const float fo = ex2_approx(m - mu), fn = has ? ex2_approx(pm - mu) : 0.0f;
             m = mn;
             float ls = pl * fn;
 #pragma unroll
@@ -681,7 +681,7 @@ cudaError_t launch_rows(const PagedAttnProblem &p, const CUtensorMap &km, const 
     a.q = p.q;
     a.qt = p.qt;
     a.qh = p.qh;
-    a.scale = p.scale;
+    a.scale = p.scale * kLog2e;
     a.ws = static_cast<float *>(p.workspace);
     a.err = err;
     e = launch_pdl(kernel, dim3(ctas), kRowThreads, smem, stream, km, vm, a);
@@ -718,6 +718,7 @@ PagedSetup paged_setup(const PagedAttnProblem &p, int rows) {
     u.c.Hkv = static_cast<int>(p.Hkv);
     u.c.page = static_cast<int>(p.page);
     u.c.box = gcd(u.c.page, kTilePositions);
+    u.c.page_shift = (u.c.page & (u.c.page - 1)) == 0 ? __builtin_ctz(u.c.page) : -1;
     return u;
 }
 

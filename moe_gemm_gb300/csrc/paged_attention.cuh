@@ -21,7 +21,12 @@ struct PagedCache {
     const float *ks, *vs;   // INT8: [P, Hkv, page]
     int W, P, Hkv, page;
     int box;                // rows of one TMA box: gcd(page, 128)
+    int page_shift;         // log2 of page, -1: not a power of two
 };
+
+__device__ __forceinline__ int page_of(const PagedCache &c, int pos) {
+    return c.page_shift >= 0 ? pos >> c.page_shift : pos / c.page;
+}
 
 // One tile of 128 positions of one (request, kv head) in shared memory: K and
 // V rows of 128 bytes with the 128-byte swizzle (16-byte piece c of row r at
@@ -56,7 +61,7 @@ __device__ __forceinline__ TileBoxes find_boxes(const PagedCache &c, int b, int 
     bool use = lane < boxes && pos < hi && pos + c.box > lo;
     int64_t row = 0;
     if (use) {
-        const int pg = pos / c.page;
+        const int pg = page_of(c, pos);
         const int id = __ldg(c.table + static_cast<int64_t>(b) * c.W + pg);
         if (id < 0 || id >= c.P) {
             use = false;
@@ -125,7 +130,8 @@ __device__ __forceinline__ void request_span(const PagedSchedule &s, const Paged
 
 // ------------------------------------------------------------------ workspace
 // Of every CTA two slots; a slot holds, of up to `rows` query rows, the sums
-// sum_j e^(s_j - m) v_j (rows x 128), then m, then sum_j e^(s_j - m).
+// sum_j 2^(t_j - m) v_j (rows x 128; t: scores in log2 units), then m, then
+// sum_j 2^(t_j - m).
 __device__ __forceinline__ float *slot_of(float *ws, int rows, int cta, int slot) {
     return ws + (static_cast<int64_t>(cta) * 2 + slot) * rows * (kHeadDim + 2);
 }
@@ -133,6 +139,9 @@ __device__ __forceinline__ float *slot_of(float *ws, int rows, int cta, int slot
 __host__ __device__ inline PagedCut *cuts_of(float *ws, int rows, int ctas) {
     return reinterpret_cast<PagedCut *>(ws + static_cast<int64_t>(ctas) * 2 * rows * (kHeadDim + 2));
 }
+
+// The attention kernels work in log2 units.
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct PagedOut {
     void *out;              // [T, Hq, 128]

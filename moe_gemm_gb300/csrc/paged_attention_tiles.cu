@@ -58,8 +58,6 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kHalfRows = 128;
 constexpr int kInfo = 4;             // tiles whose mask and scales are kept
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kMaxWeight = 256.0f; // sums of a tile's weights that move the reference
 constexpr int kOperandBytes = 128 * 128 * 2;
 // Registers of a softmax thread and of the others: 2 x 128 x 168 + 2 x 128 x
@@ -204,11 +202,6 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ unsigned long long f2_fma(unsigned long long a, unsigned long long b,
                                                      unsigned long long c) {
     unsigned long long r;
@@ -272,8 +265,8 @@ __device__ __forceinline__ void weigh(uint32_t ts, const float4 *col, float c,
                     if (hidden(mk, k, cl)) p0 = -INFINITY;
                     if (hidden(mk, k, cl + 1)) p1 = -INFINITY;
                 }
-                p0 = ex2(p0);
-                p1 = ex2(p1);
+                p0 = ex2_approx(p0);
+                p1 = ex2_approx(p1);
                 unsigned long long p2 = f2_bits(p0, p1);
                 l2[k] = f2_add(l2[k], p2);
                 uint32_t &out = pk[k >> 1][(cc * 4 + i) * 2 + (k & 1)];
@@ -545,7 +538,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                         for (int k = 0; k < 4; ++k) {
                             f[k] = turn;
                             if (top[k] > m[k]) {
-                                const float alpha = ex2(m[k] - top[k]);
+                                const float alpha = ex2_approx(m[k] - top[k]);
                                 f[k] *= alpha;
                                 l[k] *= alpha;
                                 m[k] = top[k];
@@ -610,7 +603,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                     } else {
                         at[k] = static_cast<int64_t>(irow) * kHeadDim;
                         if (quad == 0) {
-                            part[kPagedTileRows * kHeadDim + irow] = m[k] * kLn2;
+                            part[kPagedTileRows * kHeadDim + irow] = m[k];
                             part[kPagedTileRows * (kHeadDim + 1) + irow] = l[k];
                         }
                     }
