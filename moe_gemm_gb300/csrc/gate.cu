@@ -75,20 +75,32 @@ struct GateArgs {
     const float *bias;
     int64_t ldx;
     int T, E, k, n_group, topk_group;
+    int size;               // experts of a group
+    int run_shift;          // log2 of the lanes of a group, -1: groups are not such runs
     int sigmoid, renormalize;
     float scale;
     int32_t *ids;
     float *w;
 };
 
+__device__ __forceinline__ float ex2_approx(float v) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float v) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
+    return y;
+}
+
 // Out of line: it runs for few tokens, and once per expert of a lane.
 __device__ __noinline__ double exp_f64(double v) { return exp(v); }
 
-// The picks of one token: pick j and its logit are held by lane j & 31, in
-// element j >> 5 (id -1: none).
+// The picks of one token: pick j is held by lane j & 31, in element j >> 5 (-1:
+// none).
 struct Picks {
     int id[2];
-    float x[2];
 };
 
 // The two largest of the union of {a1 >= a2} and {b1 >= b2}.
@@ -99,21 +111,65 @@ __device__ __forceinline__ void top2_merge(R &a1, R &a2, R b1, R b2) {
     a2 = fmax(lo, fmax(a2, b2));
 }
 
+// Which groups stay (bit g of kept), from their scores (lane l: groups l and l +
+// 32). Returns false when the last group kept and the first one left out are within
+// `tol` of one another (relative to 1 and to their size).
+template <typename R>
+__device__ __forceinline__ bool rank_groups(const R (&gs)[2], const GateArgs &a, int lane, R tol,
+                                            unsigned (&kept)[2]) {
+    const R none = -INFINITY;
+    // rank of each group: those with a larger score, or an equal one and a lower index
+    int rank[2] = {0, 0};
+    for (int g = 0; g < min(a.n_group, 32); ++g) {
+        const R s = __shfl_sync(kFull, gs[0], g);
+        rank[0] += (s > gs[0] || (s == gs[0] && g < lane)) ? 1 : 0;
+        if (a.n_group > 32) rank[1] += s >= gs[1] ? 1 : 0;
+    }
+    for (int g = 32; g < a.n_group; ++g) {
+        const R s = __shfl_sync(kFull, gs[1], g - 32);
+        rank[0] += s > gs[0] ? 1 : 0;
+        rank[1] += (s > gs[1] || (s == gs[1] && g - 32 < lane)) ? 1 : 0;
+    }
+    bool clear = true;
+    R worst_in = INFINITY, best_out = none;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const bool exists = lane + 32 * h < a.n_group;
+        const bool in = exists && rank[h] < a.topk_group;
+        kept[h] = __ballot_sync(kFull, in);
+        if (in) worst_in = fmin(worst_in, gs[h]);
+        if (exists && !in) best_out = fmax(best_out, gs[h]);
+    }
+    if (tol > R(0)) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            worst_in = fmin(worst_in, __shfl_xor_sync(kFull, worst_in, o));
+            best_out = fmax(best_out, __shfl_xor_sync(kFull, best_out, o));
+        }
+        // (an unavailable group, -inf, is never close to an available one)
+        clear = !(worst_in - best_out <= tol * fmax(R(1), fabs(worst_in)));
+    }
+    return clear;
+}
+
 // Marks the experts outside the topk_group best groups as not available
 // (kr = -inf there). Returns false when the last group kept and the first one
 // left out are within `tol` of one another (relative to 1 and to their size).
 template <typename R, int V>
 __device__ __forceinline__ bool keep_groups(R (&kr)[V], const GateArgs &a, int lane, bool sum2,
                                             R tol) {
-    const int size = a.E / a.n_group;
+    const int size = a.size;
     const R none = -INFINITY;
     R gs[2] = {none, none};   // lane l: the scores of groups l and l + 32
-    const int run = size / V;
-    if (size % V == 0 && (run & (run - 1)) == 0) {
+    const int run = 1 << max(a.run_shift, 0);
+    if (a.run_shift >= 0) {
         // a group is a run of a power of two lanes: every group at once
         R m1 = none, m2 = none;
 #pragma unroll
-        for (int i = 0; i < V; ++i) top2_merge<R>(m1, m2, kr[i], none);
+        for (int i = 0; i < V; ++i) {
+            m2 = fmax(m2, fmin(m1, kr[i]));
+            m1 = fmax(m1, kr[i]);
+        }
         for (int o = 1; o < run; o <<= 1)
             top2_merge<R>(m1, m2, __shfl_xor_sync(kFull, m1, o), __shfl_xor_sync(kFull, m2, o));
         const R s = sum2 && m2 > none ? m1 + m2 : m1;
@@ -137,35 +193,13 @@ __device__ __forceinline__ bool keep_groups(R (&kr)[V], const GateArgs &a, int l
             }
         }
     }
-    // rank of each group: those with a larger score, or an equal one and a lower index
-    int rank[2] = {0, 0};
-    for (int g = 0; g < a.n_group; ++g) {
-        const R s = __shfl_sync(kFull, g < 32 ? gs[0] : gs[1], g & 31);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int mine = lane + 32 * h;
-            rank[h] += (s > gs[h] || (s == gs[h] && g < mine)) ? 1 : 0;
-        }
-    }
-    bool clear = true;
     unsigned kept[2];
-    R worst_in = INFINITY, best_out = none;
+    const bool clear = rank_groups<R>(gs, a, lane, tol, kept);
+    if (a.run_shift >= 0) {
+        const bool stays = (kept[0] >> (lane >> a.run_shift)) & 1u;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const bool exists = lane + 32 * h < a.n_group;
-        const bool in = exists && rank[h] < a.topk_group;
-        kept[h] = __ballot_sync(kFull, in);
-        if (in) worst_in = fmin(worst_in, gs[h]);
-        if (exists && !in) best_out = fmax(best_out, gs[h]);
-    }
-    if (tol > R(0)) {
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            worst_in = fmin(worst_in, __shfl_xor_sync(kFull, worst_in, o));
-            best_out = fmax(best_out, __shfl_xor_sync(kFull, best_out, o));
-        }
-        // (an unavailable group, -inf, is never close to an available one)
-        clear = !(worst_in - best_out <= tol * fmax(R(1), fabs(worst_in)));
+        for (int i = 0; i < V; ++i) kr[i] = stays ? kr[i] : none;
+        return clear;
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -178,8 +212,8 @@ __device__ __forceinline__ bool keep_groups(R (&kr)[V], const GateArgs &a, int l
 // Picks the k largest of the available keys (kr > -inf). Returns false when
 // two keys whose order decides are within tol of one another.
 template <typename R, int V>
-__device__ __forceinline__ bool pick(R (&kr)[V], const float (&x)[V], const GateArgs &a, int lane,
-                                     R tol, Picks &out) {
+__device__ __forceinline__ bool pick(R (&kr)[V], const GateArgs &a, int lane, R tol, Picks &out,
+                                     float &least) {
     using K = typename KeyOf<R>::type;
     K key[V];
     K best = 0;
@@ -189,7 +223,6 @@ __device__ __forceinline__ bool pick(R (&kr)[V], const float (&x)[V], const Gate
         best = best > key[i] ? best : key[i];
     }
     out.id[0] = out.id[1] = -1;
-    out.x[0] = out.x[1] = 0.0f;
     float last = INFINITY;
     bool clear = true;
     const int rounds = tol > R(0) ? a.k + 1 : a.k;   // the first key left out decides too
@@ -201,39 +234,174 @@ __device__ __forceinline__ bool pick(R (&kr)[V], const float (&x)[V], const Gate
                 const float v = unord(mx);
                 if (last - v <= tol * fmaxf(1.0f, fabsf(v))) clear = false;
                 last = v;
+                if (j < a.k) least = v;
             }
         }
         if (j == a.k) break;
         const int owner = __ffs(__ballot_sync(kFull, best == mx)) - 1;
-        int at = 0;
-        float xv = 0.0f;
-        if (lane == owner) {
+        // the owner's first element that holds it, taken out (every lane does the
+        // same steps: a branch for one lane costs as many)
+        uint32_t held = 0;
 #pragma unroll
-            for (int i = V - 1; i >= 0; --i)
-                if (key[i] == mx) {
-                    at = i;
-                    xv = x[i];
-                }
-            best = 0;
+        for (int i = 0; i < V; ++i) held |= key[i] == mx ? 1u << i : 0u;
+        const int at = __ffs(held) - 1;
+        const int gone = lane == owner ? at : -1;
+        best = 0;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                if (i == at) key[i] = 0;
-                best = best > key[i] ? best : key[i];
-            }
+        for (int i = 0; i < V; ++i) {
+            key[i] = i == gone ? K(0) : key[i];
+            best = best > key[i] ? best : key[i];
         }
         const int id = __shfl_sync(kFull, lane * V + at, owner);
-        const float xs = __shfl_sync(kFull, xv, owner);
         if (lane == (j & 31)) {
-            if (j < 32) {
-                out.id[0] = id;
-                out.x[0] = xs;
-            } else {
-                out.id[1] = id;
-                out.x[1] = xs;
-            }
+            if (j < 32) out.id[0] = id;
+            else out.id[1] = id;
         }
     }
     return clear;
+}
+
+// The same picks by fewer steps: keys as integers whose low log2(V) bits give way to
+// the element's place, each lane's sorted once, so that a pick is one redux and one
+// step of the owner's list. Returns false when keys that these bits (or, with a
+// bias, the tolerance) cannot tell apart may matter; exact: their loss is none
+// (BF16 logits).
+template <int V>
+__device__ __forceinline__ bool pick_sorted(const float (&kr)[V], const GateArgs &a, int lane,
+                                            float tol, bool exact, Picks &out, float &least) {
+    constexpr uint32_t kPlace = V - 1;
+    uint32_t c[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] = (ord(kr[i]) & ~kPlace) | (kPlace - i);
+    // Batcher's odd-even merge sort, largest first
+#pragma unroll
+    for (int p = 1; p < V; p <<= 1)
+#pragma unroll
+        for (int q = p; q >= 1; q >>= 1)
+#pragma unroll
+            for (int j = q % p; j + q < V; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i) {
+                    const int x = i + j, y = i + j + q;
+                    if (y < V && x / (2 * p) == y / (2 * p)) {
+                        const uint32_t hi = max(c[x], c[y]), lo = min(c[x], c[y]);
+                        c[x] = hi;
+                        c[y] = lo;
+                    }
+                }
+    out.id[0] = out.id[1] = -1;
+    const uint32_t none = ord(-INFINITY) | kPlace;
+    uint32_t last = 0xFFFFFFFFu;
+    float last_v = INFINITY;
+    bool clear = true;
+    for (int j = 0; j <= a.k; ++j) {    // (the first key left out decides too)
+        const uint32_t mx = warp_max(c[0]) & ~kPlace;
+        if (mx <= none) break;
+        if (tol > 0.0f) {
+            const float v = unord(mx);
+            if (last_v - v <= tol * fmaxf(1.0f, fabsf(v))) clear = false;
+            last_v = v;
+            if (j < a.k) least = v;
+        } else if (!exact && mx == last) {
+            clear = false;
+        }
+        last = mx;
+        if (j == a.k) break;
+        const int owner = __ffs(__ballot_sync(kFull, (c[0] & ~kPlace) == mx)) - 1;
+        const int id = owner * V + static_cast<int>(kPlace - (__shfl_sync(kFull, c[0], owner) & kPlace));
+        if (lane == owner) {
+#pragma unroll
+            for (int i = 0; i + 1 < V; ++i) c[i] = c[i + 1];
+            c[V - 1] = 0;
+        }
+        if (lane == (j & 31)) {
+            if (j < 32) out.id[0] = id;
+            else out.id[1] = id;
+        }
+    }
+    return clear;
+}
+
+// Decides a token with sigmoid scores again in 64 bits, on the experts that can
+// matter alone, one per lane (a whole token in 64 bits takes nine microseconds,
+// and one such token held up the call): those that are their group's two largest
+// within the tolerance, and those that reach `least`, the smallest key that the
+// 32-bit choice needed. kr: 32-bit keys, all groups. Returns false when there are
+// more than 32 of them, or too few for the groups that stay.
+template <int V, typename Tin>
+__device__ __forceinline__ bool decide_again(const Tin *row, const float (&kr)[V], const GateArgs &a,
+                                          int lane, float tol, float least, int *list, Picks &out) {
+    if (a.n_group > 32) return false;
+    const int size = a.size;
+    const bool groups = a.topk_group < a.n_group;
+    unsigned mine = 0;
+    if (groups) {
+        for (int g = 0; g < a.n_group; ++g) {
+            float m1 = -INFINITY, m2 = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int e = lane * V + i;
+                top2_merge<float>(m1, m2, e >= g * size && e < (g + 1) * size ? kr[i] : -INFINITY,
+                                  -INFINITY);
+            }
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1)
+                top2_merge<float>(m1, m2, __shfl_xor_sync(kFull, m1, o), __shfl_xor_sync(kFull, m2, o));
+            const float bar = m2 > -INFINITY ? m2 - 2.0f * tol * fmaxf(1.0f, fabsf(m2)) : m1;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int e = lane * V + i;
+                if (e >= g * size && e < (g + 1) * size && kr[i] > -INFINITY && kr[i] >= bar)
+                    mine |= 1u << i;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (kr[i] > -INFINITY && kr[i] >= least) mine |= 1u << i;
+    int at = __popc(mine);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kFull, at, o);
+        if (lane >= o) at += u;
+    }
+    const int n = __shfl_sync(kFull, at, 31);
+    if (n > 32) return false;
+    at -= __popc(mine);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if ((mine >> i) & 1u) list[at++] = lane * V + i;
+    __syncwarp();
+    const int e = lane < n ? list[lane] : -1;
+    double key = -INFINITY;
+    if (e >= 0) {
+        const float x = fminf(load_logit(row + e), 3.402823466e38f);
+        key = 1.0 / (1.0 + exp_f64(-static_cast<double>(x))) + static_cast<double>(__ldg(a.bias + e));
+    }
+    if (groups) {
+        double m1 = -INFINITY, m2 = -INFINITY;
+        for (int c = 0; c < n; ++c) {
+            const double kc = __shfl_sync(kFull, key, c);
+            if (__shfl_sync(kFull, e, c) / size == lane) top2_merge<double>(m1, m2, kc, -INFINITY);
+        }
+        const double gs[2] = {m2 > -INFINITY ? m1 + m2 : m1, -INFINITY};
+        unsigned kept[2];
+        rank_groups<double>(gs, a, lane, 0.0, kept);
+        if (e >= 0 && !((kept[0] >> (e / size)) & 1u)) key = -INFINITY;
+    }
+    // enough of those at or above `least` (all of them are here) must be left
+    const bool good = key > -INFINITY && key >= static_cast<double>(least) + tol * fmax(1.0, fabs(key));
+    if (__popc(__ballot_sync(kFull, good)) < a.k) return false;
+    uint64_t left = good ? ord(key) : 0;
+    out.id[0] = out.id[1] = -1;
+    for (int j = 0; j < a.k; ++j) {
+        const uint64_t mx = warp_max(left);
+        const int owner = __ffs(__ballot_sync(kFull, left == mx)) - 1;   // (lists rise by expert)
+        const int id = __shfl_sync(kFull, e, owner);
+        if (lane == owner) left = 0;
+        if (lane == j) out.id[0] = id;
+    }
+    return true;
 }
 
 template <int V, typename Tin>
@@ -241,6 +409,7 @@ __global__ void __launch_bounds__(kGateWarps * 32)
 moe_gate_kernel(const Tin *__restrict__ logits, const GateArgs a) {
     griddep_launch_dependents();
     griddep_wait();
+    __shared__ int s_list[kGateWarps][32];
     const int lane = threadIdx.x & 31;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + (threadIdx.x >> 5);
     if (t >= a.T) return;
@@ -269,30 +438,43 @@ moe_gate_kernel(const Tin *__restrict__ logits, const GateArgs a) {
         for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
     }
     Picks p;
+    float least = -INFINITY;    // the smallest 32-bit key picked
     if (a.bias == nullptr) {
         float kr[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) kr[i] = x[i];
         if (a.topk_group < a.n_group) keep_groups<float, V>(kr, a, lane, false, 0.0f);
-        pick<float, V>(kr, x, a, lane, 0.0f, p);
+        if (!pick_sorted<V>(kr, a, lane, 0.0f, sizeof(Tin) == 2, p, least))
+            pick<float, V>(kr, a, lane, 0.0f, p, least);
     } else {
-        // A 32-bit key is off by at most: sigmoid, 4 roundings of a number <= 1
-        // and the sum's; softmax, those of its sum of E terms as well, relative
-        // to the score. 2^-20 and 2^-18 cover twice that (two keys compared).
-        const float tol = a.sigmoid ? 0x1p-20f : 0x1p-20f + 0x1p-18f / fmaxf(sum, 1.0f);
+        // A 32-bit key is off by at most: sigmoid, by the hardware's power of two
+        // and reciprocal (2^-22 each, of a number <= 1), the argument's rounding
+        // (|x| 2^-24 s (1 - s) < 2^-25) and the sum's; softmax, by those of its sum of E
+        // terms as well, relative to the score. 2^-19 and 2^-18 cover twice that
+        // (two keys compared).
+        // The places in the keys' low bits take 2^-23 V more of each.
+        const float tol = (a.sigmoid ? 0x1p-19f : 0x1p-19f + 0x1p-18f / fmaxf(sum, 1.0f)) + V * 0x1p-22f;
+        const float inv = __fdiv_rn(1.0f, sum);
         float kr[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int e = lane * V + i;
-            const float s = a.sigmoid ? __fdiv_rn(1.0f, 1.0f + expf(-x[i]))
-                                      : __fdiv_rn(expf(x[i] - m), sum);
+            const float s = a.sigmoid ? rcp_approx(1.0f + ex2_approx(-1.44269504f * x[i]))
+                                      : expf(x[i] - m) * inv;
             kr[i] = x[i] > -INFINITY ? s + __ldg(a.bias + e) : -INFINITY;
         }
+        float all[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) all[i] = kr[i];
         bool clear = true;
         if (a.topk_group < a.n_group)
             clear = keep_groups<float, V>(kr, a, lane, true, 2.0f * tol);
-        if (clear) clear = pick<float, V>(kr, x, a, lane, tol, p);
-        if (!clear) {   // (the same in every lane)
+        clear = pick_sorted<V>(kr, a, lane, tol, false, p, least) && clear;
+        if (!clear && a.sigmoid)   // (the same in every lane)
+            clear = decide_again<V>(row, all, a, lane, tol,
+                                    least - 2.0f * tol * fmaxf(1.0f, fabsf(least)), s_list[threadIdx.x >> 5],
+                                    p);
+        if (!clear) {
             double kd[V];
             double dsum = 0.0;
 #pragma unroll
@@ -312,16 +494,19 @@ moe_gate_kernel(const Tin *__restrict__ logits, const GateArgs a) {
                 kd[i] = x[i] > -INFINITY ? s + static_cast<double>(__ldg(a.bias + e)) : -INFINITY;
             }
             if (a.topk_group < a.n_group) keep_groups<double, V>(kd, a, lane, true, 0.0);
-            pick<double, V>(kd, x, a, lane, 0.0, p);
+            pick<double, V>(kd, a, lane, 0.0, p, least);
         }
     }
     // weights. Renormalised softmax: e^(x - x_max) over the picked; sigmoid as
     // e^min(x, 0) / (1 + e^-|x|), with the common factor e^r taken out before
     // it can underflow (r = 0 when any picked logit is positive).
     float xm = -INFINITY;
+    float px[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-        if (p.id[h] >= 0) xm = fmaxf(xm, p.x[h]);
+    for (int h = 0; h < 2; ++h) {
+        px[h] = p.id[h] >= 0 ? fminf(load_logit(row + p.id[h]), 3.402823466e38f) : 0.0f;
+        if (p.id[h] >= 0) xm = fmaxf(xm, px[h]);
+    }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) xm = fmaxf(xm, __shfl_xor_sync(kFull, xm, o));
     const float r = a.sigmoid ? (a.renormalize ? fminf(xm, 0.0f) : 0.0f)
@@ -332,9 +517,9 @@ moe_gate_kernel(const Tin *__restrict__ logits, const GateArgs a) {
         num[h] = 0.0f;
         if (p.id[h] >= 0) {
             if (a.sigmoid)
-                num[h] = __fdiv_rn(expf(fminf(p.x[h], 0.0f) - r), 1.0f + expf(-fabsf(p.x[h])));
+                num[h] = __fdiv_rn(expf(fminf(px[h], 0.0f) - r), 1.0f + expf(-fabsf(px[h])));
             else
-                num[h] = expf(p.x[h] - r);
+                num[h] = expf(px[h] - r);
         }
         den += num[h];
     }
@@ -389,6 +574,11 @@ cudaError_t launch_moe_gate(const GateProblem &p, cudaStream_t stream) {
     a.k = static_cast<int>(p.k);
     a.n_group = static_cast<int>(p.n_group);
     a.topk_group = static_cast<int>(p.topk_group);
+    a.size = a.E / a.n_group;
+    const int per_lane = a.E <= 32 ? 1 : a.E <= 64 ? 2 : a.E <= 128 ? 4 : a.E <= 256 ? 8
+                                                                     : a.E <= 512 ? 16 : 32;
+    const int run = a.size / per_lane;   // (as launch_any picks V)
+    a.run_shift = a.size % per_lane == 0 && (run & (run - 1)) == 0 ? __builtin_ctz(run) : -1;
     a.sigmoid = p.sigmoid ? 1 : 0;
     a.renormalize = p.renormalize ? 1 : 0;
     a.scale = p.scale;

@@ -231,37 +231,23 @@ paged_kv_write_kernel(const WriteArgs a) {
     if (i >= a.n) return;
     const int64_t t = i / a.Hkv;
     const int h = static_cast<int>(i - t * a.Hkv);
-    const int64_t slot = a.slots[t];
-    if (slot < 0 || slot >= a.n_slots) return;   // the token has no slot
     const bool is_v = (threadIdx.x & 16) != 0;
     const int c = threadIdx.x & 15;
     const uint16_t *src = is_v ? a.v + t * a.vt + h * a.vh : a.k + t * a.kt + h * a.kh;
-    const uint4 x = __ldcs(reinterpret_cast<const uint4 *>(src) + c);
+    const uint4 x = __ldcs(reinterpret_cast<const uint4 *>(src) + c);   // (beside the slot's load)
+    const int64_t slot = a.slots[t];
+    if (slot < 0 || slot >= a.n_slots) return;   // the token has no slot
     const int64_t p = slot / a.page;
     const int64_t row = (p * a.Hkv + h) * a.page + (slot - p * a.page);
     if constexpr (!kInt8) {
         reinterpret_cast<uint4 *>(is_v ? a.vc : a.kc)[row * 16 + c] = x;
     } else {
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        uint32_t m2 = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) m2 = __vmaxu2(m2, w[j] & 0x7FFF7FFFu);
-        uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
+        uint32_t m = amax_bits8(x);
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
         const float s = __fdiv_rn(bf16_bits_to_f32(m), 127.0f);
         const bool fast = s >= 1.17549435e-38f;   // a normal scale: 1 / s is finite
-        const float r = fast ? __frcp_rn(s) : 0.0f;
-        uint32_t f[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            f[2 * j] = __float_as_uint(code_plus_round(bf16_bits_to_f32(w[j] & 0xFFFFu), s, r, fast));
-            f[2 * j + 1] = __float_as_uint(code_plus_round(bf16_bits_to_f32(w[j] >> 16), s, r, fast));
-        }
-        // the codes are the low bytes
-        uint2 q;
-        q.x = __byte_perm(__byte_perm(f[0], f[1], 0x0040), __byte_perm(f[2], f[3], 0x0040), 0x5410);
-        q.y = __byte_perm(__byte_perm(f[4], f[5], 0x0040), __byte_perm(f[6], f[7], 0x0040), 0x5410);
+        const uint2 q = quantize8(x, s, fast ? __frcp_rn(s) : 0.0f, fast);
         reinterpret_cast<uint2 *>(is_v ? a.vc : a.kc)[row * 16 + c] = q;
         if (c == 0) (is_v ? a.vs : a.ks)[row] = s;
     }
