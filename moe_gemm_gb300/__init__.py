@@ -164,6 +164,12 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 def _require(t: torch.Tensor, dtype: torch.dtype, name: str, ndim: int,
              shape: Optional[Tuple[int, ...]] = None,
              device: Optional[torch.device] = None) -> None:
+    # (a host-bound decode step spends a third of its time on such checks: the
+    # usual case, everything as it should be, takes one expression)
+    if (t.dtype is dtype and t.is_cuda and t.is_contiguous() and
+            (t.shape == shape if shape is not None else t.dim() == ndim) and
+            (device is None or t.device == device)):
+        return
     if not t.is_cuda or t.dtype != dtype or t.dim() != ndim or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous CUDA {dtype} tensor of rank {ndim}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
@@ -713,9 +719,9 @@ def paged_kv_plan(block_table: torch.Tensor, lens: torch.Tensor, target: torch.T
     _require(target, torch.int32, "target", 1, (B,), dev)
     _require(free_pages, torch.int32, "free_pages", 1, device=dev)
     _require(n_free, torch.int32, "n_free", 1, (1,), dev)
-    out = _empty((2 * B + 1 + 2 * max(n_tokens, 0),), torch.int32, dev, stream)
-    cu_new, kv_lens = out[:B + 1], out[B + 1:2 * B + 1]
-    slots, positions = out[2 * B + 1:2 * B + 1 + n_tokens], out[2 * B + 1 + n_tokens:]
+    n = max(n_tokens, 0)
+    out = _empty((2 * B + 1 + 2 * n,), torch.int32, dev, stream)
+    cu_new, kv_lens, slots, positions = out.split_with_sizes((B + 1, B, n, n))
     with _on_device(dev, stream):
         _check(_lib.w8a8_paged_kv_plan(
             _ptr(block_table), _ptr(lens), _ptr(target), _ptr(free_pages), _ptr(n_free), B, W,

@@ -73,6 +73,7 @@ __device__ __forceinline__ float load_logit(const uint16_t *p) {
 
 struct GateArgs {
     const float *bias;
+    int vec;                // rows and bias may be read 16 bytes at a time
     int64_t ldx;
     int T, E, k, n_group, topk_group;
     int size;               // experts of a group
@@ -97,6 +98,49 @@ __device__ __forceinline__ float rcp_approx(float v) {
 // Out of line: it runs for few tokens, and once per expert of a lane.
 __device__ __noinline__ double exp_f64(double v) { return exp(v); }
 
+// A lane's V logits (-inf past the last expert).
+template <int V>
+__device__ __forceinline__ void load_row(const float *row, const GateArgs &a, int lane, float (&x)[V]) {
+    if constexpr (V >= 4) {
+        if (a.vec) {
+#pragma unroll
+            for (int i = 0; i < V; i += 4) {
+                float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                if (lane * V + i < a.E) v = __ldg(reinterpret_cast<const float4 *>(row + lane * V + i));
+                x[i] = v.x;
+                x[i + 1] = v.y;
+                x[i + 2] = v.z;
+                x[i + 3] = v.w;
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = lane * V + i < a.E ? __ldg(row + lane * V + i) : -INFINITY;
+}
+template <int V>
+__device__ __forceinline__ void load_row(const uint16_t *row, const GateArgs &a, int lane,
+                                         float (&x)[V]) {
+    if constexpr (V >= 8) {
+        if (a.vec) {
+#pragma unroll
+            for (int i = 0; i < V; i += 8) {
+                uint4 v = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+                if (lane * V + i < a.E) v = __ldg(reinterpret_cast<const uint4 *>(row + lane * V + i));
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[i + 2 * j] = __uint_as_float(w[j] << 16);
+                    x[i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+                }
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = lane * V + i < a.E ? load_logit(row + lane * V + i) : -INFINITY;
+}
+
 // The picks of one token: pick j is held by lane j & 31, in element j >> 5 (-1:
 // none).
 struct Picks {
@@ -120,15 +164,18 @@ __device__ __forceinline__ bool rank_groups(const R (&gs)[2], const GateArgs &a,
     const R none = -INFINITY;
     // rank of each group: those with a larger score, or an equal one and a lower index
     int rank[2] = {0, 0};
-    for (int g = 0; g < min(a.n_group, 32); ++g) {
-        const R s = __shfl_sync(kFull, gs[0], g);
-        rank[0] += (s > gs[0] || (s == gs[0] && g < lane)) ? 1 : 0;
-        if (a.n_group > 32) rank[1] += s >= gs[1] ? 1 : 0;
-    }
-    for (int g = 32; g < a.n_group; ++g) {
-        const R s = __shfl_sync(kFull, gs[1], g - 32);
-        rank[0] += s > gs[0] ? 1 : 0;
-        rank[1] += (s > gs[1] || (s == gs[1] && g - 32 < lane)) ? 1 : 0;
+    if (a.n_group <= 32) {
+        for (int g = 0; g < a.n_group; ++g) {
+            const R s = __shfl_sync(kFull, gs[0], g);
+            rank[0] += (s > gs[0] || (s == gs[0] && g < lane)) ? 1 : 0;
+        }
+    } else {
+        for (int g = 0; g < a.n_group; ++g) {
+            const R s = __shfl_sync(kFull, g < 32 ? gs[0] : gs[1], g & 31);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                rank[h] += (s > gs[h] || (s == gs[h] && g < lane + 32 * h)) ? 1 : 0;
+        }
     }
     bool clear = true;
     R worst_in = INFINITY, best_out = none;
@@ -417,16 +464,17 @@ moe_gate_kernel(const Tin *__restrict__ logits, const GateArgs a) {
     // logits: NaN and -inf mark experts that are never picked; +inf counts as
     // the largest finite number
     float x[V];
+    load_row<V>(row, a, lane, x);
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int e = lane * V + i;
-        const float v = e < a.E ? load_logit(row + e) : -INFINITY;
-        x[i] = v == v ? fminf(v, 3.402823466e38f) : -INFINITY;
+        x[i] = x[i] == x[i] ? fminf(x[i], 3.402823466e38f) : -INFINITY;
         m = fmaxf(m, x[i]);
     }
+    if (!a.sigmoid) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+        for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    }
     if (m == -INFINITY) m = 0.0f;   // no expert is available
     // sum of e^(x - m): softmax's denominator
     float sum = 1.0f;
@@ -455,13 +503,13 @@ moe_gate_kernel(const Tin *__restrict__ logits, const GateArgs a) {
         // The places in the keys' low bits take 2^-23 V more of each.
         const float tol = (a.sigmoid ? 0x1p-19f : 0x1p-19f + 0x1p-18f / fmaxf(sum, 1.0f)) + V * 0x1p-22f;
         const float inv = __fdiv_rn(1.0f, sum);
-        float kr[V];
+        float kr[V], bias[V];
+        load_row<V>(a.bias, a, lane, bias);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int e = lane * V + i;
             const float s = a.sigmoid ? rcp_approx(1.0f + ex2_approx(-1.44269504f * x[i]))
                                       : expf(x[i] - m) * inv;
-            kr[i] = x[i] > -INFINITY ? s + __ldg(a.bias + e) : -INFINITY;
+            kr[i] = x[i] > -INFINITY ? s + bias[i] : -INFINITY;
         }
         float all[V];
 #pragma unroll
@@ -502,36 +550,44 @@ moe_gate_kernel(const Tin *__restrict__ logits, const GateArgs a) {
     // it can underflow (r = 0 when any picked logit is positive).
     float xm = -INFINITY;
     float px[2];
+    const int parts = a.k > 32 ? 2 : 1;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        px[h] = p.id[h] >= 0 ? fminf(load_logit(row + p.id[h]), 3.402823466e38f) : 0.0f;
-        if (p.id[h] >= 0) xm = fmaxf(xm, px[h]);
+        px[h] = 0.0f;
+        if (h >= parts || p.id[h] < 0) continue;
+        px[h] = fminf(load_logit(row + p.id[h]), 3.402823466e38f);
+        xm = fmaxf(xm, px[h]);
     }
+    if (a.renormalize) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) xm = fmaxf(xm, __shfl_xor_sync(kFull, xm, o));
+        for (int o = 1; o < 32; o <<= 1) xm = fmaxf(xm, __shfl_xor_sync(kFull, xm, o));
+    }
     const float r = a.sigmoid ? (a.renormalize ? fminf(xm, 0.0f) : 0.0f)
                               : (a.renormalize ? xm : m);
     float num[2], den = 0.0f;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         num[h] = 0.0f;
-        if (p.id[h] >= 0) {
-            if (a.sigmoid)
-                num[h] = __fdiv_rn(expf(fminf(px[h], 0.0f) - r), 1.0f + expf(-fabsf(px[h])));
-            else
-                num[h] = expf(px[h] - r);
-        }
+        if (h >= parts || p.id[h] < 0) continue;
+        if (a.sigmoid)
+            num[h] = __fdividef(expf(fminf(px[h], 0.0f) - r), 1.0f + expf(-fabsf(px[h])));
+        else
+            num[h] = expf(px[h] - r);
         den += num[h];
     }
+    if (a.renormalize) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) den += __shfl_xor_sync(kFull, den, o);
-    if (!a.renormalize) den = a.sigmoid ? 1.0f : sum;
+        for (int o = 1; o < 32; o <<= 1) den += __shfl_xor_sync(kFull, den, o);
+    } else {
+        den = a.sigmoid ? 1.0f : sum;
+    }
+    const float f = __fdiv_rn(a.scale, den);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int j = lane + 32 * h;
-        if (j < a.k) {
+        if (h < parts && j < a.k) {
             a.ids[t * a.k + j] = p.id[h];
-            a.w[t * a.k + j] = p.id[h] >= 0 ? __fdiv_rn(num[h], den) * a.scale : 0.0f;
+            a.w[t * a.k + j] = p.id[h] >= 0 ? num[h] * f : 0.0f;
         }
     }
 }
@@ -568,6 +624,9 @@ cudaError_t launch_any(const void *logits, const GateArgs &a, cudaStream_t strea
 cudaError_t launch_moe_gate(const GateProblem &p, cudaStream_t stream) {
     GateArgs a;
     a.bias = p.bias;
+    auto aligned16 = [](const void *q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
+    const int per16 = p.fp32 ? 4 : 8;
+    a.vec = p.E % 8 == 0 && p.ldx % per16 == 0 && aligned16(p.logits) && aligned16(p.bias);
     a.ldx = p.ldx;
     a.T = static_cast<int>(p.T);
     a.E = static_cast<int>(p.E);
