@@ -667,6 +667,11 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
             uint32_t pn = 0, on = 0, nq = 0;
             uint32_t sk = 0, ph = 0;     // slot and phase of the next operand tile
             bool ok = true;
+            auto poll = [&](uint64_t &b, uint32_t phase, unsigned site) {
+                ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait_spin(bar(b), phase & 1, abort, a.err,
+                                                                  ROLE_MMA, site, KID_ATTN));
+                tc_fence_after();
+            };
             auto wait = [&](uint64_t &b, uint32_t phase, unsigned site) {
                 ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(bar(b), phase & 1, abort, a.err, ROLE_MMA,
                                                              site, kWaitLimitNs, KID_ATTN));
@@ -677,9 +682,10 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
             // the two together, and both halves' softmax would run at once.
             auto hold = [&]() {
                 if (leader && ok) {
-                    const unsigned long long t0 = globaltimer_ns();
+                    unsigned long long t0 = 0;
                     for (uint32_t i = 1; atomicCAS_block(&sm.pipe, 0u, 1u) != 0u; ++i) {
                         if ((i & 255u) != 0) continue;
+                        if (t0 == 0) t0 = globaltimer_ns();
                         if (*abort || globaltimer_ns() - t0 > kWaitLimitNs) {
                             *abort = 1;
                             record_device_error(a.err, KID_ATTN, ROLE_MMA, 9);
