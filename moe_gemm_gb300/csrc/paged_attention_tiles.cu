@@ -93,10 +93,10 @@ struct TilesSmem {
     uint64_t op_full[kOps], op_empty[kOps], raw_full[kRaws], raw_empty[kRaws];
     uint64_t info_full[kInfo];
     uint64_t q_land[2], q_full[2], q_empty[2];
-    uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
+    uint64_t s_full[2][2], p_full[2][2];   // of a half, of each half of a tile
+    uint64_t pv_done[2][2], o_free[2];
     uint64_t q_max, fix, drain[2];
     uint32_t tmem;
-    unsigned pipe;                       // held by the warp whose products go out
     volatile int abort_flag;
 };
 
@@ -185,13 +185,13 @@ __device__ __forceinline__ void tmem_st_tile(uint32_t t, const uint32_t (&a)[16]
         "r"(t + kLane16)
         : "memory");
 }
-// 64 columns of 16 lanes from 16-bit pairs: register 2 i + j is column 4 i + l % 4
+// 32 columns of 16 lanes from 16-bit pairs: register 2 i + j is column 4 i + l % 4
 // of lane l / 4 + 8 j.
-__device__ __forceinline__ void tmem_st_p(uint32_t t, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_st_p(uint32_t t, const uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.16x128b.x16.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::
-            W8A8_I16(r, 0),
-        W8A8_I16(r, 16), "r"(t)
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%16], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::W8A8_I16(r, 0),
+        "r"(t)
         : "memory");
 }
 
@@ -209,12 +209,12 @@ __device__ __forceinline__ unsigned long long f2_fma(unsigned long long a, unsig
     return r;
 }
 
-// What hides keys from a thread's rows: of row k, the columns 8 i + 2 (l % 4) + e
-// with 8 i + e in [lo[k], hi[k]] are seen, and those whose bit in the tile's mask
-// (shifted by 2 (l % 4)) is set.
+// What hides keys of a half tile (64 columns) from a thread's rows: of row k, the
+// columns 8 i + 2 (l % 4) + e with 8 i + e in [lo[k], hi[k]] are seen, and those whose
+// bit in the mask (shifted by 2 (l % 4)) is set.
 struct RowMask {
     int lo[4], hi[4];
-    uint32_t w[4];
+    uint32_t w[2];
 };
 
 __device__ __forceinline__ bool hidden(const RowMask &m, int k, int c) {
@@ -226,25 +226,25 @@ __device__ __forceinline__ bool hidden(const RowMask &m, int k, int c) {
 // forms, for tiles without a mask too (measured: twice the time of a long chunk).
 __device__ __forceinline__ RowMask here(RowMask m) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        asm volatile("" : "+r"(m.lo[k]), "+r"(m.hi[k]), "+r"(m.w[k]));
+    for (int k = 0; k < 4; ++k) asm volatile("" : "+r"(m.lo[k]), "+r"(m.hi[k]));
+    asm volatile("" : "+r"(m.w[0]), "+r"(m.w[1]));
     return m;
 }
 
-// One tile's weights of a thread's 4 rows (row k: lanes l / 4 + 8 (k & 1) of
+// A half tile's weights of a thread's 4 rows (row k: lanes l / 4 + 8 (k & 1) of
 // block k >> 1) against the references -nm, as P's register image, and their
 // sums by row.
 template <bool kInt8, bool kMasked>
 __device__ __forceinline__ void weigh(uint32_t ts, const float4 *col, float c,
                                       const float (&nm)[4], const RowMask &mask,
-                                      uint32_t (&pk)[2][32], float (&sum)[4]) {
+                                      uint32_t (&pk)[2][16], float (&sum)[4]) {
     RowMask mk;
     if constexpr (kMasked) mk = here(mask);
     unsigned long long l2[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) l2[k] = f2_bits(0.0f, 0.0f);
 #pragma unroll
-    for (int cc = 0; cc < 4; ++cc) {
+    for (int cc = 0; cc < 2; ++cc) {
         uint32_t r[2][16];
         tmem_ld_tile(ts + cc * 32, r[0], r[1]);
         tmem_wait_tile(r[0], r[1]);
@@ -297,9 +297,9 @@ __device__ __forceinline__ void row_max(uint32_t ts, const float4 *col, float c,
 #pragma unroll
     for (int k = 0; k < 4; ++k) top[k] = -INFINITY;
 #pragma unroll 1
-    for (int cc = 0; cc < 4; ++cc) {
+    for (int cc = 0; cc < 2; ++cc) {
         uint32_t w = 0;
-        if constexpr (kMasked) w = cc == 0 ? mk.w[0] : cc == 1 ? mk.w[1] : cc == 2 ? mk.w[2] : mk.w[3];
+        if constexpr (kMasked) w = cc == 0 ? mk.w[0] : mk.w[1];
         uint32_t r[2][16];
         tmem_ld_tile(ts + cc * 32, r[0], r[1]);
         tmem_wait_tile(r[0], r[1]);
@@ -418,9 +418,11 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
             mbar_init(bar(sm.q_land[h]), 1);
             mbar_init(bar(sm.q_full[h]), kInt8 ? 128 : 1);
             mbar_init(bar(sm.q_empty[h]), 1 + kHalfRows);
-            mbar_init(bar(sm.s_full[h]), 1);
-            mbar_init(bar(sm.p_full[h]), kHalfRows);
-            mbar_init(bar(sm.o_done[h]), 1);
+            for (int e = 0; e < 2; ++e) {
+                mbar_init(bar(sm.s_full[h][e]), 1);
+                mbar_init(bar(sm.p_full[h][e]), kHalfRows);
+                mbar_init(bar(sm.pv_done[h][e]), 1);
+            }
             mbar_init(bar(sm.o_free[h]), kHalfRows);
         }
         mbar_init(bar(sm.q_max), 128);
@@ -428,7 +430,6 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
         mbar_init(bar(sm.drain[0]), 1);
         mbar_init(bar(sm.drain[1]), 1);
         sm.abort_flag = 0;
-        sm.pipe = 0;
         fence_mbarrier_init();
     }
     // rows of q past a half's whole tokens are never written: zeros, so that
@@ -465,7 +466,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
         for (int k = 0; k < 4; ++k) tok4[k] = (r4 + 8 * k) / a.o.G;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // lane 32 (warp % 4)
         const uint32_t ts = tmem + lanes + h * 128, to = tmem + lanes + 256 + h * 128;
-        uint32_t sn = 0, on = 0;    // active tiles, pieces with any
+        uint32_t sn = 0;            // active tiles
         bool ok = true;
         for (; mine && ok && !w.done(s, sh.end); w.next(s)) {
             const PagedPiece p = paged_piece(s, w, sh.begin, sh.end);
@@ -488,98 +489,114 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
             }
             float unit = 0.0f;
             bool first = true;
-            for (int x = t.from; work && x < t.upto; ++x, ++sn) {
+            for (int x = t.from; work && ok && x < t.upto; ++x, ++sn) {
                 const uint32_t ti = it + static_cast<uint32_t>(x - p.tile0 - p.first);
                 const int info = ti % kInfo;
-                if (ok)
-                    // (in this order: a half that passes over tiles would not
-                    // know which of two phases an earlier info slot is in)
-                    ok = mbar_wait(bar(sm.s_full[h]), sn & 1, abort, a.err, ROLE_EPILOGUE, 2,
-                                   kWaitLimitNs, KID_ATTN) &&
-                         mbar_wait(bar(sm.info_full[info]), (ti / kInfo) & 1, abort, a.err,
-                                   ROLE_EPILOGUE, 3, kWaitLimitNs, KID_ATTN);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
-                tc_fence_after();
-                const int c0 = x * kTilePositions;
-                RowMask mk;
-                {
-                    const TileMask tm = sm.mask[info];
+#pragma unroll 1
+                for (int e = 0; e < 2; ++e) {
+                    if (ok)
+                        // (in this order: a half that passes over tiles would not
+                        // know which of two phases an earlier info slot is in)
+                        ok = mbar_wait(bar(sm.s_full[h][e]), sn & 1, abort, a.err, ROLE_EPILOGUE, 2,
+                                       kWaitLimitNs, KID_ATTN) &&
+                             mbar_wait(bar(sm.info_full[info]), (ti / kInfo) & 1, abort, a.err,
+                                       ROLE_EPILOGUE, 3, kWaitLimitNs, KID_ATTN);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t tse = ts + e * 64;
+                    const int c0 = x * kTilePositions + e * 64;
+                    RowMask mk;
+                    mk.w[0] = sm.mask[info].w[2 * e];
+                    mk.w[1] = sm.mask[info].w[2 * e + 1];
+                    const bool masked = c0 + 63 > t.first ||
+                                        (s.window > 0 && c0 <= t.last - s.window) ||
+                                        (mk.w[0] & mk.w[1]) != 0xFFFFFFFFu;
+                    mk.w[0] >>= 2 * quad;
+                    mk.w[1] >>= 2 * quad;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        mk.w[k] = tm.w[k];
                         mk.hi[k] = pos[k] - c0 - 2 * quad;
                         mk.lo[k] = s.window > 0 ? mk.hi[k] - s.window + 1 : -kTilePositions;
                     }
-                }
-                const bool masked = c0 + kTilePositions - 1 > t.first ||
-                                    (s.window > 0 && c0 <= t.last - s.window) ||
-                                    (mk.w[0] & mk.w[1] & mk.w[2] & mk.w[3]) != 0xFFFFFFFFu;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) mk.w[k] >>= 2 * quad;
-                const float4 *col = kInt8 ? &sm.col[info][quad] : nullptr;
-                bool move = m[0] == -INFINITY || m[1] == -INFINITY || m[2] == -INFINITY ||
-                            m[3] == -INFINITY;
-                float turn = 1.0f;          // change of O's unit
-                if constexpr (kInt8) {
-                    const float un = sm.unit[info];
-                    if (un != unit && !first) turn = unit / un;
-                    unit = un;
-                }
-                uint32_t pk[2][32];
-                float sum[4];
-                for (bool again = false;; again = true) {
-                    if (__any_sync(0xFFFFFFFFu, move)) {
-                        // new references: the tile's maxima
-                        float top[4], f[4];
-                        if (masked) row_max<kInt8, true>(ts, col, a.scale_log2, mk, top);
-                        else row_max<kInt8, false>(ts, col, a.scale_log2, mk, top);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            f[k] = turn;
-                            if (top[k] > m[k]) {
-                                const float alpha = ex2_approx(m[k] - top[k]);
-                                f[k] *= alpha;
-                                l[k] *= alpha;
-                                m[k] = top[k];
-                            }
-                        }
-                        // (the products before this tile's scores are done with O)
-                        if (!first) scale_rows(to, f);
-                        turn = 1.0f;
-                        again = true;
+                    const float4 *col = kInt8 ? &sm.col[info][e * 32 + quad] : nullptr;
+                    bool move = m[0] == -INFINITY || m[1] == -INFINITY || m[2] == -INFINITY ||
+                                m[3] == -INFINITY;
+                    float turn = 1.0f;          // change of O's unit
+                    if constexpr (kInt8) {
+                        const float un = sm.unit[info];
+                        if (un != unit && !first) turn = unit / un;
+                        unit = un;
                     }
-                    float nm[4];
+                    // Before O is rescaled, the output product of the half tile before
+                    // has to be done (those before that are: their scores' buffer is
+                    // this one's).
+                    auto settle = [&]() {
+                        ok = ok && mbar_wait(bar(sm.pv_done[h][e ^ 1]), (sn + e + 1) & 1, abort, a.err,
+                                             ROLE_EPILOGUE, 5, kWaitLimitNs, KID_ATTN);
+                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        tc_fence_after();
+                    };
+                    uint32_t pk[2][16];
+                    float sum[4];
+                    for (bool again = false;; again = true) {
+                        if (__any_sync(0xFFFFFFFFu, move)) {
+                            // new references: the half tile's maxima
+                            float top[4], f[4];
+                            if (masked) row_max<kInt8, true>(tse, col, a.scale_log2, mk, top);
+                            else row_max<kInt8, false>(tse, col, a.scale_log2, mk, top);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) nm[k] = m[k] == -INFINITY ? 0.0f : -m[k];
-                    if (masked) weigh<kInt8, true>(ts, col, a.scale_log2, nm, mk, pk, sum);
-                    else weigh<kInt8, false>(ts, col, a.scale_log2, nm, mk, pk, sum);
-                    if (again) break;
-                    move = !(fmaxf(fmaxf(sum[0], sum[1]), fmaxf(sum[2], sum[3])) <= kMaxWeight);
-                    if (!__any_sync(0xFFFFFFFFu, move)) break;
-                }
-                if (turn != 1.0f) {
-                    const float f[4] = {turn, turn, turn, turn};
-                    scale_rows(to, f);
-                }
-                first = false;
+                            for (int k = 0; k < 4; ++k) {
+                                f[k] = turn;
+                                if (top[k] > m[k]) {
+                                    const float alpha = ex2_approx(m[k] - top[k]);
+                                    f[k] *= alpha;
+                                    l[k] *= alpha;
+                                    m[k] = top[k];
+                                }
+                            }
+                            if (!first) {
+                                settle();
+                                scale_rows(to, f);
+                            }
+                            turn = 1.0f;
+                            again = true;
+                        }
+                        float nm[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) l[k] += sum[k];
-                tmem_st_p(ts, pk[0]);
-                tmem_st_p(ts + kLane16, pk[1]);
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(bar(sm.p_full[h]));
+                        for (int k = 0; k < 4; ++k) nm[k] = m[k] == -INFINITY ? 0.0f : -m[k];
+                        if (masked) weigh<kInt8, true>(tse, col, a.scale_log2, nm, mk, pk, sum);
+                        else weigh<kInt8, false>(tse, col, a.scale_log2, nm, mk, pk, sum);
+                        if (again) break;
+                        move = !(fmaxf(fmaxf(sum[0], sum[1]), fmaxf(sum[2], sum[3])) <= kMaxWeight);
+                        if (!__any_sync(0xFFFFFFFFu, move)) break;
+                    }
+                    if (turn != 1.0f) {
+                        const float f[4] = {turn, turn, turn, turn};
+                        settle();
+                        scale_rows(to, f);
+                    }
+                    first = false;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) l[k] += sum[k];
+                    tmem_st_p(tse, pk[0]);
+                    tmem_st_p(tse + kLane16, pk[1]);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(bar(sm.p_full[h][e]));
+                }
             }
             if (work) it += static_cast<uint32_t>(p.last - p.first);
             // ---- the item's (or the share's) result of this row
             const bool any = work && t.upto > t.from;
             if (any) {
-                if (ok)
-                    ok = mbar_wait(bar(sm.o_done[h]), on & 1, abort, a.err, ROLE_EPILOGUE, 4,
-                                   kWaitLimitNs, KID_ATTN);
+                // the last two output products (sn counts this piece's tiles already)
+                ok = ok &&
+                     mbar_wait(bar(sm.pv_done[h][0]), (sn - 1) & 1, abort, a.err, ROLE_EPILOGUE, 4,
+                               kWaitLimitNs, KID_ATTN) &&
+                     mbar_wait(bar(sm.pv_done[h][1]), (sn - 1) & 1, abort, a.err, ROLE_EPILOGUE, 6,
+                               kWaitLimitNs, KID_ATTN);
                 ok = __all_sync(0xFFFFFFFFu, ok);
-                ++on;
             }
             if (!ok) break;
             tc_fence_after();
@@ -658,6 +675,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
             // stay in uniform registers. A warp per half, so that neither's
             // waits hold up the other's products.
             constexpr uint32_t idesc = kInt8 ? idesc_f16_f32(128, 128) : idesc_bf16_f32(128, 128);
+            constexpr uint32_t idesc64 = kInt8 ? idesc_f16_f32(128, 64) : idesc_bf16_f32(128, 64);
             auto u = [](auto v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
             const int h = warp == 8 ? 0 : 1;
             const uint32_t q0 = u(desc_kmajor(smem_u32(sm.q[h])));
@@ -667,38 +685,10 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
             uint32_t pn = 0, on = 0, nq = 0;
             uint32_t sk = 0, ph = 0;     // slot and phase of the next operand tile
             bool ok = true;
-            auto poll = [&](uint64_t &b, uint32_t phase, unsigned site) {
-                ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait_spin(bar(b), phase & 1, abort, a.err,
-                                                                  ROLE_MMA, site, KID_ATTN));
-                tc_fence_after();
-            };
             auto wait = [&](uint64_t &b, uint32_t phase, unsigned site) {
                 ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(bar(b), phase & 1, abort, a.err, ROLE_MMA,
                                                              site, kWaitLimitNs, KID_ATTN));
                 tc_fence_after();
-            };
-            // The two halves' products go out one group (output product, then the
-            // next scores) at a time: mixed, both groups would take as long as
-            // the two together, and both halves' softmax would run at once.
-            auto hold = [&]() {
-                if (leader && ok) {
-                    unsigned long long t0 = 0;
-                    for (uint32_t i = 1; atomicCAS_block(&sm.pipe, 0u, 1u) != 0u; ++i) {
-                        if ((i & 255u) != 0) continue;
-                        if (t0 == 0) t0 = globaltimer_ns();
-                        if (*abort || globaltimer_ns() - t0 > kWaitLimitNs) {
-                            *abort = 1;
-                            record_device_error(a.err, KID_ATTN, ROLE_MMA, 9);
-                            ok = false;
-                            break;
-                        }
-                    }
-                }
-                ok = __all_sync(0xFFFFFFFFu, ok);
-            };
-            auto let_go = [&]() {
-                if (leader) atomicExch_block(&sm.pipe, 0u);
-                __syncwarp();
             };
             auto advance = [&]() {
                 if (++sk == kOps) {
@@ -716,52 +706,63 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                     wait(sm.q_full[h], nq++, 1);
                     if (upto == from && leader) mma_commit(bar(sm.q_empty[h]));
                 }
-                auto scores = [&](int x) {
-                    const uint32_t k = k0 + sk * (kOperandBytes / 16);
+                // scores of half e of tile x: 64 rows of K
+                auto scores = [&](int x, int e, uint32_t slot) {
+                    const uint32_t k = k0 + slot * (kOperandBytes / 16) + e * (64 * 128 / 16);
                     if (leader) {
-                        mma_ss<false>(tsc, q0, k, idesc);
+                        mma_ss<false>(tsc + e * 64, q0, k, idesc64);
 #pragma unroll
                         for (int kk = 1; kk < 8; ++kk) {
                             const uint32_t off = (kk >> 2) * (kOperandBytes / 32) + (kk & 3) * 2;
-                            mma_ss<true>(tsc, q0 + off, k + off, idesc);
+                            mma_ss<true>(tsc + e * 64, q0 + off, k + off, idesc64);
                         }
-                        mma_commit(bar(sm.s_full[h]));
-                        if (x == upto - 1) mma_commit(bar(sm.q_empty[h]));
+                        mma_commit(bar(sm.s_full[h][e]));
+                        if (e == 1 && x == upto - 1) mma_commit(bar(sm.q_empty[h]));
                     }
                     __syncwarp();
                 };
-                // operand tiles come as K, V of each tile; the scores of tile
-                // x + 1 follow the output product of tile x
+                // Operand tiles come as K, V of each tile. The scores of half e of tile
+                // x + 1 follow the output product of half e of tile x, whose weights
+                // lay in the same columns: so one half tile's scores are there while
+                // the softmax is at the other.
                 wait(sm.op_full[sk], ph, 2);
                 if (!ok) break;
-                if (from <= cb && cb < upto) scores(cb);
+                if (from <= cb && cb < upto) {
+                    scores(cb, 0, sk);
+                    scores(cb, 1, sk);
+                }
                 if (leader) mma_commit(bar(sm.op_empty[sk]));
                 advance();
                 for (int x = cb; x < ce; ++x) {
+                    const uint32_t sv = sk;
                     wait(sm.op_full[sk], ph, 3);
-                    const uint32_t sn = sk + 1 == kOps ? 0 : sk + 1;
-                    if (x + 1 < ce) wait(sm.op_full[sn], sn == 0 ? ph ^ 1 : ph, 6);
-                    if (from <= x && x < upto) {
-                        wait(sm.p_full[h], pn++, 4);
-                        if (x == from && on > 0) wait(sm.o_free[h], on - 1, 5);
-                        hold();
-                        if (!ok) break;
-                        const uint32_t v = v0 + sk * (kOperandBytes / 16);
-                        if (leader) {
-                            mma_ts(to, tsc, v, idesc | kBNMajor, x > from ? 1u : 0u);
+                    advance();
+                    if (x + 1 < ce) wait(sm.op_full[sk], ph, 6);
+                    if (!ok) break;
+                    const bool now = from <= x && x < upto, next = x + 1 < ce && from <= x + 1 && x + 1 < upto;
 #pragma unroll
-                            for (int kk = 1; kk < 8; ++kk)
-                                mma_ts(to, tsc + kk * 8, v + kk * 128, idesc | kBNMajor, 1u);
-                            if (x == upto - 1) mma_commit(bar(sm.o_done[h]));
+                    for (int e = 0; e < 2; ++e) {
+                        if (now) {
+                            wait(sm.p_full[h][e], pn, 4);
+                            if (e == 0 && x == from && on > 0) wait(sm.o_free[h], on - 1, 5);
+                            if (!ok) break;
+                            const uint32_t v = v0 + sv * (kOperandBytes / 16) + e * 512;
+                            if (leader) {
+                                mma_ts(to, tsc + e * 64, v, idesc | kBNMajor, e > 0 || x > from ? 1u : 0u);
+#pragma unroll
+                                for (int kk = 1; kk < 4; ++kk)
+                                    mma_ts(to, tsc + e * 64 + kk * 8, v + kk * 128, idesc | kBNMajor, 1u);
+                                mma_commit(bar(sm.pv_done[h][e]));
+                            }
+                            __syncwarp();
                         }
-                        __syncwarp();
-                        if (x == upto - 1) ++on;
+                        if (next) scores(x + 1, e, sk);
                     }
                     if (!ok) break;
-                    const uint32_t sv = sk;
-                    advance();
-                    if (from <= x + 1 && x + 1 < upto && x + 1 < ce) scores(x + 1);
-                    if (from <= x && x < upto) let_go();
+                    if (now) {
+                        ++pn;
+                        if (x == upto - 1) ++on;
+                    }
                     if (leader) {
                         mma_commit(bar(sm.op_empty[sv]));
                         if (x + 1 < ce) mma_commit(bar(sm.op_empty[sk]));
