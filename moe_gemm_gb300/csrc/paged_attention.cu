@@ -707,8 +707,8 @@ PagedSetup paged_setup(const PagedAttnProblem &p, int rows) {
     u.s.capacity = p.W * p.page;
     // a window that reaches past the first position of any row masks nothing
     u.s.window = p.window >= u.s.capacity ? 0 : static_cast<int>(p.window);
-    // (the tiles kernel's start and end of an item take about as long as 3.75 tiles)
-    u.s.overhead = rows == kPagedTileRows ? 15 * kTilePositions / 4 : kTilePositions;
+    // (the tiles kernel's start and end of an item take about as long as 2.75 tiles)
+    u.s.overhead = rows == kPagedTileRows ? 11 * kTilePositions / 4 : kTilePositions;
     u.s.min_share = 2 * kTilePositions;
     u.c.table = p.block_table;
     u.c.ks = p.ks;

@@ -36,7 +36,7 @@
 // took longer than the products).
 //
 // Warps: 0-3 and 4-7 softmax of the halves, 8 and 10 issue the halves'
-// products, 9 loads, 12-15 convert (INT8).
+// products, 9 loads, 11 walks the CTA's share, 12-15 convert (INT8).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -74,6 +74,19 @@ struct TilesArgs {
     unsigned long long *err;
 };
 
+// A piece of an item, as the warps take it from shared memory. Warp 11 walks the
+// line ahead of the others (two 64-bit divisions and a walk step per piece: in each
+// of the 15 warps, between two items, they took 2000 to 4000 cycles).
+struct TilePiece {
+    int b, h, t0, base, kv;             // the request: block table row, kv head, first row, ...
+    int tok0, ntok, tile0, first, last; // paged_schedule.cuh: PagedPiece
+    int whole, slot;
+    int lo;                             // positions below it are masked for every token
+    int end;                            // no piece: the share ends
+};
+constexpr int kPieces = 4;              // pieces that warp 11 is ahead at most
+constexpr int kTakers = 15;             // warps that take them
+
 template <bool kInt8>
 struct TilesSmem {
     // BF16 operands are copied straight into 5 slots; INT8 codes land in 3 raw
@@ -96,6 +109,8 @@ struct TilesSmem {
     uint64_t s_full[2][2], p_full[2][2];   // of a half, of each half of a tile
     uint64_t pv_done[2][2], o_free[2];
     uint64_t q_max, fix, drain[2];
+    uint64_t piece_full[kPieces], piece_empty[kPieces];
+    TilePiece piece[kPieces];
     uint32_t tmem;
     volatile int abort_flag;
 };
@@ -376,13 +391,13 @@ struct HalfTiles {
     int from, upto;
 };
 
-__device__ __forceinline__ HalfTiles half_tiles(const PagedSchedule &s, const PagedWalk &w,
-                                                const PagedPiece &p, int half, int half_tokens) {
+__device__ __forceinline__ HalfTiles half_tiles(const PagedSchedule &s, const TilePiece &p, int half,
+                                                int half_tokens) {
     HalfTiles t;
     const int a = half * half_tokens, z = min(a + half_tokens, p.ntok);
     t.exists = a < p.ntok;
-    t.first = w.r.base + p.tok0 + a;
-    t.last = w.r.base + p.tok0 + z - 1;
+    t.first = p.base + p.tok0 + a;
+    t.last = p.base + p.tok0 + z - 1;
     const int lo = s.window > 0 ? max(max(t.first, 0) - s.window + 1, 0) / kTilePositions : 0;
     const int hi = t.last >= 0 ? t.last / kTilePositions + 1 : 0;
     t.from = max(p.tile0 + p.first, lo);
@@ -425,6 +440,10 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
             }
             mbar_init(bar(sm.o_free[h]), kHalfRows);
         }
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(bar(sm.piece_full[i]), 1);
+            mbar_init(bar(sm.piece_empty[i]), kInt8 ? kTakers : kTakers - 4);
+        }
         mbar_init(bar(sm.q_max), 128);
         mbar_init(bar(sm.fix), 1);
         mbar_init(bar(sm.drain[0]), 1);
@@ -453,6 +472,20 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
     if (tid == kThreads - 1)
         paged_write_cut(s, sh, w, blockIdx.x, cuts_of(a.ws, kPagedTileRows, gridDim.x));
     const bool mine = static_cast<int>(blockIdx.x) < sh.ctas;
+    // The next piece (the whole warp calls it); false: there is none, or a wait gave up.
+    uint32_t taken = 0;
+    auto take = [&](TilePiece &p, bool &ok, unsigned role) -> bool {
+        const int i = taken % kPieces;
+        ok = ok && mbar_wait(bar(sm.piece_full[i]), (taken / kPieces) & 1, abort, a.err, role, 10,
+                             kWaitLimitNs, KID_ATTN);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) return false;
+        p = sm.piece[i];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(sm.piece_empty[i]));
+        ++taken;
+        return p.end == 0;
+    };
     uint32_t it = 0;        // tiles of the pieces before this one
     uint32_t qn[2] = {0, 0};   // pieces with the half before this one
 
@@ -468,11 +501,10 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
         const uint32_t ts = tmem + lanes + h * 128, to = tmem + lanes + 256 + h * 128;
         uint32_t sn = 0;            // active tiles
         bool ok = true;
-        for (; mine && ok && !w.done(s, sh.end); w.next(s)) {
-            const PagedPiece p = paged_piece(s, w, sh.begin, sh.end);
-            if (p.first == p.last && !p.whole) continue;
+        TilePiece p;
+        while (mine && take(p, ok, ROLE_EPILOGUE)) {
             const bool work = p.last > p.first;
-            const HalfTiles t = half_tiles(s, w, p, h, a.half_tokens);
+            const HalfTiles t = half_tiles(s, p, h, a.half_tokens);
             if (work && t.exists) {
                 ok = mbar_wait(bar(sm.q_full[h]), qn[h] & 1, abort, a.err, ROLE_EPILOGUE, 1,
                                kWaitLimitNs, KID_ATTN);
@@ -615,8 +647,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                     if (tok >= a.half_tokens || h * a.half_tokens + tok >= p.ntok) continue;
                     if (p.whole) {
                         f[k] *= l[k] == 0.0f ? 0.0f : 1.0f / l[k];
-                        at[k] = ((static_cast<int64_t>(w.r.t0) + p.tok0 + h * a.half_tokens + tok) * a.o.Hq +
-                                 static_cast<int64_t>(w.h) * a.o.G + (row - tok * a.o.G)) * kHeadDim;
+                        at[k] = ((static_cast<int64_t>(p.t0) + p.tok0 + h * a.half_tokens + tok) * a.o.Hq +
+                                 static_cast<int64_t>(p.h) * a.o.G + (row - tok * a.o.G)) * kHeadDim;
                     } else {
                         at[k] = static_cast<int64_t>(irow) * kHeadDim;
                         if (quad == 0) {
@@ -696,11 +728,11 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                     ph ^= 1;
                 }
             };
-            for (; ok && u(!w.done(s, sh.end)); w.next(s)) {
-                const PagedPiece p = paged_piece(s, w, sh.begin, sh.end);
+            TilePiece p;
+            while (u(take(p, ok, ROLE_MMA))) {
                 const int cb = u(p.tile0 + p.first), ce = u(p.tile0 + p.last);
                 if (ce <= cb) continue;
-                const HalfTiles t = half_tiles(s, w, p, h, a.half_tokens);
+                const HalfTiles t = half_tiles(s, p, h, a.half_tokens);
                 const int from = u(t.from), upto = u(t.upto);
                 if (u(t.exists)) {
                     wait(sm.q_full[h], nq++, 1);
@@ -779,12 +811,11 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
             // ---------------------------------------------------------- the loads
             bool ok = true;
             uint32_t u = 0, fixes = 0;   // operand tiles, V tiles made zero in places
-            for (; ok && !w.done(s, sh.end); w.next(s)) {
-                const PagedPiece p = paged_piece(s, w, sh.begin, sh.end);
+            TilePiece p;
+            while (take(p, ok, ROLE_PRODUCER)) {
                 if (p.last <= p.first) continue;
-                int lo, hi;
-                request_span(s, w.r, lo, hi);
-                TileBoxes next = find_boxes(a.c, w.b, w.h, p.tile0 + p.first, lo, hi, a.err);
+                const int lo = p.lo, hi = p.kv;
+                TileBoxes next = find_boxes(a.c, p.b, p.h, p.tile0 + p.first, lo, hi, a.err);
                 for (int x = p.first; x < p.last && ok; ++x, ++it) {
                     const TileBoxes tb = next;
                     const int info = it % kInfo;
@@ -823,7 +854,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                         }
                         // (the table's entries for the next tile come while V waits)
                         if (kv == 0 && x + 1 < p.last)
-                            next = find_boxes(a.c, w.b, w.h, p.tile0 + x + 1, lo, hi, a.err);
+                            next = find_boxes(a.c, p.b, p.h, p.tile0 + x + 1, lo, hi, a.err);
                         if (mend) {
                             ok = mbar_wait(b, fixes & 1, abort, a.err, ROLE_PRODUCER, 2, kWaitLimitNs,
                                            KID_ATTN);
@@ -854,8 +885,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
 #pragma unroll
                                     for (int d = 0; d < 2; ++d)
                                         tma_load_3d(smem_u32(sm.q[h]) + d * (kOperandBytes / 2), &qm,
-                                                    d * 64, w.h * a.o.G,
-                                                    w.r.t0 + p.tok0 + h * a.half_tokens, qb);
+                                                    d * 64, p.h * a.o.G,
+                                                    p.t0 + p.tok0 + h * a.half_tokens, qb);
                                 }
                                 __syncwarp();
                             }
@@ -874,6 +905,51 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                         mbar_wait(bar(kInt8 ? sm.q_land[h] : sm.q_full[h]), (qn[h] - 1) & 1, &never,
                                   a.err, ROLE_PRODUCER, 5, kWaitLimitNs, KID_ATTN);
             }
+        } else if (warp == 11 && mine) {
+            // --------------------------------------------------------- the pieces
+            bool ok = true;
+            for (uint32_t n = 0; ok; ++n) {
+                PagedPiece p;
+                bool end = w.done(s, sh.end);
+                while (!end) {
+                    p = paged_piece(s, w, sh.begin, sh.end);
+                    if (p.last > p.first || p.whole) break;
+                    w.next(s);
+                    end = w.done(s, sh.end);
+                }
+                const int i = n % kPieces;
+                if (n >= kPieces)
+                    ok = mbar_wait(bar(sm.piece_empty[i]), (n / kPieces - 1) & 1, abort, a.err,
+                                   ROLE_PRODUCER, 11, kWaitLimitNs, KID_ATTN);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                if (lane == 0) {
+                    TilePiece t;
+                    t.end = end ? 1 : 0;
+                    if (!end) {
+                        int lo, hi;
+                        request_span(s, w.r, lo, hi);
+                        t.b = w.b;
+                        t.h = w.h;
+                        t.t0 = w.r.t0;
+                        t.base = w.r.base;
+                        t.kv = hi;
+                        t.lo = lo;
+                        t.tok0 = p.tok0;
+                        t.ntok = p.ntok;
+                        t.tile0 = p.tile0;
+                        t.first = p.first;
+                        t.last = p.last;
+                        t.whole = p.whole ? 1 : 0;
+                        t.slot = p.slot;
+                    }
+                    sm.piece[i] = t;
+                    mbar_arrive(bar(sm.piece_full[i]));
+                }
+                __syncwarp();
+                if (end) break;
+                w.next(s);
+            }
         }
     } else {
         setmaxnreg_dec<kOtherRegs>();
@@ -883,8 +959,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
             const int cw = ct >> 5;
             bool ok = true;
             uint32_t u = 0, items = 0;
-            for (; mine && ok && !w.done(s, sh.end); w.next(s)) {
-                const PagedPiece p = paged_piece(s, w, sh.begin, sh.end);
+            TilePiece p;
+            while (mine && take(p, ok, ROLE_CONVERT)) {
                 if (p.last <= p.first) continue;
                 int e = -100;                       // O's unit is 2^e
                 float unscale = 0.0f;               // of q's scaling, and to log2 units
