@@ -60,9 +60,14 @@ constexpr int kHalfRows = 128;
 constexpr int kInfo = 4;             // tiles whose mask and scales are kept
 constexpr float kMaxWeight = 256.0f; // sums of a tile's weights that move the reference
 constexpr int kOperandBytes = 128 * 128 * 2;
-// Registers of a softmax thread and of the others: 2 x 128 x 168 + 2 x 128 x
-// 88 = the 512 x 128 that the block is launched with.
-constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;
+// Registers of a softmax thread and of the others: together 256 for a pair, 2 x 128
+// pairs = the 512 x 128 that the block is launched with. Measured: INT8, whose
+// converters want more, 2.05 ms with 160 / 96 (2.10 with 168 / 88, 2.16 with 152 /
+// 104); BF16 1.11 ms with 168 / 88 (1.13 with 160 / 96).
+template <bool kInt8>
+struct Regs {
+    static constexpr uint32_t kSoftmax = kInt8 ? 160 : 168, kOther = 256 - kSoftmax;
+};
 
 struct TilesArgs {
     PagedSchedule s;
@@ -87,6 +92,13 @@ struct TilePiece {
 constexpr int kPieces = 4;              // pieces that warp 11 is ahead at most
 constexpr int kTakers = 15;             // warps that take them
 
+// A tile's scores come in two halves of 64 columns, so that one is ready while the
+// softmax is at the other (packed prompts of 16 thousand tokens, BF16: 1.44 -> 1.17
+// ms). INT8 gains nothing by it (a chunk over 30001 positions takes 2.1 ms either
+// way): there the bandwidth of shared memory is the bound, some 250 KB of operands, 100
+// of conversion and 130 of scales a tile, at 128 bytes a cycle.
+constexpr int kN = 2, kCols = kTilePositions / kN;
+
 template <bool kInt8>
 struct TilesSmem {
     // BF16 operands are copied straight into 5 slots; INT8 codes land in 3 raw
@@ -106,8 +118,8 @@ struct TilesSmem {
     uint64_t op_full[kOps], op_empty[kOps], raw_full[kRaws], raw_empty[kRaws];
     uint64_t info_full[kInfo];
     uint64_t q_land[2], q_full[2], q_empty[2];
-    uint64_t s_full[2][2], p_full[2][2];   // of a half, of each half of a tile
-    uint64_t pv_done[2][2], o_free[2];
+    uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];   // of a half of the rows, a part of a tile
+    uint64_t o_free[2];
     uint64_t q_max, fix, drain[2];
     uint64_t piece_full[kPieces], piece_empty[kPieces];
     TilePiece piece[kPieces];
@@ -200,8 +212,8 @@ __device__ __forceinline__ void tmem_st_tile(uint32_t t, const uint32_t (&a)[16]
         "r"(t + kLane16)
         : "memory");
 }
-// 32 columns of 16 lanes from 16-bit pairs: register 2 i + j is column 4 i + l % 4
-// of lane l / 4 + 8 j.
+// 16-bit pairs into 16 lanes: register 2 i + j is column 4 i + l % 4 of lane l / 4 +
+// 8 j.
 __device__ __forceinline__ void tmem_st_p(uint32_t t, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.16x128b.x8.b32 [%16], "
@@ -209,7 +221,6 @@ __device__ __forceinline__ void tmem_st_p(uint32_t t, const uint32_t (&r)[16]) {
         "r"(t)
         : "memory");
 }
-
 // One lane of a converged warp, the same one every time.
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
@@ -224,7 +235,7 @@ __device__ __forceinline__ unsigned long long f2_fma(unsigned long long a, unsig
     return r;
 }
 
-// What hides keys of a half tile (64 columns) from a thread's rows: of row k, the
+// What hides keys of a part of a tile from a thread's rows: of row k, the
 // columns 8 i + 2 (l % 4) + e with 8 i + e in [lo[k], hi[k]] are seen, and those whose
 // bit in the mask (shifted by 2 (l % 4)) is set.
 struct RowMask {
@@ -246,20 +257,20 @@ __device__ __forceinline__ RowMask here(RowMask m) {
     return m;
 }
 
-// A half tile's weights of a thread's 4 rows (row k: lanes l / 4 + 8 (k & 1) of
+// A part's weights of a thread's 4 rows (row k: lanes l / 4 + 8 (k & 1) of
 // block k >> 1) against the references -nm, as P's register image, and their
 // sums by row.
 template <bool kInt8, bool kMasked>
 __device__ __forceinline__ void weigh(uint32_t ts, const float4 *col, float c,
                                       const float (&nm)[4], const RowMask &mask,
-                                      uint32_t (&pk)[2][16], float (&sum)[4]) {
+                                      uint32_t (&pk)[2][32 / kN], float (&sum)[4]) {
     RowMask mk;
     if constexpr (kMasked) mk = here(mask);
     unsigned long long l2[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) l2[k] = f2_bits(0.0f, 0.0f);
 #pragma unroll
-    for (int cc = 0; cc < 2; ++cc) {
+    for (int cc = 0; cc < 4 / kN; ++cc) {
         uint32_t r[2][16];
         tmem_ld_tile(ts + cc * 32, r[0], r[1]);
         tmem_wait_tile(r[0], r[1]);
@@ -312,7 +323,7 @@ __device__ __forceinline__ void row_max(uint32_t ts, const float4 *col, float c,
 #pragma unroll
     for (int k = 0; k < 4; ++k) top[k] = -INFINITY;
 #pragma unroll 1
-    for (int cc = 0; cc < 2; ++cc) {
+    for (int cc = 0; cc < 4 / kN; ++cc) {
         uint32_t w = 0;
         if constexpr (kMasked) w = cc == 0 ? mk.w[0] : mk.w[1];
         uint32_t r[2][16];
@@ -491,7 +502,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
 
     if (warp < 8) {
         // ------------------------------------------------------------ softmax
-        setmaxnreg_inc<kSoftmaxRegs>();
+        setmaxnreg_inc<Regs<kInt8>::kSoftmax>();
         const int h = warp >> 2;
         const int quad = lane & 3, r4 = (warp & 3) * 32 + (lane >> 2);
         int tok4[4];        // the tokens, within the half, of the thread's rows r4 + 8 k
@@ -525,7 +536,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                 const uint32_t ti = it + static_cast<uint32_t>(x - p.tile0 - p.first);
                 const int info = ti % kInfo;
 #pragma unroll 1
-                for (int e = 0; e < 2; ++e) {
+                for (int e = 0; e < kN; ++e) {
                     if (ok)
                         // (in this order: a half that passes over tiles would not
                         // know which of two phases an earlier info slot is in)
@@ -536,12 +547,12 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t tse = ts + e * 64;
-                    const int c0 = x * kTilePositions + e * 64;
+                    const uint32_t tse = ts + e * kCols;
+                    const int c0 = x * kTilePositions + e * kCols;
                     RowMask mk;
                     mk.w[0] = sm.mask[info].w[2 * e];
                     mk.w[1] = sm.mask[info].w[2 * e + 1];
-                    const bool masked = c0 + 63 > t.first ||
+                    const bool masked = c0 + kCols - 1 > t.first ||
                                         (s.window > 0 && c0 <= t.last - s.window) ||
                                         (mk.w[0] & mk.w[1]) != 0xFFFFFFFFu;
                     mk.w[0] >>= 2 * quad;
@@ -551,7 +562,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                         mk.hi[k] = pos[k] - c0 - 2 * quad;
                         mk.lo[k] = s.window > 0 ? mk.hi[k] - s.window + 1 : -kTilePositions;
                     }
-                    const float4 *col = kInt8 ? &sm.col[info][e * 32 + quad] : nullptr;
+                    const float4 *col = kInt8 ? &sm.col[info][e * (kCols / 2) + quad] : nullptr;
                     bool move = m[0] == -INFINITY || m[1] == -INFINITY || m[2] == -INFINITY ||
                                 m[3] == -INFINITY;
                     float turn = 1.0f;          // change of O's unit
@@ -560,20 +571,19 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                         if (un != unit && !first) turn = unit / un;
                         unit = un;
                     }
-                    // Before O is rescaled, the output product of the half tile before
-                    // has to be done (those before that are: their scores' buffer is
-                    // this one's).
+                    // Before O is rescaled, the output product of the part before has to
+                    // be done (those before that are: this part's scores came after).
                     auto settle = [&]() {
                         ok = ok && mbar_wait(bar(sm.pv_done[h][e ^ 1]), (sn + e + 1) & 1, abort, a.err,
                                              ROLE_EPILOGUE, 5, kWaitLimitNs, KID_ATTN);
                         ok = __all_sync(0xFFFFFFFFu, ok);
                         tc_fence_after();
                     };
-                    uint32_t pk[2][16];
+                    uint32_t pk[2][32 / kN];
                     float sum[4];
                     for (bool again = false;; again = true) {
                         if (__any_sync(0xFFFFFFFFu, move)) {
-                            // new references: the half tile's maxima
+                            // new references: the part's maxima
                             float top[4], f[4];
                             if (masked) row_max<kInt8, true>(tse, col, a.scale_log2, mk, top);
                             else row_max<kInt8, false>(tse, col, a.scale_log2, mk, top);
@@ -622,7 +632,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
             // ---- the item's (or the share's) result of this row
             const bool any = work && t.upto > t.from;
             if (any) {
-                // the last two output products (sn counts this piece's tiles already)
+                // the last output products (sn counts this piece's tiles already)
                 ok = ok &&
                      mbar_wait(bar(sm.pv_done[h][0]), (sn - 1) & 1, abort, a.err, ROLE_EPILOGUE, 4,
                                kWaitLimitNs, KID_ATTN) &&
@@ -699,7 +709,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
             }
         }
     } else if (warp < 12) {
-        setmaxnreg_dec<kOtherRegs>();
+        setmaxnreg_dec<Regs<kInt8>::kOther>();
         if ((warp == 8 || warp == 10) && mine) {
             // ------------------------------------------ the products of one half
             // The whole warp walks, waits and counts, on values made uniform
@@ -707,7 +717,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
             // stay in uniform registers. A warp per half, so that neither's
             // waits hold up the other's products.
             constexpr uint32_t idesc = kInt8 ? idesc_f16_f32(128, 128) : idesc_bf16_f32(128, 128);
-            constexpr uint32_t idesc64 = kInt8 ? idesc_f16_f32(128, 64) : idesc_bf16_f32(128, 64);
+            constexpr uint32_t idesc_s = kInt8 ? idesc_f16_f32(128, kCols) : idesc_bf16_f32(128, kCols);
             auto u = [](auto v) { return __shfl_sync(0xFFFFFFFFu, v, 0); };
             const int h = warp == 8 ? 0 : 1;
             const uint32_t q0 = u(desc_kmajor(smem_u32(sm.q[h])));
@@ -738,30 +748,29 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                     wait(sm.q_full[h], nq++, 1);
                     if (upto == from && leader) mma_commit(bar(sm.q_empty[h]));
                 }
-                // scores of half e of tile x: 64 rows of K
+                // scores of part e of tile x: kCols rows of K
                 auto scores = [&](int x, int e, uint32_t slot) {
-                    const uint32_t k = k0 + slot * (kOperandBytes / 16) + e * (64 * 128 / 16);
+                    const uint32_t k = k0 + slot * (kOperandBytes / 16) + e * (kCols * 128 / 16);
                     if (leader) {
-                        mma_ss<false>(tsc + e * 64, q0, k, idesc64);
+                        mma_ss<false>(tsc + e * kCols, q0, k, idesc_s);
 #pragma unroll
                         for (int kk = 1; kk < 8; ++kk) {
                             const uint32_t off = (kk >> 2) * (kOperandBytes / 32) + (kk & 3) * 2;
-                            mma_ss<true>(tsc + e * 64, q0 + off, k + off, idesc64);
+                            mma_ss<true>(tsc + e * kCols, q0 + off, k + off, idesc_s);
                         }
                         mma_commit(bar(sm.s_full[h][e]));
-                        if (e == 1 && x == upto - 1) mma_commit(bar(sm.q_empty[h]));
+                        if (e == kN - 1 && x == upto - 1) mma_commit(bar(sm.q_empty[h]));
                     }
                     __syncwarp();
                 };
-                // Operand tiles come as K, V of each tile. The scores of half e of tile
-                // x + 1 follow the output product of half e of tile x, whose weights
-                // lay in the same columns: so one half tile's scores are there while
-                // the softmax is at the other.
+                // Operand tiles come as K, V of each tile. The scores of part e of tile x
+                // + 1 follow the output product of part e of tile x, whose weights lay
+                // in the same columns.
                 wait(sm.op_full[sk], ph, 2);
                 if (!ok) break;
                 if (from <= cb && cb < upto) {
-                    scores(cb, 0, sk);
-                    scores(cb, 1, sk);
+#pragma unroll
+                    for (int e = 0; e < kN; ++e) scores(cb, e, sk);
                 }
                 if (leader) mma_commit(bar(sm.op_empty[sk]));
                 advance();
@@ -773,17 +782,17 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                     if (!ok) break;
                     const bool now = from <= x && x < upto, next = x + 1 < ce && from <= x + 1 && x + 1 < upto;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
+                    for (int e = 0; e < kN; ++e) {
                         if (now) {
                             wait(sm.p_full[h][e], pn, 4);
                             if (e == 0 && x == from && on > 0) wait(sm.o_free[h], on - 1, 5);
                             if (!ok) break;
-                            const uint32_t v = v0 + sv * (kOperandBytes / 16) + e * 512;
+                            const uint32_t v = v0 + sv * (kOperandBytes / 16) + e * (kCols * 128 / 16);
                             if (leader) {
-                                mma_ts(to, tsc + e * 64, v, idesc | kBNMajor, e > 0 || x > from ? 1u : 0u);
+                                mma_ts(to, tsc + e * kCols, v, idesc | kBNMajor, e > 0 || x > from ? 1u : 0u);
 #pragma unroll
-                                for (int kk = 1; kk < 4; ++kk)
-                                    mma_ts(to, tsc + e * 64 + kk * 8, v + kk * 128, idesc | kBNMajor, 1u);
+                                for (int kk = 1; kk < kCols / 16; ++kk)
+                                    mma_ts(to, tsc + e * kCols + kk * 8, v + kk * 128, idesc | kBNMajor, 1u);
                                 mma_commit(bar(sm.pv_done[h][e]));
                             }
                             __syncwarp();
@@ -952,11 +961,24 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
             }
         }
     } else {
-        setmaxnreg_dec<kOtherRegs>();
+        setmaxnreg_dec<Regs<kInt8>::kOther>();
         if constexpr (kInt8) {
             // ---------------------------------------------------- INT8 to fp16
             const int ct = tid - 384;               // 0 .. 127
             const int cw = ct >> 5;
+            // Eight lanes take pieces 0-3 (4-7) of rows r and r ^ 5: reads and writes
+            // through the swizzle then fall in distinct banks. A lane's rows are two of
+            // every eight (1024 bytes), of the warp's 32.
+            uint32_t from[2], to0[2];
+            {
+                const int pc = (lane & 3) + ((lane >> 3) & 1) * 4;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int pi = i * 2 + (lane >> 4), r = (lane & 4) ? pi ^ 5 : pi;
+                    from[i] = (cw * 32 + r) * 128 + ((pc ^ r) << 4);
+                    to0[i] = (pc >> 2) * (kOperandBytes / 2) + (cw * 32 + r) * 128 + ((((pc & 3) * 2) ^ r) << 4);
+                }
+            }
             bool ok = true;
             uint32_t u = 0, items = 0;
             TilePiece p;
@@ -975,34 +997,25 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                                            ROLE_CONVERT, 2, kWaitLimitNs, KID_ATTN);
                         ok = __all_sync(0xFFFFFFFFu, ok);
                         if (!ok) break;
-                        // 16 codes to 32 bytes at a time. Eight lanes take pieces 0-3
-                        // (4-7) of rows r and r ^ 5: reads and writes through the
-                        // swizzle then fall in distinct banks.
+                        // 16 codes to 32 bytes at a time
                         const uint8_t *src = sm.raw[rs];
                         uint8_t *dst = sm.op[os];
-                        const int pc = (lane & 3) + ((lane >> 3) & 1) * 4;
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             uint4 y[4];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int pi = (i & 1) * 2 + (lane >> 4);
-                                const int r = cw * 32 + (2 * j + (i >> 1)) * 8 + ((lane & 4) ? pi ^ 5 : pi);
-                                y[i] = *reinterpret_cast<const uint4 *>(src + r * 128 + ((pc ^ (r & 7)) << 4));
-                            }
+                            for (int i = 0; i < 4; ++i)
+                                y[i] = *reinterpret_cast<const uint4 *>(src + from[i & 1] + (2 * j + (i >> 1)) * 1024);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                const int pi = (i & 1) * 2 + (lane >> 4);
-                                const int r = cw * 32 + (2 * j + (i >> 1)) * 8 + ((lane & 4) ? pi ^ 5 : pi);
                                 uint4 g, f;
                                 i8x4_to_f16x4(y[i].x, g.x, g.y);
                                 i8x4_to_f16x4(y[i].y, g.z, g.w);
                                 i8x4_to_f16x4(y[i].z, f.x, f.y);
                                 i8x4_to_f16x4(y[i].w, f.z, f.w);
-                                uint8_t *d = dst + (pc >> 2) * (kOperandBytes / 2) + r * 128;
-                                const int dp = (pc & 3) * 2;
-                                *reinterpret_cast<uint4 *>(d + ((dp ^ (r & 7)) << 4)) = g;
-                                *reinterpret_cast<uint4 *>(d + (((dp + 1) ^ (r & 7)) << 4)) = f;
+                                uint8_t *d = dst + (2 * j + (i >> 1)) * 1024;
+                                *reinterpret_cast<uint4 *>(d + to0[i & 1]) = g;
+                                *reinterpret_cast<uint4 *>(d + (to0[i & 1] ^ 16)) = f;
                             }
                         }
                         fence_proxy_async_smem();
