@@ -39,7 +39,10 @@ constexpr float kNegInf = -INFINITY;
 
 // The kernel of a call, by the query rows that a request and kv head have on
 // average: up to 16 fit one item of the rows kernel, which reads the cache
-// once; more take the tiles kernel.
+// once; more take the tiles kernel. 32 requests at 4096 positions, 8 kv heads, rows
+// kernel / tiles kernel: 16 rows INT8 85 / 150 us and BF16 128 / 100, 24 rows 152 /
+// 149 and 231 / 101. (BF16 pages pay for their place among the first 16: their
+// probabilities keep 24 bits there, and 8 in the tiles kernel.)
 bool uses_tiles(int64_t T, int64_t B, int64_t G) { return T * G > kRowsMax * B; }
 
 
@@ -55,7 +58,9 @@ struct RowsArgs {
     unsigned long long *err;
 };
 
-// Tiles that a warp keeps in flight. INT8: 2, so that three CTAs fit an SM.
+// Tiles that a warp keeps in flight, with two CTAs of INT8 pages per SM or one of BF16
+// pages (three CTAs per SM took 69 us for the 56 of the decode step below: their
+// registers spill).
 template <bool kInt8>
 constexpr int kRowStages = kInt8 ? 2 : 3;
 
@@ -125,7 +130,7 @@ __device__ __forceinline__ void value_frags(ChunkRegs<kInt8> &r, const uint4 *v,
 // K and of V and the scales, kRowStages tiles ahead, so that warps wait for one
 // another only when an item ends (a fifth warp that loaded for all held the
 // registers of one to two CTAs per SM: a decode step of 32 requests at 4096
-// positions took 62 us against this form's 50). Query row r of an item is query
+// positions took 62 us against this form's 56). Query row r of an item is query
 // head r % G of its new token r / G. Arithmetic as in the contiguous-cache
 // kernel (attention.cu): scores and outputs by mma.sync with FP32 sums, the
 // probabilities split into two fp16 (three bf16) parts, running maximum and sum
@@ -767,9 +772,10 @@ cudaError_t launch_paged_attention(const PagedAttnProblem &p, cudaStream_t strea
     if (!paged_encode_cache(&km, p.kc, int8, p, rows_box(p)) ||
         !paged_encode_cache(&vm, p.vc, int8, p, rows_box(p)))
         return cudaErrorInvalidValue;
-    // An item takes whole tokens: 8 rows when the group fits and the call has
-    // about one token per request, else 16.
-    const bool one = G <= 8 && p.T <= p.B;
+    // An item takes whole tokens: 8 rows when requests have that many on average, else
+    // 16 (two tokens of 4 query heads, 32 requests at 4096 positions: 64 us, and 82 in
+    // items of 16).
+    const bool one = G <= 8 && p.T * G <= 8 * p.B;
     if (int8)
         return one ? launch_rows<1, true>(p, km, vm, info.num_sms, err, stream)
                    : launch_rows<2, true>(p, km, vm, info.num_sms, err, stream);

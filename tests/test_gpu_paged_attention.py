@@ -332,6 +332,25 @@ def test_many_requests(int8):
 
 
 @pytest.mark.parametrize("int8", KINDS)
+@pytest.mark.parametrize("n_new,Hq", [([2, 2, 1, 3], 8), ([4, 0, 7, 1], 4), ([1, 0, 0, 3], 16),
+                                      ([2, 2, 2, 2], 10)])
+def test_few_tokens_per_request(n_new, Hq, int8):
+    b = Batch(n_new, [130, 5, 700, 0], Hq, 2, 16, int8, seed=12)
+    b.check(b.run(), split=True)
+
+
+@pytest.mark.parametrize("int8", KINDS)
+def test_every_sm_busy_gives_the_same_numbers(int8):
+    b = Batch([2048, 1500, 1, 700], [0, 2500, 4000, 65], 32, 8, 64, int8, seed=13)
+    w8.device_error()
+    out = b.run()
+    for _ in range(4):
+        assert torch.equal(b.run(), out)
+    assert w8.device_error() == 0
+    b.check(out)
+
+
+@pytest.mark.parametrize("int8", KINDS)
 def test_pool_past_32_bit_offsets(int8):
     # the pool's bytes (and, BF16, elements) pass 2^31; the request's pages lie at its end
     Hkv, page = 8, 64
