@@ -35,6 +35,14 @@
 // once for 4 rows (a row per thread reads them for one: the reads alone then
 // took longer than the products).
 //
+// What bounds it. BF16 pages: eight prompts of up to 8192 tokens (1.45e12 operations)
+// take 1.11 ms, 1.30 PFLOP/s; the softmax of a half (wait, load, exponentials, store)
+// is as long as the other half's products, and an item's start and end take some 5 us.
+// INT8 pages: 2048 tokens over 30001 positions and eight single tokens (2.08e12) take 2.06 ms, 1.01
+// PFLOP/s: shared memory, which per tile carries 250 KB of operands, 100 of
+// conversion and 130 of scales. With the scores in one part of 128 columns the softmax
+// waited for whole products: 1.44 ms for the prompts.
+//
 // Warps: 0-3 and 4-7 softmax of the halves, 8 and 10 issue the halves'
 // products, 9 loads, 11 walks the CTA's share, 12-15 convert (INT8).
 #include <cuda.h>
