@@ -678,9 +678,10 @@ w8a8_status w8a8_paged_kv_write(const void *k_bf16, int64_t k_token_stride, int6
  * positions that some new token sees is read; what those hold must be finite.
  * A table entry outside [0, P) there reads as absent: its positions are masked,
  * and w8a8_device_error() tells of it. A length past W * page is cut to it.
- * Sums and softmax statistics are FP32. Up to 16 query rows per item the
- * probabilities keep 22 (BF16 pages: 24) bits, as in the contiguous-cache
- * calls.
+ * Sums and softmax statistics are FP32. For the product with V, calls of up to
+ * 16 query rows per request and kv head on average (T * Hq / Hkv <= 16 * B) keep 22
+ * bits of the probabilities (BF16 pages: 24), as the contiguous-cache calls do;
+ * calls with more round them to fp16 (BF16 pages: to BF16).
  * Pointers to q, out, the caches and the scales 16-byte aligned, strides
  * multiples of 8; Hq a multiple of Hkv, Hq / Hkv <= 16; page a multiple of 8;
  * P * Hkv * page, W * page and T below 2^31; workspace 16-byte aligned.
