@@ -592,7 +592,7 @@ int w8a8_version(void);
  * Without a bias keys are compared by the logits (the order of the scores).
  * The weights are the picked scores, divided by their sum when renormalize is
  * set, times scale.
- * A logit of -inf or NaN marks an expert that is never picked; a token with
+ * A logit or a bias of -inf or NaN marks an expert that is never picked; a token with
  * fewer than k experts to pick has id -1 and weight 0 in its last places
  * (w8a8_moe_route does not route those). +inf counts as the largest finite
  * number. Choices are exact: two keys that 32-bit arithmetic cannot tell apart

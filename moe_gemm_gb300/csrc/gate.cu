@@ -527,7 +527,8 @@ moe_gate_kernel(const Tin *__restrict__ logits, const GateArgs a) {
         for (int i = 0; i < V; ++i) {
             const float s = a.sigmoid ? rcp_approx(1.0f + ex2_approx(-1.44269504f * x[i]))
                                       : expf(x[i] - m) * inv;
-            kr[i] = x[i] > -INFINITY ? s + bias[i] : -INFINITY;
+            const float key = s + bias[i];
+            kr[i] = x[i] > -INFINITY && key == key ? key : -INFINITY;   // (a NaN bias: never picked)
         }
         float all[V];
 #pragma unroll

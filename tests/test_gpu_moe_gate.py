@@ -163,6 +163,22 @@ def test_masked_experts(scoring, with_bias):
     check(x, 8, scoring=scoring, bias=bias, n_group=4, topk_group=2)
 
 
+@pytest.mark.parametrize("E,n_group,topk_group", [(64, 1, 1), (256, 8, 4), (60, 5, 2), (512, 4, 2)])
+def test_biases_that_mark_experts(E, n_group, topk_group):
+    x, b = logits(41, E, 31), bias_of(E, 32)
+    never = torch.arange(0, E, 3, device=DEV)
+    b[never] = torch.where(never % 2 == 0, math.nan, -math.inf)
+    kw = dict(n_group=n_group, topk_group=topk_group)
+    ids, w = w8.moe_gate(x, 8, scoring="sigmoid", bias=b, **kw)
+    masked = x.clone()
+    masked[:, never] = -math.inf
+    rid, rw = reference(masked, 8, scoring="sigmoid", bias=b.nan_to_num(0.0, neginf=0.0), **kw)
+    assert torch.equal(ids.cpu(), rid)
+    assert bool(((w.cpu().double() - rw).abs() <= TOL * rw).all())
+    ids, w = w8.moe_gate(x, 8, scoring="softmax", bias=b, **kw)
+    assert not bool(torch.isin(ids, never.int()).any()) and bool(torch.isfinite(w).all())
+
+
 def test_far_logits():
     x = logits(6, 64, 8) * 40
     x[1] -= 300
