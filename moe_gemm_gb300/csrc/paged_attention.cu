@@ -522,6 +522,7 @@ struct CombineArgs {
     float *ws;
     int rows;               // rows of a slot
     int ctas;               // the attention kernel's grid
+    int overhead;           // as in its schedule
 };
 
 // Block (c, y): when the border before CTA c is the first one inside an item
@@ -565,7 +566,7 @@ paged_combine_kernel(const CombineArgs a) {
             p.ntiles = cut.ntiles;
             p.first = p.last = 0;
             p.whole = false;
-            if (in) paged_part(p, cut.at, cut.cost, from, upto);
+            if (in) paged_part(p, cut.at, cut.cost, a.overhead, from, upto);
             if (__any_sync(0xFFFFFFFFu, p.whole)) return;   // one CTA has all its tiles: it wrote it
             const bool has = p.last > p.first;
             const float *part = a.ws + (static_cast<int64_t>(k) * 2 + p.slot) * a.rows * (kHeadDim + 2);
@@ -660,6 +661,7 @@ cudaError_t launch_combine(const PagedSetup &u, float *ws, int rows, int ctas, c
     a.ws = ws;
     a.rows = rows;
     a.ctas = ctas;
+    a.overhead = u.s.overhead;
     const unsigned y = rows <= 16 ? 2 : 8;
     return launch_pdl(paged_combine_kernel, dim3(ctas, y), kCombineThreads, 0, stream, a);
 }
@@ -720,8 +722,8 @@ PagedSetup paged_setup(const PagedAttnProblem &p, int rows) {
     u.s.capacity = p.W * p.page;
     // a window that reaches past the first position of any row masks nothing
     u.s.window = p.window >= u.s.capacity ? 0 : static_cast<int>(p.window);
-    // (the tiles kernel's start and end of an item take about as long as 2.75 tiles)
-    u.s.overhead = rows == kPagedTileRows ? 11 * kTilePositions / 4 : kTilePositions;
+    // (what an item takes beside its tiles: measured, in tiles of each kernel)
+    u.s.overhead = rows == kPagedTileRows ? 11 * kTilePositions / 4 : 3 * kTilePositions / 2;
     u.s.min_share = 2 * kTilePositions;
     u.c.table = p.block_table;
     u.c.ks = p.ks;

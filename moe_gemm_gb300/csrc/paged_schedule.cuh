@@ -194,12 +194,18 @@ struct PagedPiece {
     int slot;               // the CTA's workspace slot for it
 };
 
-// The part of an item of `ntiles` cache tiles that lies in [begin, end).
-__device__ __forceinline__ void paged_part(PagedPiece &p, long long at, long long cost,
+// The part of an item of `ntiles` cache tiles that lies in [begin, end). The item's
+// constant cost lies at its front and a border goes to the nearest tile: every CTA has
+// one piece more than item fronts, so CTAs differ by a tile at most.
+__device__ __forceinline__ void paged_part(PagedPiece &p, long long at, long long cost, int overhead,
                                            long long begin, long long end) {
     const long long x0 = max(begin - at, 0ll), x1 = min(end - at, cost);
-    p.first = x0 == 0 ? 0 : static_cast<int>(x0 * p.ntiles / cost);
-    p.last = x1 == cost ? p.ntiles : static_cast<int>(x1 * p.ntiles / cost);
+    const long long tiles = cost - overhead;
+    auto before = [&](long long x) {
+        return x <= overhead ? 0 : static_cast<int>(((x - overhead) * p.ntiles + tiles / 2) / tiles);
+    };
+    p.first = before(x0);
+    p.last = x1 == cost ? p.ntiles : before(x1);
     p.whole = p.first == 0 && p.last == p.ntiles && (p.ntiles > 0 || x0 == 0);
     p.slot = x0 > 0 ? 0 : 1;
 }
@@ -213,7 +219,7 @@ __device__ __forceinline__ PagedPiece paged_piece(const PagedSchedule &s, const 
     const int lo = s.window > 0 ? max(max(w.r.base + p.tok0, 0) - s.window + 1, 0) : 0;
     p.tile0 = lo / kTilePositions;
     p.ntiles = hi > lo ? (hi + kTilePositions - 1) / kTilePositions - p.tile0 : 0;
-    paged_part(p, w.at, w.cost, begin, end);
+    paged_part(p, w.at, w.cost, s.overhead, begin, end);
     return p;
 }
 
