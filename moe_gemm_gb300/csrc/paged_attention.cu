@@ -19,6 +19,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "attention_math.cuh"
@@ -652,17 +653,21 @@ int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 // A warp of the rows kernel copies its 32 positions in boxes of this many.
 int rows_box(const PagedAttnProblem &p) { return gcd(static_cast<int>(p.page), 32); }
 
-cudaError_t launch_combine(const PagedSetup &u, float *ws, int rows, int ctas, cudaStream_t stream) {
+// slot: rows of a slot of the workspace, item: rows of an item.
+cudaError_t launch_combine(const PagedSetup &u, float *ws, int slot, int item, int ctas,
+                           cudaStream_t stream) {
     CombineArgs a;
     a.cu = u.s.cu;
     a.B = u.s.B;
     a.T = u.s.T;
     a.o = u.o;
     a.ws = ws;
-    a.rows = rows;
+    a.rows = slot;
     a.ctas = ctas;
     a.overhead = u.s.overhead;
-    const unsigned y = rows <= 16 ? 2 : 8;
+    // a row per warp, or 4 of the tiles kernel's 256 (with 8 rows per warp a long chunk took
+    // 2.05 ms for 2.01, with 1 the blocks cost more than they save: 2.02)
+    const int y = std::min(item / (kCombineThreads / 32), 16);
     return launch_pdl(paged_combine_kernel, dim3(ctas, y), kCombineThreads, 0, stream, a);
 }
 
@@ -701,7 +706,7 @@ cudaError_t launch_rows(const PagedAttnProblem &p, const CUtensorMap &km, const 
     a.err = err;
     e = launch_pdl(kernel, dim3(ctas), kRowThreads, smem, stream, km, vm, a);
     if (e != cudaSuccess) return e;
-    return launch_combine(u, a.ws, kRowsMax, ctas, stream);
+    return launch_combine(u, a.ws, kRowsMax, 8 * NT, ctas, stream);
 }
 
 }  // namespace
@@ -775,7 +780,8 @@ cudaError_t launch_paged_attention(const PagedAttnProblem &p, cudaStream_t strea
         const int ctas = info.num_sms < kPagedTileCtas ? info.num_sms : kPagedTileCtas;
         e = launch_paged_tiles(p, u, ctas, err, stream);
         if (e != cudaSuccess) return e;
-        return launch_combine(u, static_cast<float *>(p.workspace), kPagedTileRows, ctas, stream);
+        return launch_combine(u, static_cast<float *>(p.workspace), kPagedTileRows, kPagedTileRows,
+                              ctas, stream);
     }
     const bool int8 = p.ks != nullptr;
     CUtensorMap km, vm;
