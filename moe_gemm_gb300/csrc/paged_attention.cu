@@ -41,8 +41,8 @@ constexpr float kNegInf = -INFINITY;
 // The kernel of a call, by the query rows that a request and kv head have on
 // average: up to 16 fit one item of the rows kernel, which reads the cache
 // once; more take the tiles kernel. 32 requests at 4096 positions, 8 kv heads, rows
-// kernel / tiles kernel: 16 rows INT8 85 / 150 us and BF16 128 / 100, 24 rows 152 /
-// 149 and 231 / 101. (BF16 pages pay for their place among the first 16: their
+// kernel / tiles kernel: 16 rows INT8 82 / 143 us and BF16 127 / 100, 24 rows 152 /
+// 143 and 231 / 101. (BF16 pages pay for their place among the first 16: their
 // probabilities keep 24 bits there, and 8 in the tiles kernel.)
 bool uses_tiles(int64_t T, int64_t B, int64_t G) { return T * G > kRowsMax * B; }
 
@@ -60,7 +60,7 @@ struct RowsArgs {
 };
 
 // Tiles that a warp keeps in flight, with two CTAs of INT8 pages per SM or one of BF16
-// pages (three CTAs per SM took 69 us for the 56 of the decode step below: their
+// pages (three CTAs per SM took 69 us when the decode step below took 56: their
 // registers spill).
 template <bool kInt8>
 constexpr int kRowStages = kInt8 ? 2 : 3;
@@ -131,17 +131,18 @@ __device__ __forceinline__ void value_frags(ChunkRegs<kInt8> &r, const uint4 *v,
 // K and of V and the scales, kRowStages tiles ahead, so that warps wait for one
 // another only when an item ends (a fifth warp that loaded for all held the
 // registers of one to two CTAs per SM: a decode step of 32 requests at 4096
-// positions took 62 us against this form's 56). Query row r of an item is query
+// positions took 62 us when this form took 56). Query row r of an item is query
 // head r % G of its new token r / G. Arithmetic as in the contiguous-cache
 // kernel (attention.cu): scores and outputs by mma.sync with FP32 sums, the
 // probabilities split into two fp16 (three bf16) parts, running maximum and sum
 // per warp.
 //
 // BF16 pages are an HBM stream when there is enough of one: 4 requests at 33 to 131
-// thousand positions (1.34 GB) take 203 us, 6.6 TB/s. INT8 pages halve the bytes and
-// not the instructions: 32 requests at 2 to 4 thousand positions (214 MB) take 56 us,
-// 3.8 TB/s, of which about 13 are the same for any length (the share, the table, the
-// first tiles, the join, the second kernel) and the rest runs at 5.4 TB/s.
+// thousand positions (1.34 GB) take 202 us, 6.7 TB/s. INT8 pages halve the bytes and
+// not the instructions: 32 requests at 2 to 4 thousand positions (214 MB) take 55 us,
+// 3.9 TB/s, of which about 13 are the same for any length (2 until the share is known,
+// 4 until the first tiles are there, 1.4 for the join, 5 for the second kernel) and the
+// rest runs at 5.4 TB/s.
 template <int NT, bool kInt8>
 __global__ void __launch_bounds__(kRowThreads, kInt8 ? 2 : 1)
 paged_rows_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm,

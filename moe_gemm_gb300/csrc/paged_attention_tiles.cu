@@ -36,12 +36,14 @@
 // took longer than the products).
 //
 // What bounds it. BF16 pages: eight prompts of up to 8192 tokens (1.45e12 operations)
-// take 1.11 ms, 1.30 PFLOP/s; the softmax of a half (wait, load, exponentials, store)
-// is as long as the other half's products, and an item's start and end take some 5 us.
-// INT8 pages: 2048 tokens over 30001 positions and eight single tokens (2.08e12) take 2.06 ms, 1.01
-// PFLOP/s: shared memory, which per tile carries 250 KB of operands, 100 of
-// conversion and 130 of scales. With the scores in one part of 128 columns the softmax
-// waited for whole products: 1.44 ms for the prompts.
+// take 1.11 ms, 1.31 PFLOP/s, 2.0 us per tile and SM, of which the products are 1.3 (an
+// S of 64 columns reads as many bytes of Q as one of 128, 48 cycles for 32); the
+// rest is what a half waits for the hand-over between its softmax and its products, and
+// some 5 us per item for its start and end. With the scores in one part of 128 columns
+// the softmax waited for whole products: 1.44 ms. INT8 pages: 2048 tokens over 30001
+// positions and eight single tokens (2.08e12) take 2.01 ms, 1.04 PFLOP/s; without the
+// widening of codes they would take 1.87, without the scales' part of the softmax as
+// well 1.69, the time of BF16 pages.
 //
 // Warps: 0-3 and 4-7 softmax of the halves, 8 and 10 issue the halves'
 // products, 9 loads, 11 walks the CTA's share, 12-15 convert (INT8).
@@ -70,7 +72,7 @@ constexpr float kMaxWeight = 256.0f; // sums of a tile's weights that move the r
 constexpr int kOperandBytes = 128 * 128 * 2;
 // Registers of a softmax thread and of the others: together 256 for a pair, 2 x 128
 // pairs = the 512 x 128 that the block is launched with. Measured: INT8, whose
-// converters want more, 2.05 ms with 160 / 96 (2.10 with 168 / 88, 2.16 with 152 /
+// converters want more, 2.05 ms with 160 / 96 then (2.10 with 168 / 88, 2.16 with 152 /
 // 104); BF16 1.11 ms with 168 / 88 (1.13 with 160 / 96).
 template <bool kInt8>
 struct Regs {
