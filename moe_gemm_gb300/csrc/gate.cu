@@ -25,11 +25,10 @@
 //    logits) is decided again with scores in 64 bits.
 //
 // What bounds it: instructions. 16384 x 256 FP32 logits, sigmoid with a bias, 4 of 8
-// groups, top 8, take 25 us (0.7 TB/s; the copy of its bytes takes 2.6): 8 us read
-// the rows and write, 4 are the ranks' keys and sort, 3 the groups, and 10 the tokens
-// decided again, of which one that starts late ends the call. Rows that a
-// persistent warp reads ahead took 33 us (the registers halve the warps of an SM),
-// the 64-bit part out of line 28.
+// groups, top 8, take 21.8 us (0.8 TB/s; the copy of its bytes takes 2.6), 15 without
+// the tokens decided again, of which one that starts late ends the call. Rows
+// that a persistent warp reads ahead took 8 us more (the registers halve the warps of an
+// SM), the 64-bit part out of line 3.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -56,6 +55,10 @@ __device__ __forceinline__ uint64_t ord(double v) {
 }
 __device__ __forceinline__ float unord(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+
+__device__ __forceinline__ double unord(uint64_t k) {
+    return __longlong_as_double(static_cast<long long>((k >> 63) ? k & 0x7FFFFFFFFFFFFFFFull : ~k));
 }
 
 __device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(kFull, v); }
@@ -443,22 +446,44 @@ __device__ __forceinline__ bool decide_again(const Tin *row, const float (&kr)[V
         const float x = fminf(load_logit(row + e), 3.402823466e38f);
         key = 1.0 / (1.0 + exp_f64(-static_cast<double>(x))) + static_cast<double>(__ldg(a.bias + e));
     }
+    // (The barrier keeps the compiler from putting the exponential off to its uses: with
+    // groups such a token took 9 us then, and takes 4.5.)
+    __syncwarp();
     if (groups) {
-        double m1 = -INFINITY, m2 = -INFINITY;
-        for (int c = 0; c < n; ++c) {
-            const double kc = __shfl_sync(kFull, key, c);
-            if (__shfl_sync(kFull, group, c) == lane) top2_merge<double>(m1, m2, kc, -INFINITY);
+        // The candidates of a group are neighbours: its two largest by doubling, which
+        // leaves them with its first lane. Ordered integers: numbers of 64 bits compare
+        // at a fraction of their rate.
+        uint64_t m1 = e >= 0 ? ord(key) : 0, m2 = 0;
+#pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint64_t n1 = __shfl_down_sync(kFull, m1, o), n2 = __shfl_down_sync(kFull, m2, o);
+            const int there = __shfl_down_sync(kFull, group, o);
+            if (lane + o < 32 && there == group) {
+                const uint64_t lo = m1 < n1 ? m1 : n1, second = m2 < n2 ? n2 : m2;
+                m1 = m1 < n1 ? n1 : m1;
+                m2 = lo < second ? second : lo;
+            }
         }
-        const double gs[2] = {m2 > -INFINITY ? m1 + m2 : m1, -INFINITY};
-        unsigned kept[2];
-        rank_groups<double>(gs, a, lane, 0.0, kept);
-        if (e >= 0 && !((kept[0] >> group) & 1u)) key = -INFINITY;
+        const int before = __shfl_up_sync(kFull, group, 1);
+        uint64_t gs = 0;
+        if (e >= 0 && (lane == 0 || before != group)) gs = m2 != 0 ? ord(unord(m1) + unord(m2)) : m1;
+        unsigned kept = 0;
+#pragma unroll 1
+        for (int j = 0; j < a.topk_group; ++j) {
+            const uint64_t mx = warp_max(gs);
+            if (mx == 0) break;     // the others are empty
+            const int owner = __ffs(__ballot_sync(kFull, gs == mx)) - 1;
+            kept |= 1u << __shfl_sync(kFull, group, owner);
+            if (lane == owner) gs = 0;
+        }
+        if (e >= 0 && !((kept >> group) & 1u)) key = -INFINITY;
     }
     // enough of those at or above `least` (all of them are here) must be left
     const bool good = key > -INFINITY && key >= static_cast<double>(least) + tol * fmax(1.0, fabs(key));
     if (__popc(__ballot_sync(kFull, good)) < a.k) return false;
     uint64_t left = good ? ord(key) : 0;
     out.id[0] = out.id[1] = -1;
+#pragma unroll 1
     for (int j = 0; j < a.k; ++j) {
         const uint64_t mx = warp_max(left);
         const int owner = __ffs(__ballot_sync(kFull, left == mx)) - 1;   // (lists rise by expert)
