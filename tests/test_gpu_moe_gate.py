@@ -179,6 +179,24 @@ def test_biases_that_mark_experts(E, n_group, topk_group):
     assert not bool(torch.isin(ids, never.int()).any()) and bool(torch.isfinite(w).all())
 
 
+def clustered(T, E, seed):
+    """Logits in few narrow clusters, and biases of two values:
+    keys and group scores that 32 bits cannot tell apart are common (and 1e-11
+    apart or more, which 64 bits do tell)."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randint(-3, 4, (T, E), generator=g) * 0.5 + torch.randn(T, E, generator=g) * 1e-4
+    b = torch.randint(0, 2, (E,), generator=g) * 0.05
+    return x.float().to(DEV), b.float().to(DEV)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,n_group,topk_group,k", [(24, 4, 2, 4), (64, 8, 3, 6), (60, 5, 2, 3),
+                                                    (256, 8, 4, 8), (256, 32, 5, 8)])
+def test_close_groups_resolve(E, n_group, topk_group, k, scoring):
+    x, b = clustered(64, E, E + n_group)
+    check(x, k, scoring=scoring, bias=b, n_group=n_group, topk_group=topk_group)
+
+
 def test_far_logits():
     x = logits(6, 64, 8) * 40
     x[1] -= 300
