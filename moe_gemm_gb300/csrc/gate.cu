@@ -76,9 +76,12 @@ struct KeyOf<float> { using type = uint32_t; };
 template <>
 struct KeyOf<double> { using type = uint64_t; };
 
-__device__ __forceinline__ float load_logit(const float *p) { return __ldg(p); }
+// (Ordinary loads, here and below: the kernel before may have written the logits while
+// this one had started already, and read-only loads are for what nobody writes as long as
+// a kernel lives.)
+__device__ __forceinline__ float load_logit(const float *p) { return *p; }
 __device__ __forceinline__ float load_logit(const uint16_t *p) {
-    return __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16);
+    return __uint_as_float(static_cast<uint32_t>(*p) << 16);
 }
 
 struct GateArgs {
@@ -116,7 +119,7 @@ __device__ __forceinline__ void load_row(const float *row, const GateArgs &a, in
 #pragma unroll
             for (int i = 0; i < V; i += 4) {
                 float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-                if (lane * V + i < a.E) v = __ldg(reinterpret_cast<const float4 *>(row + lane * V + i));
+                if (lane * V + i < a.E) v = *reinterpret_cast<const float4 *>(row + lane * V + i);
                 x[i] = v.x;
                 x[i + 1] = v.y;
                 x[i + 2] = v.z;
@@ -126,7 +129,7 @@ __device__ __forceinline__ void load_row(const float *row, const GateArgs &a, in
         }
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = lane * V + i < a.E ? __ldg(row + lane * V + i) : -INFINITY;
+    for (int i = 0; i < V; ++i) x[i] = lane * V + i < a.E ? row[lane * V + i] : -INFINITY;
 }
 template <int V>
 __device__ __forceinline__ void load_row(const uint16_t *row, const GateArgs &a, int lane,
@@ -136,7 +139,7 @@ __device__ __forceinline__ void load_row(const uint16_t *row, const GateArgs &a,
 #pragma unroll
             for (int i = 0; i < V; i += 8) {
                 uint4 v = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
-                if (lane * V + i < a.E) v = __ldg(reinterpret_cast<const uint4 *>(row + lane * V + i));
+                if (lane * V + i < a.E) v = *reinterpret_cast<const uint4 *>(row + lane * V + i);
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -444,7 +447,7 @@ __device__ __forceinline__ bool decide_again(const Tin *row, const float (&kr)[V
     double key = -INFINITY;
     if (e >= 0) {
         const float x = fminf(load_logit(row + e), 3.402823466e38f);
-        key = 1.0 / (1.0 + exp_f64(-static_cast<double>(x))) + static_cast<double>(__ldg(a.bias + e));
+        key = 1.0 / (1.0 + exp_f64(-static_cast<double>(x))) + static_cast<double>(a.bias[e]);
     }
     // (The barrier keeps the compiler from putting the exponential off to its uses: with
     // groups such a token took 9 us then, and takes 4.5.)
@@ -496,7 +499,7 @@ __device__ __forceinline__ bool decide_again(const Tin *row, const float (&kr)[V
 
 template <int V, typename Tin>
 __global__ void __launch_bounds__(kGateWarps * 32)
-moe_gate_kernel(const Tin *__restrict__ logits, const GateArgs a) {
+moe_gate_kernel(const Tin *logits, const GateArgs a) {
     griddep_launch_dependents();
     griddep_wait();
     __shared__ int s_list[kGateWarps][32];
@@ -583,7 +586,7 @@ moe_gate_kernel(const Tin *__restrict__ logits, const GateArgs a) {
             for (int i = 0; i < V; ++i) {
                 const int e = lane * V + i;
                 const double s = a.sigmoid ? 1.0 / (1.0 + kd[i]) : kd[i] / dsum;
-                kd[i] = x[i] > -INFINITY ? s + static_cast<double>(__ldg(a.bias + e)) : -INFINITY;
+                kd[i] = x[i] > -INFINITY ? s + static_cast<double>(a.bias[e]) : -INFINITY;
             }
             if (a.topk_group < a.n_group) keep_groups<double, V>(kd, a, lane, true, 0.0);
             pick<double, V>(kd, a, lane, 0.0, p, least);

@@ -184,7 +184,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant_
         request_span(s, w.r, lo, hi);
         const int pos = x * kTilePositions + 32 * warp + (lane << box_shift);
         if ((lane << box_shift) >= 32 || pos >= hi || pos + a.c.box <= lo) return -2;
-        return __ldg(a.c.table + static_cast<int64_t>(w.b) * a.c.W + page_of(a.c, pos));
+        return a.c.table[static_cast<int64_t>(w.b) * a.c.W + page_of(a.c, pos)];
     };
     // Where the lane's box lies in the cache (-1: not loaded), from its entry.
     auto place = [&](const PagedWalk &w, int x, int id) -> int {
@@ -278,7 +278,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant_
                     (static_cast<int64_t>(w.h) * a.o.G + g) * a.qh + 32 * t);
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const uint4 y = use ? __ldg(src + x) : make_uint4(0, 0, 0, 0);
+                    const uint4 y = use ? src[x] : make_uint4(0, 0, 0, 0);
                     qf[nt][4 * x + 0] = y.x;
                     qf[nt][4 * x + 1] = y.y;
                     qf[nt][4 * x + 2] = y.z;

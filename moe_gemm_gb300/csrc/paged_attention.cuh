@@ -62,7 +62,8 @@ __device__ __forceinline__ TileBoxes find_boxes(const PagedCache &c, int b, int 
     int64_t row = 0;
     if (use) {
         const int pg = page_of(c, pos);
-        const int id = __ldg(c.table + static_cast<int64_t>(b) * c.W + pg);
+        // (an ordinary load: the kernel that writes the table may run when this one starts)
+        const int id = c.table[static_cast<int64_t>(b) * c.W + pg];
         if (id < 0 || id >= c.P) {
             use = false;
             record_device_error(err, KID_ATTN, ROLE_PRODUCER, 9);
