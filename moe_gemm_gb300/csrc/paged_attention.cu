@@ -326,10 +326,9 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant_
             for (int x = p.first; x < p.last; ++x) {
                 const int sg = it % kStages;
                 auto landed = [&](uint64_t &bar, unsigned site) {
-                    if (ok)
-                        ok = mbar_wait(smem_u32(&bar), (it / kStages) & 1, &sm.abort_flag, a.err,
-                                       ROLE_EPILOGUE, site, kWaitLimitNs, KID_ATTN);
-                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    ok = __all_sync(0xFFFFFFFFu,
+                                    ok && mbar_wait(smem_u32(&bar), (it / kStages) & 1, &sm.abort_flag,
+                                                    a.err, ROLE_EPILOGUE, site, kWaitLimitNs, KID_ATTN));
                 };
                 landed(sm.kfull[warp][sg], 3);
                 const uint32_t mw = sm.mask[warp][sg];

@@ -45,6 +45,9 @@
 // widening of codes they would take 1.87, without the scales' part of the softmax as
 // well 1.69, the time of BF16 pages.
 //
+// A wait that gives up is voted on by the warp: its lanes go on to votes and shuffles
+// of all of them, so they must leave together.
+//
 // Warps: 0-3 and 4-7 softmax of the halves, 8 and 10 issue the halves'
 // products, 9 loads, 11 walks the CTA's share, 12-15 convert (INT8).
 #include <cuda.h>
@@ -497,9 +500,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
     uint32_t taken = 0;
     auto take = [&](TilePiece &p, bool &ok, unsigned role) -> bool {
         const int i = taken % kPieces;
-        ok = ok && mbar_wait(bar(sm.piece_full[i]), (taken / kPieces) & 1, abort, a.err, role, 10,
-                             kWaitLimitNs, KID_ATTN);
-        ok = __all_sync(0xFFFFFFFFu, ok);
+        ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(bar(sm.piece_full[i]), (taken / kPieces) & 1, abort,
+                                                     a.err, role, 10, kWaitLimitNs, KID_ATTN));
         if (!ok) return false;
         p = sm.piece[i];
         __syncwarp();
@@ -527,8 +529,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
             const bool work = p.last > p.first;
             const HalfTiles t = half_tiles(s, p, h, a.half_tokens);
             if (work && t.exists) {
-                ok = mbar_wait(bar(sm.q_full[h]), qn[h] & 1, abort, a.err, ROLE_EPILOGUE, 1,
-                               kWaitLimitNs, KID_ATTN);
+                ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(bar(sm.q_full[h]), qn[h] & 1, abort, a.err,
+                                                             ROLE_EPILOGUE, 1, kWaitLimitNs, KID_ATTN));
                 mbar_arrive(bar(sm.q_empty[h]));
                 ++qn[h];
             }
@@ -547,14 +549,14 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                 const int info = ti % kInfo;
 #pragma unroll 1
                 for (int e = 0; e < kN; ++e) {
-                    if (ok)
-                        // (in this order: a half that passes over tiles would not
-                        // know which of two phases an earlier info slot is in)
-                        ok = mbar_wait(bar(sm.s_full[h][e]), sn & 1, abort, a.err, ROLE_EPILOGUE, 2,
-                                       kWaitLimitNs, KID_ATTN) &&
-                             mbar_wait(bar(sm.info_full[info]), (ti / kInfo) & 1, abort, a.err,
-                                       ROLE_EPILOGUE, 3, kWaitLimitNs, KID_ATTN);
-                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    // (in this order: a half that passes over tiles would not
+                    // know which of two phases an earlier info slot is in)
+                    ok = __all_sync(0xFFFFFFFFu,
+                                    ok &&
+                                        mbar_wait(bar(sm.s_full[h][e]), sn & 1, abort, a.err,
+                                                  ROLE_EPILOGUE, 2, kWaitLimitNs, KID_ATTN) &&
+                                        mbar_wait(bar(sm.info_full[info]), (ti / kInfo) & 1, abort,
+                                                  a.err, ROLE_EPILOGUE, 3, kWaitLimitNs, KID_ATTN));
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t tse = ts + e * kCols;
@@ -584,9 +586,9 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                     // Before O is rescaled, the output product of the part before has to
                     // be done (those before that are: this part's scores came after).
                     auto settle = [&]() {
-                        ok = ok && mbar_wait(bar(sm.pv_done[h][e ^ 1]), (sn + e + 1) & 1, abort, a.err,
-                                             ROLE_EPILOGUE, 5, kWaitLimitNs, KID_ATTN);
-                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(bar(sm.pv_done[h][e ^ 1]), (sn + e + 1) & 1,
+                                                                     abort, a.err, ROLE_EPILOGUE, 5,
+                                                                     kWaitLimitNs, KID_ATTN));
                         tc_fence_after();
                     };
                     uint32_t pk[2][32 / kN];
@@ -643,12 +645,11 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
             const bool any = work && t.upto > t.from;
             if (any) {
                 // the last output products (sn counts this piece's tiles already)
-                ok = ok &&
-                     mbar_wait(bar(sm.pv_done[h][0]), (sn - 1) & 1, abort, a.err, ROLE_EPILOGUE, 4,
-                               kWaitLimitNs, KID_ATTN) &&
-                     mbar_wait(bar(sm.pv_done[h][1]), (sn - 1) & 1, abort, a.err, ROLE_EPILOGUE, 6,
-                               kWaitLimitNs, KID_ATTN);
-                ok = __all_sync(0xFFFFFFFFu, ok);
+                ok = __all_sync(0xFFFFFFFFu, ok &&
+                                                 mbar_wait(bar(sm.pv_done[h][0]), (sn - 1) & 1, abort, a.err,
+                                                           ROLE_EPILOGUE, 4, kWaitLimitNs, KID_ATTN) &&
+                                                 mbar_wait(bar(sm.pv_done[h][1]), (sn - 1) & 1, abort, a.err,
+                                                           ROLE_EPILOGUE, 6, kWaitLimitNs, KID_ATTN));
             }
             if (!ok) break;
             tc_fence_after();
@@ -846,10 +847,10 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                         const uint32_t sl = u % kSlots;
                         uint64_t &full_bar = kInt8 ? sm.raw_full[sl] : sm.op_full[sl];
                         uint64_t &empty_bar = kInt8 ? sm.raw_empty[sl] : sm.op_empty[sl];
-                        if (ok && u >= kSlots)
-                            ok = mbar_wait(bar(empty_bar), (u / kSlots - 1) & 1, abort, a.err,
-                                           ROLE_PRODUCER, 1, kWaitLimitNs, KID_ATTN);
-                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        if (u >= kSlots)
+                            ok = __all_sync(0xFFFFFFFFu,
+                                            ok && mbar_wait(bar(empty_bar), (u / kSlots - 1) & 1, abort,
+                                                            a.err, ROLE_PRODUCER, 1, kWaitLimitNs, KID_ATTN));
                         if (!ok) break;
                         const uint32_t dst = kInt8 ? smem_u32(sm.raw[sl]) : smem_u32(sm.op[sl]);
                         // A V tile with masked positions is made zero there
@@ -875,8 +876,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                         if (kv == 0 && x + 1 < p.last)
                             next = find_boxes(a.c, p.b, p.h, p.tile0 + x + 1, lo, hi, a.err);
                         if (mend) {
-                            ok = mbar_wait(b, fixes & 1, abort, a.err, ROLE_PRODUCER, 2, kWaitLimitNs,
-                                           KID_ATTN);
+                            ok = __all_sync(0xFFFFFFFFu, mbar_wait(b, fixes & 1, abort, a.err, ROLE_PRODUCER,
+                                                                   2, kWaitLimitNs, KID_ATTN));
                             ++fixes;
                             for (int i = lane; i < kOperandBytes / 16; i += 32) {
                                 const int r = (i >> 3) & 127;
@@ -892,10 +893,11 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 if (h * a.half_tokens >= p.ntok) continue;
-                                if (ok && qn[h] > 0)
-                                    ok = mbar_wait(bar(sm.q_empty[h]), (qn[h] - 1) & 1, abort, a.err,
-                                                   ROLE_PRODUCER, 3, kWaitLimitNs, KID_ATTN);
-                                ok = __all_sync(0xFFFFFFFFu, ok);
+                                if (qn[h] > 0)
+                                    ok = __all_sync(0xFFFFFFFFu,
+                                                    ok && mbar_wait(bar(sm.q_empty[h]), (qn[h] - 1) & 1, abort,
+                                                                    a.err, ROLE_PRODUCER, 3, kWaitLimitNs,
+                                                                    KID_ATTN));
                                 if (!ok) break;
                                 ++qn[h];
                                 if (lane == 0) {
@@ -938,9 +940,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                 }
                 const int i = n % kPieces;
                 if (n >= kPieces)
-                    ok = mbar_wait(bar(sm.piece_empty[i]), (n / kPieces - 1) & 1, abort, a.err,
-                                   ROLE_PRODUCER, 11, kWaitLimitNs, KID_ATTN);
-                ok = __all_sync(0xFFFFFFFFu, ok);
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(sm.piece_empty[i]), (n / kPieces - 1) & 1, abort,
+                                                           a.err, ROLE_PRODUCER, 11, kWaitLimitNs, KID_ATTN));
                 if (!ok) break;
                 if (lane == 0) {
                     TilePiece t;
@@ -1000,12 +1001,13 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                     const int info = it % kInfo;
                     for (int kv = 0; kv < 2; ++kv, ++u) {
                         const uint32_t rs = u % kRaws, os = u % kOps;
-                        ok = ok && mbar_wait(bar(sm.raw_full[rs]), (u / kRaws) & 1, abort, a.err,
-                                             ROLE_CONVERT, 1, kWaitLimitNs, KID_ATTN);
-                        if (ok && u >= kOps)
-                            ok = mbar_wait(bar(sm.op_empty[os]), (u / kOps - 1) & 1, abort, a.err,
-                                           ROLE_CONVERT, 2, kWaitLimitNs, KID_ATTN);
-                        ok = __all_sync(0xFFFFFFFFu, ok);
+                        ok = __all_sync(0xFFFFFFFFu,
+                                        ok &&
+                                            mbar_wait(bar(sm.raw_full[rs]), (u / kRaws) & 1, abort, a.err,
+                                                      ROLE_CONVERT, 1, kWaitLimitNs, KID_ATTN) &&
+                                            (u < kOps ||
+                                             mbar_wait(bar(sm.op_empty[os]), (u / kOps - 1) & 1, abort,
+                                                       a.err, ROLE_CONVERT, 2, kWaitLimitNs, KID_ATTN)));
                         if (!ok) break;
                         // 16 codes to 32 bytes at a time
                         const uint8_t *src = sm.raw[rs];
@@ -1040,8 +1042,9 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                             const int halves = a.half_tokens < p.ntok ? 2 : 1;
                             uint32_t mq = 0;
                             for (int h = 0; h < halves; ++h) {
-                                ok = ok && mbar_wait(bar(sm.q_land[h]), qn[h] & 1, abort, a.err,
-                                                     ROLE_CONVERT, 3, kWaitLimitNs, KID_ATTN);
+                                ok = __all_sync(0xFFFFFFFFu,
+                                                ok && mbar_wait(bar(sm.q_land[h]), qn[h] & 1, abort, a.err,
+                                                                ROLE_CONVERT, 3, kWaitLimitNs, KID_ATTN));
                                 ++qn[h];
 #pragma unroll 4
                                 for (int j = 0; j < 16; ++j)
@@ -1051,10 +1054,10 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                             if (lane == 0) sm.qmax[cw] = mq;
                             __syncwarp();
                             mbar_arrive(bar(sm.q_max));
-                            ok = ok && mbar_wait(bar(sm.q_max), items & 1, abort, a.err, ROLE_CONVERT,
-                                                 4, kWaitLimitNs, KID_ATTN);
+                            ok = __all_sync(0xFFFFFFFFu, ok && mbar_wait(bar(sm.q_max), items & 1, abort, a.err,
+                                                                         ROLE_CONVERT, 4, kWaitLimitNs,
+                                                                         KID_ATTN));
                             ++items;
-                            ok = __all_sync(0xFFFFFFFFu, ok);
                             if (!ok) break;
                             mq = max(max(sm.qmax[0], sm.qmax[1]), max(sm.qmax[2], sm.qmax[3]));
                             const int be = static_cast<int>(mq >> 7);

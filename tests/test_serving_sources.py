@@ -24,3 +24,13 @@ def test_no_read_only_loads(name):
     # pointers to const that are __restrict__.
     found = re.findall(r"__ldg|ld\.global(?:\.\w+)*\.nc|__restrict__", code_of(name))
     assert found == []
+
+
+@pytest.mark.parametrize("name", ["paged_attention.cu", "paged_attention_tiles.cu"])
+def test_waits_that_give_up_are_voted_on(name):
+    # What follows a wait are votes and shuffles of the whole warp. A lane that leaves alone,
+    # because the barrier completed for the others just as its own wait ran out, would leave
+    # them waiting for it. (The waits with `never` end a warp's work.)
+    waits = [s for s in code_of(name).split(";") if re.search(r"\bmbar_wait\(", s)]
+    assert waits
+    assert [s for s in waits if "__all_sync" not in s and "&never" not in s] == []
