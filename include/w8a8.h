@@ -674,7 +674,8 @@ w8a8_status w8a8_paged_kv_write(const void *k_bf16, int64_t k_token_stride, int6
  * Token i of a request's n stands at position p = kv_len - n + i and sees the
  * keys of positions max(0, p - window + 1) .. p (window 0: from 0). Query
  * head h uses kv head h / (Hq / Hkv). A token that sees nothing (p < 0), and
- * rows of q that belong to no request, get zeros. Nothing outside the
+ * rows of q that belong to no request, get zeros; such rows may hold anything, and
+ * no request's answer depends on another's rows. Nothing outside the
  * positions that some new token sees is read; what those hold must be finite.
  * A table entry outside [0, P) there reads as absent: its positions are masked,
  * and w8a8_device_error() tells of it. A length past W * page is cut to it.

@@ -430,6 +430,14 @@ __device__ __forceinline__ HalfTiles half_tiles(const PagedSchedule &s, const Ti
     return t;
 }
 
+// The rows of a half that are the item's: the copy of q always brings half_tokens
+// tokens, and in a request's last item those after its own are another request's, or
+// nobody's, and may hold anything. They take no part in what rows decide together (the
+// scaling of INT8 pages' q, when references move).
+__device__ __forceinline__ int own_rows(const TilePiece &p, int half, int half_tokens, int G) {
+    return min(p.ntok - half * half_tokens, half_tokens) * G;
+}
+
 template <bool kInt8>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap km,
@@ -536,9 +544,11 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
             }
             float m[4], l[4];
             int pos[4];
+            bool own[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                m[k] = -INFINITY;
+                own[k] = r4 + 8 * k < own_rows(p, h, a.half_tokens, a.o.G);
+                m[k] = own[k] ? -INFINITY : 0.0f;   // (a reference that needs no first maximum)
                 l[k] = 0.0f;
                 pos[k] = t.first + tok4[k];
             }
@@ -622,7 +632,10 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                         if (masked) weigh<kInt8, true>(tse, col, a.scale_log2, nm, mk, pk, sum);
                         else weigh<kInt8, false>(tse, col, a.scale_log2, nm, mk, pk, sum);
                         if (again) break;
-                        move = !(fmaxf(fmaxf(sum[0], sum[1]), fmaxf(sum[2], sum[3])) <= kMaxWeight);
+                        float most = 0.0f;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) most = fmaxf(most, own[k] ? sum[k] : 0.0f);
+                        move = !(most <= kMaxWeight);
                         if (!__any_sync(0xFFFFFFFFu, move)) break;
                     }
                     if (turn != 1.0f) {
@@ -1038,7 +1051,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                         }
                         if (x == p.first) {
                             // the item's q to fp16, a row of each half per thread, scaled
-                            // so that the largest value lies in [2^14, 2^15)
+                            // so that the largest value lies in [2^14, 2^15); rows that are
+                            // not its own become zeros
                             const int halves = a.half_tokens < p.ntok ? 2 : 1;
                             uint32_t mq = 0;
                             for (int h = 0; h < halves; ++h) {
@@ -1046,9 +1060,10 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                                                 ok && mbar_wait(bar(sm.q_land[h]), qn[h] & 1, abort, a.err,
                                                                 ROLE_CONVERT, 3, kWaitLimitNs, KID_ATTN));
                                 ++qn[h];
+                                if (ct < own_rows(p, h, a.half_tokens, a.o.G))
 #pragma unroll 4
-                                for (int j = 0; j < 16; ++j)
-                                    mq = max(mq, amax_bits8(*q_piece(sm.q[h], ct, j)));
+                                    for (int j = 0; j < 16; ++j)
+                                        mq = max(mq, amax_bits8(*q_piece(sm.q[h], ct, j)));
                             }
                             mq = __reduce_max_sync(0xFFFFFFFFu, mq);
                             if (lane == 0) sm.qmax[cw] = mq;
@@ -1065,9 +1080,10 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                             const float qs = __uint_as_float(static_cast<uint32_t>(se + 127) << 23);
                             unscale = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - se) << 23);
                             for (int h = 0; h < halves; ++h) {
+                                const bool own = ct < own_rows(p, h, a.half_tokens, a.o.G);
 #pragma unroll 4
                                 for (int j = 0; j < 16; ++j) {
-                                    uint4 y = *q_piece(sm.q[h], ct, j);
+                                    uint4 y = own ? *q_piece(sm.q[h], ct, j) : make_uint4(0, 0, 0, 0);
                                     y.x = pack_f16x2(__uint_as_float(y.x << 16) * qs, __uint_as_float(y.x & 0xFFFF0000u) * qs);
                                     y.y = pack_f16x2(__uint_as_float(y.y << 16) * qs, __uint_as_float(y.y & 0xFFFF0000u) * qs);
                                     y.z = pack_f16x2(__uint_as_float(y.z << 16) * qs, __uint_as_float(y.z & 0xFFFF0000u) * qs);

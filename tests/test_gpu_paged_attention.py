@@ -372,3 +372,24 @@ def test_pool_past_32_bit_offsets(int8):
                              v_scale=vs, out_dtype=torch.float32)
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf, -3e38, 1e30])
+@pytest.mark.parametrize("int8", KINDS)
+@pytest.mark.parametrize("n_new,spare", [([1, 1, 1], 2), ([2, 1, 3], 5), ([20, 33, 5], 37),
+                                         ([1, 200, 70], 64)])
+def test_rows_of_q_that_are_not_a_requests_own(n_new, spare, int8, value):
+    # rows past the last request's (a padded step's) hold anything; so may a neighbour's
+    b = Batch(n_new, [40, 300, 129], 8, 2, 16, int8, seed=21)
+    T = b.q.shape[0]
+    b.q = torch.cat([b.q, b.q[:1].expand(spare, -1, -1)])
+    clean = b.run()
+    b.check(clean[:T], split=(T + spare) * 4 <= 16 * 3)
+    b.q[T:] = value
+    assert torch.equal(b.run(), clean)
+    for r in range(3):
+        q = b.q.clone()
+        b.q[b.cu[r]:b.cu[r + 1]] = value
+        out, b.q = b.run(), q
+        out[b.cu[r]:b.cu[r + 1]] = clean[b.cu[r]:b.cu[r + 1]]
+        assert torch.equal(out, clean)
