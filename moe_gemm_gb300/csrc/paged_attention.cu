@@ -293,7 +293,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant_
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) mq = __vmaxu2(mq, qf[nt][x] & 0x7FFF7FFFu);
+                    for (int x = 0; x < 16; ++x) mq = __vmaxu2(mq, finite_bits2(qf[nt][x]));
                 mq = max(mq & 0xFFFFu, mq >> 16);
                 mq = __reduce_max_sync(0xFFFFFFFFu, mq);
                 const int bexp = static_cast<int>((mq >> 7) & 0xFFu);

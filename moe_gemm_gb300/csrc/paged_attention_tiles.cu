@@ -1062,10 +1062,13 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                                 ++qn[h];
                                 if (ct < own_rows(p, h, a.half_tokens, a.o.G))
 #pragma unroll 4
-                                    for (int j = 0; j < 16; ++j)
-                                        mq = max(mq, amax_bits8(*q_piece(sm.q[h], ct, j)));
+                                    for (int j = 0; j < 16; ++j) {
+                                        const uint4 y = *q_piece(sm.q[h], ct, j);
+                                        mq = __vmaxu2(__vmaxu2(mq, finite_bits2(y.x)), finite_bits2(y.y));
+                                        mq = __vmaxu2(__vmaxu2(mq, finite_bits2(y.z)), finite_bits2(y.w));
+                                    }
                             }
-                            mq = __reduce_max_sync(0xFFFFFFFFu, mq);
+                            mq = __reduce_max_sync(0xFFFFFFFFu, max(mq & 0xFFFFu, mq >> 16));
                             if (lane == 0) sm.qmax[cw] = mq;
                             __syncwarp();
                             mbar_arrive(bar(sm.q_max));

@@ -393,3 +393,19 @@ def test_rows_of_q_that_are_not_a_requests_own(n_new, spare, int8, value):
         out, b.q = b.run(), q
         out[b.cu[r]:b.cu[r + 1]] = clean[b.cu[r]:b.cu[r + 1]]
         assert torch.equal(out, clean)
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("int8", KINDS)
+@pytest.mark.parametrize("n_new", [[1, 1], [3, 1], [70, 9]])
+def test_a_row_that_is_no_number_is_so_alone(n_new, int8, value):
+    # one head of one token: the other heads and tokens of the request keep their answers
+    b = Batch(n_new, [200, 90], 8, 2, 16, int8, seed=23)
+    q = b.q.clone()
+    at = (n_new[0] - 1, 5)
+    b.q[at][7] = value
+    out, b.q = b.run(), q
+    if math.isnan(value):
+        assert bool(torch.isnan(out[at]).all())
+    out[at] = b.run()[at]
+    b.check(out, split=sum(n_new) * 4 <= 16 * 2)
