@@ -586,7 +586,9 @@ moe_gate_kernel(const Tin *logits, const GateArgs a) {
             for (int i = 0; i < V; ++i) {
                 const int e = lane * V + i;
                 const double s = a.sigmoid ? 1.0 / (1.0 + kd[i]) : kd[i] / dsum;
-                kd[i] = x[i] > -INFINITY ? s + static_cast<double>(a.bias[e]) : -INFINITY;
+                const double key = s + static_cast<double>(e < a.E ? a.bias[e] : 0.0f);
+                // (a NaN must not reach the groups' maxima, which would take it for a number)
+                kd[i] = x[i] > -INFINITY && key == key ? key : -INFINITY;
             }
             if (a.topk_group < a.n_group) keep_groups<double, V>(kd, a, lane, true, 0.0);
             pick<double, V>(kd, a, lane, 0.0, p, least);

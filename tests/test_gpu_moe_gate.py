@@ -252,3 +252,19 @@ def test_feeds_the_expert_ffn():
     rid, rw = reference(lg, k)
     y2 = w8.moe_ffn(x, rid.to(DEV), rw.float().to(DEV), *args, out_dtype=torch.float32)
     assert bool(((y - y2).abs() <= 2 * TOL * y2.abs().max()).all())
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,n_group,topk_group,k", [(24, 4, 2, 4), (64, 8, 3, 6), (60, 5, 2, 3),
+                                                    (256, 8, 4, 8), (256, 32, 5, 8), (64, 1, 1, 8)])
+def test_nan_biases_among_close_groups(E, n_group, topk_group, k, scoring):
+    # (for the reference: keys far below all others, never among a group's two largest here)
+    x, b = clustered(64, E, 2 * E + n_group)
+    never = torch.arange(1, E, 3, device=DEV)
+    low = b.clone()
+    b[never], low[never] = math.nan, -1e30
+    kw = dict(scoring=scoring, n_group=n_group, topk_group=topk_group)
+    ids, w = w8.moe_gate(x, k, bias=b, **kw)
+    rid, rw = reference(x, k, bias=low, **kw)
+    assert torch.equal(ids.cpu(), rid)
+    assert bool(((w.cpu().double() - rw).abs() <= TOL * rw).all())
