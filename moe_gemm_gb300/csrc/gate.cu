@@ -169,11 +169,12 @@ __device__ __forceinline__ void top2_merge(R &a1, R &a2, R b1, R b2) {
 }
 
 // Which groups stay (bit g of kept), from their scores (lane l: groups l and l +
-// 32). Returns false when the last group kept and the first one left out are within
-// `tol` of one another (relative to 1 and to their size).
+// 32). size: the sum of the magnitudes of the keys that make up a score (they may
+// cancel: a score's error goes by them, not by itself). Returns false when scores off by
+// tol / 2 each, relative to 1 and to their size, may change which groups stay.
 template <typename R>
-__device__ __forceinline__ bool rank_groups(const R (&gs)[2], const GateArgs &a, int lane, R tol,
-                                            unsigned (&kept)[2]) {
+__device__ __forceinline__ bool rank_groups(const R (&gs)[2], const R (&size)[2], const GateArgs &a,
+                                            int lane, R tol, unsigned (&kept)[2]) {
     const R none = -INFINITY;
     // rank of each group: those with a larger score, or an equal one and a lower index
     int rank[2] = {0, 0};
@@ -191,14 +192,16 @@ __device__ __forceinline__ bool rank_groups(const R (&gs)[2], const GateArgs &a,
         }
     }
     bool clear = true;
-    R worst_in = INFINITY, best_out = none;
+    R worst_in = INFINITY, best_out = none;   // at their worst
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const bool exists = lane + 32 * h < a.n_group;
         const bool in = exists && rank[h] < a.topk_group;
         kept[h] = __ballot_sync(kFull, in);
-        if (in) worst_in = fmin(worst_in, gs[h]);
-        if (exists && !in) best_out = fmax(best_out, gs[h]);
+        const R err = R(0.5) * tol * fmax(R(1), size[h]);
+        const bool known = size[h] < R(INFINITY);   // (else a sum may have overflowed)
+        if (in) worst_in = fmin(worst_in, known ? gs[h] - err : none);
+        if (exists && !in) best_out = fmax(best_out, known ? gs[h] + err : R(INFINITY));
     }
     if (tol > R(0)) {
 #pragma unroll
@@ -206,21 +209,24 @@ __device__ __forceinline__ bool rank_groups(const R (&gs)[2], const GateArgs &a,
             worst_in = fmin(worst_in, __shfl_xor_sync(kFull, worst_in, o));
             best_out = fmax(best_out, __shfl_xor_sync(kFull, best_out, o));
         }
-        // (an unavailable group, -inf, is never close to an available one)
-        clear = !(worst_in - best_out <= tol * fmax(R(1), fabs(worst_in)));
+        // (which of the unavailable groups stay, all -inf, does not matter)
+        clear = worst_in > best_out || best_out == none;
     }
     return clear;
 }
 
 // Marks the experts outside the topk_group best groups as not available
-// (kr = -inf there). Returns false when the last group kept and the first one
-// left out are within `tol` of one another (relative to 1 and to their size).
+// (kr = -inf there). tol, and what is returned: as above.
 template <typename R, int V>
 __device__ __forceinline__ bool keep_groups(R (&kr)[V], const GateArgs &a, int lane, bool sum2,
                                             R tol) {
     const int size = a.size;
     const R none = -INFINITY;
     R gs[2] = {none, none};   // lane l: the scores of groups l and l + 32
+    R sizes[2] = {0, 0};      // and the magnitudes in them
+    auto magnitude = [&](R m1, R m2) {
+        return m1 > none ? fabs(m1) + (sum2 && m2 > none ? fabs(m2) : R(0)) : R(0);
+    };
     const int run = 1 << max(a.run_shift, 0);
     if (a.run_shift >= 0) {
         // a group is a run of a power of two lanes: every group at once
@@ -234,6 +240,7 @@ __device__ __forceinline__ bool keep_groups(R (&kr)[V], const GateArgs &a, int l
             top2_merge<R>(m1, m2, __shfl_xor_sync(kFull, m1, o), __shfl_xor_sync(kFull, m2, o));
         const R s = sum2 && m2 > none ? m1 + m2 : m1;
         gs[0] = __shfl_sync(kFull, s, (lane * run) & 31);
+        if (tol > R(0)) sizes[0] = __shfl_sync(kFull, magnitude(m1, m2), (lane * run) & 31);
         if (lane >= a.n_group) gs[0] = none;
     } else {
         for (int g = 0; g < a.n_group; ++g) {
@@ -250,11 +257,12 @@ __device__ __forceinline__ bool keep_groups(R (&kr)[V], const GateArgs &a, int l
             if (lane == (g & 31)) {
                 if (g < 32) gs[0] = s;
                 else gs[1] = s;
+                if (tol > R(0)) sizes[g < 32 ? 0 : 1] = magnitude(m1, m2);
             }
         }
     }
     unsigned kept[2];
-    const bool clear = rank_groups<R>(gs, a, lane, tol, kept);
+    const bool clear = rank_groups<R>(gs, sizes, a, lane, tol, kept);
     if (a.run_shift >= 0) {
         const bool stays = (kept[0] >> (lane >> a.run_shift)) & 1u;
 #pragma unroll

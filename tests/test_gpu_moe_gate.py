@@ -268,3 +268,20 @@ def test_nan_biases_among_close_groups(E, n_group, topk_group, k, scoring):
     rid, rw = reference(x, k, bias=low, **kw)
     assert torch.equal(ids.cpu(), rid)
     assert bool(((w.cpu().double() - rw).abs() <= TOL * rw).all())
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,n_group,topk_group", [(64, 8, 4), (256, 32, 9), (256, 8, 3), (96, 8, 4),
+                                                  (1024, 32, 8)])
+@pytest.mark.parametrize("size", [100.0, 300.0, 1000.0])
+def test_group_sums_of_large_opposite_keys(size, E, n_group, topk_group, scoring):
+    # a group's two largest keys nearly cancel: its score is small, its 32-bit error that of the keys.
+    # (No two groups' keys are close, so the picks themselves are clear.)
+    g = torch.Generator().manual_seed(int(size) + E)
+    T, per = 96, E // n_group
+    x = torch.randn(T, n_group, per, generator=g) * 1e-4
+    b = torch.full((n_group, per), -4 * size)
+    up = size + 7 * torch.arange(n_group)
+    b[:, per // 2], b[:, 1] = up, 0.25 - up
+    x, b = x.view(T, E).to(DEV), b.view(E).to(DEV)
+    check(x, 2 * topk_group, scoring=scoring, bias=b, n_group=n_group, topk_group=topk_group)
