@@ -682,7 +682,9 @@ w8a8_status w8a8_paged_kv_write(const void *k_bf16, int64_t k_token_stride, int6
  * Sums and softmax statistics are FP32. For the product with V, calls of up to
  * 16 query rows per request and kv head on average (T * Hq / Hkv <= 16 * B) keep 22
  * bits of the probabilities (BF16 pages: 24), as the contiguous-cache calls do;
- * calls with more round them to fp16 (BF16 pages: to BF16). INT8 pages: q is taken in
+ * calls with more round them to fp16 (BF16 pages: to BF16), and on INT8 pages those below
+ * fp16's normal range lose up to 2^-22 of the largest v scale among the 128 positions of their
+ * tile (positions 128 i .. 128 i + 127). INT8 pages: q is taken in
  * fp16, scaled by one power of two for up to 16 (calls with more rows: 256) neighbouring
  * rows of one request and kv head; values below 2^-28 of the largest finite one among
  * them lose bits. A row of q that holds a NaN gets NaN, one that holds an infinity

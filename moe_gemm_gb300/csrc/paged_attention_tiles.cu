@@ -25,8 +25,10 @@
 // INT8 pages: a converter warpgroup widens the codes to fp16 (exact) into
 // shared memory. Scores are S * (k scale); a weight carries its v scale,
 // P_j = p_j * vs_j * 2^-e, rounded to fp16 (half a step 2^-11). e follows the
-// largest v scale of the tiles so far (P stays below 2^12, and what falls below
-// fp16's normal range is under 2^-25 of the largest), and O is in units of 2^e.
+// largest v scale s of the tiles, up and down, to within 2^3: P stays below 2^12, and a
+// weight loses no more than 2^-25 2^e <= 2^-22 s in fp16's subnormals. So a vector
+// far larger than the rest costs the other vectors of its own tile their bits, whether or
+// not a row gives it weight. O is in units of 2^e.
 // q goes to fp16 too, scaled by one power of two per item, which the k scales
 // take back exactly.
 //
@@ -1008,7 +1010,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
             TilePiece p;
             while (mine && take(p, ok, ROLE_CONVERT)) {
                 if (p.last <= p.first) continue;
-                int e = -100;                       // O's unit is 2^e
+                int e = -100, top = -100;           // O's unit is 2^e; the largest so far
                 float unscale = 0.0f;               // of q's scaling, and to log2 units
                 for (int x = p.first; x < p.last && ok; ++x, ++it) {
                     const int info = it % kInfo;
@@ -1110,9 +1112,12 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                         const float rk = live ? sm.rks[info][ct] : 0.0f;
                         const float rv = live ? sm.rvs[info][ct] : 0.0f;
                         mbar_arrive(bar(sm.raw_empty[rs]));
-                        // a new unit when the largest weight would pass 16 of it
+                        // a new unit when the largest weight would pass 16 of it, or
+                        // stay below 1/8 (not more than 2^60 below the item's largest unit:
+                        // O is FP32; a tile of zero vectors needs none)
                         const int te = max(-100, min(100, static_cast<int>(wm >> 23) - 127));
-                        if (te >= e + 4) e = te;
+                        if (te >= e + 4 || (te <= e - 4 && wm != 0)) e = max(te, top - 60);
+                        top = max(top, e);
                         const float un = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
                         const float ui = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
                         float *c4 = reinterpret_cast<float *>(&sm.col[info][ct >> 1]) + (ct & 1);

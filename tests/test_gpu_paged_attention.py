@@ -409,3 +409,51 @@ def test_a_row_that_is_no_number_is_so_alone(n_new, int8, value):
         assert bool(torch.isnan(out[at]).all())
     out[at] = b.run()[at]
     b.check(out, split=sum(n_new) * 4 <= 16 * 2)
+
+
+def check_by_tile(b, out):
+    """One request, INT8 pages, the many-rows kernel: Batch.check with the absolute
+    term of each weight taken of its own tile of 128 positions. A weight times its v scale
+    is held as fp16 in units of 2^e, 2^e <= 2^3 s with s the tile's largest v scale: it
+    loses 2^-25 2^e <= 2^-22 s at most, and no more than itself; the sum of weights that
+    it is divided by is 1 at least (2^-10 for what that sum is off)."""
+    G, L, n = b.Hq // b.Hkv, b.kv[0], b.n_new[0]
+    pos = torch.arange(L, device=DEV)
+    pg, off = b.table[0].long()[pos // b.page], pos % b.page
+    seen = pos <= L - n + torch.arange(n, device=DEV)[:, None]
+    for h in range(b.Hq):
+        codes, vs = b.vc[pg, h // G, off].double(), b.vs[pg, h // G, off].double()
+        k = b.kc[pg, h // G, off].double() * b.ks[pg, h // G, off].double()[:, None]
+        v, q = codes * vs[:, None], b.q[:, h].double()
+        s = torch.where(seen, (q @ k.T) * SCALE, -math.inf)
+        p = torch.softmax(s, -1)
+        tiles = torch.nn.functional.pad(vs, (0, -L % 128)).view(-1, 128)
+        tile = tiles.amax(-1).repeat_interleave(128)[:L]
+        lost = torch.minimum(2.0 ** -22 * tile, p * vs) @ codes.abs() * (1 + 2.0 ** -10)
+        want, bound = p @ v, lost
+        # (the error of a score moves its own weight: keys of next to no weight by themselves)
+        for part in (p >= 2.0 ** -40, p < 2.0 ** -40):
+            A = torch.where(part & seen, (q.abs() @ k.abs().T) * SCALE, 0.0).amax(-1, keepdim=True)
+            rel = 2 * A * (D + 2) * 2.0 ** -24 + 2 * A * 2.0 ** -22 + (L + 64) * 2.0 ** -24 \
+                + 16 * 2.0 ** -22 + 2.0 ** -11
+            bound = bound + rel * (torch.where(part, p, 0.0) @ v.abs())
+        bound = bound + 2.0 ** -24 * want.abs()
+        err = (out[:, h].double() - want).abs()
+        assert bool((err <= bound).all()), (h, float((err / bound).max()))
+
+
+@pytest.mark.parametrize("power", [12, 20, 30])
+@pytest.mark.parametrize("every", [1000, 2, 3])
+@pytest.mark.parametrize("n,ctx", [(70, 900), (300, 128), (513, 1000)])
+def test_large_value_vectors_cost_their_own_tiles(n, ctx, every, power):
+    # tiles whose vectors are 2^power larger, and that no query gives weight (their keys point
+    # away from what the queries share), take no bits from the others
+    b = Batch([n], [ctx], 8, 2, 32, True, seed=22)
+    pos = torch.arange(ctx // 128 * 128, device=DEV)
+    pos = pos[pos // 128 % every == 0]
+    pg, off = b.table[0].long()[pos // 32], pos % 32
+    b.vs[pg, :, off] *= 2.0 ** power
+    b.q[..., 1] = 256.0
+    b.kc[..., 1] = 0
+    b.kc[pg, :, off, 1] = -127
+    check_by_tile(b, b.run())
