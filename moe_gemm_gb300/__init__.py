@@ -737,6 +737,13 @@ def _require_heads(x: torch.Tensor, name: str, device: Optional[torch.device] = 
                          f"stride in the last dimension")
 
 
+def _head_strides(x: torch.Tensor) -> Tuple[int, int]:
+    """Token and head strides of [T, heads, 128]; a dimension of one element has
+    none (whatever torch says there), and gets that of a contiguous tensor."""
+    T, heads, d = x.shape
+    return x.stride(0) if T > 1 else heads * d, x.stride(1) if heads > 1 else d
+
+
 def _require_pages(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: Optional[torch.Tensor],
                    v_scale: Optional[torch.Tensor], device: torch.device):
     """Checks a paged cache; returns (P, Hkv, page)."""
@@ -777,9 +784,9 @@ def paged_kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cach
     _require(slots, torch.int32, "slots", 1, (T,), dev)
     with _on_device(dev, stream):
         _check(_lib.w8a8_paged_kv_write(
-            _ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0), v.stride(1), _ptr(slots), T,
-            Hkv, d, P, page, _ptr(k_cache), _ptr(k_scale), _ptr(v_cache), _ptr(v_scale),
-            _stream(stream)), "w8a8_paged_kv_write")
+            _ptr(k), *_head_strides(k), _ptr(v), *_head_strides(v), _ptr(slots), T, Hkv, d, P, page,
+            _ptr(k_cache), _ptr(k_scale), _ptr(v_cache), _ptr(v_scale), _stream(stream)),
+            "w8a8_paged_kv_write")
 
 
 def attention_paged_workspace_size(T: int, B: int, Hq: int, Hkv: int) -> int:
@@ -819,7 +826,7 @@ def attention_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         _require_workspace(workspace, dev)
     with _on_device(dev, stream):
         _check(_lib.w8a8_attention_paged(
-            _ptr(q), q.stride(0), q.stride(1), _ptr(k_cache), _ptr(k_scale), _ptr(v_cache),
+            _ptr(q), *_head_strides(q), _ptr(k_cache), _ptr(k_scale), _ptr(v_cache),
             _ptr(v_scale), _ptr(block_table), _ptr(kv_lens), _ptr(cu_new), T, B, W, Hq, Hkv, d, P,
             page, float(softmax_scale), window, _ptr(out), code, _ptr(workspace),
             workspace.numel(), _stream(stream)), "w8a8_attention_paged")
@@ -841,7 +848,7 @@ def moe_gate(logits: torch.Tensor, k: int, scoring: str = "softmax",
     topk_group best of n_group expert groups are picked, and weighted by their
     scores (over their sum with renormalize), times scale."""
     if (not logits.is_cuda or logits.dtype not in (torch.float32, torch.bfloat16)
-            or logits.dim() != 2 or logits.stride(1) != 1):
+            or logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1)):
         raise ValueError("logits: expected a CUDA fp32 or bf16 [T, E] tensor with unit column "
                          "stride")
     if scoring not in GATE_SCORES:
@@ -860,7 +867,7 @@ def moe_gate(logits: torch.Tensor, k: int, scoring: str = "softmax",
         _require(topk_w, torch.float32, "topk_w", 2, (T, k), dev)
     with _on_device(dev, stream):
         _check(_lib.w8a8_moe_gate(
-            _ptr(logits), _dtype_code(logits.dtype), logits.stride(0), T, E, k,
+            _ptr(logits), _dtype_code(logits.dtype), logits.stride(0) if T > 1 else E, T, E, k,
             GATE_SCORES[scoring], _ptr(bias), n_group, topk_group, int(renormalize), float(scale),
             _ptr(topk_ids), _ptr(topk_w), _stream(stream)), "w8a8_moe_gate")
     return topk_ids, topk_w

@@ -285,3 +285,17 @@ def test_group_sums_of_large_opposite_keys(size, E, n_group, topk_group, scoring
     b[:, per // 2], b[:, 1] = up, 0.25 - up
     x, b = x.view(T, E).to(DEV), b.view(E).to(DEV)
     check(x, 2 * topk_group, scoring=scoring, bias=b, n_group=n_group, topk_group=topk_group)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_one_token_has_no_row_stride(dtype):
+    x = logits(64, 1, 3, dtype).t()
+    assert x.shape == (1, 64) and x.stride() == (1, 1)
+    check(x, 8)
+    check(logits(64, 1, 3, dtype).t()[:, :40], 8, scoring="sigmoid", bias=bias_of(40, 1))
+
+
+def test_one_expert_has_no_column_stride():
+    x = logits(2, 7, 3).t()[:, 1:]
+    assert x.shape == (7, 1) and x.stride() == (1, 7)
+    check(x, 1, scoring="sigmoid")

@@ -457,3 +457,24 @@ def test_large_value_vectors_cost_their_own_tiles(n, ctx, every, power):
     b.kc[..., 1] = 0
     b.kc[pg, :, off, 1] = -127
     check_by_tile(b, b.run())
+
+
+@pytest.mark.parametrize("int8", KINDS)
+@pytest.mark.parametrize("shape,strides", [((1, 8, D), (3, D, 1)), ((5, 1, D), (D, 1, 1)),
+                                           ((1, 1, D), (1, 2, 1)), ((40, 1, D), (2 * D, 7, 1))])
+def test_dimensions_of_one_have_no_stride(shape, strides, int8):
+    T, H = shape[:2]
+    b = Batch([T], [100], H, H, 16, int8, seed=24)
+    want = b.run()
+    rows = torch.zeros(T, 2 * H, D, dtype=torch.bfloat16, device=DEV)
+    rows = rows.view(-1)
+    view = rows.as_strided(shape, strides)
+    view.copy_(b.q)
+    b.q = view
+    assert b.q.stride() == strides and torch.equal(b.run(), want)
+    slots = torch.arange(T, dtype=torch.int32, device=DEV)
+    for k in (view, view.contiguous()):
+        kc = torch.zeros(T, H, 16, D, dtype=torch.bfloat16, device=DEV)
+        vc = torch.zeros_like(kc)
+        w8.paged_kv_write(k, k, slots, kc, vc)
+        assert torch.equal(kc.transpose(1, 2).reshape(-1, H, D)[:T], view) and torch.equal(kc, vc)
