@@ -299,6 +299,7 @@ attn_decode_kernel(const uint16_t *__restrict__ q, const void *__restrict__ kc,
 #pragma unroll
             for (int k = 0; k < 4; ++k) st.o[i][nt][k] = 0.0f;
     st.se = 0;
+    st.low = 100;
 
     for (int cc = c_begin; cc < c_end; ++cc) {
         cp_async_wait_group<1>();   // this chunk's group has landed (the next may be in flight)

@@ -98,7 +98,7 @@ struct WarpState {
     float m[NT][2];
     float l[NT][2];
     float o[8][NT][4];
-    int se;
+    int se, low;    // low: the smallest se so far (its start: 100)
 };
 
 // One chunk into the warp's running state (online softmax: the state is
@@ -192,10 +192,14 @@ __device__ __forceinline__ void attend_chunk(WarpState<NT> &st, ChunkRegs<kInt8>
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xFFFFFFFFu, vmax, o));
         const int bexp = static_cast<int>((__float_as_uint(vmax) >> 23) & 0xFFu);
-        if (bexp != 0) se = max(-100, min(100, 14 - (bexp - 127)));
+        // (at most 2^60 finer than the coarsest unit so far: the FP32 sums in it stay finite)
+        if (bexp != 0) se = max(-100, min(min(100, st.low + 60), 14 - (bexp - 127)));
+        st.low = min(st.low, se);
     }
-    // rescale the state's output: exp(m_old - m_new) and the change of units
-    const float ratio = __uint_as_float(static_cast<uint32_t>(se - st.se + 127) << 23);
+    // rescale the state's output: exp(m_old - m_new) and the change of units (at most
+    // 2^100 finer, from the start's; coarser by more than binary32 has: nothing is left)
+    const float ratio =
+        se - st.se < -126 ? 0.0f : __uint_as_float(static_cast<uint32_t>(se - st.se + 127) << 23);
     st.se = se;
 #pragma unroll
     for (int i = 0; i < 8; ++i)

@@ -265,6 +265,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant_
 #pragma unroll
                 for (int k = 0; k < 4; ++k) st.o[i][nt][k] = 0.0f;
         st.se = 0;
+        st.low = 100;
         if (p.first < p.last) {
             // q rows 8 nt + gid, dims [32 t, 32 t + 32), as bf16 pairs
             uint32_t qf[NT][16];

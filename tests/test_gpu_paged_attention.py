@@ -478,3 +478,25 @@ def test_dimensions_of_one_have_no_stride(shape, strides, int8):
         vc = torch.zeros_like(kc)
         w8.paged_kv_write(k, k, slots, kc, vc)
         assert torch.equal(kc.transpose(1, 2).reshape(-1, H, D)[:T], view) and torch.equal(kc, vc)
+
+
+@pytest.mark.parametrize("n", [1, 70])
+@pytest.mark.parametrize("first", [0, 1])
+def test_scales_at_both_ends_of_binary32(first, n):
+    # (tiles in turn; the weights' unit changes by 2^130 between them)
+    b = Batch([n], [900], 4, 1, 32, True, seed=25)
+    pos = torch.arange(b.kv[0], device=DEV)
+    pg, off = b.table[0].long()[pos // 32], pos % 32
+    far = torch.where(pos // 128 % 2 == first, 50.0, -100.0)
+    b.vs[pg, :, off] *= torch.exp2(far)[:, None]
+    b.check(b.run(), split=n == 1)
+
+
+def test_scales_at_both_ends_in_the_contiguous_cache():
+    b = Batch([1], [900], 4, 1, 1024, True, seed=25, spare=0)
+    far = torch.where(torch.arange(1024, device=DEV) // 128 % 2 == 0, 50.0, -100.0)
+    b.vs *= torch.exp2(far)
+    lens = torch.tensor([901], dtype=torch.int32, device=DEV)
+    out = w8.attention_decode(b.q, b.kc, b.vc, lens, SCALE, k_scale=b.ks, v_scale=b.vs,
+                              out_dtype=torch.float32)
+    b.check(out, split=True)
