@@ -135,7 +135,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 // paid on every step. Costs issue slots while it waits.
 __device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity, volatile int *abort,
                                                unsigned long long *err, unsigned role,
-                                               unsigned site, unsigned kid = KID_GEMM) {
+                                               unsigned site) {
     if (mbar_test_wait(bar, parity)) return true;
     const unsigned long long t0 = globaltimer_ns();
     for (uint32_t i = 1;; ++i) {
@@ -144,7 +144,7 @@ __device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity, vo
             if (*abort) return false;
             if (globaltimer_ns() - t0 > kWaitLimitNs) {
                 *abort = 1;
-                record_device_error(err, kid, role, site);
+                record_device_error(err, KID_GEMM, role, site);
                 return false;
             }
         }
