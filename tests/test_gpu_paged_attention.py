@@ -500,3 +500,71 @@ def test_scales_at_both_ends_in_the_contiguous_cache():
     out = w8.attention_decode(b.q, b.kc, b.vc, lens, SCALE, k_scale=b.ks, v_scale=b.vs,
                               out_dtype=torch.float32)
     b.check(out, split=True)
+
+
+@pytest.mark.parametrize("int8", KINDS)
+@pytest.mark.parametrize("window", [1, 31, 100, 128, 129, 1000])
+@pytest.mark.parametrize("n_new", [[1, 1, 1, 1], [2, 1, 3, 4]])
+def test_few_rows_with_a_window(n_new, window, int8):
+    b = Batch(n_new, [0, 130, 900, 2000], 8, 2, 16, int8, seed=26)
+    whole = b.run(window=window)
+    b.check(whole, window=window, split=True)
+    # pages before every new token's window may be gone, and hold anything
+    for r, (c, n) in enumerate(zip(b.ctx, n_new)):
+        first = max(0, c - window + 1) // 16
+        where = torch.zeros(b.P, 16, dtype=torch.bool, device=DEV)
+        where[b.table[r, :first].long()] = True
+        b.poison(where)
+        b.table[r, :first] = -1
+    w8.device_error()
+    assert torch.equal(b.run(window=window), whole) and w8.device_error() == 0
+
+
+@pytest.mark.parametrize("int8", KINDS)
+def test_few_rows_that_see_nothing(int8):
+    # refused requests (no positions) and tokens before position 0 in a decode step
+    b = Batch([1, 1, 3, 1, 2], [50, 0, 0, 700, 0], 8, 2, 16, int8, seed=27)
+    b.kv = [51, 0, 0, 701, 1]
+    b.kv_lens = torch.tensor(b.kv, dtype=torch.int32, device=DEV)
+    b.q = torch.cat([b.q, b.q[:1]])
+    out = torch.full((9, 8, D), math.nan, device=DEV)
+    b.run(out=out)
+    assert bool((out[1:5] == 0).all()) and bool((out[6] == 0).all()) and bool((out[8] == 0).all())
+    b.check(out, split=True)
+
+
+@pytest.mark.parametrize("int8", KINDS)
+@pytest.mark.parametrize("qt,qh", [(80, 8), (8, 128), (1024, 64), (0, 128)])
+def test_rows_of_q_that_overlap(qt, qh, int8):
+    # strides below a row's length take the few-rows kernel at any number of rows
+    b = Batch([90, 1, 40], [10, 300, 0], 8, 2, 16, int8, seed=28)
+    T = b.q.shape[0]
+    g = torch.Generator(device=DEV).manual_seed(5)
+    store = torch.randn(T * 1024 + 2048, generator=g, device=DEV).to(torch.bfloat16)
+    b.q = store.as_strided((T, 8, D), (qt, qh, 1))
+    b.check(b.run(), split=True)
+
+
+def test_few_rows_with_scales_of_very_different_size():
+    b = Batch([1], [400], 8, 2, 32, True, seed=13)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    b.vs *= torch.exp2(torch.randint(-30, 10, b.vs.shape, generator=g, device=DEV).float())
+    b.poison(torch.zeros(b.P, 32, dtype=torch.bool, device=DEV))
+    b.check(b.run(), split=True)
+
+
+@pytest.mark.parametrize("int8", KINDS)
+def test_many_requests_keep_all_bits(int8):
+    g = torch.Generator().manual_seed(3)
+    n = torch.randint(0, 4, (600,), generator=g).tolist()
+    c = torch.randint(0, 90, (600,), generator=g).tolist()
+    b = Batch(n, c, 4, 2, 16, int8, seed=15)
+    b.check(b.run(), split=True)
+
+
+@pytest.mark.parametrize("int8", KINDS)
+@pytest.mark.parametrize("page", [8, 24, 48, 128, 256])
+@pytest.mark.parametrize("window", [0, 100])
+def test_many_rows_over_pages_of_other_sizes(window, page, int8):
+    b = Batch([70, 1, 150], [500, 130, 0], 14, 2, page, int8, seed=29)
+    b.check(b.run(window=window), window=window)

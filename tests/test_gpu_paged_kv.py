@@ -275,3 +275,40 @@ def test_plan_then_write_in_a_graph():
         assert torch.equal(flat[slots.long()], k)
     held = sorted(t for t in table.flatten().tolist() if t >= 0)
     assert sorted(held + free[:int(n_free)].tolist()) == list(range(P))
+
+
+@pytest.mark.parametrize("int8", [True, False])
+@pytest.mark.parametrize("T,Hkv,page", [(8192, 5, 16), (16385, 2, 24), (32768, 1, 64), (4096, 8, 128),
+                                        (5000, 7, 8)])
+def test_write_of_long_prompts(T, Hkv, page, int8):
+    # several heads per warp, their last ones fewer; some tokens without a slot
+    g = torch.Generator(device=DEV).manual_seed(T + Hkv)
+    qkv = (torch.randn(T, 2 * Hkv + 3, D, generator=g, device=DEV) * 3).to(torch.bfloat16)
+    qkv[5] = 0
+    qkv[6] *= 1e-38
+    k, v = qkv[:, 1:1 + Hkv], qkv[:, 2 + Hkv:2 + 2 * Hkv]
+    P = T // page + 5
+    slots = torch.randperm(P * page, generator=g, device=DEV)[:T].to(torch.int32)
+    slots[3::97] = -1
+    slots[4::89] = P * page
+    dt = torch.int8 if int8 else torch.bfloat16
+    kc = torch.full((P, Hkv, page, D), 7, dtype=dt, device=DEV)
+    vc = torch.full_like(kc, 9)
+    ks = torch.full((P, Hkv, page), -1.0, device=DEV) if int8 else None
+    vs = torch.full((P, Hkv, page), -2.0, device=DEV) if int8 else None
+    w8.paged_kv_write(k, v, slots, kc, vc, k_scale=ks, v_scale=vs)
+    has = (slots >= 0) & (slots < P * page)
+    at = slots[has].long()
+    for x, cache, scales, fill, sfill in ((k, kc, ks, 7, -1.0), (v, vc, vs, 9, -2.0)):
+        got = cache.transpose(1, 2).reshape(P * page, Hkv, D)
+        want = torch.full_like(got, fill)
+        if int8:
+            codes, s = _definition(x[has])
+            want[at] = torch.from_numpy(codes).to(DEV)
+            sw = torch.full((P * page, Hkv), sfill, device=DEV)
+            sw[at] = torch.from_numpy(s).to(DEV)
+            assert torch.equal(scales.transpose(1, 2).reshape(P * page, Hkv), sw)
+            assert torch.equal(got, want)
+        else:
+            want[at] = x[has]
+            assert torch.equal(got.view(torch.int16), want.view(torch.int16))
