@@ -169,13 +169,10 @@ __device__ __forceinline__ void top2_merge(R &a1, R &a2, R b1, R b2) {
 }
 
 // Which groups stay (bit g of kept), from their scores (lane l: groups l and l +
-// 32). size: the sum of the magnitudes of the keys that make up a score (they may
-// cancel: a score's error goes by them, not by itself). Returns false when scores off by
-// tol / 2 each, relative to 1 and to their size, may change which groups stay.
+// 32).
 template <typename R>
-__device__ __forceinline__ bool rank_groups(const R (&gs)[2], const R (&size)[2], const GateArgs &a,
-                                            int lane, R tol, unsigned (&kept)[2]) {
-    const R none = -INFINITY;
+__device__ __forceinline__ void rank_groups(const R (&gs)[2], const GateArgs &a, int lane,
+                                            unsigned (&kept)[2]) {
     // rank of each group: those with a larger score, or an equal one and a lower index
     int rank[2] = {0, 0};
     if (a.n_group <= 32) {
@@ -191,43 +188,46 @@ __device__ __forceinline__ bool rank_groups(const R (&gs)[2], const R (&size)[2]
                 rank[h] += (s > gs[h] || (s == gs[h] && g < lane + 32 * h)) ? 1 : 0;
         }
     }
-    bool clear = true;
-    R worst_in = INFINITY, best_out = none;   // at their worst
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const bool exists = lane + 32 * h < a.n_group;
-        const bool in = exists && rank[h] < a.topk_group;
-        kept[h] = __ballot_sync(kFull, in);
-        const R err = R(0.5) * tol * fmax(R(1), size[h]);
-        const bool known = size[h] < R(INFINITY);   // (else a sum may have overflowed)
-        if (in) worst_in = fmin(worst_in, known ? gs[h] - err : none);
-        if (exists && !in) best_out = fmax(best_out, known ? gs[h] + err : R(INFINITY));
-    }
-    if (tol > R(0)) {
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            worst_in = fmin(worst_in, __shfl_xor_sync(kFull, worst_in, o));
-            best_out = fmax(best_out, __shfl_xor_sync(kFull, best_out, o));
-        }
-        // (which of the unavailable groups stay, all -inf, does not matter)
-        clear = worst_in > best_out || best_out == none;
-    }
-    return clear;
+    for (int h = 0; h < 2; ++h)
+        kept[h] = __ballot_sync(kFull, lane + 32 * h < a.n_group && rank[h] < a.topk_group);
 }
 
+// The last group kept and the first one left out, over the groups of all lanes, each
+// score at its worst: off by tol / 2, relative to 1 and to the sum of the
+// magnitudes of the keys in it (they may cancel: the error goes by them, not by the score).
+struct GroupBorder {
+    float in = INFINITY, out = -INFINITY;
+    __device__ __forceinline__ void add(bool stays, float score, float size, float tol) {
+        const float err = 0.5f * tol * fmaxf(1.0f, size);
+        const bool known = size < INFINITY;     // (else a sum may have overflowed)
+        if (stays) in = fminf(in, known ? score - err : -INFINITY);
+        else out = fmaxf(out, known ? score + err : INFINITY);
+    }
+    // (which of the unavailable groups stay, all -inf, does not matter)
+    __device__ __forceinline__ bool clear() const {
+        const uint32_t worst_in = __reduce_min_sync(kFull, ord(in));
+        const uint32_t best_out = __reduce_max_sync(kFull, ord(out));
+        return worst_in > best_out || best_out == ord(-INFINITY);
+    }
+};
+
 // Marks the experts outside the topk_group best groups as not available
-// (kr = -inf there). tol, and what is returned: as above.
+// (kr = -inf there). Returns false when errors within tol (GroupBorder; 0: none) may
+// change which those are.
 template <typename R, int V>
 __device__ __forceinline__ bool keep_groups(R (&kr)[V], const GateArgs &a, int lane, bool sum2,
                                             R tol) {
     const int size = a.size;
     const R none = -INFINITY;
     R gs[2] = {none, none};   // lane l: the scores of groups l and l + 32
-    R sizes[2] = {0, 0};      // and the magnitudes in them
+    [[maybe_unused]] float size_of[2] = {0.0f, 0.0f};   // and the magnitudes in them
     auto magnitude = [&](R m1, R m2) {
-        return m1 > none ? fabs(m1) + (sum2 && m2 > none ? fabs(m2) : R(0)) : R(0);
+        return m1 > none ? static_cast<float>(fabs(m1) + (sum2 && m2 > none ? fabs(m2) : R(0))) : 0.0f;
     };
     const int run = 1 << max(a.run_shift, 0);
+    GroupBorder border;
+    unsigned kept[2];
     if (a.run_shift >= 0) {
         // a group is a run of a power of two lanes: every group at once
         R m1 = none, m2 = none;
@@ -240,41 +240,53 @@ __device__ __forceinline__ bool keep_groups(R (&kr)[V], const GateArgs &a, int l
             top2_merge<R>(m1, m2, __shfl_xor_sync(kFull, m1, o), __shfl_xor_sync(kFull, m2, o));
         const R s = sum2 && m2 > none ? m1 + m2 : m1;
         gs[0] = __shfl_sync(kFull, s, (lane * run) & 31);
-        if (tol > R(0)) sizes[0] = __shfl_sync(kFull, magnitude(m1, m2), (lane * run) & 31);
         if (lane >= a.n_group) gs[0] = none;
-    } else {
-        for (int g = 0; g < a.n_group; ++g) {
-            R m1 = none, m2 = none;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int e = lane * V + i;
-                top2_merge<R>(m1, m2, e >= g * size && e < (g + 1) * size ? kr[i] : none, none);
-            }
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1)
-                top2_merge<R>(m1, m2, __shfl_xor_sync(kFull, m1, o), __shfl_xor_sync(kFull, m2, o));
-            const R s = sum2 && m2 > none ? m1 + m2 : m1;
-            if (lane == (g & 31)) {
-                if (g < 32) gs[0] = s;
-                else gs[1] = s;
-                if (tol > R(0)) sizes[g < 32 ? 0 : 1] = magnitude(m1, m2);
-            }
-        }
-    }
-    unsigned kept[2];
-    const bool clear = rank_groups<R>(gs, sizes, a, lane, tol, kept);
-    if (a.run_shift >= 0) {
+        rank_groups<R>(gs, a, lane, kept);
         const bool stays = (kept[0] >> (lane >> a.run_shift)) & 1u;
 #pragma unroll
         for (int i = 0; i < V; ++i) kr[i] = stays ? kr[i] : none;
-        return clear;
+        if constexpr (sizeof(R) == 4) {
+            if (tol > R(0)) {
+                if ((lane >> a.run_shift) < a.n_group) border.add(stays, s, magnitude(m1, m2), tol);
+                return border.clear();
+            }
+        }
+        return true;
     }
+    for (int g = 0; g < a.n_group; ++g) {
+        R m1 = none, m2 = none;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = lane * V + i;
+            top2_merge<R>(m1, m2, e >= g * size && e < (g + 1) * size ? kr[i] : none, none);
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1)
+            top2_merge<R>(m1, m2, __shfl_xor_sync(kFull, m1, o), __shfl_xor_sync(kFull, m2, o));
+        const R s = sum2 && m2 > none ? m1 + m2 : m1;
+        if (lane == (g & 31)) {
+            if (g < 32) gs[0] = s;
+            else gs[1] = s;
+            if (g < 32) size_of[0] = magnitude(m1, m2);
+            else size_of[1] = magnitude(m1, m2);
+        }
+    }
+    rank_groups<R>(gs, a, lane, kept);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int g = min((lane * V + i) / size, 63);
         if (!((kept[g >> 5] >> (g & 31)) & 1u)) kr[i] = none;
     }
-    return clear;
+    if constexpr (sizeof(R) == 4) {
+        if (tol > R(0)) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (lane + 32 * h < a.n_group)
+                    border.add((kept[h] >> lane) & 1u, gs[h], size_of[h], tol);
+            return border.clear();
+        }
+    }
+    return true;
 }
 
 // Picks the k largest of the available keys (kr > -inf). Returns false when
