@@ -148,6 +148,11 @@ __device__ __forceinline__ uint32_t finite_bits2(uint32_t bf16_pair) {
     const uint32_t m = bf16_pair & 0x7FFF7FFFu;
     return m & ~__vcmpgeu2(m, 0x7F807F80u);
 }
+__device__ __forceinline__ uint32_t finite_amax8(const uint4 &v) {
+    const uint32_t m = __vmaxu2(__vmaxu2(finite_bits2(v.x), finite_bits2(v.y)),
+                                __vmaxu2(finite_bits2(v.z), finite_bits2(v.w)));
+    return max(m & 0xFFFFu, m >> 16);
+}
 
 // The attention kernels work in log2 units.
 constexpr float kLog2e = 1.4426950408889634f;

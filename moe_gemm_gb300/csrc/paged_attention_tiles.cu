@@ -434,8 +434,8 @@ __device__ __forceinline__ HalfTiles half_tiles(const PagedSchedule &s, const Ti
 
 // The rows of a half that are the item's: the copy of q always brings half_tokens
 // tokens, and in a request's last item those after its own are another request's, or
-// nobody's, and may hold anything. They take no part in what rows decide together (the
-// scaling of INT8 pages' q, when references move).
+// nobody's, and may hold anything. They become zeros, so that what rows decide together
+// (the scaling of INT8 pages' q, when references move) does not depend on them.
 __device__ __forceinline__ int own_rows(const TilePiece &p, int half, int half_tokens, int G) {
     return min(p.ntok - half * half_tokens, half_tokens) * G;
 }
@@ -546,11 +546,9 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
             }
             float m[4], l[4];
             int pos[4];
-            bool own[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                own[k] = r4 + 8 * k < own_rows(p, h, a.half_tokens, a.o.G);
-                m[k] = own[k] ? -INFINITY : 0.0f;   // (a reference that needs no first maximum)
+                m[k] = -INFINITY;
                 l[k] = 0.0f;
                 pos[k] = t.first + tok4[k];
             }
@@ -634,10 +632,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                         if (masked) weigh<kInt8, true>(tse, col, a.scale_log2, nm, mk, pk, sum);
                         else weigh<kInt8, false>(tse, col, a.scale_log2, nm, mk, pk, sum);
                         if (again) break;
-                        float most = 0.0f;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) most = fmaxf(most, own[k] ? sum[k] : 0.0f);
-                        move = !(most <= kMaxWeight);
+                        move = !(fmaxf(fmaxf(sum[0], sum[1]), fmaxf(sum[2], sum[3])) <= kMaxWeight);
                         if (!__any_sync(0xFFFFFFFFu, move)) break;
                     }
                     if (turn != 1.0f) {
@@ -846,6 +841,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
             // ---------------------------------------------------------- the loads
             bool ok = true;
             uint32_t u = 0, fixes = 0;   // operand tiles, V tiles made zero in places
+            uint32_t lands[2] = {0, 0};  // q's halves with rows to be made zero
             TilePiece p;
             while (take(p, ok, ROLE_PRODUCER)) {
                 if (p.last <= p.first) continue;
@@ -915,8 +911,11 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                                                                     KID_ATTN));
                                 if (!ok) break;
                                 ++qn[h];
+                                // (INT8: the converters do what spare rows need)
+                                const bool spare = !kInt8 && own_rows(p, h, a.half_tokens, a.o.G) <
+                                                                 a.half_tokens * a.o.G;
                                 if (lane == 0) {
-                                    const uint32_t qb = bar(kInt8 ? sm.q_land[h] : sm.q_full[h]);
+                                    const uint32_t qb = bar(kInt8 || spare ? sm.q_land[h] : sm.q_full[h]);
                                     mbar_arrive_expect_tx(qb, a.half_tokens * a.o.G * kHeadDim * 2);
 #pragma unroll
                                     for (int d = 0; d < 2; ++d)
@@ -925,6 +924,17 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                                                     p.t0 + p.tok0 + h * a.half_tokens, qb);
                                 }
                                 __syncwarp();
+                                if (spare) {
+                                    ok = __all_sync(0xFFFFFFFFu,
+                                                    mbar_wait(bar(sm.q_land[h]), lands[h]++ & 1, abort, a.err,
+                                                              ROLE_PRODUCER, 6, kWaitLimitNs, KID_ATTN));
+                                    for (int i = own_rows(p, h, a.half_tokens, a.o.G) * 16 + lane;
+                                         i < a.half_tokens * a.o.G * 16; i += 32)
+                                        *q_piece(sm.q[h], i >> 4, i & 15) = make_uint4(0, 0, 0, 0);
+                                    fence_proxy_async_smem();
+                                    __syncwarp();
+                                    if (lane == 0) mbar_arrive(bar(sm.q_full[h]));
+                                }
                             }
                         }
                     }
@@ -936,10 +946,14 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                 for (uint32_t x = u > kSlots ? u - kSlots : 0; x < u; ++x)
                     mbar_wait(bar(kInt8 ? sm.raw_full[x % kSlots] : sm.op_full[x % kSlots]),
                               (x / kSlots) & 1, &never, a.err, ROLE_PRODUCER, 4, kWaitLimitNs, KID_ATTN);
-                for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < 2; ++h) {
                     if (qn[h] > 0)
                         mbar_wait(bar(kInt8 ? sm.q_land[h] : sm.q_full[h]), (qn[h] - 1) & 1, &never,
                                   a.err, ROLE_PRODUCER, 5, kWaitLimitNs, KID_ATTN);
+                    if (lands[h] > 0)
+                        mbar_wait(bar(sm.q_land[h]), (lands[h] - 1) & 1, &never, a.err,
+                                  ROLE_PRODUCER, 7, kWaitLimitNs, KID_ATTN);
+                }
             }
         } else if (warp == 11 && mine) {
             // --------------------------------------------------------- the pieces
@@ -1053,8 +1067,9 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                         }
                         if (x == p.first) {
                             // the item's q to fp16, a row of each half per thread, scaled
-                            // so that the largest value lies in [2^14, 2^15); rows that are
-                            // not its own become zeros
+                            // so that the largest value lies in [2^14, 2^15). (Once per item,
+                            // so kept small: unrolled, its instructions pushed the tiles' out
+                            // of the cache: 2.04 -> 2.11 ms for the long chunk.)
                             const int halves = a.half_tokens < p.ntok ? 2 : 1;
                             uint32_t mq = 0;
                             for (int h = 0; h < halves; ++h) {
@@ -1062,15 +1077,21 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                                                 ok && mbar_wait(bar(sm.q_land[h]), qn[h] & 1, abort, a.err,
                                                                 ROLE_CONVERT, 3, kWaitLimitNs, KID_ATTN));
                                 ++qn[h];
-                                if (ct < own_rows(p, h, a.half_tokens, a.o.G))
+                                if (ct >= own_rows(p, h, a.half_tokens, a.o.G))
+#pragma unroll 1
+                                    for (int j = 0; j < 16; ++j)
+                                        *q_piece(sm.q[h], ct, j) = make_uint4(0, 0, 0, 0);
 #pragma unroll 4
-                                    for (int j = 0; j < 16; ++j) {
-                                        const uint4 y = *q_piece(sm.q[h], ct, j);
-                                        mq = __vmaxu2(__vmaxu2(mq, finite_bits2(y.x)), finite_bits2(y.y));
-                                        mq = __vmaxu2(__vmaxu2(mq, finite_bits2(y.z)), finite_bits2(y.w));
-                                    }
+                                for (int j = 0; j < 16; ++j)
+                                    mq = max(mq, amax_bits8(*q_piece(sm.q[h], ct, j)));
                             }
-                            mq = __reduce_max_sync(0xFFFFFFFFu, max(mq & 0xFFFFu, mq >> 16));
+                            if (mq >= 0x7F80u) {    // no finite number: those that are
+                                mq = 0;
+#pragma unroll 1
+                                for (int j = 0; j < 16 * halves; ++j)
+                                    mq = max(mq, finite_amax8(*q_piece(sm.q[j >> 4], ct, j & 15)));
+                            }
+                            mq = __reduce_max_sync(0xFFFFFFFFu, mq);
                             if (lane == 0) sm.qmax[cw] = mq;
                             __syncwarp();
                             mbar_arrive(bar(sm.q_max));
@@ -1085,10 +1106,9 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                             const float qs = __uint_as_float(static_cast<uint32_t>(se + 127) << 23);
                             unscale = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - se) << 23);
                             for (int h = 0; h < halves; ++h) {
-                                const bool own = ct < own_rows(p, h, a.half_tokens, a.o.G);
-#pragma unroll 4
+#pragma unroll 1
                                 for (int j = 0; j < 16; ++j) {
-                                    uint4 y = own ? *q_piece(sm.q[h], ct, j) : make_uint4(0, 0, 0, 0);
+                                    uint4 y = *q_piece(sm.q[h], ct, j);
                                     y.x = pack_f16x2(__uint_as_float(y.x << 16) * qs, __uint_as_float(y.x & 0xFFFF0000u) * qs);
                                     y.y = pack_f16x2(__uint_as_float(y.y << 16) * qs, __uint_as_float(y.y & 0xFFFF0000u) * qs);
                                     y.z = pack_f16x2(__uint_as_float(y.z << 16) * qs, __uint_as_float(y.z & 0xFFFF0000u) * qs);
@@ -1116,8 +1136,10 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant
                         // stay below 1/8 (not more than 2^60 below the item's largest unit:
                         // O is FP32; a tile of zero vectors needs none)
                         const int te = max(-100, min(100, static_cast<int>(wm >> 23) - 127));
-                        if (te >= e + 4 || (te <= e - 4 && wm != 0)) e = max(te, top - 60);
-                        top = max(top, e);
+                        if (static_cast<unsigned>(te - e + 3) > 6u && wm != 0) {
+                            e = max(te, top - 60);
+                            top = max(top, e);
+                        }
                         const float un = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
                         const float ui = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
                         float *c4 = reinterpret_cast<float *>(&sm.col[info][ct >> 1]) + (ct & 1);
