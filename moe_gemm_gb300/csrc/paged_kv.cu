@@ -182,7 +182,10 @@ paged_kv_plan_kernel(const PlanArgs a) {
         for (int j = lane; j < n; j += 32) row[j] = a.free_pages[itop - 1 - (e.first + j)];
     }
     // a slot and a position for every new token
-    for (int t = rank * kPlanThreads + tid; t < a.n_tokens; t += ranks * kPlanThreads) {
+    // (counted without a sign: the last step passes 2^31 when n_tokens is near it)
+    for (unsigned n = rank * kPlanThreads + tid; n < static_cast<unsigned>(a.n_tokens);
+         n += ranks * kPlanThreads) {
+        const int t = static_cast<int>(n);
         int slot = -1, pos = -1;
         if (t < n_asked) {
             int lo = 0, hi = a.B;   // the last request with cu <= t

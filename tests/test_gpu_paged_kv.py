@@ -312,3 +312,18 @@ def test_write_of_long_prompts(T, Hkv, page, int8):
         else:
             want[at] = x[has]
             assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+
+
+def test_plan_with_room_for_the_most_tokens():
+    n = (1 << 31) - 1
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    one = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    table, lens = torch.full((1, 4), -1, dtype=torch.int32, device=DEV), one(0)
+    cu, kv, slots, pos = w8.paged_kv_plan(table, lens, one(20), one(2, 0, 1), one(3), 16, n)
+    assert cu.tolist() == [0, 20] and kv.tolist() == [20] and table.tolist() == [[1, 0, -1, -1]]
+    assert slots[:20].tolist() == [16 + i for i in range(16)] + [0, 1, 2, 3]
+    assert pos[:20].tolist() == list(range(20))
+    assert slots.shape == pos.shape == (n,)
+    assert int(slots[20:].max()) == int(slots[20:].min()) == -1
+    assert int(pos[20:].max()) == int(pos[20:].min()) == -1
