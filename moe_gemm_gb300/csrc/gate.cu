@@ -25,8 +25,9 @@
 //    logits) is decided again with scores in 64 bits.
 //
 // What bounds it: instructions. 16384 x 256 FP32 logits, sigmoid with a bias, 4 of 8
-// groups, top 8, take 21.8 us (0.8 TB/s; the copy of its bytes takes 2.6), 15 without
-// the tokens decided again, of which one that starts late ends the call. Rows
+// groups, top 8, take 21.6 us (0.8 TB/s; the copy of its bytes takes 2.6), 15 without
+// the tokens decided again, of which one that starts late ends the call. Softmax with a
+// bias takes 35 (30 without groups): its close tokens take all experts' scores in 64 bits. Rows
 // that a persistent warp reads ahead took 8 us more (the registers halve the warps of an
 // SM), the 64-bit part out of line 3.
 #include <cuda_bf16.h>

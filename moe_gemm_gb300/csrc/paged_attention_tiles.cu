@@ -17,7 +17,8 @@
 // The reference m of the exponentials p_j = 2^(t_j - m) (t: scores in log2 units)
 // is a maximum that was seen, not the running one: it stays while the tile's
 // sums show that no weight passes 2^8, so most tiles take no maximum at all, and
-// O is rescaled a few times per item instead of at every tile. Weights above 1
+// O is rescaled a few times per item instead of at every tile (rescaling only past a
+// threshold is a published method for attention on this generation). Weights above 1
 // cost no accuracy. Sums and statistics are FP32.
 //
 // BF16 pages: P is rounded to BF16 for the product (half a step 2^-8 of each
@@ -38,14 +39,15 @@
 // took longer than the products).
 //
 // What bounds it. BF16 pages: eight prompts of up to 8192 tokens (1.45e12 operations)
-// take 1.11 ms, 1.31 PFLOP/s, 2.0 us per tile and SM, of which the products are 1.3 (an
+// take 1.12 ms, 1.29 PFLOP/s, and 1.17 after half a second of such calls, when the power
+// limit holds the SMs at 1.97 GHz instead of 2.07: 2.0 us per tile and SM, of which the products are 1.3 (an
 // S of 64 columns reads as many bytes of Q as one of 128, 48 cycles for 32); the
 // rest is what a half waits for the hand-over between its softmax and its products, and
 // some 5 us per item for its start and end. With the scores in one part of 128 columns
 // the softmax waited for whole products: 1.44 ms. INT8 pages: 2048 tokens over 30001
 // positions and eight single tokens (2.08e12) take 2.01 ms, 1.04 PFLOP/s; without the
 // widening of codes they would take 1.87, without the scales' part of the softmax as
-// well 1.69, the time of BF16 pages.
+// well 1.69. BF16 pages of the same call take 1.47.
 //
 // A wait that gives up is voted on by the warp: its lanes go on to votes and shuffles
 // of all of them, so they must leave together.
@@ -109,9 +111,10 @@ constexpr int kTakers = 15;             // warps that take them
 
 // A tile's scores come in two halves of 64 columns, so that one is ready while the
 // softmax is at the other (packed prompts of 16 thousand tokens, BF16: 1.44 -> 1.17
-// ms). INT8 gains nothing by it (a chunk over 30001 positions takes 2.1 ms either
-// way): there the bandwidth of shared memory is the bound, some 250 KB of operands, 100
-// of conversion and 130 of scales a tile, at 128 bytes a cycle.
+// ms). INT8 neither gains nor loses by it (a chunk over 30001 positions takes 2.1 ms
+// either way) and has it for the one form of the products. A tile moves some 250 KB of
+// operands, 100 of conversion and 130 of scales through shared memory there; leaving
+// out the latter two saves 16 %, so its bandwidth alone is not the bound.
 constexpr int kN = 2, kCols = kTilePositions / kN;
 
 template <bool kInt8>

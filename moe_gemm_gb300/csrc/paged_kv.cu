@@ -11,7 +11,8 @@
 // The plan is bound by latency: a chain of loads, three scans and the stores, 4.8 us
 // for 32 requests and 6.2 for 1021 requests with 8.6 thousand new tokens, which eight
 // CTAs of a cluster share. So is the write at decode sizes (2.3 us for 32 tokens); the
-// write of 8192 tokens' 8 heads takes 14.4 us (51 MB: 3.5 TB/s), bound by instructions.
+// INT8 write of 8192 tokens' 8 heads takes 14.5 us (51 MB: 3.5 TB/s) and waits for its
+// loads: 26 warps per SM use 44 % of the issue slots, and the first stall is for memory.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -226,10 +227,10 @@ struct WriteArgs {
 // 16-31 the V vectors, 8 values (16 bytes) of each, all of them loaded before the
 // first is worked on (and beside the slot). The INT8 form takes a vector's amax by
 // four shuffles, the scale by one division, and rounds x / scale as the activation
-// quantizer does. Instruction issue bounds a long call before memory does, so what a
-// vector costs beside its values is shared: 8192 tokens of 8 heads take 19.2 us
-// with H = 1, 14.4 with 4 and 16.4 with 8. A decode step has no instructions to
-// save, but warps to fill: 32 tokens take 2.3 us with H = 1, 3.7 with 4.
+// quantizer does. A long call takes several heads per warp, for more loads in flight
+// and one look at the slot: 8192 tokens of 8 heads take 19.2 us
+// with H = 1, 14.5 with 4 and 16.4 with 8 (whose registers cost warps). A decode step
+// has warps to fill: 32 tokens take 2.3 us with H = 1, 3.7 with 4.
 template <bool kInt8, int H>
 __global__ void __launch_bounds__(kWriteThreads)
 paged_kv_write_kernel(const WriteArgs a) {
