@@ -178,28 +178,35 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant_
     bool ok = true;
     const int box_shift = __ffs(a.c.box) - 1;
 
-    // The block-table entry of the lane's box of the warp's part of tile x (of the
-    // request's tiles), -2 when the box holds no key. Asked for one tile ahead of
-    // the copies: the answer takes as long as a tile.
-    auto lookup = [&](const PagedWalk &w, int x) -> int {
+    // Where the boxes of the warp's part of the tiles from x on (of the request's, before
+    // end) lie in the cache, through the block table: 2^box_shift tiles at a time, lane l
+    // has box l % boxes of tile x + l / boxes (its first row; -1: not loaded).
+    const int boxes_log2 = 5 - box_shift;
+    auto find = [&](const PagedWalk &w, int x, int end) -> int {
         int lo, hi;
         request_span(s, w.r, lo, hi);
-        const int pos = x * kTilePositions + 32 * warp + (lane << box_shift);
-        if ((lane << box_shift) >= 32 || pos >= hi || pos + a.c.box <= lo) return -2;
-        return a.c.table[static_cast<int64_t>(w.b) * a.c.W + page_of(a.c, pos)];
-    };
-    // Where the lane's box lies in the cache (-1: not loaded), from its entry.
-    auto place = [&](const PagedWalk &w, int x, int id) -> int {
-        if (id == -2) return -1;
+        x += lane >> boxes_log2;
+        if (x >= end) return -1;
+        const int pos = x * kTilePositions + 32 * warp + ((lane << box_shift) & 31);
+        if (pos >= hi || pos + a.c.box <= lo) return -1;
+        const int pg = page_of(a.c, pos);
+        const int id = a.c.table[static_cast<int64_t>(w.b) * a.c.W + pg];
         if (id < 0 || id >= a.c.P) {
             record_device_error(a.err, KID_ATTN, ROLE_PRODUCER, 9);
             return -1;
         }
-        const int pos = x * kTilePositions + 32 * warp + (lane << box_shift);
-        return (id * a.c.Hkv + w.h) * a.c.page + pos - page_of(a.c, pos) * a.c.page;   // (rows of the cache: below 2^31)
+        return (id * a.c.Hkv + w.h) * a.c.page + pos - pg * a.c.page;   // (rows of the cache: below 2^31)
     };
-    // Starts the copies of K, or of V, of the boxes at `row` into stage n % kStages
-    // (whose last reader, this warp, is done with it).
+    int found = -1, found_at = 0;   // from find, and its x
+    // The lane's box of tile x, one of those found.
+    auto place = [&](int x) -> int {
+        const int row = __shfl_sync(0xFFFFFFFFu, found, (((x - found_at) << boxes_log2) + lane) & 31);
+        return (lane >> boxes_log2) == 0 ? row : -1;
+    };
+    // Starts the copies of K, or of V, of the boxes at `row` into stage n % kStages.
+    // Its last reader is this warp, every lane of which has put a fence between its reads
+    // and here: the copy is another proxy's, and orders itself after nothing else. (Without,
+    // copies from L2 overtook reads, mostly of BF16 pages with 16 rows per item.)
     auto copy = [&](bool v, int row, uint32_t n) {
         const int sg = n % kStages;
         const uint32_t bar = smem_u32(v ? &sm.vfull[warp][sg] : &sm.kfull[warp][sg]);
@@ -227,17 +234,14 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant_
         return __ballot_sync(0xFFFFFFFFu,
                              ((used >> (lane >> box_shift)) & 1u) && pos >= lo && pos < hi);
     };
-    int ahead = -2;
+    // (the fences of the piece before cover all its reads)
     auto begin = [&](const PagedWalk &w, const PagedPiece &p) {
-        int id[kStages];
-#pragma unroll
-        for (int j = 0; j < kStages; ++j)
-            id[j] = p.first + j < p.last ? lookup(w, p.tile0 + p.first + j) : -2;
-        if (p.first + kStages < p.last) ahead = lookup(w, p.tile0 + p.first + kStages);
+        found_at = p.tile0 + p.first;
+        found = find(w, found_at, p.tile0 + p.last);    // (8 tiles or more)
 #pragma unroll
         for (int j = 0; j < kStages; ++j) {
             if (p.first + j >= p.last) continue;
-            const int x = p.tile0 + p.first + j, row = place(w, x, id[j]);
+            const int x = p.tile0 + p.first + j, row = place(x);
             copy(false, row, it + j);
             copy(true, row, it + j);
             const uint32_t mask = keys(w, x, row);
@@ -337,25 +341,30 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant_
                 const uint32_t mw = sm.mask[warp][sg];
                 ChunkRegs<kInt8> r;
                 key_frags<kInt8>(r, sm.k[warp][sg], sm.ks[warp][sg], gid, t);
-                __syncwarp();   // every lane has its fragments: K's stage is free
                 const bool more = ok && x + kStages < p.last;
                 const int next = p.tile0 + x + kStages;
                 int row = -1;
                 uint32_t mask = 0;
                 if (more) {
-                    row = place(w, next, ahead);
-                    if (x + kStages + 1 < p.last) ahead = lookup(w, next + 1);
+                    row = place(next);
                     mask = keys(w, next, row);
-                    copy(false, row, it + kStages);
                 }
                 auto values = [&](ChunkRegs<kInt8> &r) {
+                    fence_proxy_async_smem();   // (the scores are done: K's fragments are read)
+                    __syncwarp();
+                    if (more) copy(false, row, it + kStages);
                     landed(sm.vfull[warp][sg], 4);
                     value_frags<kInt8>(r, sm.v[warp][sg], sm.vs[warp][sg], mw, gid, t);
+                    fence_proxy_async_smem();
                     __syncwarp();
                     if (more) {
                         copy(true, row, it + kStages);
                         if (lane == 0) sm.mask[warp][sg] = mask;
                         issued = it + kStages + 1;
+                        if (next + 1 - found_at == 1 << box_shift) {
+                            found_at = next + 1;
+                            found = find(w, found_at, p.tile0 + p.last);
+                        }
                     }
                 };
                 const int c0 = (p.tile0 + x) * kTilePositions + 32 * warp;

@@ -568,3 +568,28 @@ def test_many_requests_keep_all_bits(int8):
 def test_many_rows_over_pages_of_other_sizes(window, page, int8):
     b = Batch([70, 1, 150], [500, 130, 0], 14, 2, page, int8, seed=29)
     b.check(b.run(window=window), window=window)
+
+
+@pytest.mark.parametrize("int8", KINDS)
+@pytest.mark.parametrize("n_new,Hq,Hkv,page", [([1] * 30, 16, 2, 128), ([1] * 14, 8, 8, 64),
+                                               ([2] * 20 + [1] * 4, 16, 2, 16), ([7, 8, 5, 1] * 4, 4, 2, 32)])
+def test_few_rows_repeat_themselves(n_new, Hq, Hkv, page, int8):
+    # a cache in L2, so that copies are as fast as they get: none may overtake a read
+    g = torch.Generator().manual_seed(9)
+    ctx = torch.randint(300, 4000, (len(n_new),), generator=g).tolist()
+    b = Batch(n_new, ctx, Hq, Hkv, page, int8, seed=30)
+    b.q = torch.cat([b.q, b.q[:2]])                     # (16 rows per item)
+    out = b.run()
+    b.check(out[:-2], split=True)
+    for _ in range(100):
+        assert torch.equal(b.run(), out)
+
+
+@pytest.mark.parametrize("int8", KINDS)
+@pytest.mark.parametrize("page", [8, 16, 24, 128])
+def test_many_tiles_of_one_request_per_block(page, int8):
+    # more tiles than a warp looks up in the block table at once
+    b = Batch([1] * 32, [8000 - 13 * i for i in range(32)], 8, 8, page, int8, seed=31)
+    w8.device_error()
+    b.check(b.run(), split=True)
+    assert w8.device_error() == 0
