@@ -41,11 +41,11 @@ constexpr float kNegInf = -INFINITY;
 // The kernel of a call, by the query rows that a request and kv head have on
 // average: up to 16 fit one item of the rows kernel, which reads the cache
 // once; more take the tiles kernel. 32 requests at 4096 positions, 8 kv heads, rows
-// kernel / tiles kernel: 16 rows INT8 82 / 143 us and BF16 136 / 102, 24 rows 151 /
-// 144 and 245 / 103. (BF16 pages pay for their place among the first 16: their
+// kernel / tiles kernel: 16 rows INT8 80 / 144 us and BF16 135 / 102, 24 rows 144 /
+// 144 and 247 / 103. (BF16 pages pay for their place among the first 16: their
 // probabilities keep 24 bits there, and 8 in the tiles kernel.) The lengths are on the
 // device, so one kernel takes the whole call: 32 single tokens over 4096 positions
-// (INT8 64 us, BF16 101) with a chunk of 512 over 4096 (118, 89) take 254 and 181 in
+// (INT8 63 us, BF16 102) with a chunk of 512 over 4096 (118, 90) take 255 and 181 in
 // one call.
 bool uses_tiles(int64_t T, int64_t B, int64_t G) { return T * G > kRowsMax * B; }
 
@@ -140,7 +140,9 @@ __device__ __forceinline__ void value_frags(ChunkRegs<kInt8> &r, const uint4 *v,
 // per warp.
 //
 // BF16 pages are an HBM stream when there is enough of one: 4 requests at 33 to 131
-// thousand positions (1.34 GB) take 204 us, 6.6 TB/s. INT8 pages halve the bytes and
+// thousand positions (1.34 GB) take 218 us, 6.2 TB/s. (A stage is copied into again when
+// the scores are done, or V's fragments read. Both at once, or both later, took 228 to 232;
+// mbarriers in place of the fences 224, and INT8 57 for 55 below.) INT8 pages halve the bytes and
 // not the instructions: 32 requests at 2 to 4 thousand positions (214 MB) take 55 us,
 // 3.9 TB/s, of which about 13 are the same for any length (2 until the share is known,
 // 4 until the first tiles are there, 1.4 for the join, 5 for the second kernel) and the
