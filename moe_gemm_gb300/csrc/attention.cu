@@ -257,7 +257,7 @@ attn_decode_kernel(const uint16_t *__restrict__ q, const void *__restrict__ kc,
     }
     // INT8 cache: the score product runs in fp16 (the codes widen to fp16 in
     // half the instructions bf16 takes). q goes to fp16 scaled by the power of
-    // two 2^(14 - e), e the exponent of the largest |q| of the CTA's heads (the
+    // two 2^(14 - e), e the exponent of the largest finite |q| of the CTA's heads (the
     // warp holds all of them), so the largest value sits in [2^14, 2^15) and
     // every value of at least 2^-14 of the scaled range converts exactly; the
     // scores are scaled back by qinv exactly.
@@ -267,7 +267,7 @@ attn_decode_kernel(const uint16_t *__restrict__ q, const void *__restrict__ kc,
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int w = 0; w < 16; ++w) mq = __vmaxu2(mq, qf[nt][w] & 0x7FFF7FFFu);
+            for (int w = 0; w < 16; ++w) mq = __vmaxu2(mq, finite_bits2(qf[nt][w]));
         mq = max(mq & 0xFFFFu, mq >> 16);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) mq = max(mq, __shfl_xor_sync(0xFFFFFFFFu, mq, o));

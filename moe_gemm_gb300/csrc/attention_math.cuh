@@ -77,6 +77,15 @@ __device__ __forceinline__ float ex2_approx(float x) {
     return y;
 }
 
+// The magnitudes of a pair of BF16 values, as bits. For INT8 caches q goes to fp16 scaled
+// by one power of two for neighbouring rows, from the largest of these. What is no finite
+// number makes its own row none, and would turn all others into zeros if it set the
+// scale: it counts as 0.
+__device__ __forceinline__ uint32_t finite_bits2(uint32_t bf16_pair) {
+    const uint32_t m = bf16_pair & 0x7FFF7FFFu;
+    return m & ~__vcmpgeu2(m, 0x7F807F80u);
+}
+
 // One chunk's operands in registers: K rows pw + 16 mt + gid (+ 8), dims
 // [32 t, 32 t + 32); V rows pw + 16 mt + 2 t + {0, 1, 8, 9}, dims [16 gid,
 // 16 gid + 16); the K and V scales of the K rows (zero past the sequence).

@@ -141,13 +141,7 @@ __host__ __device__ inline PagedCut *cuts_of(float *ws, int rows, int ctas) {
     return reinterpret_cast<PagedCut *>(ws + static_cast<int64_t>(ctas) * 2 * rows * (kHeadDim + 2));
 }
 
-// INT8 pages: q goes to fp16 scaled by one power of two per item, from the largest of
-// these. What is no finite number makes its own row none, and would turn all others into
-// zeros if it set the scale: it counts as 0.
-__device__ __forceinline__ uint32_t finite_bits2(uint32_t bf16_pair) {
-    const uint32_t m = bf16_pair & 0x7FFF7FFFu;
-    return m & ~__vcmpgeu2(m, 0x7F807F80u);
-}
+// The largest |x| of 8 BF16 values, as bits (attention_math.cuh: finite_bits2).
 __device__ __forceinline__ uint32_t finite_amax8(const uint4 &v) {
     const uint32_t m = __vmaxu2(__vmaxu2(finite_bits2(v.x), finite_bits2(v.y)),
                                 __vmaxu2(finite_bits2(v.z), finite_bits2(v.w)));

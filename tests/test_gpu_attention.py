@@ -174,3 +174,27 @@ def test_decode_workload_sampled():
         yv = y[b:b + 1].float().cpu().numpy().astype(np.float64)
         assert np.all(np.abs(yv - y_ref) <= bound)
     assert w8.device_error() == 0
+
+
+@pytest.mark.parametrize("int8", [True, False])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_head_that_is_no_number_is_so_alone(value, int8):
+    # the other query heads of its kv head keep their answers (INT8: q is scaled by a power
+    # of two, so another choice of it changes no bit)
+    q, k, v, lens = _problem(44)
+    B, Hkv, S, _ = k.shape
+    ks = vs = None
+    kc, vc = bf16_dev(k), bf16_dev(v)
+    if int8:
+        kc, vc = (torch.empty((B, Hkv, S, D), dtype=torch.int8, device=DEV) for _ in range(2))
+        ks, vs = (torch.empty((B, Hkv, S), dtype=torch.float32, device=DEV) for _ in range(2))
+        w8.kv_quant(bf16_dev(k.reshape(-1, D)), kc, ks)
+        w8.kv_quant(bf16_dev(v.reshape(-1, D)), vc, vs)
+    L, x = torch.from_numpy(lens).to(DEV), bf16_dev(q)
+    clean = _run(x, kc, vc, L, 0.09, ks, vs)
+    x[0, 3, 7] = value
+    y = _run(x, kc, vc, L, 0.09, ks, vs)
+    if value != value:
+        assert bool(torch.isnan(y[0, 3]).all())
+    y[0, 3] = clean[0, 3]
+    assert torch.equal(y, clean)
