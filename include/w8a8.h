@@ -607,6 +607,29 @@ w8a8_status w8a8_moe_gate(const void *logits, w8a8_dtype logits_dtype, int64_t l
                           int64_t n_group, int64_t topk_group, int renormalize, float scale,
                           int32_t *ids, float *w, w8a8_stream_t stream);
 
+/*
+ * A whole mixture-of-experts layer: w8a8_moe_gate, then the FFN of the picked experts,
+ * the same numbers as w8a8_moe_gate followed by w8a8_moe_ffn, bit for bit (finite x).
+ *   x [T, ldx] BF16, logits [T, ld] and the gate's arguments as for w8a8_moe_gate;
+ *   weights, scales and y as for w8a8_moe_ffn; ids, w [T, k] out: the gate's choice.
+ * For T <= 32 tokens with T * k <= 512 it is two kernels, the gate and a cooperative
+ * one that reads the picked experts' weights once (all its CTAs, one per SM, must
+ * be resident: it starts when the device has room for them); more tokens run the kernels of
+ * those two calls. H, I, k, E as for w8a8_moe_ffn. T == 0 is a no-op.
+ *   workspace: w8a8_moe_layer_workspace_size bytes, 256-byte aligned; scratch, but calls
+ *   that may overlap on the GPU must not share one.
+ */
+size_t w8a8_moe_layer_workspace_size(int64_t T, int64_t k, int64_t H, int64_t I, int64_t E);
+
+w8a8_status w8a8_moe_layer(const void *x_bf16, int64_t ldx, const void *logits,
+                           w8a8_dtype logits_dtype, int64_t ld, int64_t T, int64_t k, int64_t H,
+                           int64_t I, int64_t E, w8a8_gate_score score, const float *bias,
+                           int64_t n_group, int64_t topk_group, int renormalize, float scale,
+                           const int8_t *qw_up, const float *sw_up, const int8_t *qw_down,
+                           const float *sw_down, int32_t *ids, float *w, void *y,
+                           w8a8_dtype y_dtype, void *workspace, size_t workspace_bytes,
+                           w8a8_stream_t stream);
+
 /* ---------------------------------------------------------------------------
  * The paged KV cache. The cache of a layer is a pool of P pages,
  *   [P, Hkv, page, 128]  INT8 codes with one float scale per vector
@@ -662,6 +685,36 @@ w8a8_status w8a8_paged_kv_write(const void *k_bf16, int64_t k_token_stride, int6
                                 const int32_t *slots, int64_t T, int64_t Hkv, int64_t head_dim,
                                 int64_t P, int64_t page, void *k_cache, float *k_scale,
                                 void *v_cache, float *v_scale, w8a8_stream_t stream);
+
+/*
+ * The same write with the position rotation of queries and keys on the way: one pass
+ * between a layer's projection and its attention.
+ *   q [T, Hq, 128], k, v [T, Hkv, 128] BF16 with the given strides in elements;
+ *   positions [T], slots [T]  as w8a8_paged_kv_plan gives them;
+ *   inv_freq [rot / 2] float: pair i of a token at position p is turned by the angle
+ *        p * inv_freq[i] (the real product of the two): a cos - b sin, b cos + a sin, cos and
+ *        sin times amplitude. (a, b) are elements i and rot / 2 + i of a head
+ *        or, interleaved, 2 i and 2 i + 1; elements rot .. 127 stay as they are;
+ *   q_out [T, Hq, 128] BF16 with the given strides: the queries, rounded once; it may be
+ *        q itself (same strides). Hq 0 (q and q_out NULL): keys and values only.
+ * k is turned in FP32, and rounded once: to BF16 pages, or to INT8 codes with the scale
+ * amax / 127 of the turned vector. v is written as w8a8_paged_kv_write does.
+ * Angles are exact to 2^-23 of a turn at any position for inv_freq up to 1 in magnitude
+ * (sines and cosines are off by a few 2^-24 at positions up to 2^24).
+ * A token whose position is negative is not served: none of its rows is written. One
+ * whose slot is outside [0, P * page) has its queries turned, its k and v not
+ * written. Two tokens of one call must not share a slot. Inputs must be finite.
+ * 16 <= rot <= 128, a multiple of 16; Hq <= 65535; strides, alignments and the other
+ * limits as for w8a8_paged_kv_write. T == 0 is a no-op.
+ */
+w8a8_status w8a8_paged_kv_append(
+    const void *q_bf16, int64_t q_token_stride, int64_t q_head_stride, int64_t Hq,
+    const void *k_bf16, int64_t k_token_stride, int64_t k_head_stride, const void *v_bf16,
+    int64_t v_token_stride, int64_t v_head_stride, const int32_t *positions, const int32_t *slots,
+    const float *inv_freq, int64_t rot, int interleaved, float amplitude, int64_t T, int64_t Hkv,
+    int64_t head_dim, int64_t P, int64_t page, void *q_out, int64_t out_token_stride,
+    int64_t out_head_stride, void *k_cache, float *k_scale, void *v_cache, float *v_scale,
+    w8a8_stream_t stream);
 
 /*
  * Attention of each request's new tokens over its pages: prompts, chunks of

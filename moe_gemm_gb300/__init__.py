@@ -10,8 +10,9 @@ Functions (names match the C entry points):
   quant_weight(w_f32)                     -> (qw int8 [N,K], sw f32 [N,K/128])
   gemm(qa, sa, qw, sw, out_dtype, ...)    -> y [M,N]  (+ partials when debug)
   grouped_gemm(qa, sa, offsets, qw, sw, out_dtype, ...) -> y [R,N]
-Serving: moe_gate (expert ids and weights for moe_ffn), and the paged KV cache:
-paged_kv_plan (block tables and slots), paged_kv_write, attention_paged.
+Serving: moe_gate (expert ids and weights for moe_ffn), moe_layer (both, for a decode
+step's tokens in two kernels), and the paged KV cache: paged_kv_plan (block tables and
+slots), paged_kv_write, paged_kv_append (with the position rotation), attention_paged.
 """
 from __future__ import annotations
 
@@ -109,6 +110,14 @@ def _load() -> ctypes.CDLL:
     lib.w8a8_attention_paged.argtypes = [vp, i64, i64, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64,
                                          i64, i64, i64, i64, i64, ctypes.c_float, i64, vp, i32, vp,
                                          ctypes.c_size_t, vp]
+    lib.w8a8_paged_kv_append.argtypes = [vp, i64, i64, i64, vp, i64, i64, vp, i64, i64, vp, vp,
+                                         vp, i64, i32, ctypes.c_float, i64, i64, i64, i64, i64,
+                                         vp, i64, i64, vp, vp, vp, vp, vp]
+    lib.w8a8_moe_layer_workspace_size.argtypes = [i64, i64, i64, i64, i64]
+    lib.w8a8_moe_layer_workspace_size.restype = ctypes.c_size_t
+    lib.w8a8_moe_layer.argtypes = [vp, i64, vp, i32, i64, i64, i64, i64, i64, i64, i32, vp, i64,
+                                   i64, i32, ctypes.c_float, vp, vp, vp, vp, vp, vp, vp, i32, vp,
+                                   ctypes.c_size_t, vp]
     lib.w8a8_version.restype = i32
     for name in ("w8a8_quant_act", "w8a8_quant_weight", "w8a8_gemm", "w8a8_grouped_gemm",
                  "w8a8_gemm_noalloc", "w8a8_device_error", "w8a8_selftest_wait_timeout",
@@ -120,7 +129,8 @@ def _load() -> ctypes.CDLL:
                  "w8a8_w8a16_grouped_gemm", "w8a8_kv_quant", "w8a8_attention_decode_int8kv",
                  "w8a8_attention_decode_bf16kv", "w8a8_rmsnorm", "w8a8_rmsnorm_quant",
                  "w8a8_rmsnorm_linear", "w8a8_moe_gate", "w8a8_paged_kv_plan",
-                 "w8a8_paged_kv_write", "w8a8_attention_paged"):
+                 "w8a8_paged_kv_write", "w8a8_attention_paged", "w8a8_paged_kv_append",
+                 "w8a8_moe_layer"):
         getattr(lib, name).restype = i32
     return lib
 
@@ -789,6 +799,56 @@ def paged_kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cach
             "w8a8_paged_kv_write")
 
 
+def paged_kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+                    positions: torch.Tensor, slots: torch.Tensor, inv_freq: torch.Tensor,
+                    k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                    interleaved: bool = False, amplitude: float = 1.0,
+                    q_out: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None) -> Optional[torch.Tensor]:
+    """Turns queries q [T, Hq, 128] and keys k [T, Hkv, 128] (BF16) by their positions [T]
+    and writes k and v into slots [T] of the pages, as paged_kv_write does; returns the
+    turned queries (q_out, which may be q; a new tensor when None). Pair i of the
+    first 2 * len(inv_freq) elements of a head (i and len(inv_freq) + i; interleaved: 2 i and
+    2 i + 1) is turned by position * inv_freq[i] (float32). Tokens with a negative position
+    are not written. q None: keys and values only."""
+    _require_heads(k, "k")
+    dev = k.device
+    _require_heads(v, "v", dev)
+    T, Hkv, d = k.shape
+    if v.shape != k.shape:
+        raise ValueError(f"v: expected shape {tuple(k.shape)}, got {tuple(v.shape)}")
+    P, heads, page = _require_pages(k_cache, v_cache, k_scale, v_scale, dev)
+    if heads != Hkv:
+        raise ValueError(f"the cache has {heads} kv heads, k has {Hkv}")
+    _require(positions, torch.int32, "positions", 1, (T,), dev)
+    _require(slots, torch.int32, "slots", 1, (T,), dev)
+    _require(inv_freq, torch.float32, "inv_freq", 1, device=dev)
+    Hq, q_at, out_at = 0, (0, 0), (0, 0)
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+    else:
+        _require_heads(q, "q", dev)
+        Hq = q.shape[1]
+        if q.shape[0] != T:
+            raise ValueError(f"q: expected {T} tokens, got {q.shape[0]}")
+        if q_out is None:
+            q_out = _empty((T, Hq, d), torch.bfloat16, dev, stream)
+        else:
+            _require_heads(q_out, "q_out", dev)
+            if q_out.shape != q.shape:
+                raise ValueError(f"q_out: expected shape {tuple(q.shape)}, got {tuple(q_out.shape)}")
+        q_at, out_at = _head_strides(q), _head_strides(q_out)
+    with _on_device(dev, stream):
+        _check(_lib.w8a8_paged_kv_append(
+            _ptr(q), *q_at, Hq, _ptr(k), *_head_strides(k), _ptr(v), *_head_strides(v),
+            _ptr(positions), _ptr(slots), _ptr(inv_freq), 2 * inv_freq.shape[0], int(interleaved),
+            float(amplitude), T, Hkv, d, P, page, _ptr(q_out), *out_at, _ptr(k_cache),
+            _ptr(k_scale), _ptr(v_cache), _ptr(v_scale), _stream(stream)), "w8a8_paged_kv_append")
+    return q_out
+
+
 def attention_paged_workspace_size(T: int, B: int, Hq: int, Hkv: int) -> int:
     return int(_lib.w8a8_attention_paged_workspace_size(T, B, Hq, Hkv))
 
@@ -1010,6 +1070,71 @@ def moe_ffn(x: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor,
                                  _ptr(out), code, _ptr(workspace), workspace.numel(),
                                  _stream(stream)), "w8a8_moe_ffn")
     return out
+
+
+def moe_layer_workspace_size(T: int, k: int, H: int, I: int, E: int) -> int:
+    return int(_lib.w8a8_moe_layer_workspace_size(T, k, H, I, E))
+
+
+def moe_layer(x: torch.Tensor, logits: torch.Tensor, k: int, qw_up: torch.Tensor,
+              sw_up: torch.Tensor, qw_down: torch.Tensor, sw_down: torch.Tensor,
+              scoring: str = "softmax", bias: Optional[torch.Tensor] = None, n_group: int = 1,
+              topk_group: int = 1, renormalize: bool = True, scale: float = 1.0,
+              out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+              topk_ids: Optional[torch.Tensor] = None, topk_w: Optional[torch.Tensor] = None,
+              workspace: Optional[torch.Tensor] = None,
+              stream: Optional[torch.cuda.Stream] = None
+              ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """The whole MoE layer: moe_gate on logits [T, E], then moe_ffn of tokens x [T, H]
+    with its choice, the same numbers; a decode step's tokens (T <= 32, T k <= 512) take two
+    kernels. Returns (y [T, H], topk_ids [T, k], topk_w [T, k])."""
+    ldx = _require_act(x)
+    dev = x.device
+    T, H = x.shape
+    if (logits.device != dev or logits.dtype not in (torch.float32, torch.bfloat16)
+            or logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1)):
+        raise ValueError(f"logits: expected an fp32 or bf16 [T, E] tensor with unit column stride "
+                         f"on {dev}")
+    if scoring not in GATE_SCORES:
+        raise ValueError(f"scoring: one of {sorted(GATE_SCORES)}")
+    _require(qw_up, torch.int8, "qw_up", 3, device=dev)
+    E, I2, H2 = qw_up.shape
+    if H2 != H or I2 % 2:
+        raise ValueError("qw_up must be [E, 2I, H]")
+    if tuple(logits.shape) != (T, E):
+        raise ValueError(f"logits: expected shape {(T, E)}, got {tuple(logits.shape)}")
+    I = I2 // 2
+    _require(sw_up, torch.float32, "sw_up", 3, (E, I2, H // GROUP), dev)
+    _require(qw_down, torch.int8, "qw_down", 3, (E, H, I), dev)
+    _require(sw_down, torch.float32, "sw_down", 3, (E, H, I // GROUP), dev)
+    if bias is not None:
+        _require(bias, torch.float32, "bias", 1, (E,), dev)
+    code = _dtype_code(out_dtype)
+    if out is None:
+        out = _empty((T, H), out_dtype, dev, stream)
+    else:
+        _require_out(out, out_dtype, (T, H), dev)
+    if topk_ids is None:
+        topk_ids = _empty((T, k), torch.int32, dev, stream)
+    else:
+        _require(topk_ids, torch.int32, "topk_ids", 2, (T, k), dev)
+    if topk_w is None:
+        topk_w = _empty((T, k), torch.float32, dev, stream)
+    else:
+        _require(topk_w, torch.float32, "topk_w", 2, (T, k), dev)
+    if workspace is None:
+        workspace = _empty((max(moe_layer_workspace_size(T, k, H, I, E), 1),), torch.uint8, dev,
+                           stream)
+    else:
+        _require_workspace(workspace, dev)
+    with _on_device(dev, stream):
+        _check(_lib.w8a8_moe_layer(
+            _ptr(x), ldx if T > 1 else H, _ptr(logits), _dtype_code(logits.dtype),
+            logits.stride(0) if T > 1 else E, T, k, H, I, E, GATE_SCORES[scoring], _ptr(bias),
+            n_group, topk_group, int(renormalize), float(scale), _ptr(qw_up), _ptr(sw_up),
+            _ptr(qw_down), _ptr(sw_down), _ptr(topk_ids), _ptr(topk_w), _ptr(out), code,
+            _ptr(workspace), workspace.numel(), _stream(stream)), "w8a8_moe_layer")
+    return out, topk_ids, topk_w
 
 
 def selftest_wait_timeout(limit_us: int = 20000,

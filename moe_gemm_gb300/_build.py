@@ -13,9 +13,9 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libw8a8.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.cu", "quant.cu", "gemm.cu", "probe.cu", "moe.cu", "attention.cu",
-           "gate.cu", "paged_kv.cu", "paged_attention.cu",
+           "gate.cu", "moe_layer.cu", "paged_kv.cu", "paged_append.cu", "paged_attention.cu",
            "paged_attention_tiles.cu"]
-HEADERS = ["common.cuh", "quant_math.cuh", "attention_math.cuh", "paged_schedule.cuh",
+HEADERS = ["common.cuh", "quant_math.cuh", "moe_math.cuh", "attention_math.cuh", "paged_schedule.cuh",
            "paged_attention.cuh",
            "tensor_map.h", "internal.h"]
 GENCODE = "-gencode=arch=compute_103a,code=sm_103a"

@@ -314,6 +314,54 @@ w8a8_status check_ffn_shape(int64_t T, int64_t k, int64_t H, int64_t I, int64_t 
     return W8A8_OK;
 }
 
+// Validates the gate's arguments and fills its problem.
+w8a8_status check_gate(const void *logits, w8a8_dtype logits_dtype, int64_t ld, int64_t T,
+                       int64_t E, int64_t k, w8a8_gate_score score, const float *bias,
+                       int64_t n_group, int64_t topk_group, int renormalize, float scale,
+                       int32_t *ids, float *w, w8a8::GateProblem *p) {
+    if (logits_dtype != W8A8_BF16 && logits_dtype != W8A8_FP32) return W8A8_ERR_INVALID_ARG;
+    if (score != W8A8_GATE_SOFTMAX && score != W8A8_GATE_SIGMOID) return W8A8_ERR_INVALID_ARG;
+    if (T < 0 || E < 1 || E > w8a8::kMaxExperts || n_group < 1 ||
+        n_group > w8a8::kGateMaxGroups || E % n_group != 0 || topk_group < 1 ||
+        topk_group > n_group || k < 1 || k > w8a8::kMoeMaxTopK || k > topk_group * (E / n_group) ||
+        ld < E || !std::isfinite(scale))
+        return W8A8_ERR_INVALID_ARG;
+    if (T > kMaxElems / ld || T > kMaxElems / k) return W8A8_ERR_INVALID_ARG;
+    if (T == 0) return W8A8_OK;
+    if (!logits || !ids || !w || !aligned(logits, logits_dtype == W8A8_FP32 ? 4 : 2) ||
+        !aligned(bias, 4) || !aligned(ids, 4) || !aligned(w, 4))
+        return W8A8_ERR_INVALID_ARG;
+    p->logits = logits;
+    p->fp32 = logits_dtype == W8A8_FP32;
+    p->ldx = ld;
+    p->T = T;
+    p->E = E;
+    p->k = k;
+    p->n_group = n_group;
+    p->topk_group = topk_group;
+    p->bias = bias;
+    p->sigmoid = score == W8A8_GATE_SIGMOID;
+    p->renormalize = renormalize != 0;
+    p->scale = scale;
+    p->ids = ids;
+    p->w = w;
+    return W8A8_OK;
+}
+
+// Validates the tokens, weights and output of the expert FFN (after its shape).
+w8a8_status check_ffn_operands(const void *x_bf16, int64_t ldx, int64_t T, int64_t H,
+                               const int8_t *qw_up, const float *sw_up, const int8_t *qw_down,
+                               const float *sw_down, const void *y, w8a8_dtype y_dtype) {
+    if (y_dtype != W8A8_BF16 && y_dtype != W8A8_FP32) return W8A8_ERR_INVALID_ARG;
+    if (ldx < H || T > kMaxElems / ldx) return W8A8_ERR_INVALID_ARG;
+    if (T == 0) return W8A8_OK;
+    if (!x_bf16 || !qw_up || !sw_up || !qw_down || !sw_down || !y) return W8A8_ERR_INVALID_ARG;
+    if (!aligned(x_bf16, 2) || !aligned(qw_up, 16) || !aligned(qw_down, 16) ||
+        !aligned(sw_up, 4) || !aligned(sw_down, 4) || !aligned(y, 16))
+        return W8A8_ERR_INVALID_ARG;
+    return W8A8_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -681,36 +729,13 @@ w8a8_status w8a8_moe_gate(const void *logits, w8a8_dtype logits_dtype, int64_t l
                           int64_t E, int64_t k, w8a8_gate_score score, const float *bias,
                           int64_t n_group, int64_t topk_group, int renormalize, float scale,
                           int32_t *ids, float *w, w8a8_stream_t stream) {
-    if (logits_dtype != W8A8_BF16 && logits_dtype != W8A8_FP32) return W8A8_ERR_INVALID_ARG;
-    if (score != W8A8_GATE_SOFTMAX && score != W8A8_GATE_SIGMOID) return W8A8_ERR_INVALID_ARG;
-    if (T < 0 || E < 1 || E > w8a8::kMaxExperts || n_group < 1 ||
-        n_group > w8a8::kGateMaxGroups || E % n_group != 0 || topk_group < 1 ||
-        topk_group > n_group || k < 1 || k > w8a8::kMoeMaxTopK || k > topk_group * (E / n_group) ||
-        ld < E || !std::isfinite(scale))
-        return W8A8_ERR_INVALID_ARG;
-    if (T > kMaxElems / ld || T > kMaxElems / k) return W8A8_ERR_INVALID_ARG;
-    if (T == 0) return W8A8_OK;
-    if (!logits || !ids || !w || !aligned(logits, logits_dtype == W8A8_FP32 ? 4 : 2) ||
-        !aligned(bias, 4) || !aligned(ids, 4) || !aligned(w, 4))
-        return W8A8_ERR_INVALID_ARG;
-    w8a8::DeviceInfo info;
-    w8a8_status st = check_device(&info);
-    if (st != W8A8_OK) return st;
     w8a8::GateProblem p;
-    p.logits = logits;
-    p.fp32 = logits_dtype == W8A8_FP32;
-    p.ldx = ld;
-    p.T = T;
-    p.E = E;
-    p.k = k;
-    p.n_group = n_group;
-    p.topk_group = topk_group;
-    p.bias = bias;
-    p.sigmoid = score == W8A8_GATE_SIGMOID;
-    p.renormalize = renormalize != 0;
-    p.scale = scale;
-    p.ids = ids;
-    p.w = w;
+    w8a8_status st = check_gate(logits, logits_dtype, ld, T, E, k, score, bias, n_group,
+                                topk_group, renormalize, scale, ids, w, &p);
+    if (st != W8A8_OK || T == 0) return st;
+    w8a8::DeviceInfo info;
+    st = check_device(&info);
+    if (st != W8A8_OK) return st;
     return from_cuda(w8a8::launch_moe_gate(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -790,6 +815,67 @@ w8a8_status w8a8_paged_kv_write(const void *k_bf16, int64_t k_token_stride, int6
     p.ks = k_scale;
     p.vs = v_scale;
     return from_cuda(w8a8::launch_paged_kv_write(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+w8a8_status w8a8_paged_kv_append(
+    const void *q_bf16, int64_t q_token_stride, int64_t q_head_stride, int64_t Hq,
+    const void *k_bf16, int64_t k_token_stride, int64_t k_head_stride, const void *v_bf16,
+    int64_t v_token_stride, int64_t v_head_stride, const int32_t *positions, const int32_t *slots,
+    const float *inv_freq, int64_t rot, int interleaved, float amplitude, int64_t T, int64_t Hkv,
+    int64_t head_dim, int64_t P, int64_t page, void *q_out, int64_t out_token_stride,
+    int64_t out_head_stride, void *k_cache, float *k_scale, void *v_cache, float *v_scale,
+    w8a8_stream_t stream) {
+    if (T < 0 || Hq < 0 || Hq > 65535 || Hkv < 1 || Hkv > 65535 ||
+        head_dim != w8a8::kAttnHeadDim || P < 1 || page < 1 || P > kMaxElems / page ||
+        P * page > kMaxElems / Hkv || T > kMaxElems / (Hq + 2 * Hkv))
+        return W8A8_ERR_INVALID_ARG;
+    if (rot < 16 || rot > head_dim || rot % 16 != 0 || !std::isfinite(amplitude))
+        return W8A8_ERR_INVALID_ARG;
+    for (const int64_t s : {q_token_stride, q_head_stride, k_token_stride, k_head_stride,
+                            v_token_stride, v_head_stride, out_token_stride, out_head_stride})
+        if (s < 0 || s % 8 != 0 || s > kMaxElems) return W8A8_ERR_INVALID_ARG;
+    if ((k_scale == nullptr) != (v_scale == nullptr)) return W8A8_ERR_INVALID_ARG;
+    if (T == 0) return W8A8_OK;
+    if (!k_bf16 || !v_bf16 || !positions || !slots || !inv_freq || !k_cache || !v_cache ||
+        (Hq > 0 && (!q_bf16 || !q_out)) || !aligned(q_bf16, 16) || !aligned(q_out, 16) ||
+        !aligned(k_bf16, 16) || !aligned(v_bf16, 16) || !aligned(k_cache, 16) ||
+        !aligned(v_cache, 16) || !aligned(positions, 4) || !aligned(slots, 4) ||
+        !aligned(inv_freq, 4) || !aligned(k_scale, 4) || !aligned(v_scale, 4))
+        return W8A8_ERR_INVALID_ARG;
+    w8a8::DeviceInfo info;
+    w8a8_status st = check_device(&info);
+    if (st != W8A8_OK) return st;
+    w8a8::PagedAppendProblem p;
+    p.w.k = static_cast<const uint16_t *>(k_bf16);
+    p.w.v = static_cast<const uint16_t *>(v_bf16);
+    p.w.kt = k_token_stride;
+    p.w.kh = k_head_stride;
+    p.w.vt = v_token_stride;
+    p.w.vh = v_head_stride;
+    p.w.slots = slots;
+    p.w.T = T;
+    p.w.Hkv = Hkv;
+    p.w.P = P;
+    p.w.page = page;
+    p.w.int8 = k_scale != nullptr;
+    p.w.kc = k_cache;
+    p.w.vc = v_cache;
+    p.w.ks = k_scale;
+    p.w.vs = v_scale;
+    p.q = static_cast<const uint16_t *>(q_bf16);
+    p.qt = q_token_stride;
+    p.qh = q_head_stride;
+    p.Hq = Hq;
+    p.positions = positions;
+    p.inv_freq = inv_freq;
+    p.rot = rot;
+    p.interleaved = interleaved != 0;
+    p.amplitude = amplitude;
+    p.q_out = static_cast<uint16_t *>(q_out);
+    p.ot = out_token_stride;
+    p.oh = out_head_stride;
+    return from_cuda(w8a8::launch_paged_kv_append(p, info.num_sms,
+                                                  reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t w8a8_attention_paged_workspace_size(int64_t T, int64_t B, int64_t Hq, int64_t Hkv) {
@@ -1008,16 +1094,11 @@ w8a8_status w8a8_moe_ffn(const void *x_bf16, int64_t ldx, const int32_t *topk_id
                          int64_t E, const int8_t *qw_up, const float *sw_up,
                          const int8_t *qw_down, const float *sw_down, void *y, w8a8_dtype y_dtype,
                          void *workspace, size_t workspace_bytes, w8a8_stream_t stream) {
-    if (y_dtype != W8A8_BF16 && y_dtype != W8A8_FP32) return W8A8_ERR_INVALID_ARG;
     w8a8_status st = check_ffn_shape(T, k, H, I, E);
     if (st != W8A8_OK) return st;
-    if (ldx < H || T > kMaxElems / ldx) return W8A8_ERR_INVALID_ARG;
-    if (T == 0) return W8A8_OK;
-    if (!x_bf16 || !topk_ids || !topk_w || !qw_up || !sw_up || !qw_down || !sw_down || !y)
-        return W8A8_ERR_INVALID_ARG;
-    if (!aligned(x_bf16, 2) || !aligned(topk_ids, 4) || !aligned(topk_w, 4) ||
-        !aligned(qw_up, 16) || !aligned(qw_down, 16) || !aligned(sw_up, 4) ||
-        !aligned(sw_down, 4) || !aligned(y, 16))
+    st = check_ffn_operands(x_bf16, ldx, T, H, qw_up, sw_up, qw_down, sw_down, y, y_dtype);
+    if (st != W8A8_OK || T == 0) return st;
+    if (!topk_ids || !topk_w || !aligned(topk_ids, 4) || !aligned(topk_w, 4))
         return W8A8_ERR_INVALID_ARG;
     const FfnLayout L = ffn_layout(T, k, H, I, E);
     if (!workspace || workspace_bytes < L.total || !aligned(workspace, kWsAlign))
@@ -1085,6 +1166,63 @@ w8a8_status w8a8_moe_ffn(const void *x_bf16, int64_t ldx, const int32_t *topk_id
     // 6. weighted un-permute into y [T, H]
     if (e == cudaSuccess)
         e = w8a8::launch_moe_unpermute(D, row_of, topk_w, T, k, H, y, y_dtype == W8A8_FP32, s);
+    return from_cuda(e);
+}
+
+size_t w8a8_moe_layer_workspace_size(int64_t T, int64_t k, int64_t H, int64_t I, int64_t E) {
+    if (check_ffn_shape(T, k, H, I, E) != W8A8_OK || T == 0) return 0;
+    return w8a8::uses_moe_few(T, k) ? w8a8::moe_few_workspace_bytes(T, k, H, I)
+                                    : ffn_layout(T, k, H, I, E).total;
+}
+
+w8a8_status w8a8_moe_layer(const void *x_bf16, int64_t ldx, const void *logits,
+                           w8a8_dtype logits_dtype, int64_t ld, int64_t T, int64_t k, int64_t H,
+                           int64_t I, int64_t E, w8a8_gate_score score, const float *bias,
+                           int64_t n_group, int64_t topk_group, int renormalize, float scale,
+                           const int8_t *qw_up, const float *sw_up, const int8_t *qw_down,
+                           const float *sw_down, int32_t *ids, float *w, void *y,
+                           w8a8_dtype y_dtype, void *workspace, size_t workspace_bytes,
+                           w8a8_stream_t stream) {
+    w8a8_status st = check_ffn_shape(T, k, H, I, E);
+    if (st != W8A8_OK) return st;
+    w8a8::GateProblem gate;
+    st = check_gate(logits, logits_dtype, ld, T, E, k, score, bias, n_group, topk_group,
+                    renormalize, scale, ids, w, &gate);
+    if (st != W8A8_OK) return st;
+    st = check_ffn_operands(x_bf16, ldx, T, H, qw_up, sw_up, qw_down, sw_down, y, y_dtype);
+    if (st != W8A8_OK || T == 0) return st;
+    if (!workspace || !aligned(workspace, kWsAlign) ||
+        workspace_bytes < w8a8_moe_layer_workspace_size(T, k, H, I, E))
+        return W8A8_ERR_WORKSPACE;
+    w8a8::DeviceInfo info;
+    st = check_device(&info);
+    if (st != W8A8_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (!w8a8::uses_moe_few(T, k)) {
+        if (w8a8::launch_moe_gate(gate, s) != cudaSuccess) return W8A8_ERR_CUDA;
+        return w8a8_moe_ffn(x_bf16, ldx, ids, w, T, k, H, I, E, qw_up, sw_up, qw_down, sw_down, y,
+                            y_dtype, workspace, workspace_bytes, stream);
+    }
+    w8a8::MoeFewProblem p;
+    p.x = static_cast<const uint16_t *>(x_bf16);
+    p.ldx = ldx;
+    p.ids = ids;
+    p.w = w;
+    p.T = T;
+    p.k = k;
+    p.E = E;
+    p.H = H;
+    p.I = I;
+    p.qw_up = qw_up;
+    p.qw_down = qw_down;
+    p.sw_up = sw_up;
+    p.sw_down = sw_down;
+    p.y = y;
+    p.out_fp32 = y_dtype == W8A8_FP32;
+    p.workspace = workspace;
+    w8a8::moe_few_zeroes(p, &gate.zero, &gate.n_zero);
+    cudaError_t e = w8a8::launch_moe_gate(gate, s);
+    if (e == cudaSuccess) e = w8a8::launch_moe_few(p, info.num_sms, s);
     return from_cuda(e);
 }
 

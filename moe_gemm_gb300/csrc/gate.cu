@@ -96,6 +96,8 @@ struct GateArgs {
     float scale;
     int32_t *ids;
     float *w;
+    uint32_t *zero;         // words that the next kernel wants zeroed
+    int n_zero;
 };
 
 __device__ __forceinline__ float ex2_approx(float v) {
@@ -526,6 +528,9 @@ moe_gate_kernel(const Tin *logits, const GateArgs a) {
     __shared__ int s_list[kGateWarps][32];
     const int lane = threadIdx.x & 31;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + (threadIdx.x >> 5);
+    for (int i = blockIdx.x * kGateWarps * 32 + threadIdx.x; i < a.n_zero;
+         i += gridDim.x * kGateWarps * 32)
+        a.zero[i] = 0;
     if (t >= a.T) return;
     const Tin *row = logits + t * a.ldx;
     // logits: NaN and -inf mark experts that are never picked; +inf counts as
@@ -713,6 +718,8 @@ cudaError_t launch_moe_gate(const GateProblem &p, cudaStream_t stream) {
     a.scale = p.scale;
     a.ids = p.ids;
     a.w = p.w;
+    a.zero = p.zero;
+    a.n_zero = p.n_zero;
     return p.fp32 ? launch_any<float>(p.logits, a, stream)
                   : launch_any<uint16_t>(p.logits, a, stream);
 }

@@ -166,6 +166,8 @@ struct GateProblem {
     float scale;
     int32_t *ids;           // [T, k]
     float *w;               // [T, k]
+    uint32_t *zero = nullptr;   // words that the kernel launched next wants zeroed
+    int n_zero = 0;
 };
 constexpr int kGateMaxGroups = 64;
 cudaError_t launch_moe_gate(const GateProblem &p, cudaStream_t stream);
@@ -192,6 +194,21 @@ struct PagedWriteProblem {
 };
 cudaError_t launch_paged_kv_write(const PagedWriteProblem &p, cudaStream_t stream);
 
+// The same write behind the position rotation of q and k (paged_append.cu).
+struct PagedAppendProblem {
+    PagedWriteProblem w;
+    const uint16_t *q;               // BF16 [T, Hq, 128]; Hq may be 0
+    int64_t qt, qh, Hq;
+    const int32_t *positions;        // [T]
+    const float *inv_freq;           // [rot / 2]
+    int64_t rot;
+    bool interleaved;
+    float amplitude;
+    uint16_t *q_out;                 // BF16 [T, Hq, 128]
+    int64_t ot, oh;
+};
+cudaError_t launch_paged_kv_append(const PagedAppendProblem &p, int num_sms, cudaStream_t stream);
+
 // Attention of each request's new tokens over its pages (paged_attention.cu).
 struct PagedAttnProblem {
     const uint16_t *q;               // BF16 [T, Hq, 128]
@@ -214,6 +231,29 @@ cudaError_t launch_paged_attention(const PagedAttnProblem &p, cudaStream_t strea
 
 // Maximum number of experts a grouped call may have.
 constexpr int kMaxExperts = 1024;
+
+// The experts of a few tokens in one kernel (moe_layer.cu), after the gate, whose
+// launch zeroes moe_few_zeroes().
+constexpr int64_t kMoeFewMaxTokens = 32;
+constexpr int64_t kMoeFewMaxPairs = 512;
+struct MoeFewProblem {
+    const uint16_t *x;               // BF16 [T, ldx]
+    int64_t ldx;
+    const int32_t *ids;              // [T, k], each token's different
+    const float *w;                  // [T, k]
+    int64_t T, k, E, H, I;
+    const int8_t *qw_up, *qw_down;
+    const float *sw_up, *sw_down;
+    void *y;                         // [T, H]
+    bool out_fp32;
+    void *workspace;
+};
+inline bool uses_moe_few(int64_t T, int64_t k) {
+    return T <= kMoeFewMaxTokens && T * k <= kMoeFewMaxPairs;
+}
+size_t moe_few_workspace_bytes(int64_t T, int64_t k, int64_t H, int64_t I);
+void moe_few_zeroes(const MoeFewProblem &p, uint32_t **words, int *n);
+cudaError_t launch_moe_few(const MoeFewProblem &p, int num_sms, cudaStream_t stream);
 
 cudaError_t launch_gemm(const GemmProblem &p, int num_sms, cudaStream_t stream);
 

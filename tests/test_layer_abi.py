@@ -1,0 +1,99 @@
+"""CPU tests of the refusals of a decoder layer's calls: bad arguments are rejected on the
+host, by status, before any device work; and a rule of their sources."""
+import os
+import re
+
+import pytest
+
+OK, INVALID, WORKSPACE = 0, 1, 4
+A = 1 << 20          # an aligned address that is never read
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                    "moe_gemm_gb300", "csrc")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import __graft_entry__
+    __graft_entry__._build_module().build()
+    import moe_gemm_gb300 as w8
+    return w8.lib()
+
+
+def call(f, order, base, **change):
+    args = dict(base, **change)
+    return f(*[args[n] for n in order])
+
+
+APPEND = ("q qt qh Hq k kt kh v vt vh positions slots inv_freq rot interleaved amplitude T Hkv d P "
+          "page out ot oh kc ks vc vs stream").split()
+APPEND_OK = dict(q=A, qt=8192, qh=128, Hq=64, k=A, kt=1024, kh=128, v=A, vt=1024, vh=128,
+                 positions=A, slots=A, inv_freq=A, rot=128, interleaved=0, amplitude=1.0, T=0,
+                 Hkv=8, d=128, P=10, page=64, out=A, ot=8192, oh=128, kc=A, ks=A, vc=A, vs=A,
+                 stream=None)
+
+
+def test_append(lib):
+    f = lib.w8a8_paged_kv_append
+    assert call(f, APPEND, APPEND_OK) == OK                      # no tokens
+    assert call(f, APPEND, APPEND_OK, ks=None, vs=None, q=None, out=None, Hq=0) == OK
+    for bad in (dict(T=-1), dict(Hq=-1), dict(Hq=65536), dict(Hkv=0), dict(Hkv=65536), dict(d=64),
+                dict(P=0), dict(page=0), dict(P=1 << 26), dict(T=1 << 30), dict(rot=0),
+                dict(rot=8), dict(rot=24), dict(rot=144), dict(amplitude=float("inf")),
+                dict(qt=4), dict(qh=-8), dict(kt=1028), dict(vh=4), dict(ot=12), dict(oh=-8),
+                dict(ks=None), dict(vs=None), dict(T=1, q=None), dict(T=1, out=None),
+                dict(T=1, q=A + 8), dict(T=1, out=A + 8), dict(T=1, k=None), dict(T=1, v=A + 8),
+                dict(T=1, positions=None), dict(T=1, positions=A + 2), dict(T=1, slots=None),
+                dict(T=1, inv_freq=None), dict(T=1, inv_freq=A + 1), dict(T=1, kc=A + 4),
+                dict(T=1, vc=None), dict(T=1, ks=A + 2)):
+        assert call(f, APPEND, APPEND_OK, **bad) == INVALID, bad
+
+
+LAYER = ("x ldx logits ldt ld T k H I E score bias n_group topk_group renorm scale qu su qd sd ids "
+         "w y ydt ws wsb stream").split()
+LAYER_OK = dict(x=A, ldx=1024, logits=A, ldt=1, ld=64, T=0, k=8, H=1024, I=512, E=64, score=0,
+                bias=None, n_group=1, topk_group=1, renorm=1, scale=1.0, qu=A, su=A, qd=A, sd=A,
+                ids=A, w=A, y=A, ydt=0, ws=A, wsb=1 << 40, stream=None)
+
+
+def test_layer(lib):
+    f = lib.w8a8_moe_layer
+    assert call(f, LAYER, LAYER_OK) == OK
+    for bad in (dict(T=-1), dict(k=0), dict(k=65), dict(H=1000), dict(I=0), dict(I=100),
+                dict(I=8320), dict(E=0), dict(E=1025), dict(E=4), dict(ld=63), dict(ldt=2),
+                dict(ydt=2), dict(score=3), dict(n_group=7), dict(topk_group=2),
+                dict(scale=float("nan")), dict(ldx=1023), dict(T=1, x=None), dict(T=1, x=A + 1),
+                dict(T=1, logits=None), dict(T=1, qu=A + 8), dict(T=1, qd=None), dict(T=1, su=A + 2),
+                dict(T=1, sd=None), dict(T=1, ids=None), dict(T=1, w=A + 2), dict(T=1, y=A + 8),
+                dict(T=1, bias=A + 1)):
+        assert call(f, LAYER, LAYER_OK, **bad) == INVALID, bad
+    for T in (1, 32, 33):
+        need = lib.w8a8_moe_layer_workspace_size(T, 8, 1024, 512, 64)
+        assert need > 0 and need % 256 == 0
+        for bad in (dict(ws=None), dict(ws=A + 128), dict(wsb=need - 1)):
+            assert call(f, LAYER, dict(LAYER_OK, T=T), **bad) == WORKSPACE, bad
+    assert lib.w8a8_moe_layer_workspace_size(0, 8, 1024, 512, 64) == 0
+    assert lib.w8a8_moe_layer_workspace_size(4, 8, 1000, 512, 64) == 0
+
+
+@pytest.mark.parametrize("name", ["paged_append.cu", "moe_layer.cu"])
+def test_no_read_only_loads(name):
+    # They start while the kernel before may still write what they read.
+    with open(os.path.join(CSRC, name)) as f:
+        code = re.sub(r"//[^\n]*", "", f.read())
+    assert re.findall(r"__ldg|ld\.global(?:\.\w+)*\.nc|__restrict__", code) == []
+
+
+def test_binding_refuses_host_tensors(lib):
+    import torch
+
+    import moe_gemm_gb300 as w8
+    i = torch.zeros(1, dtype=torch.int32)
+    k = torch.zeros(1, 2, 128, dtype=torch.bfloat16)
+    c = torch.zeros(4, 2, 16, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        w8.paged_kv_append(k, k, k, i, i, torch.zeros(64), c, c)
+    x = torch.zeros(1, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        w8.moe_layer(x, torch.zeros(1, 4), 1, torch.zeros(4, 256, 128, dtype=torch.int8),
+                     torch.zeros(4, 256, 1), torch.zeros(4, 128, 128, dtype=torch.int8),
+                     torch.zeros(4, 128, 1))
