@@ -329,6 +329,57 @@ w8a8_status w8a8_w8a16_grouped_gemm(const void *a_bf16, int64_t lda, const int32
                                     int64_t K, w8a8_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * FP8 (e4m3) linear layers with a scale for each block of 128 ("Running DeepSeek-V4-
+ * Flash-Vision on 4xA800", §一: FP8 weights in [128, 128] blocks, power-of-two
+ * UE8M0 scales). Codes are e4m3 bytes (largest 448); activations have one FP32 scale
+ * per token and 128 K, weights one per [128, 128] block (the last rows' block
+ * may be lower). K is a positive multiple of 128.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Activations: a_bf16 [M, lda] BF16 (the first K columns); qa [M, K] codes, sa [M, K / 128]:
+ *   sa = amax / 448 of a token's group (IEEE division), or with W8A8_SCALE_POW2 the
+ *   smallest power of two >= amax / 448 (exponent in [-127, 127]);
+ *   qa = e4m3(a / sa): the quotient rounded to FP32 (exact for powers of two), then to
+ *   e4m3, ties to even.
+ * A group of zeros has codes 0 and scale 0 (2^-127). Inputs must be finite. qa 16-byte
+ * aligned. M == 0 is a no-op.
+ */
+w8a8_status w8a8_quant_act_fp8(const void *a_bf16, int64_t M, int64_t K, int64_t lda, void *qa,
+                               float *sa, w8a8_scale_mode mode, w8a8_stream_t stream);
+
+/* Weights: w [N, K] float (16-byte aligned); qw [N, K] codes, sw [ceil(N / 128), K / 128], in
+ * the same way over [128, 128] blocks. N <= 8,388,480; N == 0 is a no-op. */
+w8a8_status w8a8_quant_weight_fp8(const float *w, int64_t N, int64_t K, w8a8_scale_mode mode,
+                                  void *qw, float *sw, w8a8_stream_t stream);
+
+/*
+ * y[m, n] = sum_g sa[m, g] * sw[n / 128, g] * P[m, n, g], P[m, n, g] = sum over the 128 k of
+ * group g of qa[m, k] * qw[n, k].
+ *   qa [M, K], sa [M, K / 128], qw [N, K], sw [ceil(N / 128), K / 128]; y [M, N] BF16 or FP32.
+ * Any scales whose products sa * sw are finite. The products of two e4m3 numbers are
+ * exact in FP32; the tensor cores sum a group's in FP32 (128 additions, each off by 2^-23 of
+ * its result at most), then the groups are added in K order, acc = fma(P, sa * sw, acc).
+ * FP32 outputs are within (2^-16 + (K / 128 + 1) * 2^-24) * T of the exact value, T =
+ * sum |sa * sw * qa * qw| (tested).
+ * Results do not depend on the other rows of the call. No workspace. qa, qw 16-byte aligned;
+ * M * K, N * K and M * N below 2^31. M == 0 is a no-op.
+ */
+w8a8_status w8a8_gemm_fp8(const void *qa, const float *sa, const void *qw, const float *sw,
+                          void *y, w8a8_dtype y_dtype, int64_t M, int64_t N, int64_t K,
+                          w8a8_stream_t stream);
+
+/*
+ * w8a8_quant_act_fp8 and w8a8_gemm_fp8 in one call, the same result. workspace:
+ * w8a8_linear_fp8_workspace_size bytes (codes and scales), 256-byte aligned, scratch.
+ */
+size_t w8a8_linear_fp8_workspace_size(int64_t M, int64_t N, int64_t K);
+w8a8_status w8a8_linear_fp8(const void *a_bf16, int64_t lda, w8a8_scale_mode act_mode,
+                            const void *qw, const float *sw, void *y, w8a8_dtype y_dtype, int64_t M,
+                            int64_t N, int64_t K, void *workspace, size_t workspace_bytes,
+                            w8a8_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * MoE expert FFN ("Deploying Hunyuan 770B in INT8 on domestic accelerators":
  * §4.4, tokens are counted per destination expert first and then
  * transferred; §4.1 operator table, SwiGLU between the INT8 expert GEMMs;

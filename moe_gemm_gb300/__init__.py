@@ -10,6 +10,7 @@ Functions (names match the C entry points):
   quant_weight(w_f32)                     -> (qw int8 [N,K], sw f32 [N,K/128])
   gemm(qa, sa, qw, sw, out_dtype, ...)    -> y [M,N]  (+ partials when debug)
   grouped_gemm(qa, sa, offsets, qw, sw, out_dtype, ...) -> y [R,N]
+FP8 with a scale per block of 128: quant_act_fp8, quant_weight_fp8, gemm_fp8, linear_fp8.
 Serving: moe_gate (expert ids and weights for moe_ffn), moe_layer (both, for a decode
 step's tokens in two kernels), and the paged KV cache: paged_kv_plan (block tables and
 slots), paged_kv_write, paged_kv_append (with the position rotation), attention_paged.
@@ -118,6 +119,13 @@ def _load() -> ctypes.CDLL:
     lib.w8a8_moe_layer.argtypes = [vp, i64, vp, i32, i64, i64, i64, i64, i64, i64, i32, vp, i64,
                                    i64, i32, ctypes.c_float, vp, vp, vp, vp, vp, vp, vp, i32, vp,
                                    ctypes.c_size_t, vp]
+    lib.w8a8_quant_act_fp8.argtypes = [vp, i64, i64, i64, vp, vp, i32, vp]
+    lib.w8a8_quant_weight_fp8.argtypes = [vp, i64, i64, i32, vp, vp, vp]
+    lib.w8a8_gemm_fp8.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i64, vp]
+    lib.w8a8_linear_fp8_workspace_size.argtypes = [i64, i64, i64]
+    lib.w8a8_linear_fp8_workspace_size.restype = ctypes.c_size_t
+    lib.w8a8_linear_fp8.argtypes = [vp, i64, i32, vp, vp, vp, i32, i64, i64, i64, vp,
+                                    ctypes.c_size_t, vp]
     lib.w8a8_version.restype = i32
     for name in ("w8a8_quant_act", "w8a8_quant_weight", "w8a8_gemm", "w8a8_grouped_gemm",
                  "w8a8_gemm_noalloc", "w8a8_device_error", "w8a8_selftest_wait_timeout",
@@ -130,7 +138,8 @@ def _load() -> ctypes.CDLL:
                  "w8a8_attention_decode_bf16kv", "w8a8_rmsnorm", "w8a8_rmsnorm_quant",
                  "w8a8_rmsnorm_linear", "w8a8_moe_gate", "w8a8_paged_kv_plan",
                  "w8a8_paged_kv_write", "w8a8_attention_paged", "w8a8_paged_kv_append",
-                 "w8a8_moe_layer"):
+                 "w8a8_moe_layer", "w8a8_quant_act_fp8", "w8a8_quant_weight_fp8", "w8a8_gemm_fp8",
+                 "w8a8_linear_fp8"):
         getattr(lib, name).restype = i32
     return lib
 
@@ -626,6 +635,104 @@ def w8a16_grouped_gemm(a: torch.Tensor, offsets: torch.Tensor, qw: torch.Tensor,
         _check(_lib.w8a8_w8a16_grouped_gemm(_ptr(a), lda, _ptr(offsets), _ptr(qw), _ptr(sw),
                                             sw_block_rows, _ptr(out), code, R, E, N, K,
                                             _stream(stream)), "w8a8_w8a16_grouped_gemm")
+    return out
+
+
+# --------------------------------------- FP8 (e4m3) with a scale per block of 128
+def quant_act_fp8(a: torch.Tensor, qa: Optional[torch.Tensor] = None,
+                  sa: Optional[torch.Tensor] = None, scale_mode: int = SCALE_AMAX,
+                  stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """FP8 quantization of BF16 activations a [M, K] per token and 128 K: (qa
+    float8_e4m3fn [M, K], sa float32 [M, K / 128]); scales amax / 448, or powers of two."""
+    lda = _require_act(a)
+    dev = a.device
+    M, K = a.shape
+    if qa is None:
+        qa = _empty((M, K), torch.float8_e4m3fn, dev, stream)
+    else:
+        _require(qa, torch.float8_e4m3fn, "qa", 2, (M, K), dev)
+    if sa is None:
+        sa = _empty((M, K // GROUP), torch.float32, dev, stream)
+    else:
+        _require(sa, torch.float32, "sa", 2, (M, K // GROUP), dev)
+    with _on_device(dev, stream):
+        _check(_lib.w8a8_quant_act_fp8(_ptr(a), M, K, lda if M > 1 else K, _ptr(qa), _ptr(sa),
+                                       scale_mode, _stream(stream)), "w8a8_quant_act_fp8")
+    return qa, sa
+
+
+def quant_weight_fp8(w: torch.Tensor, scale_mode: int = SCALE_AMAX,
+                     stream: Optional[torch.cuda.Stream] = None
+                     ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """FP8 quantization of FP32 weights w [N, K] over [128, 128] blocks: (qw float8_e4m3fn
+    [N, K], sw float32 [ceil(N / 128), K / 128])."""
+    _require(w, torch.float32, "w", 2)
+    N, K = w.shape
+    qw = _empty((N, K), torch.float8_e4m3fn, w.device, stream)
+    sw = _empty(((N + 127) // 128, K // GROUP), torch.float32, w.device, stream)
+    with _on_device(w.device, stream):
+        _check(_lib.w8a8_quant_weight_fp8(_ptr(w), N, K, scale_mode, _ptr(qw), _ptr(sw),
+                                          _stream(stream)), "w8a8_quant_weight_fp8")
+    return qw, sw
+
+
+def _require_fp8_weights(qw: torch.Tensor, sw: torch.Tensor, K: int, device: torch.device) -> int:
+    _require(qw, torch.float8_e4m3fn, "qw", 2, device=device)
+    N = qw.shape[0]
+    if qw.shape[1] != K:
+        raise ValueError(f"qw: expected K = {K} columns, got {qw.shape[1]}")
+    _require(sw, torch.float32, "sw", 2, ((N + 127) // 128, K // GROUP), device)
+    return N
+
+
+def gemm_fp8(qa: torch.Tensor, sa: torch.Tensor, qw: torch.Tensor, sw: torch.Tensor,
+             out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+             stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Y[M,N] = sum_g sa[m, g] * sw[n / 128, g] * P[m,n,g] of e4m3 codes qa [M, K], qw
+    [N, K] (float8_e4m3fn) with scales sa [M, K/128], sw [ceil(N/128), K/128]."""
+    _require(qa, torch.float8_e4m3fn, "qa", 2)
+    dev = qa.device
+    M, K = qa.shape
+    _require(sa, torch.float32, "sa", 2, (M, K // GROUP), dev)
+    N = _require_fp8_weights(qw, sw, K, dev)
+    code = _dtype_code(out_dtype)
+    if out is None:
+        out = _empty((M, N), out_dtype, dev, stream)
+    else:
+        _require_out(out, out_dtype, (M, N), dev)
+    with _on_device(dev, stream):
+        _check(_lib.w8a8_gemm_fp8(_ptr(qa), _ptr(sa), _ptr(qw), _ptr(sw), _ptr(out), code, M, N, K,
+                                  _stream(stream)), "w8a8_gemm_fp8")
+    return out
+
+
+def linear_fp8_workspace_size(M: int, N: int, K: int) -> int:
+    return int(_lib.w8a8_linear_fp8_workspace_size(M, N, K))
+
+
+def linear_fp8(a: torch.Tensor, qw: torch.Tensor, sw: torch.Tensor,
+               out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None,
+               stream: Optional[torch.cuda.Stream] = None,
+               act_scale_mode: int = SCALE_AMAX) -> torch.Tensor:
+    """quant_act_fp8 + gemm_fp8 in one call: Y[M,N] from BF16 activations a [M, K]."""
+    lda = _require_act(a)
+    dev = a.device
+    M, K = a.shape
+    N = _require_fp8_weights(qw, sw, K, dev)
+    code = _dtype_code(out_dtype)
+    if out is None:
+        out = _empty((M, N), out_dtype, dev, stream)
+    else:
+        _require_out(out, out_dtype, (M, N), dev)
+    if workspace is None:
+        workspace = _empty((max(linear_fp8_workspace_size(M, N, K), 1),), torch.uint8, dev, stream)
+    else:
+        _require_workspace(workspace, dev)
+    with _on_device(dev, stream):
+        _check(_lib.w8a8_linear_fp8(_ptr(a), lda if M > 1 else K, act_scale_mode, _ptr(qw),
+                                    _ptr(sw), _ptr(out), code, M, N, K, _ptr(workspace),
+                                    workspace.numel(), _stream(stream)), "w8a8_linear_fp8")
     return out
 
 

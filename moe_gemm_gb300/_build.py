@@ -13,7 +13,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libw8a8.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["api.cu", "quant.cu", "gemm.cu", "probe.cu", "moe.cu", "attention.cu",
-           "gate.cu", "moe_layer.cu", "paged_kv.cu", "paged_append.cu", "paged_attention.cu",
+           "gemm_fp8.cu", "quant_fp8.cu", "gate.cu", "moe_layer.cu", "paged_kv.cu", "paged_append.cu", "paged_attention.cu",
            "paged_attention_tiles.cu"]
 HEADERS = ["common.cuh", "quant_math.cuh", "moe_math.cuh", "attention_math.cuh", "paged_schedule.cuh",
            "paged_attention.cuh",

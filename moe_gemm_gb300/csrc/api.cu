@@ -1226,6 +1226,114 @@ w8a8_status w8a8_moe_layer(const void *x_bf16, int64_t ldx, const void *logits,
     return from_cuda(e);
 }
 
+namespace {
+
+// Shapes of the FP8 calls; the tokens' and the weights' operands.
+w8a8_status check_fp8(const void *a, int64_t a_align, const void *qw, const float *sw,
+                      const void *y, w8a8_dtype y_dtype, int64_t M, int64_t N, int64_t K) {
+    if (y_dtype != W8A8_BF16 && y_dtype != W8A8_FP32) return W8A8_ERR_INVALID_ARG;
+    if (M < 0 || N < 1 || K < 1 || K % W8A8_GROUP != 0 || M > kMaxElems / K ||
+        N > kMaxElems / K || M > kMaxElems / N)
+        return W8A8_ERR_INVALID_ARG;
+    if (M == 0) return W8A8_OK;
+    if (!a || !qw || !sw || !y || !aligned(a, a_align) || !aligned(qw, 16) || !aligned(sw, 4) ||
+        !aligned(y, y_dtype == W8A8_FP32 ? 4 : 2))
+        return W8A8_ERR_INVALID_ARG;
+    return W8A8_OK;
+}
+
+w8a8_status run_gemm_fp8(const void *qa, const float *sa, const void *qw, const float *sw, void *y,
+                         w8a8_dtype y_dtype, int64_t M, int64_t N, int64_t K, int num_sms,
+                         w8a8_stream_t stream) {
+    w8a8::Fp8Problem p;
+    p.qa = qa;
+    p.sa = sa;
+    p.qw = qw;
+    p.sw = sw;
+    p.y = y;
+    p.out_fp32 = y_dtype == W8A8_FP32;
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    return from_cuda(w8a8::launch_gemm_fp8(p, num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+w8a8_status w8a8_quant_act_fp8(const void *a_bf16, int64_t M, int64_t K, int64_t lda, void *qa,
+                               float *sa, w8a8_scale_mode mode, w8a8_stream_t stream) {
+    if (mode != W8A8_SCALE_AMAX && mode != W8A8_SCALE_POW2) return W8A8_ERR_INVALID_ARG;
+    if (M < 0 || K < 1 || K % W8A8_GROUP != 0 || lda < K || M > kMaxElems / lda)
+        return W8A8_ERR_INVALID_ARG;
+    if (M == 0) return W8A8_OK;
+    if (!a_bf16 || !qa || !sa || !aligned(a_bf16, 2) || !aligned(qa, 16) || !aligned(sa, 4))
+        return W8A8_ERR_INVALID_ARG;
+    w8a8::DeviceInfo info;
+    w8a8_status st = check_device(&info);
+    if (st != W8A8_OK) return st;
+    return from_cuda(w8a8::launch_quant_act_fp8(static_cast<const uint16_t *>(a_bf16), M, K, lda,
+                                                qa, sa, mode == W8A8_SCALE_POW2,
+                                                reinterpret_cast<cudaStream_t>(stream)));
+}
+
+w8a8_status w8a8_quant_weight_fp8(const float *w, int64_t N, int64_t K, w8a8_scale_mode mode,
+                                  void *qw, float *sw, w8a8_stream_t stream) {
+    if (mode != W8A8_SCALE_AMAX && mode != W8A8_SCALE_POW2) return W8A8_ERR_INVALID_ARG;
+    // (a grid's second dimension holds 65535 blocks of rows)
+    if (N < 0 || K < 1 || K % W8A8_GROUP != 0 || N > kMaxElems / K || N > 65535 * 128)
+        return W8A8_ERR_INVALID_ARG;
+    if (N == 0) return W8A8_OK;
+    if (!w || !qw || !sw || !aligned(w, 16) || !aligned(qw, 16) || !aligned(sw, 4))
+        return W8A8_ERR_INVALID_ARG;
+    w8a8::DeviceInfo info;
+    w8a8_status st = check_device(&info);
+    if (st != W8A8_OK) return st;
+    return from_cuda(w8a8::launch_quant_weight_fp8(w, N, K, mode == W8A8_SCALE_POW2, qw, sw,
+                                                   reinterpret_cast<cudaStream_t>(stream)));
+}
+
+w8a8_status w8a8_gemm_fp8(const void *qa, const float *sa, const void *qw, const float *sw,
+                          void *y, w8a8_dtype y_dtype, int64_t M, int64_t N, int64_t K,
+                          w8a8_stream_t stream) {
+    w8a8_status st = check_fp8(qa, 16, qw, sw, y, y_dtype, M, N, K);
+    if (st != W8A8_OK || M == 0) return st;
+    if (!sa || !aligned(sa, 4)) return W8A8_ERR_INVALID_ARG;
+    w8a8::DeviceInfo info;
+    st = check_device(&info);
+    if (st != W8A8_OK) return st;
+    return run_gemm_fp8(qa, sa, qw, sw, y, y_dtype, M, N, K, info.num_sms, stream);
+}
+
+size_t w8a8_linear_fp8_workspace_size(int64_t M, int64_t N, int64_t K) {
+    if (M <= 0 || N < 1 || K < 1 || K % W8A8_GROUP != 0 || M > kMaxElems / K) return 0;
+    return round_up(static_cast<size_t>(M) * K, kWsAlign) +
+           round_up(static_cast<size_t>(M) * (K / W8A8_GROUP) * 4, kWsAlign);
+}
+
+w8a8_status w8a8_linear_fp8(const void *a_bf16, int64_t lda, w8a8_scale_mode act_mode,
+                            const void *qw, const float *sw, void *y, w8a8_dtype y_dtype, int64_t M,
+                            int64_t N, int64_t K, void *workspace, size_t workspace_bytes,
+                            w8a8_stream_t stream) {
+    if (act_mode != W8A8_SCALE_AMAX && act_mode != W8A8_SCALE_POW2) return W8A8_ERR_INVALID_ARG;
+    w8a8_status st = check_fp8(a_bf16, 2, qw, sw, y, y_dtype, M, N, K);
+    if (st != W8A8_OK) return st;
+    if (lda < K || M > kMaxElems / lda) return W8A8_ERR_INVALID_ARG;
+    if (M == 0) return W8A8_OK;
+    if (!workspace || !aligned(workspace, kWsAlign) ||
+        workspace_bytes < w8a8_linear_fp8_workspace_size(M, N, K))
+        return W8A8_ERR_WORKSPACE;
+    w8a8::DeviceInfo info;
+    st = check_device(&info);
+    if (st != W8A8_OK) return st;
+    float *sa = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) +
+                                          round_up(static_cast<size_t>(M) * K, kWsAlign));
+    if (w8a8::launch_quant_act_fp8(static_cast<const uint16_t *>(a_bf16), M, K, lda, workspace, sa,
+                                   act_mode == W8A8_SCALE_POW2,
+                                   reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return W8A8_ERR_CUDA;
+    return run_gemm_fp8(workspace, sa, qw, sw, y, y_dtype, M, N, K, info.num_sms, stream);
+}
+
 w8a8_status w8a8_selftest_wait_timeout(uint32_t limit_us, w8a8_stream_t stream) {
     if (limit_us == 0 || limit_us > 2000000u) return W8A8_ERR_INVALID_ARG;
     w8a8::DeviceInfo info;

@@ -1,0 +1,488 @@
+// Product of FP8 (e4m3) activations and weights with a scale for each block of 128, on the
+// tcgen05 tensor cores of sm_103a ("Running DeepSeek-V4-Flash-Vision on 4xA800", §一:
+// FP8 weights in [128, 128] blocks):
+//
+//   y[m, n] = sum_g (sa[m, g] sw[n / 128, g]) P_g[m, n],  P_g = sum over k in group g of
+//   qa[m, k] qw[n, k]
+//
+// The scales change every 128 K, so a group's products are summed by themselves in tensor
+// memory (kind::f8f6f4, FP32), and the groups are added up in registers, acc = fma(P_g,
+// sa sw, acc), in K order. A token is a lane of tensor memory, so a thread has one token and
+// its scale is one number per group and block.
+//
+// A tile is 128 tokens (the M of an instruction) by a slice of w <= 256 weight rows, over
+// all of K. A step is a group: 128 bytes of every row, one 128-byte swizzle atom
+// wide, four instructions of 32 K. The slices are as wide as makes the waves of
+// tiles fullest: a decode step's weights then divide evenly among the SMs with no split of K.
+//
+// Warps: 0 loads (TMA), 1 issues the products, 4-7 and 8-11 add up a half of the slice
+// each (128 lanes), 2 and 3 only give up their registers.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+#include "internal.h"
+#include "quant_math.cuh"
+#include "tensor_map.h"
+
+namespace w8a8 {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kTokens = 128;
+constexpr int kMaxSlice = 256;
+constexpr int kMaxStages = 16, kMaxBufs = 8;
+constexpr int kSmemBytes = 227 * 1024;
+constexpr int kOffStages = 1024;           // barriers and flags before them
+constexpr int kTmemCols = 512;
+// 384 threads are launched with 168 registers; the 256 that add up get 216, the others 72.
+constexpr uint32_t kSumRegs = 216, kOtherRegs = 72;
+static_assert(256 * kSumRegs + 128 * kOtherRegs == kThreads * 168);
+
+struct Fp8Args {
+    const float *sa, *sw;
+    void *y;
+    int M, N, G;
+    int w, half;               // rows of a slice, and of the first half of it
+    int a_bytes, b_bytes;      // of a stage
+    int a_box, b_box;          // bytes that a copy brings
+    int stages, bufs, buf_cols;
+    int m_tiles, tiles;
+    int n_mma;                 // the slice in an instruction's N
+    int out_fp32, wide_store;  // rows of y allow 32-byte stores
+    unsigned long long *err;
+};
+
+struct Bars {
+    uint64_t full[kMaxStages], empty[kMaxStages], d_full[kMaxBufs], d_empty[kMaxBufs], drain;
+    uint32_t tmem;
+    volatile int abort_flag;
+};
+static_assert(sizeof(Bars) <= kOffStages);
+
+struct Ring {
+    uint32_t idx = 0, phase = 0;
+    __device__ __forceinline__ void advance(uint32_t n) {
+        if (++idx == n) {
+            idx = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
+}
+
+// Instruction descriptor, kind::f8f6f4: e4m3 operands (format 0), FP32 sums, both K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3(uint32_t M, uint32_t N) {
+    return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
+// Upper word of a K-major operand's descriptor with the 128-byte swizzle, 8-row groups
+// 1024 bytes apart; the lower word is the address in units of 16 bytes.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+
+template <bool kAccumulate>
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n"
+        " mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "n"(kAccumulate ? 1 : 0), "n"(kDescHi)
+        : "memory");
+}
+
+// 32 columns of the warp's 32 lanes; the registers are valid after tmem_wait32 on them.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                   "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                   "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+
+// A load that stays where it is written (an ordinary one: the kernel before may have
+// written the scales while this one had started).
+__device__ __forceinline__ float ld_now(const float *p) {
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ unsigned long long f2_fma(unsigned long long a, unsigned long long b,
+                                                     unsigned long long c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+__device__ __forceinline__ void store32(void *p, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// One thread's outputs: kCols consecutive columns of a row, `cols` of them in the matrix.
+template <int kCols>
+__device__ __forceinline__ void store_row(const Fp8Args &a, int64_t at, int cols,
+                                          const unsigned long long (&acc)[kCols / 2]) {
+    if (a.out_fp32) {
+        float *y = static_cast<float *>(a.y) + at;
+#pragma unroll
+        for (int i = 0; i < kCols / 8; ++i) {
+            if (8 * i >= cols) break;
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f2_split(acc[4 * i + j], v[2 * j], v[2 * j + 1]);
+            if (a.wide_store && 8 * i + 8 <= cols) {
+                uint32_t u[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(v[j]);
+                store32(y + 8 * i, u);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (8 * i + j < cols) y[8 * i + j] = v[j];
+            }
+        }
+    } else {
+        __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(a.y) + at;
+#pragma unroll
+        for (int i = 0; i < kCols / 16; ++i) {
+            if (16 * i >= cols) break;
+            float v[16];
+            uint32_t u[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                f2_split(acc[8 * i + j], v[2 * j], v[2 * j + 1]);
+                const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+                u[j] = *reinterpret_cast<const uint32_t *>(&b);
+            }
+            if (a.wide_store && 16 * i + 16 <= cols) {
+                store32(y + 16 * i, u);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (16 * i + j < cols) y[16 * i + j] = __float2bfloat16_rn(v[j]);
+            }
+        }
+    }
+}
+
+// kCols: columns of a half of the slice, at most (32, 64 or 128).
+template <int kCols>
+__global__ void __launch_bounds__(kThreads, 1)
+gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmap_a,
+                const __grid_constant__ CUtensorMap tmap_b, const Fp8Args a) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    Bars &s = *reinterpret_cast<Bars *>(smem_raw + (base - raw));
+    const uint32_t sA = base + kOffStages;
+    const uint32_t sB = sA + a.stages * a.a_bytes;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < a.stages; ++i) {
+            mbar_init(smem_u32(&s.full[i]), 1);
+            mbar_init(smem_u32(&s.empty[i]), 1);
+        }
+        for (int i = 0; i < a.bufs; ++i) {
+            mbar_init(smem_u32(&s.d_full[i]), 1);
+            mbar_init(smem_u32(&s.d_empty[i]), 8);
+        }
+        mbar_init(smem_u32(&s.drain), 1);
+        s.abort_flag = 0;
+        fence_mbarrier_init();
+        tma_prefetch_desc(&tmap_a);
+        tma_prefetch_desc(&tmap_b);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&s.tmem), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s.tmem;
+    volatile int *abort_flag = &s.abort_flag;
+    griddep_launch_dependents();
+    griddep_wait();          // the codes and scales may come from the kernel launched before
+
+    if (warp < 4) {
+        setmaxnreg_dec<kOtherRegs>();
+        if (warp == 0 && lane == 0) {
+            // ------------------------------------------------------- TMA producer
+            Ring r;
+            uint32_t issued = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; t < a.tiles && ok; t += gridDim.x) {
+                const int n = t / a.m_tiles;
+                const int m0 = (t - n * a.m_tiles) * kTokens, n0 = n * a.w;
+                for (int g = 0; g < a.G; ++g) {
+                    if (!mbar_wait(smem_u32(&s.empty[r.idx]), r.phase ^ 1u, abort_flag, a.err,
+                                   ROLE_PRODUCER, 0, kWaitLimitNs, KID_FP8)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = smem_u32(&s.full[r.idx]);
+                    mbar_arrive_expect_tx(bar, a.a_box + a.b_box);
+                    tma_load_2d(sB + r.idx * a.b_bytes, &tmap_b, g * 128, n0, bar);
+                    tma_load_2d(sA + r.idx * a.a_bytes, &tmap_a, g * 128, m0, bar);
+                    r.advance(a.stages);
+                    ++issued;
+                }
+            }
+            if (!ok) {       // the copies in flight land before the CTA goes
+                const uint32_t n = a.stages;
+                for (uint32_t i = issued > n ? issued - n : 0; i < issued; ++i) {
+                    const unsigned long long t0 = globaltimer_ns();
+                    while (!mbar_try_wait(smem_u32(&s.full[i % n]), (i / n) & 1u) &&
+                           globaltimer_ns() - t0 < kWaitLimitNs) {
+                    }
+                }
+            }
+        } else if (warp == 1) {
+            // ------------------------------------------------------- products
+            Ring r, d;
+            bool ok = true;
+            const uint32_t idesc = idesc_e4m3(kTokens, a.n_mma);
+            for (int t = blockIdx.x; t < a.tiles && ok; t += gridDim.x) {
+                for (int g = 0; g < a.G; ++g) {
+                    ok = mbar_wait(smem_u32(&s.d_empty[d.idx]), d.phase ^ 1u, abort_flag, a.err,
+                                   ROLE_MMA, 0, kWaitLimitNs, KID_FP8) &&
+                         mbar_wait(smem_u32(&s.full[r.idx]), r.phase, abort_flag, a.err, ROLE_MMA,
+                                   1, kWaitLimitNs, KID_FP8);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t da = desc_lo(sA + r.idx * a.a_bytes);
+                    const uint32_t db = desc_lo(sB + r.idx * a.b_bytes);
+                    const uint32_t dt = tmem + d.idx * a.buf_cols;
+                    if (elect_one()) {
+                        mma_e4m3<false>(dt, da, db, idesc);
+                        mma_e4m3<true>(dt, da + 2, db + 2, idesc);
+                        mma_e4m3<true>(dt, da + 4, db + 4, idesc);
+                        mma_e4m3<true>(dt, da + 6, db + 6, idesc);
+                        mma_commit(smem_u32(&s.empty[r.idx]));
+                        mma_commit(smem_u32(&s.d_full[d.idx]));
+                    }
+                    __syncwarp();
+                    r.advance(a.stages);
+                    d.advance(a.bufs);
+                }
+            }
+            if (elect_one()) mma_commit(smem_u32(&s.drain));
+            __syncwarp();
+            const unsigned long long t0 = globaltimer_ns();
+            while (!mbar_try_wait(smem_u32(&s.drain), 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
+            }
+        }
+    } else {
+        // ----------------------------------------------------------- sums of groups
+        setmaxnreg_inc<kSumRegs>();
+        const int h = (warp >> 2) - 1, q = warp & 3;
+        const uint32_t my_tmem = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * a.half;
+        Ring d;
+        bool ok = true;
+        for (int t = blockIdx.x; t < a.tiles && ok; t += gridDim.x) {
+            const int n = t / a.m_tiles;
+            const int m0 = (t - n * a.m_tiles) * kTokens;
+            const int c0 = n * a.w + h * a.half;
+            const int cols = min(h == 0 ? a.half : a.w - a.half, a.N - c0);
+            const bool on = m0 + q * 32 < a.M && cols > 0;   // the same for the warp
+            const int m = m0 + q * 32 + lane;
+            // columns before `edge` have the scale of block c0 / 128, the others of the next
+            const int edge = 128 - (c0 & 127);
+            const float *sa = a.sa + static_cast<int64_t>(min(m, a.M - 1)) * a.G;
+            const float *sw0 = a.sw + static_cast<int64_t>(on ? c0 >> 7 : 0) * a.G;
+            const float *sw1 = on && cols > edge ? sw0 + a.G : sw0;
+            unsigned long long acc[kCols / 2];
+#pragma unroll
+            for (int j = 0; j < kCols / 2; ++j) acc[j] = 0ull;
+            float fa = 0.0f, f0 = 0.0f, f1 = 0.0f;
+            if (on) {
+                fa = ld_now(sa);
+                f0 = ld_now(sw0);
+                f1 = ld_now(sw1);
+            }
+            for (int g = 0; g < a.G; ++g) {
+                const float s0 = fa * f0, s1 = fa * f1;
+                if (on && g + 1 < a.G) {
+                    fa = ld_now(sa + g + 1);
+                    f0 = ld_now(sw0 + g + 1);
+                    f1 = ld_now(sw1 + g + 1);
+                }
+                ok = mbar_wait(smem_u32(&s.d_full[d.idx]), d.phase, abort_flag, a.err,
+                               ROLE_EPILOGUE, 0, kWaitLimitNs, KID_FP8);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                if (on) {
+                    const uint32_t at = my_tmem + d.idx * a.buf_cols;
+                    uint32_t v[2][32];
+                    tmem_ld32(at, v[0]);
+#pragma unroll
+                    for (int c = 0; c < kCols / 32; ++c) {
+                        if (32 * c >= cols) break;
+                        tmem_wait32(v[c & 1]);
+                        if (c + 1 < kCols / 32 && 32 * c + 32 < cols)
+                            tmem_ld32(at + 32 * c + 32, v[(c + 1) & 1]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float f = 32 * c + 8 * i < edge ? s0 : s1;
+                            const unsigned long long f2 = f2_bits(f, f);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                unsigned long long &o = acc[16 * c + 4 * i + j];
+                                o = f2_fma(f2_bits(__uint_as_float(v[c & 1][8 * i + 2 * j]),
+                                                   __uint_as_float(v[c & 1][8 * i + 2 * j + 1])),
+                                           f2, o);
+                            }
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_relaxed(smem_u32(&s.d_empty[d.idx]));
+                d.advance(a.bufs);
+            }
+            if (ok && on && m < a.M)
+                store_row<kCols>(a, static_cast<int64_t>(m) * a.N + c0, cols, acc);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// A matrix of bytes [rows, K] in boxes of box_rows rows x 128 K.
+bool encode(CUtensorMap *map, const void *ptr, int64_t K, int64_t rows, int box_rows) {
+    auto fn = tensor_map_encode_fn();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(K)};
+    cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(ptr), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kCols>
+cudaError_t launch_as(const CUtensorMap &ta, const CUtensorMap &tb, const Fp8Args &a, int grid,
+                      cudaStream_t stream) {
+    static int attr_done[64] = {0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64 && !attr_done[dev]) {
+        // setmaxnreg.inc can only take registers that the CTA was launched with
+        cudaFuncAttributes fa;
+        if ((e = cudaFuncGetAttributes(&fa, gemm_fp8_kernel<kCols>)) != cudaSuccess) return e;
+        if (fa.numRegs * kThreads < static_cast<int>(256 * kSumRegs + 128 * kOtherRegs))
+            return cudaErrorInvalidConfiguration;
+        e = cudaFuncSetAttribute(gemm_fp8_kernel<kCols>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kSmemBytes);
+        if (e != cudaSuccess) return e;
+        attr_done[dev] = 1;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, gemm_fp8_kernel<kCols>, ta, tb, a);
+    if (e != cudaSuccess) return e;
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_fp8(const Fp8Problem &p, int num_sms, cudaStream_t stream) {
+    Fp8Args a;
+    a.sa = p.sa;
+    a.sw = p.sw;
+    a.y = p.y;
+    a.M = static_cast<int>(p.M);
+    a.N = static_cast<int>(p.N);
+    a.G = static_cast<int>(p.K >> 7);
+    a.m_tiles = (a.M + kTokens - 1) / kTokens;
+    // The slice's width: the least waves x width (a wave takes as long as its tiles are
+    // wide), the wider where two are level (fewer reads of the tokens).
+    int64_t best = INT64_MAX;
+    a.w = 8;
+    for (int w = 8; w <= kMaxSlice; w += w < 32 ? 8 : 16) {
+        const int64_t tiles = static_cast<int64_t>(a.m_tiles) * ((a.N + w - 1) / w);
+        const int64_t cost = (tiles + num_sms - 1) / num_sms * (w + 16);
+        if (cost <= best) {
+            best = cost;
+            a.w = w;
+        }
+    }
+    a.n_mma = (a.w + 15) / 16 * 16;
+    a.half = a.w <= 32 ? a.w : (a.w / 2 + 15) / 16 * 16;
+    const int a_rows = a.M >= kTokens ? kTokens : (a.M + 7) / 8 * 8;
+    a.a_box = a_rows * 128;
+    a.b_box = a.w * 128;
+    a.a_bytes = a.a_box;
+    a.b_bytes = a.n_mma * 128;
+    // An instruction reads 128 rows of tokens, past the last stage's where they are fewer:
+    // into the weights' stages, or what is kept free behind them. (Those lanes of
+    // tensor memory are never read.)
+    const int room = kSmemBytes - 1024 - kOffStages - 128 * 128;
+    a.stages = room / (a.a_bytes + a.b_bytes);
+    if (a.stages > kMaxStages) a.stages = kMaxStages;
+    a.buf_cols = a.w <= 64 ? 64 : a.w <= 128 ? 128 : 256;
+    a.bufs = kTmemCols / a.buf_cols;
+    const int64_t tiles = static_cast<int64_t>(a.m_tiles) * ((a.N + a.w - 1) / a.w);
+    if (tiles > INT32_MAX - 4096) return cudaErrorInvalidValue;
+    a.tiles = static_cast<int>(tiles);
+    a.out_fp32 = p.out_fp32;
+    const int per32 = p.out_fp32 ? 8 : 16;
+    a.wide_store = (reinterpret_cast<uintptr_t>(p.y) & 31) == 0 && a.N % per32 == 0 && a.w % per32 == 0;
+    cudaError_t e = device_error_word(&a.err);
+    if (e != cudaSuccess) return e;
+    CUtensorMap ta, tb;
+    if (!encode(&ta, p.qa, p.K, p.M, a_rows) || !encode(&tb, p.qw, p.K, p.N, a.w))
+        return cudaErrorInvalidValue;
+    const int grid = a.tiles < num_sms ? a.tiles : num_sms;
+    if (a.half <= 32) return launch_as<32>(ta, tb, a, grid, stream);
+    if (a.half <= 64) return launch_as<64>(ta, tb, a, grid, stream);
+    return launch_as<128>(ta, tb, a, grid, stream);
+}
+
+}  // namespace w8a8

@@ -257,6 +257,21 @@ cudaError_t launch_moe_few(const MoeFewProblem &p, int num_sms, cudaStream_t str
 
 cudaError_t launch_gemm(const GemmProblem &p, int num_sms, cudaStream_t stream);
 
+// FP8 (e4m3) with a scale per block of 128: quantizers (quant_fp8.cu) and the product
+// (gemm_fp8.cu).
+cudaError_t launch_quant_act_fp8(const uint16_t *a, int64_t M, int64_t K, int64_t lda, void *qa,
+                                 float *sa, bool pow2, cudaStream_t stream);
+cudaError_t launch_quant_weight_fp8(const float *w, int64_t N, int64_t K, bool pow2, void *qw,
+                                    float *sw, cudaStream_t stream);
+struct Fp8Problem {
+    const void *qa, *qw;             // e4m3 [M, K], [N, K]
+    const float *sa, *sw;            // [M, K / 128], [ceil(N / 128), K / 128]
+    void *y;                         // [M, N]
+    bool out_fp32;
+    int64_t M, N, K;
+};
+cudaError_t launch_gemm_fp8(const Fp8Problem &p, int num_sms, cudaStream_t stream);
+
 // Launches the bounded-wait diagnostic (see gemm.cu): its wait gives up after
 // limit_ns and records a code in the device error word.
 cudaError_t launch_selftest_wait(unsigned long long limit_ns, cudaStream_t stream);

@@ -75,7 +75,7 @@ def test_layer(lib):
     assert lib.w8a8_moe_layer_workspace_size(4, 8, 1000, 512, 64) == 0
 
 
-@pytest.mark.parametrize("name", ["paged_append.cu", "moe_layer.cu"])
+@pytest.mark.parametrize("name", ["paged_append.cu", "moe_layer.cu", "quant_fp8.cu", "gemm_fp8.cu"])
 def test_no_read_only_loads(name):
     # They start while the kernel before may still write what they read.
     with open(os.path.join(CSRC, name)) as f:
@@ -97,3 +97,44 @@ def test_binding_refuses_host_tensors(lib):
         w8.moe_layer(x, torch.zeros(1, 4), 1, torch.zeros(4, 256, 128, dtype=torch.int8),
                      torch.zeros(4, 256, 1), torch.zeros(4, 128, 128, dtype=torch.int8),
                      torch.zeros(4, 128, 1))
+
+
+GEMM8 = "qa sa qw sw y dtype M N K stream".split()
+GEMM8_OK = dict(qa=A, sa=A, qw=A, sw=A, y=A, dtype=0, M=0, N=1000, K=512, stream=None)
+LINEAR8 = "a lda mode qw sw y dtype M N K ws wsb stream".split()
+LINEAR8_OK = dict(a=A, lda=512, mode=0, qw=A, sw=A, y=A, dtype=0, M=0, N=1000, K=512, ws=A,
+                  wsb=1 << 40, stream=None)
+
+
+def test_fp8(lib):
+    f = lib.w8a8_gemm_fp8
+    assert call(f, GEMM8, GEMM8_OK) == OK
+    for bad in (dict(M=-1), dict(N=0), dict(K=0), dict(K=500), dict(dtype=2), dict(M=1 << 23),
+                dict(N=1 << 22), dict(M=1 << 21, K=128, N=1 << 10), dict(M=1, qa=None),
+                dict(M=1, qa=A + 8), dict(M=1, sa=None), dict(M=1, sa=A + 2), dict(M=1, qw=A + 4),
+                dict(M=1, sw=None), dict(M=1, y=None), dict(M=1, y=A + 1),
+                dict(M=1, y=A + 2, dtype=1)):
+        assert call(f, GEMM8, GEMM8_OK, **bad) == INVALID, bad
+    f = lib.w8a8_linear_fp8
+    assert call(f, LINEAR8, LINEAR8_OK) == OK
+    for bad in (dict(mode=2), dict(lda=511), dict(K=64), dict(M=1, a=None), dict(M=1, a=A + 1),
+                dict(M=-1), dict(M=1 << 20, lda=1 << 20)):
+        assert call(f, LINEAR8, LINEAR8_OK, **bad) == INVALID, bad
+    need = lib.w8a8_linear_fp8_workspace_size(3, 1000, 512)
+    assert need == 3 * 512 + 256
+    for bad in (dict(ws=None), dict(ws=A + 64), dict(wsb=need - 1)):
+        assert call(f, LINEAR8, dict(LINEAR8_OK, M=3), **bad) == WORKSPACE, bad
+    f = lib.w8a8_quant_act_fp8
+    order = "a M K lda qa sa mode stream".split()
+    ok = dict(a=A, M=0, K=256, lda=256, qa=A, sa=A, mode=0, stream=None)
+    assert call(f, order, ok) == OK
+    for bad in (dict(M=-1), dict(K=200), dict(lda=255), dict(mode=3), dict(M=1, qa=A + 8),
+                dict(M=1, a=None), dict(M=1, sa=A + 2)):
+        assert call(f, order, ok, **bad) == INVALID, bad
+    f = lib.w8a8_quant_weight_fp8
+    order = "w N K mode qw sw stream".split()
+    ok = dict(w=A, N=0, K=256, mode=0, qw=A, sw=A, stream=None)
+    assert call(f, order, ok) == OK
+    for bad in (dict(N=-1), dict(K=200), dict(mode=3), dict(N=1, w=A + 8), dict(N=1, qw=None),
+                dict(N=65535 * 128 + 1, K=128)):
+        assert call(f, order, ok, **bad) == INVALID, bad
