@@ -37,9 +37,11 @@ constexpr int kMaxSlice = 256;
 constexpr int kMaxStages = 16, kMaxBufs = 8;
 constexpr int kSmemBytes = 227 * 1024;
 constexpr int kOffStages = 1024;           // barriers and flags before them
+constexpr int kStagedBytes = 8 * 32 * 17 * 4;   // outputs on their way, at the end
 constexpr int kTmemCols = 512;
-// 384 threads are launched with 168 registers; the 256 that add up get 216, the others 72.
-constexpr uint32_t kSumRegs = 216, kOtherRegs = 72;
+// 384 threads are launched with 168 registers; the 256 that add up get 232, the others 40
+// (216 and 72: 221 -> 216 us at 4096 x 8192 x 8192).
+constexpr uint32_t kSumRegs = 232, kOtherRegs = 40;
 static_assert(256 * kSumRegs + 128 * kOtherRegs == kThreads * 168);
 
 struct Fp8Args {
@@ -53,6 +55,7 @@ struct Fp8Args {
     int m_tiles, tiles;
     int n_mma;                 // the slice in an instruction's N
     int out_fp32, wide_store;  // rows of y allow 32-byte stores
+    int words;                 // ... or 4-byte stores
     unsigned long long *err;
 };
 
@@ -147,48 +150,87 @@ __device__ __forceinline__ void store32(void *p, const uint32_t (&v)[8]) {
                  : "memory");
 }
 
-// One thread's outputs: kCols consecutive columns of a row, `cols` of them in the matrix.
+// One thread's outputs: kCols consecutive columns of a row, `cols` of them in the matrix (a
+// multiple of what a store of 32 bytes holds).
 template <int kCols>
 __device__ __forceinline__ void store_row(const Fp8Args &a, int64_t at, int cols,
                                           const unsigned long long (&acc)[kCols / 2]) {
-    if (a.out_fp32) {
-        float *y = static_cast<float *>(a.y) + at;
 #pragma unroll
-        for (int i = 0; i < kCols / 8; ++i) {
-            if (8 * i >= cols) break;
-            float v[8];
+    for (int i = 0; i < kCols / 16; ++i) {
+        if (16 * i >= cols) break;
+        float v[16];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) f2_split(acc[4 * i + j], v[2 * j], v[2 * j + 1]);
-            if (a.wide_store && 8 * i + 8 <= cols) {
-                uint32_t u[8];
+        for (int j = 0; j < 8; ++j) f2_split(acc[8 * i + j], v[2 * j], v[2 * j + 1]);
+        uint32_t u[8];
+        if (a.out_fp32) {
+            float *y = static_cast<float *>(a.y) + at + 16 * i;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(v[j]);
-                store32(y + 8 * i, u);
-            } else {
+            for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(v[j]);
+            store32(y, u);
+            if (16 * i + 8 < cols) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (8 * i + j < cols) y[8 * i + j] = v[j];
+                for (int j = 0; j < 8; ++j) u[j] = __float_as_uint(v[8 + j]);
+                store32(y + 8, u);
             }
-        }
-    } else {
-        __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(a.y) + at;
-#pragma unroll
-        for (int i = 0; i < kCols / 16; ++i) {
-            if (16 * i >= cols) break;
-            float v[16];
-            uint32_t u[8];
+        } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                f2_split(acc[8 * i + j], v[2 * j], v[2 * j + 1]);
                 const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
                 u[j] = *reinterpret_cast<const uint32_t *>(&b);
             }
-            if (a.wide_store && 16 * i + 16 <= cols) {
-                store32(y + 16 * i, u);
-            } else {
+            store32(static_cast<__nv_bfloat16 *>(a.y) + at + 16 * i, u);
+        }
+    }
+}
+
+// The same for a warp's 32 rows where rows of y do not allow that: through shared memory, so that
+// a store covers 64 bytes of a row instead of one value in each of 32.
+template <int kCols>
+__device__ __forceinline__ void store_staged(const Fp8Args &a, uint32_t *buf, int m0, int c0,
+                                             int cols,
+                                             const unsigned long long (&acc)[kCols / 2]) {
+    const int lane = threadIdx.x & 31;
+    const int per = a.out_fp32 ? 16 : 32;         // columns of 64 bytes
+    const int rows = min(32, a.M - m0);
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (16 * i + j < cols) y[16 * i + j] = __float2bfloat16_rn(v[j]);
+    for (int i = 0; i < kCols / 16; ++i) {
+        if (!a.out_fp32 && (i & 1)) continue;
+        if (16 * i >= cols) break;
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float x, y;
+            f2_split(acc[8 * i + j], x, y);
+            if (a.out_fp32) {
+                buf[lane * 17 + 2 * j] = __float_as_uint(x);
+                buf[lane * 17 + 2 * j + 1] = __float_as_uint(y);
+            } else {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+                buf[lane * 17 + j] = *reinterpret_cast<const uint32_t *>(&b);
+                if (i + 1 < kCols / 16) {
+                    f2_split(acc[8 * (i + 1 < kCols / 16 ? i + 1 : i) + j], x, y);
+                    const __nv_bfloat162 b2 = __floats2bfloat162_rn(x, y);
+                    buf[lane * 17 + 8 + j] = *reinterpret_cast<const uint32_t *>(&b2);
+                }
+            }
+        }
+        __syncwarp();
+        const int left = cols - 16 * i;           // columns from here on
+        if (a.words) {
+            const int w = lane & 15;
+            const bool mine = (a.out_fp32 ? w : 2 * w) < min(left, per);
+            for (int r = lane >> 4; r < rows; r += 2) {
+                const int64_t at = static_cast<int64_t>(m0 + r) * a.N + c0 + 16 * i;
+                uint32_t *row = a.out_fp32 ? static_cast<uint32_t *>(a.y) + at
+                                           : reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.y) + at);
+                if (mine) row[w] = buf[r * 17 + w];
+            }
+        } else {                                  // BF16, rows at odd places
+            for (int r = 0; r < rows; ++r) {
+                const int64_t at = static_cast<int64_t>(m0 + r) * a.N + c0 + 16 * i;
+                if (lane < min(left, per))
+                    static_cast<uint16_t *>(a.y)[at + lane] =
+                        reinterpret_cast<const uint16_t *>(buf + r * 17)[lane];
             }
         }
     }
@@ -307,6 +349,8 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmap_a,
         setmaxnreg_inc<kSumRegs>();
         const int h = (warp >> 2) - 1, q = warp & 3;
         const uint32_t my_tmem = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * a.half;
+        uint32_t *stage_buf = reinterpret_cast<uint32_t *>(smem_raw + kSmemBytes - kStagedBytes) +
+                              (warp - 4) * 32 * 17;
         Ring d;
         bool ok = true;
         for (int t = blockIdx.x; t < a.tiles && ok; t += gridDim.x) {
@@ -371,8 +415,13 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmap_a,
                 if (lane == 0) mbar_arrive_relaxed(smem_u32(&s.d_empty[d.idx]));
                 d.advance(a.bufs);
             }
-            if (ok && on && m < a.M)
-                store_row<kCols>(a, static_cast<int64_t>(m) * a.N + c0, cols, acc);
+            if (ok && on) {
+                if (a.wide_store) {
+                    if (m < a.M) store_row<kCols>(a, static_cast<int64_t>(m) * a.N + c0, cols, acc);
+                } else {
+                    store_staged<kCols>(a, stage_buf, m - lane, c0, cols, acc);
+                }
+            }
         }
     }
     __syncwarp();
@@ -381,6 +430,276 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmap_a,
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// ------------------------------------------------------------------ pairs of CTAs
+// The same product for many tokens, where shared memory's bandwidth bounds the form
+// above: a group's instructions read 48 KB of operands in the 512 cycles that they take, and as
+// much is written. Two CTAs on neighbouring SMs take a tile of 256 tokens x 256 weight
+// rows together (cta_group::2): each holds its 128 tokens and half of the weights, so a
+// group reads and writes 32 KB per SM, and each adds up its own tokens. One thread of the
+// first CTA issues for both; its barriers collect the copies of both and the releases
+// of both CTAs' tensor memory.
+constexpr int kPairTokens = 256, kPairRows = 256;
+constexpr int kPairStageBytes = 2 * 128 * 128;
+constexpr int kPairStages = (kSmemBytes - 1024 - kOffStages - kStagedBytes) / kPairStageBytes;
+constexpr int kPairBand = 8;              // token tiles that share weights in L2
+
+constexpr int kPairCols = kPairRows / 2;  // columns of a warp
+
+struct PairTile {
+    int m0, n0;
+};
+// Tiles in bands of kPairBand token tiles, the weights' tiles one after the other.
+__device__ __forceinline__ PairTile pair_tile(int t, int m_tiles, int n_tiles) {
+    const int band = t / (kPairBand * n_tiles);
+    const int in = t - band * kPairBand * n_tiles;
+    const int rows = min(kPairBand, m_tiles - band * kPairBand);
+    const int n = in / rows;
+    return {(band * kPairBand + in - n * rows) * kPairTokens, n * kPairRows};
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of the same shared memory in the pair's first CTA.
+__device__ __forceinline__ uint32_t in_first(uint32_t saddr) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(saddr));
+    return r;
+}
+// (Relaxed, and waited for with the CTA's scope: what the barrier guards is tensor memory, whose
+// reads have completed before. A release or an acquire over the cluster would wait for
+// the thread's outstanding loads and drop what L1 holds, twice per group: 277 -> 546 us at
+// 4096 x 8192 x 8192.)
+__device__ __forceinline__ void arrive_remote(uint32_t bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// A load into this CTA whose bytes count at a barrier of the pair's first.
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const void *tmap, int x, int y,
+                                              uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(tmap), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+template <bool kAccumulate>
+__device__ __forceinline__ void mma_pair(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+    asm volatile(
+        "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n"
+        " mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n"
+        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], da, db, %3, p;\n}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "n"(kAccumulate ? 1 : 0), "n"(kDescHi)
+        : "memory");
+}
+// An arrival at the barrier of both CTAs when what was issued is done.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
+                     const __grid_constant__ CUtensorMap tmap_b, const Fp8Args a) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    Bars &s = *reinterpret_cast<Bars *>(smem_raw + (base - raw));
+    const uint32_t sA = base + kOffStages;
+    const uint32_t sB = sA + kPairStages * 128 * 128;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kPairStages; ++i) {
+            mbar_init(smem_u32(&s.full[i]), 1);
+            mbar_init(smem_u32(&s.empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&s.d_full[i]), 1);
+            mbar_init(smem_u32(&s.d_empty[i]), 16);
+        }
+        mbar_init(smem_u32(&s.drain), 1);
+        s.abort_flag = 0;
+        fence_mbarrier_init();
+        tma_prefetch_desc(&tmap_a);
+        tma_prefetch_desc(&tmap_b);
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s.tmem)),
+                     "r"(static_cast<uint32_t>(kTmemCols))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = s.tmem;
+    volatile int *abort_flag = &s.abort_flag;
+    const int pairs = gridDim.x >> 1, first = blockIdx.x >> 1;
+    const int n_tiles = (a.N + kPairRows - 1) / kPairRows;
+    griddep_launch_dependents();
+    griddep_wait();
+
+    if (warp < 4) {
+        setmaxnreg_dec<kOtherRegs>();
+        if (warp == 0 && lane == 0) {
+            // ------------------------------------------------------- TMA producer
+            Ring r;
+            uint32_t issued = 0;
+            bool ok = true;
+            for (int t = first; t < a.tiles && ok; t += pairs) {
+                const PairTile p = pair_tile(t, a.m_tiles, n_tiles);
+                for (int g = 0; g < a.G; ++g) {
+                    if (!mbar_wait(smem_u32(&s.empty[r.idx]), r.phase ^ 1u, abort_flag, a.err, ROLE_PRODUCER, 10,
+ kWaitLimitNs, KID_FP8)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = in_first(smem_u32(&s.full[r.idx]));
+                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(&s.full[r.idx]), 2 * kPairStageBytes);
+                    tma_load_pair(sB + r.idx * 128 * 128, &tmap_b, g * 128, p.n0 + 128 * rank, bar);
+                    tma_load_pair(sA + r.idx * 128 * 128, &tmap_a, g * 128, p.m0 + 128 * rank, bar);
+                    r.advance(kPairStages);
+                    ++issued;
+                }
+            }
+            if (!ok) {       // the copies in flight land before the CTA goes
+                if (rank == 0) {
+                    const uint32_t n = kPairStages;
+                    for (uint32_t i = issued > n ? issued - n : 0; i < issued; ++i) {
+                        const unsigned long long t0 = globaltimer_ns();
+                        while (!mbar_try_wait(smem_u32(&s.full[i % n]), (i / n) & 1u) &&
+                               globaltimer_ns() - t0 < kWaitLimitNs) {
+                        }
+                    }
+                } else {     // (counted at the other CTA: a time that no copy takes)
+                    const unsigned long long t0 = globaltimer_ns();
+                    while (globaltimer_ns() - t0 < 10000000ull) {
+                    }
+                }
+            }
+        } else if (warp == 1 && rank == 0) {
+            // ------------------------------------------------------- products
+            Ring r, d;
+            bool ok = true;
+            const uint32_t idesc = idesc_e4m3(kPairTokens, kPairRows);
+            for (int t = first; t < a.tiles && ok; t += pairs) {
+                for (int g = 0; g < a.G; ++g) {
+                    ok = mbar_wait(smem_u32(&s.d_empty[d.idx]), d.phase ^ 1u, abort_flag, a.err, ROLE_MMA, 10,
+ kWaitLimitNs, KID_FP8) &&
+                         mbar_wait(smem_u32(&s.full[r.idx]), r.phase, abort_flag, a.err, ROLE_MMA, 11,
+ kWaitLimitNs, KID_FP8);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t da = desc_lo(sA + r.idx * 128 * 128);
+                    const uint32_t db = desc_lo(sB + r.idx * 128 * 128);
+                    const uint32_t dt = tmem + d.idx * 256;
+                    if (elect_one()) {
+                        mma_pair<false>(dt, da, db, idesc);
+                        mma_pair<true>(dt, da + 2, db + 2, idesc);
+                        mma_pair<true>(dt, da + 4, db + 4, idesc);
+                        mma_pair<true>(dt, da + 6, db + 6, idesc);
+                        commit_pair(smem_u32(&s.empty[r.idx]));
+                        commit_pair(smem_u32(&s.d_full[d.idx]));
+                    }
+                    __syncwarp();
+                    r.advance(kPairStages);
+                    d.advance(2);
+                }
+            }
+            if (elect_one()) commit_pair(smem_u32(&s.drain));
+            __syncwarp();
+        }
+        if (warp == 1) {     // both CTAs: no product and no arrival is left on its way
+            const unsigned long long t0 = globaltimer_ns();
+            while (!mbar_try_wait(smem_u32(&s.drain), 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
+            }
+        }
+    } else {
+        // ----------------------------------------------------------- sums of groups
+        setmaxnreg_inc<kSumRegs>();
+        const int h = (warp >> 2) - 1, q = warp & 3;
+        const uint32_t my_tmem = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * kPairCols;
+        uint32_t *stage_buf = reinterpret_cast<uint32_t *>(smem_raw + kSmemBytes - kStagedBytes) +
+                              (warp - 4) * 32 * 17;
+        Ring d;
+        bool ok = true;
+        for (int t = first; t < a.tiles && ok; t += pairs) {
+            const PairTile p = pair_tile(t, a.m_tiles, n_tiles);
+            const int c0 = p.n0 + h * kPairCols;
+            const int cols = min(kPairCols, a.N - c0);
+            const int m0 = p.m0 + 128 * static_cast<int>(rank) + q * 32;
+            const bool on = m0 < a.M && cols > 0;            // the same for the warp
+            const int m = m0 + lane;
+            const float *sa = a.sa + static_cast<int64_t>(min(m, a.M - 1)) * a.G;
+            const float *sw = a.sw + static_cast<int64_t>(on ? c0 >> 7 : 0) * a.G;
+            unsigned long long acc[kPairCols / 2];
+#pragma unroll
+            for (int j = 0; j < kPairCols / 2; ++j) acc[j] = 0ull;
+            float fa = ld_now(sa), fw = ld_now(sw);
+            for (int g = 0; g < a.G; ++g) {
+                const float f = fa * fw;
+                if (g + 1 < a.G) {
+                    fa = ld_now(sa + g + 1);
+                    fw = ld_now(sw + g + 1);
+                }
+                ok = mbar_wait(smem_u32(&s.d_full[d.idx]), d.phase, abort_flag, a.err,
+                               ROLE_EPILOGUE, 10, kWaitLimitNs, KID_FP8);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t at = my_tmem + d.idx * 256;
+                const unsigned long long f2 = f2_bits(f, f);
+                uint32_t v[2][16];
+                tmem_ld_16cols(at, v[0]);
+#pragma unroll
+                for (int c = 0; c < kPairCols / 16; ++c) {
+                    tmem_wait_ld_dep16(v[c & 1]);
+                    if (c < kPairCols / 16 - 1) {
+                        tmem_ld_16cols(at + 16 * c + 16, v[(c + 1) & 1]);
+                    } else {                                 // all is read
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_remote(in_first(smem_u32(&s.d_empty[d.idx])));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        acc[8 * c + j] = f2_fma(f2_bits(__uint_as_float(v[c & 1][2 * j]),
+                                                        __uint_as_float(v[c & 1][2 * j + 1])),
+                                                f2, acc[8 * c + j]);
+                }
+                d.advance(2);
+            }
+            if (ok && on) {
+                if (a.wide_store) {
+                    if (m < a.M) store_row<kPairCols>(a, static_cast<int64_t>(m) * a.N + c0, cols, acc);
+                } else {
+                    store_staged<kPairCols>(a, stage_buf, m0, c0, cols, acc);
+                }
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();      // (nobody leaves while the other may still reach its memory)
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(static_cast<uint32_t>(kTmemCols))
+                     : "memory");
     }
 }
 
@@ -397,7 +716,7 @@ bool encode(CUtensorMap *map, const void *ptr, int64_t K, int64_t rows, int box_
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kCols>
+template <auto kernel>
 cudaError_t launch_as(const CUtensorMap &ta, const CUtensorMap &tb, const Fp8Args &a, int grid,
                       cudaStream_t stream) {
     static int attr_done[64] = {0};
@@ -407,11 +726,10 @@ cudaError_t launch_as(const CUtensorMap &ta, const CUtensorMap &tb, const Fp8Arg
     if (dev >= 0 && dev < 64 && !attr_done[dev]) {
         // setmaxnreg.inc can only take registers that the CTA was launched with
         cudaFuncAttributes fa;
-        if ((e = cudaFuncGetAttributes(&fa, gemm_fp8_kernel<kCols>)) != cudaSuccess) return e;
+        if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
         if (fa.numRegs * kThreads < static_cast<int>(256 * kSumRegs + 128 * kOtherRegs))
             return cudaErrorInvalidConfiguration;
-        e = cudaFuncSetAttribute(gemm_fp8_kernel<kCols>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kSmemBytes);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
         if (e != cudaSuccess) return e;
         attr_done[dev] = 1;
     }
@@ -425,7 +743,7 @@ cudaError_t launch_as(const CUtensorMap &ta, const CUtensorMap &tb, const Fp8Arg
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, gemm_fp8_kernel<kCols>, ta, tb, a);
+    e = cudaLaunchKernelEx(&cfg, kernel, ta, tb, a);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
@@ -453,6 +771,25 @@ cudaError_t launch_gemm_fp8(const Fp8Problem &p, int num_sms, cudaStream_t strea
             a.w = w;
         }
     }
+    a.out_fp32 = p.out_fp32;
+    const int per32 = p.out_fp32 ? 8 : 16;
+    cudaError_t e = device_error_word(&a.err);
+    if (e != cudaSuccess) return e;
+    a.words = p.out_fp32 || (a.N % 2 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 3) == 0);
+    CUtensorMap ta, tb;
+    // Pairs of CTAs, where their waves of tiles take less: a group of a pair's tile takes some
+    // 600 cycles, one of a tile of w rows some 4.4 w.
+    const int64_t m2 = (a.M + kPairTokens - 1) / kPairTokens, n2 = (a.N + kPairRows - 1) / kPairRows;
+    const int64_t pairs = num_sms / 2;
+    if ((m2 * n2 + pairs - 1) / pairs * 600 < best * 44 / 10 && m2 * n2 <= INT32_MAX - 4096) {
+        a.m_tiles = static_cast<int>(m2);
+        a.tiles = static_cast<int>(m2 * n2);
+        a.wide_store = (reinterpret_cast<uintptr_t>(p.y) & 31) == 0 && a.N % per32 == 0;
+        if (!encode(&ta, p.qa, p.K, p.M, 128) || !encode(&tb, p.qw, p.K, p.N, 128))
+            return cudaErrorInvalidValue;
+        const int grid = 2 * static_cast<int>(a.tiles < pairs ? a.tiles : pairs);
+        return launch_as<gemm_fp8_pair_kernel>(ta, tb, a, grid, stream);
+    }
     a.n_mma = (a.w + 15) / 16 * 16;
     a.half = a.w <= 32 ? a.w : (a.w / 2 + 15) / 16 * 16;
     const int a_rows = a.M >= kTokens ? kTokens : (a.M + 7) / 8 * 8;
@@ -461,9 +798,10 @@ cudaError_t launch_gemm_fp8(const Fp8Problem &p, int num_sms, cudaStream_t strea
     a.a_bytes = a.a_box;
     a.b_bytes = a.n_mma * 128;
     // An instruction reads 128 rows of tokens, past the last stage's where they are fewer:
-    // into the weights' stages, or what is kept free behind them. (Those lanes of
-    // tensor memory are never read.)
-    const int room = kSmemBytes - 1024 - kOffStages - 128 * 128;
+    // into the weights' stages and the outputs' place behind them, 16 KB at least. (Those
+    // lanes of tensor memory are never read.)
+    static_assert(kStagedBytes >= 128 * 128);
+    const int room = kSmemBytes - 1024 - kOffStages - kStagedBytes;
     a.stages = room / (a.a_bytes + a.b_bytes);
     if (a.stages > kMaxStages) a.stages = kMaxStages;
     a.buf_cols = a.w <= 64 ? 64 : a.w <= 128 ? 128 : 256;
@@ -471,18 +809,13 @@ cudaError_t launch_gemm_fp8(const Fp8Problem &p, int num_sms, cudaStream_t strea
     const int64_t tiles = static_cast<int64_t>(a.m_tiles) * ((a.N + a.w - 1) / a.w);
     if (tiles > INT32_MAX - 4096) return cudaErrorInvalidValue;
     a.tiles = static_cast<int>(tiles);
-    a.out_fp32 = p.out_fp32;
-    const int per32 = p.out_fp32 ? 8 : 16;
     a.wide_store = (reinterpret_cast<uintptr_t>(p.y) & 31) == 0 && a.N % per32 == 0 && a.w % per32 == 0;
-    cudaError_t e = device_error_word(&a.err);
-    if (e != cudaSuccess) return e;
-    CUtensorMap ta, tb;
     if (!encode(&ta, p.qa, p.K, p.M, a_rows) || !encode(&tb, p.qw, p.K, p.N, a.w))
         return cudaErrorInvalidValue;
     const int grid = a.tiles < num_sms ? a.tiles : num_sms;
-    if (a.half <= 32) return launch_as<32>(ta, tb, a, grid, stream);
-    if (a.half <= 64) return launch_as<64>(ta, tb, a, grid, stream);
-    return launch_as<128>(ta, tb, a, grid, stream);
+    if (a.half <= 32) return launch_as<gemm_fp8_kernel<32>>(ta, tb, a, grid, stream);
+    if (a.half <= 64) return launch_as<gemm_fp8_kernel<64>>(ta, tb, a, grid, stream);
+    return launch_as<gemm_fp8_kernel<128>>(ta, tb, a, grid, stream);
 }
 
 }  // namespace w8a8
