@@ -1171,8 +1171,11 @@ w8a8_status w8a8_moe_ffn(const void *x_bf16, int64_t ldx, const int32_t *topk_id
 
 size_t w8a8_moe_layer_workspace_size(int64_t T, int64_t k, int64_t H, int64_t I, int64_t E) {
     if (check_ffn_shape(T, k, H, I, E) != W8A8_OK || T == 0) return 0;
-    return w8a8::uses_moe_few(T, k) ? w8a8::moe_few_workspace_bytes(T, k, H, I)
-                                    : ffn_layout(T, k, H, I, E).total;
+    // (which of the two forms a call takes depends on the device's SMs as well)
+    const size_t few = w8a8::uses_moe_few(T, k, H, INT32_MAX)
+                           ? w8a8::moe_few_workspace_bytes(T, k, H, I) : 0;
+    const size_t many = ffn_layout(T, k, H, I, E).total;
+    return few > many ? few : many;
 }
 
 w8a8_status w8a8_moe_layer(const void *x_bf16, int64_t ldx, const void *logits,
@@ -1198,7 +1201,7 @@ w8a8_status w8a8_moe_layer(const void *x_bf16, int64_t ldx, const void *logits,
     st = check_device(&info);
     if (st != W8A8_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (!w8a8::uses_moe_few(T, k)) {
+    if (!w8a8::uses_moe_few(T, k, H, info.num_sms)) {
         if (w8a8::launch_moe_gate(gate, s) != cudaSuccess) return W8A8_ERR_CUDA;
         return w8a8_moe_ffn(x_bf16, ldx, ids, w, T, k, H, I, E, qw_up, sw_up, qw_down, sw_down, y,
                             y_dtype, workspace, workspace_bytes, stream);
@@ -1220,7 +1223,8 @@ w8a8_status w8a8_moe_layer(const void *x_bf16, int64_t ldx, const void *logits,
     p.y = y;
     p.out_fp32 = y_dtype == W8A8_FP32;
     p.workspace = workspace;
-    w8a8::moe_few_zeroes(p, &gate.zero, &gate.n_zero);
+    const w8a8::MoeFewTokens tokens = w8a8::moe_few_tokens(p);
+    gate.tokens = &tokens;
     cudaError_t e = w8a8::launch_moe_gate(gate, s);
     if (e == cudaSuccess) e = w8a8::launch_moe_few(p, info.num_sms, s);
     return from_cuda(e);

@@ -37,6 +37,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "quant_math.cuh"
 
 namespace w8a8 {
 namespace {
@@ -96,8 +97,8 @@ struct GateArgs {
     float scale;
     int32_t *ids;
     float *w;
-    uint32_t *zero;         // words that the next kernel wants zeroed
-    int n_zero;
+    int blocks;             // CTAs of the gate; those behind them take a token of `few` each
+    MoeFewTokens few;
 };
 
 __device__ __forceinline__ float ex2_approx(float v) {
@@ -520,17 +521,53 @@ __device__ __forceinline__ bool decide_again(const Tin *row, const float (&kr)[V
     return true;
 }
 
+// For the expert kernel of few tokens: the codes and the scale of token t, as
+// w8a8_quant_act makes them, and (the first) zeros.
+__device__ __noinline__ void take_token(const MoeFewTokens &f, int t) {
+    constexpr int kN = kGateWarps * 32;
+    __shared__ uint32_t s_max[kGateWarps];
+    if (t == 0)
+        for (int i = threadIdx.x; i < f.n_zeros; i += kN) f.zeros[i] = 0;
+    const uint16_t *row = f.x + t * f.ldx;
+    auto load8 = [&](int i) {
+        if (f.vec) return reinterpret_cast<const uint4 *>(row)[i];
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[j] = row[8 * i + 2 * j] | static_cast<uint32_t>(row[8 * i + 2 * j + 1]) << 16;
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    };
+    uint32_t m = 0;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < f.H >> 3; i += kN) m = max(m, amax_bits8(load8(i)));
+    m = __reduce_max_sync(kFull, m);
+    if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kGateWarps; ++i) m = max(m, s_max[i]);
+    const float s = __fdiv_rn(bf16_bits_to_f32(m), 127.0f);
+    const bool fast = s >= 1.17549435e-38f;   // a normal scale: 1 / s is finite
+    const float rcp = fast ? __frcp_rn(s) : 0.0f;
+    if (threadIdx.x == 0) f.sx[t] = s;
+    const int64_t at = static_cast<int64_t>(t) * (f.H >> 3);
+#pragma unroll 2
+    for (int i = threadIdx.x; i < f.H >> 3; i += kN) {
+        reinterpret_cast<uint2 *>(f.xq)[at + i] = quantize8(load8(i), s, rcp, fast);
+    }
+}
+
 template <int V, typename Tin>
 __global__ void __launch_bounds__(kGateWarps * 32)
 moe_gate_kernel(const Tin *logits, const GateArgs a) {
     griddep_launch_dependents();
     griddep_wait();
+    if (blockIdx.x >= a.blocks) {
+        take_token(a.few, blockIdx.x - a.blocks);
+        return;
+    }
     __shared__ int s_list[kGateWarps][32];
     const int lane = threadIdx.x & 31;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * kGateWarps + (threadIdx.x >> 5);
-    for (int i = blockIdx.x * kGateWarps * 32 + threadIdx.x; i < a.n_zero;
-         i += gridDim.x * kGateWarps * 32)
-        a.zero[i] = 0;
     if (t >= a.T) return;
     const Tin *row = logits + t * a.ldx;
     // logits: NaN and -inf mark experts that are never picked; +inf counts as
@@ -670,7 +707,7 @@ moe_gate_kernel(const Tin *logits, const GateArgs a) {
 template <int V, typename Tin>
 cudaError_t launch_v(const Tin *x, const GateArgs &a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((a.T + kGateWarps - 1) / kGateWarps));
+    cfg.gridDim = dim3(static_cast<unsigned>(a.blocks + a.few.T));
     cfg.blockDim = dim3(kGateWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -718,8 +755,8 @@ cudaError_t launch_moe_gate(const GateProblem &p, cudaStream_t stream) {
     a.scale = p.scale;
     a.ids = p.ids;
     a.w = p.w;
-    a.zero = p.zero;
-    a.n_zero = p.n_zero;
+    a.blocks = (a.T + kGateWarps - 1) / kGateWarps;
+    a.few = p.tokens != nullptr ? *p.tokens : MoeFewTokens{};
     return p.fp32 ? launch_any<float>(p.logits, a, stream)
                   : launch_any<uint16_t>(p.logits, a, stream);
 }

@@ -166,8 +166,7 @@ struct GateProblem {
     float scale;
     int32_t *ids;           // [T, k]
     float *w;               // [T, k]
-    uint32_t *zero = nullptr;   // words that the kernel launched next wants zeroed
-    int n_zero = 0;
+    const struct MoeFewTokens *tokens = nullptr;   // what the kernel launched next wants made too
 };
 constexpr int kGateMaxGroups = 64;
 cudaError_t launch_moe_gate(const GateProblem &p, cudaStream_t stream);
@@ -233,7 +232,7 @@ cudaError_t launch_paged_attention(const PagedAttnProblem &p, cudaStream_t strea
 constexpr int kMaxExperts = 1024;
 
 // The experts of a few tokens in one kernel (moe_layer.cu), after the gate, whose
-// launch zeroes moe_few_zeroes().
+// launch makes moe_few_tokens() as well: the tokens' codes and scales, and zeros.
 constexpr int64_t kMoeFewMaxTokens = 32;
 constexpr int64_t kMoeFewMaxPairs = 512;
 struct MoeFewProblem {
@@ -248,11 +247,18 @@ struct MoeFewProblem {
     bool out_fp32;
     void *workspace;
 };
-inline bool uses_moe_few(int64_t T, int64_t k) {
-    return T <= kMoeFewMaxTokens && T * k <= kMoeFewMaxPairs;
-}
+struct MoeFewTokens {
+    const uint16_t *x;               // BF16 [T, ldx]
+    int64_t ldx;
+    int T, H, vec;                   // vec: rows may be read 16 bytes at a time
+    float *sx;                       // [T]
+    int8_t *xq;                      // [T, H] codes
+    uint32_t *zeros;
+    int n_zeros;
+};
+bool uses_moe_few(int64_t T, int64_t k, int64_t H, int num_sms);
 size_t moe_few_workspace_bytes(int64_t T, int64_t k, int64_t H, int64_t I);
-void moe_few_zeroes(const MoeFewProblem &p, uint32_t **words, int *n);
+MoeFewTokens moe_few_tokens(const MoeFewProblem &p);
 cudaError_t launch_moe_few(const MoeFewProblem &p, int num_sms, cudaStream_t stream);
 
 cudaError_t launch_gemm(const GemmProblem &p, int num_sms, cudaStream_t stream);

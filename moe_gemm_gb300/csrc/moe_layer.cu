@@ -8,27 +8,26 @@
 //   h = silu(gate) * up, quantized per (token, expert)
 //   d = (h's codes . W_down[e]), y[t] = sum_j w[t, j] d[t, j]
 //
-// Every step is that of moe_ffn, rounding for rounding, so y is the same bits.
+// Every step is that of moe_ffn, rounding for rounding, so y is the same bits. The tokens'
+// codes come from the gate's launch.
 //
 // The grid is one CTA per SM, launched cooperatively, since its parts wait on one
-// another three times: for the tokens' codes, for h (its scale needs whole
-// rows), and for h's codes.
+// another twice: for h (its scale needs whole rows), and for h's codes.
 //
-// Work. The rows of all picked experts form a line, and every warp of the grid takes
-// an equal stretch of it, whatever the routing: rows of gate and up in pairs for
-// the first product; for the second a CTA has the same output rows of every
-// expert, so that it adds up its tokens' experts by itself, and its warps share
-// those. A warp takes its rows 16 at a time (8 pairs), one K group of 128 per
-// step, through a ring of its own in shared memory (cp.async, no barrier with other
-// warps). The ring runs on through the waits: the first weights of a product are
-// asked for before what they are multiplied with is there.
+// Work. The rows of all picked experts form a line, which is cut into stretches of equal
+// cost for the warps of the grid. Of the second product a CTA has the same output rows
+// of every expert, so that it adds up its tokens' experts by itself, and its warps cut
+// that line. A warp takes its rows 16 at a time (of the first product 8 rows of gate and the
+// 8 of up that belong to them), one K group of 128 per step, through a ring of its own in
+// shared memory (cp.async, no barrier with other warps). The ring runs on through the waits.
 //
-// A step is eight mma.sync m16n8k16 on fp16 (weights' rows x tokens x 128 K): codes are
-// exact in fp16 and a group's sum in FP32, as in the other products here. K is permuted
-// alike on both sides, so that a lane has 32 consecutive codes of its rows, and of its
-// token's codes, which are kept as fp16.
+// A step of an expert with three and more tokens is eight mma.sync m16n8k16 on fp16 (weights'
+// rows x tokens x 128 K): codes are exact in fp16 and a group's sum in FP32, as in the other
+// products here. K is permuted alike on both sides, so that a lane has 32 consecutive
+// codes of its rows, and of its token's codes. With one or two tokens it is dp4a on the
+// codes as they are: widening 16 x 128 of them takes 80 instructions, 16 warps of
+// which cost more than HBM takes for a tile that is not full.
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -46,13 +45,15 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 4;
 constexpr int kStageBytes = 16 * 128;
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
-constexpr int kSyncs = 3;                    // grid-wide waits
+constexpr int kMaxOutputBytes = 80 << 10;   // d of a CTA's rows, in shared memory
+constexpr int kSyncs = 2;                    // grid-wide waits
+constexpr int kQueue = 8;                    // tiles that a ring is ahead at most
 constexpr unsigned kFull = 0xFFFFFFFFu;
+// What a row of an expert costs, by its tokens: warps that stream alike take so much longer for
+// two tokens, and for the tensor cores' form.
+constexpr int kCostOne = 6, kCostTwo = 7, kCostMore = 8;
 
 struct LayerArgs {
-    const uint16_t *x;
-    int64_t ldx;
-    int vec;                                 // rows of x may be read 16 bytes at a time
     const int32_t *ids;
     const float *w;
     int T, k, E, H, I;
@@ -62,12 +63,19 @@ struct LayerArgs {
     int out_fp32;
     unsigned *sync;                          // [kSyncs], zeros
     unsigned *hmax;                          // [T k], zeros: largest |h| as bits
-    float *sx;                               // [T]
-    __half *xq;                              // [T, H] codes
+    const float *sx;                         // [T]
+    const int8_t *xq;                        // [T, H] codes
     float *h;                                // [T k, I]
-    __half *hq;                              // [T k, I] codes
-    float *d;                                // [T k, H]
+    int8_t *hq;                              // [T k, I] codes
     unsigned long long *err;
+};
+
+// A warp's stretch of the line of rows, and the tiles it has been cut into.
+struct Stretch {
+    int pos, end;            // rows of the line
+    int unit, at;            // the unit that pos lies in, and its row there
+    int opened;              // tiles so far
+    int2 tile[kQueue];       // the last of them: {unit << 8 | rows, first row}
 };
 
 // What the gate picked, by expert: those with tokens, in order of their index, and the
@@ -76,8 +84,11 @@ struct Routes {
     int count[kMaxExperts];                  // then the expert's first pair
     int expert[kMoeFewMaxPairs];
     int first[kMoeFewMaxPairs + 1];
+    int cost[kMoeFewMaxPairs + 1];           // of a row of all experts before
     int pair[kMoeFewMaxPairs];
     int part[kWarps];
+    Stretch stretch[kWarps];
+    float w[kMoeFewMaxPairs];                // of the pairs; 0 where there is no expert
     int n;
     int abort;
 };
@@ -102,13 +113,13 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     return v;
 }
 
-// D[16 x 8] += A[16 x 16] B[16 x 8], fp16 operands, FP32 sums.
-__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+// D[16 x 8] += A[16 x 32] B[32 x 8], int8 operands, int32 sums.
+__device__ __forceinline__ void mma_16832(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, "
         "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
@@ -118,7 +129,6 @@ __device__ __forceinline__ bool grid_wait(unsigned *counter, int *abort, unsigne
                                           unsigned site) {
     __syncthreads();
     if (threadIdx.x == 0) {
-        __threadfence();
         unsigned seen;
         asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
                      : "=r"(seen) : "l"(counter) : "memory");
@@ -134,7 +144,6 @@ __device__ __forceinline__ bool grid_wait(unsigned *counter, int *abort, unsigne
                 break;
             }
         }
-        __threadfence();
     }
     __syncthreads();
     return *abort == 0;
@@ -168,6 +177,7 @@ __device__ __forceinline__ void make_routes(const LayerArgs &a, Routes &r) {
     if (threadIdx.x < n) {
         id = a.ids[threadIdx.x];
         if (id < 0 || id >= a.E) id = -1;
+        r.w[threadIdx.x] = id >= 0 ? a.w[threadIdx.x] : 0.0f;
         // (an expert's pairs come in any order: each is a column of its own)
         if (id >= 0) place = atomicAdd(&r.count[id], 1);
     }
@@ -195,79 +205,137 @@ __device__ __forceinline__ void make_routes(const LayerArgs &a, Routes &r) {
     }
     __syncthreads();
     if (id >= 0) r.pair[r.count[id] + place] = threadIdx.x;
+    const int unit = threadIdx.x;
+    const int n_tok = unit < r.n ? r.first[unit + 1] - r.first[unit] : 0;
+    const int cost = n_tok == 0 ? 0 : n_tok == 1 ? kCostOne : n_tok == 2 ? kCostTwo : kCostMore;
+    const int before = block_scan(cost, r.part, total);
+    if (unit <= r.n) r.cost[unit] = before;
+    if (unit == 0) r.cost[r.n] = total;
     __syncthreads();
 }
 
-// A warp's stretch of the line of rows: units (experts) of L rows, of which a tile takes
-// up to kMost from one unit; `steps` groups of K per tile.
-struct Cursor {
-    int pos, end;            // in rows of the line
-    int unit, at;            // the unit that pos lies in, and its row there
-    __device__ __forceinline__ Cursor(int64_t units, int L, int part, int parts) {
-        const int64_t total = units * L;
-        pos = static_cast<int>(total * part / parts);
-        end = static_cast<int>(total * (part + 1) / parts);
-        unit = pos / L;
-        at = pos - unit * L;
-    }
-    __device__ __forceinline__ int rows(int L, int most) const {
-        return min(min(most, end - pos), L - at);
-    }
-    __device__ __forceinline__ void next(int n, int L) {
-        pos += n;
-        at += n;
-        if (at == L) {
-            at = 0;
-            ++unit;
-        }
-    }
-};
+// Groups of K that a step of a tile takes: tiles that are not full, of experts with one or two
+// tokens, take 2 or 4 so that the ring still has as many bytes on their way (a step lasts a
+// third of HBM's latency, whatever it holds).
+template <bool kUp>
+__device__ __forceinline__ int tile_groups(int rows, int n_tok, int K) {
+    const int full = (kUp ? 8 : 16) / rows;
+    if (n_tok > 2 || full < 2 || K % 256 != 0) return 1;
+    return full >= 4 && K % 512 == 0 ? 4 : 2;
+}
+// Where a 16-byte piece of a row of a stage lies, such that what eight lanes read at once
+// (take_tile, take_tile_dot) is in different banks.
+__device__ __forceinline__ int swizzled(int piece, int row, int wide) {
+    return wide == 1   ? piece ^ (row & 7)
+           : wide == 2 ? piece ^ ((row & 1) | (piece >> 3 << 1))
+                       : piece ^ (piece >> 3);
+}
 
 // The weights' side of a product: kUp, pairs of rows (i, I + i) of W_gate_up, else rows
-// [r0, r0 + L) of W_down.
+// [r0, r0 + L) of W_down. The line has r.n units (experts) of L rows; the warp takes stretches
+// of it, a tile of up to kMost rows of one unit at a time, K group by K group. Tiles
+// are told to the other side through the queue. What a step does not need lies in
+// shared memory.
 template <bool kUp>
 struct Feed {
     static constexpr int kMost = kUp ? 8 : 16;
-    Cursor c;
-    int step, rows;
-    uint32_t dst;            // the lane's piece of the stage that the next copy goes to
+    int left;                // steps of the tile that are not asked for yet; 0: no more tiles
+    int rows;                // rows of the tile from the lane's first on
+    int wide;                // groups of a step
+    uint32_t dst, off;       // the stage that the next copy goes to, the lane's piece in it
     const int8_t *src;       // the lane's piece of the tile's first row, at that step
 
-    __device__ __forceinline__ Feed(const LayerArgs &a, const Routes &r, uint32_t ring, int r0,
-                                    int L, int part, int parts)
-        : c(r.n, L, part, parts), step(0), rows(0), src(nullptr) {
-        const int lane = threadIdx.x & 31;
-        dst = ring + (lane >> 3) * 128 + (((lane & 7) ^ (lane >> 3)) << 4);
-        open(a, r, r0, L);
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) issue(a, r, ring, r0, L);
+    // What part `part` of `parts` has of n rows begins here. (n * part / parts in 32 bits: a
+    // 64-bit division takes a microsecond.)
+    static __device__ __forceinline__ int share(int n, int part, int parts) {
+        const unsigned q = static_cast<unsigned>(n) / parts, rest = n - q * parts;
+        return q * part + rest * part / parts;
     }
-    __device__ __forceinline__ void open(const LayerArgs &a, const Routes &r, int r0, int L) {
-        if (c.pos >= c.end) return;
+    // The row of the line where part `part` of `parts` begins, and its unit: equal costs.
+    static __device__ __forceinline__ int begin(const Routes &r, int L, int part, int parts,
+                                                int &unit) {
+        const int at = share(r.cost[r.n] * L, part, parts);      // <= 512 * 8 * 8192
+        int lo = 0, hi = r.n;                                    // cost[lo] L <= at < cost[hi] L
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (r.cost[mid] * L <= at) lo = mid; else hi = mid;
+        }
+        unit = lo;
+        if (r.n == 0) return 0;
+        return lo * L + min(L, (at - r.cost[lo] * L) / (r.cost[lo + 1] - r.cost[lo]));
+    }
+
+    __device__ __forceinline__ Feed(const LayerArgs &a, Routes &r, uint32_t ring, int r0, int L,
+                                    int part, int parts)
+        : left(0), rows(0), wide(1), dst(ring), off(0), src(nullptr) {
         const int lane = threadIdx.x & 31;
-        rows = c.rows(L, kMost) - (lane >> 3);       // rows from the lane's first on
-        const int64_t e = r.expert[c.unit];
-        src = kUp ? a.qw_up + (e * 2 * a.I + c.at + (lane >> 3)) * a.H
-                  : a.qw_down + (e * a.H + r0 + c.at + (lane >> 3)) * a.I;
-        src += (lane & 7) * 16;
+        Stretch &w = r.stretch[threadIdx.x >> 5];
+        if (lane == 0) {
+            int end_unit;
+            w.pos = begin(r, L, part, parts, w.unit);
+            w.end = begin(r, L, part + 1, parts, end_unit);
+            w.at = w.pos - w.unit * L;
+            if (w.at == L) {                         // (a border at a unit's end)
+                w.at = 0;
+                ++w.unit;
+            }
+            w.opened = 0;
+        }
+        __syncwarp();
+        open(a, r, r0, L);
+#pragma unroll 1
+        for (int i = 0; i < kStages - 1; ++i) issue(a, r, ring, r0, L);
+        __syncwarp();
+    }
+    // The next tile, if there is one.
+    __device__ __forceinline__ void open(const LayerArgs &a, Routes &r, int r0, int L) {
+        const int lane = threadIdx.x & 31;
+        Stretch &w = r.stretch[threadIdx.x >> 5];
+        int n = min(w.end - w.pos, L - w.at);
+        if (n <= 0) return;
+        n = (n + (n - 1) / kMost) / ((n - 1) / kMost + 1);    // tiles of even height
+        const int unit = w.unit, at = w.at;
+        const int n_tok = r.first[unit + 1] - r.first[unit];
+        const int K = kUp ? a.H : a.I;
+        // (half a tile and the rest after it take fewer steps than 5/8 or 3/4 of one)
+        if (n > kMost / 2 && n <= kMost * 3 / 4 && tile_groups<kUp>(kMost / 2, n_tok, K) > 1)
+            n = kMost / 2;
+        __syncwarp();
+        if (lane == 0) {
+            w.tile[w.opened & (kQueue - 1)] = make_int2(unit << 8 | n, at);
+            ++w.opened;
+            w.pos += n;
+            w.at = at + n == L ? 0 : at + n;
+            w.unit = at + n == L ? unit + 1 : unit;
+        }
+        __syncwarp();
+        wide = tile_groups<kUp>(n, n_tok, K);
+        left = (K >> 7) / wide;
+        // a stage is 16 / wide rows of 128 wide bytes; the lane's first row and piece of it
+        const int row = wide == 1 ? lane >> 3 : wide == 2 ? lane >> 4 : 0;
+        const int piece = lane & (8 * wide - 1);
+        off = row * 128 * wide + (swizzled(piece, row, wide) << 4);
+        rows = n - row;
+        const int64_t e = r.expert[unit];
+        src = (kUp ? a.qw_up + (e * 2 * a.I + at + row) * a.H
+                   : a.qw_down + (e * a.H + r0 + at + row) * a.I) + piece * 16;
     }
     // Asks for the next step's weights.
-    __device__ __forceinline__ void issue(const LayerArgs &a, const Routes &r, uint32_t ring,
-                                          int r0, int L) {
-        if (c.pos < c.end) {
-            // rows 0-3, 4-7 (whose swizzle differs in bit 2), 8-11, 12-15
+    __device__ __forceinline__ void issue(const LayerArgs &a, Routes &r, uint32_t ring, int r0,
+                                          int L) {
+        if (left > 0) {
+            // the lane's rows are 4 / wide apart: 512 bytes of the stage (whose swizzle differs
+            // by the row's bit 2, where a group is a step); the second two of W_gate_up are up
             const int K = kUp ? a.H : a.I;
-            const int64_t third = kUp ? static_cast<int64_t>(a.I) * a.H : 8 * K;
-            if (rows > 0) cp_async_16(dst, src);
-            if (rows > 4) cp_async_16((dst ^ 64) + 512, src + 4 * K);
-            if (rows > (kUp ? 0 : 8)) cp_async_16(dst + 1024, src + third);
-            if (rows > (kUp ? 4 : 12)) cp_async_16((dst ^ 64) + 1536, src + third + 4 * K);
-            src += 128;
-            if (++step == K >> 7) {
-                step = 0;
-                c.next(c.rows(L, kMost), L);
-                open(a, r, r0, L);
-            }
+            const int apart = 4 / wide;
+            const int64_t third = kUp ? static_cast<int64_t>(a.I) * a.H : 2 * apart * K;
+            const uint32_t to = dst + off, odd = wide == 1 ? to ^ 64 : to;
+            if (rows > 0) cp_async_16(to, src);
+            if (rows > apart) cp_async_16(odd + 512, src + apart * K);
+            if (rows > (kUp ? 0 : 2 * apart)) cp_async_16(to + 1024, src + third);
+            if (rows > (kUp ? apart : 3 * apart)) cp_async_16(odd + 1536, src + third + apart * K);
+            src += 128 * wide;
+            if (--left == 0) open(a, r, r0, L);
         }
         cp_async_commit();
         dst += kStageBytes;
@@ -275,68 +343,77 @@ struct Feed {
     }
 };
 
-// One tile: 16 rows of weights by up to 8 NT tokens, over all of K. acc: [token tile][the
-// lane's outputs: rows g and g + 8, tokens 2 c and 2 c + 1], g = lane / 4, c = lane % 4.
+// One step of the ring: waits for the stage at `read`, asks for one more.
+template <bool kUp>
+__device__ __forceinline__ uint32_t next_stage(const LayerArgs &a, Routes &r, Feed<kUp> &f,
+                                               uint32_t ring, int r0, int L, uint32_t &read) {
+    cp_async_wait<kStages - 2>();
+    __syncwarp();                            // the stage is there; the one before is read
+    f.issue(a, r, ring, r0, L);
+    const uint32_t at = read;
+    read = read + kStageBytes - ring >= kStages * kStageBytes ? ring : read + kStageBytes;
+    return at;
+}
+
+// A tile of an expert with two and more tokens: 16 rows of weights by up to 8 NT tokens, over
+// all of K. acc: [token tile][the lane's outputs: rows g and g + 8, tokens 2 c and 2 c + 1],
+// g = lane / 4, c = lane % 4.
 template <int NT, bool kUp>
-__device__ __forceinline__ void tile_product(const LayerArgs &a, const Routes &r, Feed<kUp> &f,
+__device__ __forceinline__ void tile_product(const LayerArgs &a, Routes &r, Feed<kUp> &f,
                                              uint32_t ring, int r0, int L, uint32_t &read,
-                                             const __half *codes, const int (&tok)[NT],
-                                             const float *sw0, const float *sw1,
-                                             float (&acc)[NT][4]) {
+                                             const int (&tok)[NT], const float *sw0,
+                                             const float *sw1, float (&acc)[NT][4]) {
+    const int lane = threadIdx.x & 31;
+    // row lane / 4, 16-byte pieces 2 (lane % 4) and the next, swizzled by the row
+    const uint32_t mine = (lane >> 2) * 128 + (((2 * (lane & 3)) ^ (lane >> 2)) << 4);
+    const int8_t *codes = kUp ? a.xq : a.hq;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[n][j] = 0.0f;
     const int steps = (kUp ? a.H : a.I) >> 7;
     for (int s = 0; s < steps; ++s) {
-        uint4 b[4];
+        uint4 b[NT][2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) b[i] = reinterpret_cast<const uint4 *>(codes + tok[0] + s * 128)[i];
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                b[n][i] = reinterpret_cast<const uint4 *>(codes + tok[n] + s * 128)[i];
         const float w0 = sw0[s], w1 = sw1[s];
-        cp_async_wait<kStages - 2>();
-        __syncwarp();                        // the stage is there; the one before is read
-        f.issue(a, r, ring, r0, L);
-        const uint32_t at = read;
-        read += kStageBytes;
-        if (read - ring >= kStages * kStageBytes) read -= kStages * kStageBytes;
-        uint4 q[4] = {lds128(at), lds128(at ^ 16), lds128(at + 1024), lds128((at ^ 16) + 1024)};
-        uint32_t lo[2][8], hi[2][8];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t word[8] = {q[2 * i].x,     q[2 * i].y,     q[2 * i].z,     q[2 * i].w,
-                                      q[2 * i + 1].x, q[2 * i + 1].y, q[2 * i + 1].z, q[2 * i + 1].w};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) i8x4_to_f16x4(word[j], lo[i][j], hi[i][j]);
-        }
+        const uint32_t at = next_stage(a, r, f, ring, r0, L, read) + mine;
+        const uint4 lo[2] = {lds128(at), lds128(at ^ 16)};                      // row g
+        const uint4 hi[2] = {lds128(at + 1024), lds128((at ^ 16) + 1024)};      // row g + 8
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            if (n > 0) {
+            int p[4] = {};
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    b[i] = reinterpret_cast<const uint4 *>(codes + tok[n] + s * 128)[i];
+            for (int i = 0; i < 2; ++i) {
+                mma_16832(p, lo[i].x, hi[i].x, lo[i].y, hi[i].y, b[n][i].x, b[n][i].y);
+                mma_16832(p, lo[i].z, hi[i].z, lo[i].w, hi[i].w, b[n][i].z, b[n][i].w);
             }
-            float p[2][4] = {};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                mma_16816(p[0], lo[0][2 * j], lo[1][2 * j], hi[0][2 * j], hi[1][2 * j], b[j].x, b[j].y);
-                mma_16816(p[1], lo[0][2 * j + 1], lo[1][2 * j + 1], hi[0][2 * j + 1],
-                          hi[1][2 * j + 1], b[j].z, b[j].w);
-            }
-            // (sums of integers below 2^24: exact in any order)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                acc[n][j] = fmaf(p[0][j] + p[1][j], j < 2 ? w0 : w1, acc[n][j]);
+                acc[n][j] = fmaf(static_cast<float>(p[j]), j < 2 ? w0 : w1, acc[n][j]);
         }
     }
 }
 
+// Row `row` of a tile: the weight row's scales, its output.
+template <bool kUp>
+__device__ __forceinline__ const float *scales_of(const LayerArgs &a, int64_t e, int at, int r0,
+                                                  int row, int rows) {
+    if (!kUp) return a.sw_down + (e * a.H + r0 + at + min(row, rows - 1)) * (a.I >> 7);
+    // rows 0-7 of gate, 8-15 of up
+    return a.sw_up + (e * 2 * a.I + (row & 8 ? a.I : 0) + at + min(row & 7, rows - 1)) * (a.H >> 7);
+}
+
 template <int NT, bool kUp>
-__device__ __forceinline__ void take_tile(const LayerArgs &a, const Routes &r, Feed<kUp> &f,
-                                          const Cursor &c, int rows, uint32_t ring, int r0, int L,
-                                          uint32_t &read, int p0, int n_tok) {
+__device__ __forceinline__ void take_tile(const LayerArgs &a, Routes &r, Feed<kUp> &f, int unit,
+                                          int row0, int rows, uint32_t ring, int r0, int L,
+                                          uint32_t &read, int p0, int n_tok, float *s_d) {
     const int lane = threadIdx.x & 31;
     const int g = lane >> 2, q = lane & 3;
-    const int64_t e = r.expert[c.unit];
+    const int64_t e = r.expert[unit];
     const int K = kUp ? a.H : a.I;
     int tok[NT];                             // where the lane's tokens' codes are
 #pragma unroll
@@ -345,17 +422,10 @@ __device__ __forceinline__ void take_tile(const LayerArgs &a, const Routes &r, F
         const int pair = r.pair[p0 + min(8 * n + g, n_tok - 1)];
         tok[n] = (kUp ? pair / a.k : pair) * K + q * 32;
     }
-    const int groups = K >> 7;
-    const float *sw0, *sw1;
-    if (kUp) {
-        sw0 = a.sw_up + (e * 2 * a.I + c.at + min(g, rows - 1)) * groups;
-        sw1 = sw0 + static_cast<int64_t>(a.I) * groups;
-    } else {
-        sw0 = a.sw_down + (e * a.H + r0 + c.at + min(g, rows - 1)) * groups;
-        sw1 = a.sw_down + (e * a.H + r0 + c.at + min(g + 8, rows - 1)) * groups;
-    }
     float acc[NT][4];
-    tile_product<NT, kUp>(a, r, f, ring, r0, L, read, kUp ? a.xq : a.hq, tok, sw0, sw1, acc);
+    tile_product<NT, kUp>(a, r, f, ring, r0, L, read, tok,
+                          scales_of<kUp>(a, e, row0, r0, g, rows),
+                          scales_of<kUp>(a, e, row0, r0, g + 8, rows), acc);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -367,7 +437,7 @@ __device__ __forceinline__ void take_tile(const LayerArgs &a, const Routes &r, F
                 if (col < n_tok && g < rows) {
                     const float s = a.sx[pair / a.k];
                     h = swiglu_f32(__fmul_rn(acc[n][j], s), __fmul_rn(acc[n][j + 2], s));
-                    a.h[static_cast<int64_t>(pair) * a.I + c.at + g] = h;
+                    a.h[static_cast<int64_t>(pair) * a.I + row0 + g] = h;
                 }
                 unsigned m = __float_as_uint(fabsf(h));
 #pragma unroll
@@ -375,7 +445,7 @@ __device__ __forceinline__ void take_tile(const LayerArgs &a, const Routes &r, F
                 if (g == 0 && col < n_tok) atomicMax(a.hmax + pair, m);
             } else if (col < n_tok) {
                 const float s = __fdiv_rn(__uint_as_float(a.hmax[pair]), 127.0f);
-                float *d = a.d + static_cast<int64_t>(pair) * a.H + r0 + c.at;
+                float *d = s_d + pair * L + row0;
                 if (g < rows) d[g] = __fmul_rn(acc[n][j], s);
                 if (g + 8 < rows) d[g + 8] = __fmul_rn(acc[n][j + 2], s);
             }
@@ -383,56 +453,110 @@ __device__ __forceinline__ void take_tile(const LayerArgs &a, const Routes &r, F
     }
 }
 
-// The warp's share of a product.
-template <bool kUp>
-__device__ __forceinline__ void product(const LayerArgs &a, const Routes &r, Feed<kUp> &f,
-                                        Cursor c, uint32_t ring, int L, int r0) {
-    // the lane's first piece of a stage: row lane / 4, 16-byte pieces 2 (lane % 4) and the
-    // next, swizzled by the row
+// A tile of an expert with NT = 1 or 2 tokens, kWide groups a step: 2 kWide lanes have a row, 64
+// bytes of it each.
+template <int NT, int kWide, bool kUp>
+__device__ __forceinline__ void take_tile_dot(const LayerArgs &a, Routes &r, Feed<kUp> &f, int unit,
+                                              int row0, int rows, uint32_t ring, int r0, int L,
+                                              uint32_t &read, int p0, float *s_d) {
     const int lane = threadIdx.x & 31;
-    uint32_t read = ring + (lane >> 2) * 128 + (((2 * (lane & 3)) ^ (lane >> 2)) << 4);
-    while (c.pos < c.end) {
-        const int rows = c.rows(L, Feed<kUp>::kMost);
-        const int p0 = r.first[c.unit], n_tok = r.first[c.unit + 1] - p0;
-        if (n_tok <= 8)
-            take_tile<1, kUp>(a, r, f, c, rows, ring, r0, L, read, p0, n_tok);
-        else if (n_tok <= 16)
-            take_tile<2, kUp>(a, r, f, c, rows, ring, r0, L, read, p0, n_tok);
-        else
-            take_tile<4, kUp>(a, r, f, c, rows, ring, r0, L, read, p0, n_tok);
-        c.next(rows, L);
+    constexpr int kLanes = 2 * kWide, kRows = 16 / kWide;
+    const int row = lane / kLanes, part = lane % kLanes;
+    const int64_t e = r.expert[unit];
+    const int K = kUp ? a.H : a.I;
+    const int8_t *codes = kUp ? a.xq : a.hq;
+    int tok[NT], pair[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        pair[n] = r.pair[p0 + n];
+        tok[n] = (kUp ? pair[n] / a.k : pair[n]) * K + part * 64;
     }
-    cp_async_wait<0>();
+    // (gate rows, then as many of up)
+    const float *sw = kUp ? scales_of<kUp>(a, e, row0, r0, row % (kRows / 2) + (row / (kRows / 2)) * 8, rows)
+                          : scales_of<kUp>(a, e, row0, r0, row, rows);
+    // pieces 4 part .. 4 part + 3 of the row
+    const uint32_t mine = row * 128 * kWide + (swizzled(4 * part, row, kWide) << 4);
+    float acc[NT] = {};
+    for (int s = 0; s < K >> 7; s += kWide) {
+        uint4 b[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                b[n][i] = reinterpret_cast<const uint4 *>(codes + tok[n] + s * 128)[i];
+        float w[kWide];
+#pragma unroll
+        for (int i = 0; i < kWide; ++i) w[i] = sw[s + i];
+        const uint32_t at = next_stage(a, r, f, ring, r0, L, read) + mine;
+        uint4 q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = lds128(at ^ (i << 4));
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            int sum = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                sum = __dp4a(static_cast<int>(q[i].x), static_cast<int>(b[n][i].x), sum);
+                sum = __dp4a(static_cast<int>(q[i].y), static_cast<int>(b[n][i].y), sum);
+                sum = __dp4a(static_cast<int>(q[i].z), static_cast<int>(b[n][i].z), sum);
+                sum = __dp4a(static_cast<int>(q[i].w), static_cast<int>(b[n][i].w), sum);
+            }
+            sum += __shfl_xor_sync(kFull, sum, 1);
+#pragma unroll
+            for (int i = 0; i < kWide; ++i) {        // the groups in order
+                const int p = kWide == 1 ? sum : __shfl_sync(kFull, sum, 2 * i, kLanes);
+                acc[n] = fmaf(static_cast<float>(p), w[i], acc[n]);
+            }
+        }
+    }
+    const bool first = part == 0;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        if (kUp) {
+            const float u = __fmul_rn(acc[n], a.sx[pair[n] / a.k]);
+            const float h = swiglu_f32(u, __shfl_down_sync(kFull, u, 16));   // (lanes 0-15)
+            const bool gate = lane < 16 && row < rows;
+            if (gate && first) a.h[static_cast<int64_t>(pair[n]) * a.I + row0 + row] = h;
+            const unsigned m = __reduce_max_sync(kFull, gate ? __float_as_uint(fabsf(h)) : 0u);
+            if (lane == 0) atomicMax(a.hmax + pair[n], m);
+        } else if (row < rows && first) {
+            s_d[pair[n] * L + row0 + row] =
+                __fmul_rn(acc[n], __fdiv_rn(__uint_as_float(a.hmax[pair[n]]), 127.0f));
+        }
+    }
 }
 
-// Codes and scales of the tokens blockIdx.x, + gridDim.x, ...
-__device__ __forceinline__ void quantize_tokens(const LayerArgs &a, int *red) {
-    for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-        const uint16_t *row = a.x + t * a.ldx;
-        auto load8 = [&](int i) {
-            if (a.vec) return reinterpret_cast<const uint4 *>(row)[i];
-            uint4 v;
-            uint32_t *w = reinterpret_cast<uint32_t *>(&v);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                w[j] = row[8 * i + 2 * j] | static_cast<uint32_t>(row[8 * i + 2 * j + 1]) << 16;
-            return v;
-        };
-        unsigned m = 0;
-        for (int i = threadIdx.x; i < a.H >> 3; i += kThreads) m = max(m, amax_bits8(load8(i)));
-        m = __reduce_max_sync(kFull, m);
-        __syncthreads();
-        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
-        __syncthreads();
-        m = __reduce_max_sync(kFull, (threadIdx.x & 31) < kWarps ? red[threadIdx.x & 31] : 0u);
-        const float s = __fdiv_rn(bf16_bits_to_f32(m), 127.0f);
-        const bool fast = s >= 1.17549435e-38f;      // a normal scale: 1 / s is finite
-        const float rcp = fast ? __frcp_rn(s) : 0.0f;
-        if (threadIdx.x == 0) a.sx[t] = s;
-        for (int i = threadIdx.x; i < a.H >> 3; i += kThreads)
-            reinterpret_cast<uint4 *>(a.xq + static_cast<int64_t>(t) * a.H)[i] =
-                quantize8_f16(load8(i), s, rcp, fast);
+// The warp's share of a product.
+template <bool kUp>
+__device__ __forceinline__ void product(const LayerArgs &a, Routes &r, Feed<kUp> &f, uint32_t ring,
+                                        int L, int r0, float *s_d) {
+    uint32_t read = ring;
+    volatile Stretch &w = r.stretch[threadIdx.x >> 5];
+    for (int taken = 0; taken < w.opened; ++taken) {
+        const int2 tile = make_int2(w.tile[taken & (kQueue - 1)].x, w.tile[taken & (kQueue - 1)].y);
+        const int unit = tile.x >> 8, rows = tile.x & 255;
+        const int p0 = r.first[unit], n_tok = r.first[unit + 1] - p0;
+        const int wide = tile_groups<kUp>(rows, n_tok, kUp ? a.H : a.I);
+        if (n_tok == 1 && wide == 1)
+            take_tile_dot<1, 1, kUp>(a, r, f, unit, tile.y, rows, ring, r0, L, read, p0, s_d);
+        else if (n_tok == 1 && wide == 2)
+            take_tile_dot<1, 2, kUp>(a, r, f, unit, tile.y, rows, ring, r0, L, read, p0, s_d);
+        else if (n_tok == 1)
+            take_tile_dot<1, 4, kUp>(a, r, f, unit, tile.y, rows, ring, r0, L, read, p0, s_d);
+        else if (n_tok == 2 && wide == 1)
+            take_tile_dot<2, 1, kUp>(a, r, f, unit, tile.y, rows, ring, r0, L, read, p0, s_d);
+        else if (n_tok == 2 && wide == 2)
+            take_tile_dot<2, 2, kUp>(a, r, f, unit, tile.y, rows, ring, r0, L, read, p0, s_d);
+        else if (n_tok == 2)
+            take_tile_dot<2, 4, kUp>(a, r, f, unit, tile.y, rows, ring, r0, L, read, p0, s_d);
+        else if (n_tok <= 8)
+            take_tile<1, kUp>(a, r, f, unit, tile.y, rows, ring, r0, L, read, p0, n_tok, s_d);
+        else if (n_tok <= 16)
+            take_tile<2, kUp>(a, r, f, unit, tile.y, rows, ring, r0, L, read, p0, n_tok, s_d);
+        else
+            take_tile<4, kUp>(a, r, f, unit, tile.y, rows, ring, r0, L, read, p0, n_tok, s_d);
     }
+    cp_async_wait<0>();
 }
 
 // Codes of h, 8 values per thread at a time, spread over the grid. (By the pairs' own
@@ -450,72 +574,52 @@ __device__ __forceinline__ void quantize_h(const LayerArgs &a) {
         const float4 u = __ldcg(reinterpret_cast<const float4 *>(a.h + at));
         const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.h + at) + 1);
         const float x[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-        uint32_t o[4];
+        float f[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const __half2 p =
-                __floats2half2_rn(code_plus_round(x[2 * j], s, rcp, fast) - kRoundAdd,
-                                  code_plus_round(x[2 * j + 1], s, rcp, fast) - kRoundAdd);
-            o[j] = *reinterpret_cast<const uint32_t *>(&p);
-        }
-        *reinterpret_cast<uint4 *>(a.hq + at) = make_uint4(o[0], o[1], o[2], o[3]);
+        for (int j = 0; j < 8; ++j) f[j] = code_plus_round(x[j], s, rcp, fast);
+        const uint2 c = make_uint2(pack_code_bytes(f[0], f[1], f[2], f[3]),
+                                   pack_code_bytes(f[4], f[5], f[6], f[7]));
+        *reinterpret_cast<uint2 *>(a.hq + at) = c;
     }
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
 moe_layer_kernel(const LayerArgs a) {
-    extern __shared__ __align__(128) uint8_t s_ring[];
+    extern __shared__ __align__(128) uint8_t s_ring[];   // the rings, then s_d
     __shared__ Routes r;
-    __shared__ int s_red[kWarps];
     griddep_wait();
     make_routes(a, r);
     const int warp = threadIdx.x >> 5;
     const uint32_t ring = smem_u32(s_ring) + warp * kStages * kStageBytes;
-    const int part = blockIdx.x * kWarps + warp, parts = gridDim.x * kWarps;
+    float *s_d = reinterpret_cast<float *>(s_ring + kRingBytes);     // [T k][L]
     {
-        Feed<true> f(a, r, ring, 0, a.I, part, parts);
-        const Cursor c(r.n, a.I, part, parts);
-        quantize_tokens(a, s_red);
-        if (!grid_wait(a.sync + 0, &r.abort, a.err, 0)) {
-            cp_async_wait<0>();
-            return;
-        }
-        product<true>(a, r, f, c, ring, a.I, 0);
+        Feed<true> f(a, r, ring, 0, a.I, blockIdx.x * kWarps + warp, gridDim.x * kWarps);
+        product<true>(a, r, f, ring, a.I, 0, s_d);
     }
     // the CTA's output rows
-    const int r0 = static_cast<int>(static_cast<int64_t>(a.H) * blockIdx.x / gridDim.x);
-    const int L = static_cast<int>(static_cast<int64_t>(a.H) * (blockIdx.x + 1) / gridDim.x) - r0;
-    if (L > 0) {
-        __syncwarp();
-        Feed<false> f(a, r, ring, r0, L, warp, kWarps);
-        const Cursor c(r.n, L, warp, kWarps);
-        bool ok = grid_wait(a.sync + 1, &r.abort, a.err, 1);
-        if (ok) {
-            quantize_h(a);
-            ok = grid_wait(a.sync + 2, &r.abort, a.err, 2);
-        }
-        griddep_launch_dependents();
-        if (!ok) {
-            cp_async_wait<0>();
-            return;
-        }
-        product<false>(a, r, f, c, ring, L, r0);
-    } else {
-        if (!grid_wait(a.sync + 1, &r.abort, a.err, 1)) return;
+    const int r0 = Feed<false>::share(a.H, blockIdx.x, gridDim.x);
+    const int L = Feed<false>::share(a.H, blockIdx.x + 1, gridDim.x) - r0;
+    __syncwarp();
+    Feed<false> f(a, r, ring, r0, max(L, 1), warp, L > 0 ? kWarps : INT32_MAX);
+    bool ok = grid_wait(a.sync + 0, &r.abort, a.err, 0);
+    if (ok) {
         quantize_h(a);
-        grid_wait(a.sync + 2, &r.abort, a.err, 2);
+        ok = grid_wait(a.sync + 1, &r.abort, a.err, 1);
+    }
+    griddep_launch_dependents();
+    if (!ok) {
+        cp_async_wait<0>();
         return;
     }
+    product<false>(a, r, f, ring, L, r0, s_d);
     __syncthreads();
     for (int i = threadIdx.x; i < a.T * L; i += kThreads) {
-        const int t = i / L, n = r0 + i - t * L;
+        const int t = i / L, n = i - t * L;
         float acc = 0.0f;
-        for (int j = 0; j < a.k; ++j) {
-            const int id = a.ids[t * a.k + j];
-            if (id < 0 || id >= a.E) continue;
-            acc = fmaf(a.w[t * a.k + j], a.d[static_cast<int64_t>(t * a.k + j) * a.H + n], acc);
-        }
-        const int64_t at = static_cast<int64_t>(t) * a.H + n;
+        // (the gate gives a place without an expert the weight 0: s_d is not written there)
+        for (int j = t * a.k; j < (t + 1) * a.k; ++j)
+            if (r.w[j] != 0.0f) acc = fmaf(r.w[j], s_d[j * L + n], acc);
+        const int64_t at = static_cast<int64_t>(t) * a.H + r0 + n;
         if (a.out_fp32)
             static_cast<float *>(a.y)[at] = acc;
         else
@@ -524,7 +628,7 @@ moe_layer_kernel(const LayerArgs a) {
 }
 
 struct FewLayout {
-    size_t sync, hmax, sx, xq, h, hq, d, total;
+    size_t zeros, sx, xq, h, hq, total;
 };
 FewLayout few_layout(int64_t T, int64_t k, int64_t H, int64_t I) {
     size_t off = 0;
@@ -535,36 +639,50 @@ FewLayout few_layout(int64_t T, int64_t k, int64_t H, int64_t I) {
     };
     const size_t n = static_cast<size_t>(T * k);
     FewLayout l;
-    l.sync = take((kSyncs + n) * 4);
-    l.hmax = l.sync + kSyncs * 4;
+    l.zeros = take((kSyncs + n) * 4);
     l.sx = take(T * 4);
-    l.xq = take(static_cast<size_t>(T) * H * 2);
+    l.xq = take(static_cast<size_t>(T) * H);
     l.h = take(n * I * 4);
-    l.hq = take(n * I * 2);
-    l.d = take(n * H * 4);
+    l.hq = take(n * I);
     l.total = off;
     return l;
 }
 
+size_t few_outputs_bytes(int64_t T, int64_t k, int64_t H, int num_sms) {
+    return static_cast<size_t>(T * k) * ((H + num_sms - 1) / num_sms) * sizeof(float);
+}
+
 }  // namespace
+
+bool uses_moe_few(int64_t T, int64_t k, int64_t H, int num_sms) {
+    return T <= kMoeFewMaxTokens && T * k <= kMoeFewMaxPairs &&
+           few_outputs_bytes(T, k, H, num_sms) <= kMaxOutputBytes;
+}
 
 size_t moe_few_workspace_bytes(int64_t T, int64_t k, int64_t H, int64_t I) {
     return few_layout(T, k, H, I).total;
 }
 
-void moe_few_zeroes(const MoeFewProblem &p, uint32_t **words, int *n) {
+MoeFewTokens moe_few_tokens(const MoeFewProblem &p) {
     const FewLayout l = few_layout(p.T, p.k, p.H, p.I);
-    *words = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(p.workspace) + l.sync);
-    *n = static_cast<int>(kSyncs + p.T * p.k);
+    uint8_t *ws = static_cast<uint8_t *>(p.workspace);
+    MoeFewTokens t;
+    t.x = p.x;
+    t.ldx = p.ldx;
+    t.T = static_cast<int>(p.T);
+    t.H = static_cast<int>(p.H);
+    t.vec = p.ldx % 8 == 0 && (reinterpret_cast<uintptr_t>(p.x) & 15) == 0;
+    t.sx = reinterpret_cast<float *>(ws + l.sx);
+    t.xq = reinterpret_cast<int8_t *>(ws + l.xq);
+    t.zeros = reinterpret_cast<uint32_t *>(ws + l.zeros);
+    t.n_zeros = static_cast<int>(kSyncs + p.T * p.k);
+    return t;
 }
 
 cudaError_t launch_moe_few(const MoeFewProblem &p, int num_sms, cudaStream_t stream) {
     const FewLayout l = few_layout(p.T, p.k, p.H, p.I);
     uint8_t *ws = static_cast<uint8_t *>(p.workspace);
     LayerArgs a;
-    a.x = p.x;
-    a.ldx = p.ldx;
-    a.vec = p.ldx % 8 == 0 && (reinterpret_cast<uintptr_t>(p.x) & 15) == 0;
     a.ids = p.ids;
     a.w = p.w;
     a.T = static_cast<int>(p.T);
@@ -578,13 +696,12 @@ cudaError_t launch_moe_few(const MoeFewProblem &p, int num_sms, cudaStream_t str
     a.sw_down = p.sw_down;
     a.y = p.y;
     a.out_fp32 = p.out_fp32;
-    a.sync = reinterpret_cast<unsigned *>(ws + l.sync);
-    a.hmax = reinterpret_cast<unsigned *>(ws + l.hmax);
-    a.sx = reinterpret_cast<float *>(ws + l.sx);
-    a.xq = reinterpret_cast<__half *>(ws + l.xq);
+    a.sync = reinterpret_cast<unsigned *>(ws + l.zeros);
+    a.hmax = a.sync + kSyncs;
+    a.sx = reinterpret_cast<const float *>(ws + l.sx);
+    a.xq = reinterpret_cast<const int8_t *>(ws + l.xq);
     a.h = reinterpret_cast<float *>(ws + l.h);
-    a.hq = reinterpret_cast<__half *>(ws + l.hq);
-    a.d = reinterpret_cast<float *>(ws + l.d);
+    a.hq = reinterpret_cast<int8_t *>(ws + l.hq);
     cudaError_t e = device_error_word(&a.err);
     if (e != cudaSuccess) return e;
     static int attr_done[64] = {0};
@@ -592,14 +709,14 @@ cudaError_t launch_moe_few(const MoeFewProblem &p, int num_sms, cudaStream_t str
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if (dev >= 0 && dev < 64 && !attr_done[dev]) {
         e = cudaFuncSetAttribute(moe_layer_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kRingBytes);
+                                 kRingBytes + kMaxOutputBytes);
         if (e != cudaSuccess) return e;
         attr_done[dev] = 1;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(num_sms));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kRingBytes;
+    cfg.dynamicSmemBytes = kRingBytes + few_outputs_bytes(p.T, p.k, p.H, num_sms);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeCooperative;
