@@ -45,7 +45,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 4;
 constexpr int kStageBytes = 16 * 128;
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
-constexpr int kMaxOutputBytes = 80 << 10;   // d of a CTA's rows, in shared memory
+constexpr int kMaxOutputBytes = 64 << 10;   // d of a CTA's rows, in shared memory
 constexpr int kSyncs = 2;                    // grid-wide waits
 constexpr int kQueue = 8;                    // tiles that a ring is ahead at most
 constexpr unsigned kFull = 0xFFFFFFFFu;
@@ -87,11 +87,13 @@ struct Routes {
     int cost[kMoeFewMaxPairs + 1];           // of a row of all experts before
     int pair[kMoeFewMaxPairs];
     int part[kWarps];
-    Stretch stretch[kWarps];
+    Stretch stretch[2][kWarps];              // of both products
     float w[kMoeFewMaxPairs];                // of the pairs; 0 where there is no expert
     int n;
     int abort;
 };
+
+static_assert(kRingBytes + kMaxOutputBytes + sizeof(Routes) <= 227 * 1024);
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -173,6 +175,7 @@ __device__ __forceinline__ void make_routes(const LayerArgs &a, Routes &r) {
     for (int e = threadIdx.x; e < a.E; e += kThreads) r.count[e] = 0;
     if (threadIdx.x == 0) r.abort = 0;
     __syncthreads();
+    griddep_wait();                          // (the ids, and the tokens' codes)
     int id = -1, place = 0;
     if (threadIdx.x < n) {
         id = a.ids[threadIdx.x];
@@ -182,35 +185,37 @@ __device__ __forceinline__ void make_routes(const LayerArgs &a, Routes &r) {
         if (id >= 0) place = atomicAdd(&r.count[id], 1);
     }
     __syncthreads();
-    // two experts per thread; experts with tokens and pairs are counted together
+    // two experts per thread; experts with tokens (10 bits), pairs (10 bits) and what a row costs
+    // beyond the least (at most 512 * (kCostMore - kCostOne)) are summed together
+    static_assert(kCostMore - kCostOne <= 4 && kMoeFewMaxPairs <= 512);
     const int e0 = 2 * threadIdx.x;
     const int c0 = e0 < a.E ? r.count[e0] : 0, c1 = e0 + 1 < a.E ? r.count[e0 + 1] : 0;
+    auto more = [](int n) { return n <= 1 ? 0 : n == 2 ? kCostTwo - kCostOne : kCostMore - kCostOne; };
     int total;
-    const int at = block_scan(((c0 > 0) + (c1 > 0)) << 16 | (c0 + c1), r.part, total);
-    int slot = at >> 16, pairs = at & 0xFFFF;
+    const int at = block_scan(((c0 > 0) + (c1 > 0)) | (c0 + c1) << 10 | (more(c0) + more(c1)) << 20,
+                              r.part, total);
+    int slot = at & 1023, pairs = at >> 10 & 1023, cost = slot * kCostOne + (at >> 20);
     if (c0 > 0) {
         r.expert[slot] = e0;
-        r.first[slot++] = pairs;
+        r.first[slot] = pairs;
+        r.cost[slot++] = cost;
         r.count[e0] = pairs;
         pairs += c0;
+        cost += kCostOne + more(c0);
     }
     if (c1 > 0) {
         r.expert[slot] = e0 + 1;
         r.first[slot] = pairs;
+        r.cost[slot] = cost;
         r.count[e0 + 1] = pairs;
     }
     if (threadIdx.x == 0) {
-        r.n = total >> 16;
-        r.first[total >> 16] = total & 0xFFFF;
+        r.n = total & 1023;
+        r.first[r.n] = total >> 10 & 1023;
+        r.cost[r.n] = r.n * kCostOne + (total >> 20);
     }
     __syncthreads();
     if (id >= 0) r.pair[r.count[id] + place] = threadIdx.x;
-    const int unit = threadIdx.x;
-    const int n_tok = unit < r.n ? r.first[unit + 1] - r.first[unit] : 0;
-    const int cost = n_tok == 0 ? 0 : n_tok == 1 ? kCostOne : n_tok == 2 ? kCostTwo : kCostMore;
-    const int before = block_scan(cost, r.part, total);
-    if (unit <= r.n) r.cost[unit] = before;
-    if (unit == 0) r.cost[r.n] = total;
     __syncthreads();
 }
 
@@ -231,6 +236,40 @@ __device__ __forceinline__ int swizzled(int piece, int row, int wide) {
                        : piece ^ (piece >> 3);
 }
 
+// Where part `part` of `parts` equal parts of n begins. (n * part / parts in 32 bits: a 64-bit
+// division takes a microsecond.)
+__device__ __forceinline__ int share(int n, int part, int parts) {
+    const unsigned q = static_cast<unsigned>(n) / parts, rest = n - q * parts;
+    return q * part + rest * part / parts;
+}
+
+// The warp's stretches of both lines, of units of L rows (part of parts) and of R rows (the warp's of
+// the CTA's): four borders, a lane each.
+__device__ __forceinline__ void cut_line(Routes &r, int L, int part, int parts, int R) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool second = lane & 2;
+    const int rows = second ? R : L;
+    const int at = second ? share(r.cost[r.n] * rows, warp + (lane & 1), kWarps)
+                          : share(r.cost[r.n] * rows, part + (lane & 1), parts);  // <= 512 * 8 * 8192
+    int lo = 0, hi = r.n;                    // cost[lo] rows <= at < cost[hi] rows
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (r.cost[mid] * rows <= at) lo = mid; else hi = mid;
+    }
+    int row = 0;
+    if (r.n > 0 && rows > 0) row = min(rows, (at - r.cost[lo] * rows) / (r.cost[lo + 1] - r.cost[lo]));
+    const int pos = lo * rows + row, end = __shfl_down_sync(kFull, pos, 1);
+    if (lane == 0 || lane == 2) {
+        Stretch &w = r.stretch[lane >> 1][warp];
+        w.pos = pos;
+        w.end = end;
+        w.unit = row == rows ? lo + 1 : lo;  // (a border at a unit's end)
+        w.at = row == rows ? 0 : row;
+        w.opened = 0;
+    }
+    __syncwarp();
+}
+
 // The weights' side of a product: kUp, pairs of rows (i, I + i) of W_gate_up, else rows
 // [r0, r0 + L) of W_down. The line has r.n units (experts) of L rows; the warp takes stretches
 // of it, a tile of up to kMost rows of one unit at a time, K group by K group. Tiles
@@ -245,52 +284,19 @@ struct Feed {
     uint32_t dst, off;       // the stage that the next copy goes to, the lane's piece in it
     const int8_t *src;       // the lane's piece of the tile's first row, at that step
 
-    // What part `part` of `parts` has of n rows begins here. (n * part / parts in 32 bits: a
-    // 64-bit division takes a microsecond.)
-    static __device__ __forceinline__ int share(int n, int part, int parts) {
-        const unsigned q = static_cast<unsigned>(n) / parts, rest = n - q * parts;
-        return q * part + rest * part / parts;
-    }
-    // The row of the line where part `part` of `parts` begins, and its unit: equal costs.
-    static __device__ __forceinline__ int begin(const Routes &r, int L, int part, int parts,
-                                                int &unit) {
-        const int at = share(r.cost[r.n] * L, part, parts);      // <= 512 * 8 * 8192
-        int lo = 0, hi = r.n;                                    // cost[lo] L <= at < cost[hi] L
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (r.cost[mid] * L <= at) lo = mid; else hi = mid;
-        }
-        unit = lo;
-        if (r.n == 0) return 0;
-        return lo * L + min(L, (at - r.cost[lo] * L) / (r.cost[lo + 1] - r.cost[lo]));
-    }
-
-    __device__ __forceinline__ Feed(const LayerArgs &a, Routes &r, uint32_t ring, int r0, int L,
-                                    int part, int parts)
+    // `w`: the warp's stretch (cut_line).
+    __device__ __forceinline__ Feed(const LayerArgs &a, Routes &r, Stretch &w, uint32_t ring, int r0,
+                                    int L)
         : left(0), rows(0), wide(1), dst(ring), off(0), src(nullptr) {
-        const int lane = threadIdx.x & 31;
-        Stretch &w = r.stretch[threadIdx.x >> 5];
-        if (lane == 0) {
-            int end_unit;
-            w.pos = begin(r, L, part, parts, w.unit);
-            w.end = begin(r, L, part + 1, parts, end_unit);
-            w.at = w.pos - w.unit * L;
-            if (w.at == L) {                         // (a border at a unit's end)
-                w.at = 0;
-                ++w.unit;
-            }
-            w.opened = 0;
-        }
-        __syncwarp();
-        open(a, r, r0, L);
+        open(a, r, w, r0, L);
 #pragma unroll 1
-        for (int i = 0; i < kStages - 1; ++i) issue(a, r, ring, r0, L);
+        for (int i = 0; i < kStages - 1; ++i) issue(a, r, w, ring, r0, L);
         __syncwarp();
     }
     // The next tile, if there is one.
-    __device__ __forceinline__ void open(const LayerArgs &a, Routes &r, int r0, int L) {
+    __device__ __forceinline__ void open(const LayerArgs &a, const Routes &r, Stretch &w, int r0,
+                                         int L) {
         const int lane = threadIdx.x & 31;
-        Stretch &w = r.stretch[threadIdx.x >> 5];
         int n = min(w.end - w.pos, L - w.at);
         if (n <= 0) return;
         n = (n + (n - 1) / kMost) / ((n - 1) / kMost + 1);    // tiles of even height
@@ -321,8 +327,8 @@ struct Feed {
                    : a.qw_down + (e * a.H + r0 + at + row) * a.I) + piece * 16;
     }
     // Asks for the next step's weights.
-    __device__ __forceinline__ void issue(const LayerArgs &a, Routes &r, uint32_t ring, int r0,
-                                          int L) {
+    __device__ __forceinline__ void issue(const LayerArgs &a, const Routes &r, Stretch &w,
+                                          uint32_t ring, int r0, int L) {
         if (left > 0) {
             // the lane's rows are 4 / wide apart: 512 bytes of the stage (whose swizzle differs
             // by the row's bit 2, where a group is a step); the second two of W_gate_up are up
@@ -335,7 +341,7 @@ struct Feed {
             if (rows > (kUp ? 0 : 2 * apart)) cp_async_16(to + 1024, src + third);
             if (rows > (kUp ? apart : 3 * apart)) cp_async_16(odd + 1536, src + third + apart * K);
             src += 128 * wide;
-            if (--left == 0) open(a, r, r0, L);
+            if (--left == 0) open(a, r, w, r0, L);
         }
         cp_async_commit();
         dst += kStageBytes;
@@ -349,7 +355,7 @@ __device__ __forceinline__ uint32_t next_stage(const LayerArgs &a, Routes &r, Fe
                                                uint32_t ring, int r0, int L, uint32_t &read) {
     cp_async_wait<kStages - 2>();
     __syncwarp();                            // the stage is there; the one before is read
-    f.issue(a, r, ring, r0, L);
+    f.issue(a, r, r.stretch[kUp ? 0 : 1][threadIdx.x >> 5], ring, r0, L);
     const uint32_t at = read;
     read = read + kStageBytes - ring >= kStages * kStageBytes ? ring : read + kStageBytes;
     return at;
@@ -531,7 +537,7 @@ template <bool kUp>
 __device__ __forceinline__ void product(const LayerArgs &a, Routes &r, Feed<kUp> &f, uint32_t ring,
                                         int L, int r0, float *s_d) {
     uint32_t read = ring;
-    volatile Stretch &w = r.stretch[threadIdx.x >> 5];
+    volatile Stretch &w = r.stretch[kUp ? 0 : 1][threadIdx.x >> 5];
     for (int taken = 0; taken < w.opened; ++taken) {
         const int2 tile = make_int2(w.tile[taken & (kQueue - 1)].x, w.tile[taken & (kQueue - 1)].y);
         const int unit = tile.x >> 8, rows = tile.x & 255;
@@ -587,20 +593,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 moe_layer_kernel(const LayerArgs a) {
     extern __shared__ __align__(128) uint8_t s_ring[];   // the rings, then s_d
     __shared__ Routes r;
-    griddep_wait();
-    make_routes(a, r);
     const int warp = threadIdx.x >> 5;
     const uint32_t ring = smem_u32(s_ring) + warp * kStages * kStageBytes;
     float *s_d = reinterpret_cast<float *>(s_ring + kRingBytes);     // [T k][L]
+    // the CTA's output rows
+    const int r0 = share(a.H, blockIdx.x, gridDim.x);
+    const int L = share(a.H, blockIdx.x + 1, gridDim.x) - r0;
+    make_routes(a, r);
+    cut_line(r, a.I, blockIdx.x * kWarps + warp, gridDim.x * kWarps, L);
     {
-        Feed<true> f(a, r, ring, 0, a.I, blockIdx.x * kWarps + warp, gridDim.x * kWarps);
+        Feed<true> f(a, r, r.stretch[0][warp], ring, 0, a.I);
         product<true>(a, r, f, ring, a.I, 0, s_d);
     }
-    // the CTA's output rows
-    const int r0 = Feed<false>::share(a.H, blockIdx.x, gridDim.x);
-    const int L = Feed<false>::share(a.H, blockIdx.x + 1, gridDim.x) - r0;
     __syncwarp();
-    Feed<false> f(a, r, ring, r0, max(L, 1), warp, L > 0 ? kWarps : INT32_MAX);
+    Feed<false> f(a, r, r.stretch[1][warp], ring, r0, L);
     bool ok = grid_wait(a.sync + 0, &r.abort, a.err, 0);
     if (ok) {
         quantize_h(a);
