@@ -1276,7 +1276,7 @@ w8a8_status w8a8_quant_act_fp8(const void *a_bf16, int64_t M, int64_t K, int64_t
     w8a8_status st = check_device(&info);
     if (st != W8A8_OK) return st;
     return from_cuda(w8a8::launch_quant_act_fp8(static_cast<const uint16_t *>(a_bf16), M, K, lda,
-                                                qa, sa, mode == W8A8_SCALE_POW2,
+                                                qa, sa, mode == W8A8_SCALE_POW2, false,
                                                 reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -1332,7 +1332,7 @@ w8a8_status w8a8_linear_fp8(const void *a_bf16, int64_t lda, w8a8_scale_mode act
     float *sa = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) +
                                           round_up(static_cast<size_t>(M) * K, kWsAlign));
     if (w8a8::launch_quant_act_fp8(static_cast<const uint16_t *>(a_bf16), M, K, lda, workspace, sa,
-                                   act_mode == W8A8_SCALE_POW2,
+                                   act_mode == W8A8_SCALE_POW2, true,
                                    reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
         return W8A8_ERR_CUDA;
     return run_gemm_fp8(workspace, sa, qw, sw, y, y_dtype, M, N, K, info.num_sms, stream);

@@ -34,7 +34,7 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kTokens = 128;
 constexpr int kMaxSlice = 256;
-constexpr int kMaxStages = 16, kMaxBufs = 8;
+constexpr int kMaxStages = 16, kMaxBufs = 8, kMaxPerStep = 4;
 constexpr int kSmemBytes = 227 * 1024;
 constexpr int kOffStages = 1024;           // barriers and flags before them
 constexpr int kStagedBytes = 8 * 32 * 17 * 4;   // outputs on their way, at the end
@@ -52,6 +52,7 @@ struct Fp8Args {
     int a_bytes, b_bytes;      // of a stage
     int a_box, b_box;          // bytes that a copy brings
     int stages, bufs, buf_cols;
+    int per_step;              // groups of a step: of a stage, of a buffer
     int m_tiles, tiles;
     int n_mma;                 // the slice in an instruction's N
     int out_fp32, wide_store;  // rows of y allow 32-byte stores
@@ -236,7 +237,9 @@ __device__ __forceinline__ void store_staged(const Fp8Args &a, uint32_t *buf, in
     }
 }
 
-// kCols: columns of a half of the slice, at most (32, 64 or 128).
+// kCols: columns of a half of the slice, rounded up to 32 (what is read past the half is not
+// stored, and lies within tensor memory: launch_gemm_fp8). Slices of more than 128 rows have one
+// group per step.
 template <int kCols>
 __global__ void __launch_bounds__(kThreads, 1)
 gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmap_a,
@@ -246,7 +249,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmap_a,
     const uint32_t base = (raw + 1023u) & ~1023u;
     Bars &s = *reinterpret_cast<Bars *>(smem_raw + (base - raw));
     const uint32_t sA = base + kOffStages;
-    const uint32_t sB = sA + a.stages * a.a_bytes;
+    const uint32_t sB = sA + a.stages * a.per_step * a.a_bytes;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < a.stages; ++i) {
@@ -273,7 +276,6 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmap_a,
     const uint32_t tmem = s.tmem;
     volatile int *abort_flag = &s.abort_flag;
     griddep_launch_dependents();
-    griddep_wait();          // the codes and scales may come from the kernel launched before
 
     if (warp < 4) {
         setmaxnreg_dec<kOtherRegs>();
@@ -282,19 +284,49 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmap_a,
             Ring r;
             uint32_t issued = 0;
             bool ok = true;
+            // The first weights are asked for while the kernel before, which may write the
+            // tokens' codes and scales, still runs.
+            const int steps = (a.G + a.per_step - 1) / a.per_step;
+            const int ahead = a.stages < steps ? a.stages : steps;
+            auto load = [&](const void *map, uint32_t to, int bytes, int step, int row,
+                            uint32_t bar) {
+                const int groups = min(a.per_step, a.G - step * a.per_step);
+                for (int i = 0; i < groups; ++i)
+                    tma_load_2d(to + i * bytes, map, (step * a.per_step + i) * 128, row, bar);
+            };
+            auto expect = [&](int step, uint32_t bar) {
+                mbar_arrive_expect_tx(bar, min(a.per_step, a.G - step * a.per_step) *
+                                               (a.a_box + a.b_box));
+            };
+            {
+                const int n = blockIdx.x / a.m_tiles;
+                for (int i = 0; i < ahead; ++i) {
+                    const uint32_t bar = smem_u32(&s.full[i]);
+                    expect(i, bar);
+                    load(&tmap_b, sB + i * a.per_step * a.b_bytes, a.b_bytes, i, n * a.w, bar);
+                }
+                griddep_wait();
+                const int m0 = (blockIdx.x - n * a.m_tiles) * kTokens;
+                for (int i = 0; i < ahead; ++i)
+                    load(&tmap_a, sA + i * a.per_step * a.a_bytes, a.a_bytes, i, m0,
+                         smem_u32(&s.full[i]));
+                issued = ahead;
+                r.idx = ahead == a.stages ? 0 : ahead;
+                r.phase = ahead == a.stages ? 1 : 0;
+            }
             for (int t = blockIdx.x; t < a.tiles && ok; t += gridDim.x) {
                 const int n = t / a.m_tiles;
                 const int m0 = (t - n * a.m_tiles) * kTokens, n0 = n * a.w;
-                for (int g = 0; g < a.G; ++g) {
+                for (int i = t == blockIdx.x ? ahead : 0; i < steps; ++i) {
                     if (!mbar_wait(smem_u32(&s.empty[r.idx]), r.phase ^ 1u, abort_flag, a.err,
                                    ROLE_PRODUCER, 0, kWaitLimitNs, KID_FP8)) {
                         ok = false;
                         break;
                     }
                     const uint32_t bar = smem_u32(&s.full[r.idx]);
-                    mbar_arrive_expect_tx(bar, a.a_box + a.b_box);
-                    tma_load_2d(sB + r.idx * a.b_bytes, &tmap_b, g * 128, n0, bar);
-                    tma_load_2d(sA + r.idx * a.a_bytes, &tmap_a, g * 128, m0, bar);
+                    expect(i, bar);
+                    load(&tmap_b, sB + r.idx * a.per_step * a.b_bytes, a.b_bytes, i, n0, bar);
+                    load(&tmap_a, sA + r.idx * a.per_step * a.a_bytes, a.a_bytes, i, m0, bar);
                     r.advance(a.stages);
                     ++issued;
                 }
@@ -314,7 +346,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmap_a,
             bool ok = true;
             const uint32_t idesc = idesc_e4m3(kTokens, a.n_mma);
             for (int t = blockIdx.x; t < a.tiles && ok; t += gridDim.x) {
-                for (int g = 0; g < a.G; ++g) {
+                for (int g = 0; g < a.G; g += a.per_step) {
                     ok = mbar_wait(smem_u32(&s.d_empty[d.idx]), d.phase ^ 1u, abort_flag, a.err,
                                    ROLE_MMA, 0, kWaitLimitNs, KID_FP8) &&
                          mbar_wait(smem_u32(&s.full[r.idx]), r.phase, abort_flag, a.err, ROLE_MMA,
@@ -322,14 +354,23 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmap_a,
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t da = desc_lo(sA + r.idx * a.a_bytes);
-                    const uint32_t db = desc_lo(sB + r.idx * a.b_bytes);
-                    const uint32_t dt = tmem + d.idx * a.buf_cols;
+                    const int groups = min(a.per_step, a.G - g);
+                    const uint32_t da = desc_lo(sA + r.idx * a.per_step * a.a_bytes);
+                    const uint32_t db = desc_lo(sB + r.idx * a.per_step * a.b_bytes);
+                    const uint32_t dt = tmem + d.idx * a.per_step * a.buf_cols;
+                    const uint32_t ka = a.a_bytes >> 4, kb = a.b_bytes >> 4, kd = a.buf_cols;
                     if (elect_one()) {
-                        mma_e4m3<false>(dt, da, db, idesc);
-                        mma_e4m3<true>(dt, da + 2, db + 2, idesc);
-                        mma_e4m3<true>(dt, da + 4, db + 4, idesc);
-                        mma_e4m3<true>(dt, da + 6, db + 6, idesc);
+                        // (the groups' instructions take turns: one that adds to what the one
+                        // before it wrote waits for it)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                            for (int i = 0; i < kMaxPerStep; ++i) {
+                                if (i >= groups) break;
+                                if (k == 0) mma_e4m3<false>(dt + i * kd, da + i * ka, db + i * kb, idesc);
+                                else mma_e4m3<true>(dt + i * kd, da + i * ka + 2 * k, db + i * kb + 2 * k, idesc);
+                            }
+                        }
                         mma_commit(smem_u32(&s.empty[r.idx]));
                         mma_commit(smem_u32(&s.d_full[d.idx]));
                     }
@@ -347,6 +388,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmap_a,
     } else {
         // ----------------------------------------------------------- sums of groups
         setmaxnreg_inc<kSumRegs>();
+        griddep_wait();
         const int h = (warp >> 2) - 1, q = warp & 3;
         const uint32_t my_tmem = tmem + (static_cast<uint32_t>(q * 32) << 16) + h * a.half;
         uint32_t *stage_buf = reinterpret_cast<uint32_t *>(smem_raw + kSmemBytes - kStagedBytes) +
@@ -368,54 +410,65 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmap_a,
             unsigned long long acc[kCols / 2];
 #pragma unroll
             for (int j = 0; j < kCols / 2; ++j) acc[j] = 0ull;
-            float fa = 0.0f, f0 = 0.0f, f1 = 0.0f;
-            if (on) {
-                fa = ld_now(sa);
-                f0 = ld_now(sw0);
-                f1 = ld_now(sw1);
+            uint32_t at = 0;
+            if (!on) {                               // (only hands the buffers on)
+                for (int g = 0; g < a.G; g += a.per_step) {
+                    ok = mbar_wait(smem_u32(&s.d_full[d.idx]), d.phase, abort_flag, a.err,
+                                   ROLE_EPILOGUE, 1, kWaitLimitNs, KID_FP8);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_relaxed(smem_u32(&s.d_empty[d.idx]));
+                    d.advance(a.bufs);
+                }
+                continue;
             }
+            float fa = ld_now(sa), f0 = ld_now(sw0), f1 = ld_now(sw1);
+            int left = 0;                            // groups of the step
             for (int g = 0; g < a.G; ++g) {
                 const float s0 = fa * f0, s1 = fa * f1;
-                if (on && g + 1 < a.G) {
+                if (g + 1 < a.G) {
                     fa = ld_now(sa + g + 1);
                     f0 = ld_now(sw0 + g + 1);
                     f1 = ld_now(sw1 + g + 1);
                 }
-                ok = mbar_wait(smem_u32(&s.d_full[d.idx]), d.phase, abort_flag, a.err,
-                               ROLE_EPILOGUE, 0, kWaitLimitNs, KID_FP8);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
-                tc_fence_after();
-                if (on) {
-                    const uint32_t at = my_tmem + d.idx * a.buf_cols;
-                    uint32_t v[2][32];
-                    tmem_ld32(at, v[0]);
+                if (kCols > 64 || left == 0) {
+                    ok = mbar_wait(smem_u32(&s.d_full[d.idx]), d.phase, abort_flag, a.err,
+                                   ROLE_EPILOGUE, 0, kWaitLimitNs, KID_FP8);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (kCols <= 64) left = min(a.per_step, a.G - g);
+                    at = my_tmem + d.idx * a.per_step * a.buf_cols;
+                }
+                uint32_t v[2][32];
+                tmem_ld32(at, v[0]);
 #pragma unroll
-                    for (int c = 0; c < kCols / 32; ++c) {
-                        if (32 * c >= cols) break;
-                        tmem_wait32(v[c & 1]);
-                        if (c + 1 < kCols / 32 && 32 * c + 32 < cols)
-                            tmem_ld32(at + 32 * c + 32, v[(c + 1) & 1]);
+                for (int c = 0; c < kCols / 32; ++c) {
+                    tmem_wait32(v[c & 1]);
+                    if (c + 1 < kCols / 32)
+                        tmem_ld32(at + 32 * c + 32, v[(c + 1) & 1]);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float f = 32 * c + 8 * i < edge ? s0 : s1;
-                            const unsigned long long f2 = f2_bits(f, f);
+                    for (int i = 0; i < 4; ++i) {
+                        const float f = 32 * c + 8 * i < edge ? s0 : s1;
+                        const unsigned long long f2 = f2_bits(f, f);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                unsigned long long &o = acc[16 * c + 4 * i + j];
-                                o = f2_fma(f2_bits(__uint_as_float(v[c & 1][8 * i + 2 * j]),
-                                                   __uint_as_float(v[c & 1][8 * i + 2 * j + 1])),
-                                           f2, o);
-                            }
+                        for (int j = 0; j < 4; ++j) {
+                            unsigned long long &o = acc[16 * c + 4 * i + j];
+                            o = f2_fma(f2_bits(__uint_as_float(v[c & 1][8 * i + 2 * j]),
+                                               __uint_as_float(v[c & 1][8 * i + 2 * j + 1])),
+                                       f2, o);
                         }
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_relaxed(smem_u32(&s.d_empty[d.idx]));
-                d.advance(a.bufs);
+                at += a.buf_cols;
+                if (kCols > 64 || --left == 0) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_relaxed(smem_u32(&s.d_empty[d.idx]));
+                    d.advance(a.bufs);
+                }
             }
-            if (ok && on) {
+            if (ok) {
                 if (a.wide_store) {
                     if (m < a.M) store_row<kCols>(a, static_cast<int64_t>(m) * a.N + c0, cols, acc);
                 } else {
@@ -802,10 +855,21 @@ cudaError_t launch_gemm_fp8(const Fp8Problem &p, int num_sms, cudaStream_t strea
     // lanes of tensor memory are never read.)
     static_assert(kStagedBytes >= 128 * 128);
     const int room = kSmemBytes - 1024 - kOffStages - kStagedBytes;
-    a.stages = room / (a.a_bytes + a.b_bytes);
+    a.buf_cols = (a.w + 31) / 32 * 32;
+    // Groups of a step. Handing a stage and a buffer on takes some 400 cycles a step, more than the
+    // weights of a narrow slice: as many as leave two buffers and four stages.
+    a.per_step = kMaxPerStep;
+    while (a.per_step > 1 && (2 * a.per_step * a.buf_cols > kTmemCols ||
+                              4 * a.per_step * (a.a_bytes + a.b_bytes) > room || a.per_step > a.G))
+        a.per_step /= 2;
+    a.stages = room / (a.per_step * (a.a_bytes + a.b_bytes));
     if (a.stages > kMaxStages) a.stages = kMaxStages;
-    a.buf_cols = a.w <= 64 ? 64 : a.w <= 128 ? 128 : 256;
-    a.bufs = kTmemCols / a.buf_cols;
+    a.bufs = kTmemCols / (a.per_step * a.buf_cols);
+    if (a.bufs > kMaxBufs) a.bufs = kMaxBufs;
+    // (the second half's columns are read up to a multiple of 32)
+    const int last = (a.bufs * a.per_step - 1) * a.buf_cols + (a.w > a.half ? a.half : 0);
+    if (last + (a.half + 31) / 32 * 32 > kTmemCols || (a.half > 64 && a.per_step != 1))
+        return cudaErrorInvalidValue;
     const int64_t tiles = static_cast<int64_t>(a.m_tiles) * ((a.N + a.w - 1) / a.w);
     if (tiles > INT32_MAX - 4096) return cudaErrorInvalidValue;
     a.tiles = static_cast<int>(tiles);
@@ -815,6 +879,7 @@ cudaError_t launch_gemm_fp8(const Fp8Problem &p, int num_sms, cudaStream_t strea
     const int grid = a.tiles < num_sms ? a.tiles : num_sms;
     if (a.half <= 32) return launch_as<gemm_fp8_kernel<32>>(ta, tb, a, grid, stream);
     if (a.half <= 64) return launch_as<gemm_fp8_kernel<64>>(ta, tb, a, grid, stream);
+    if (a.half <= 96) return launch_as<gemm_fp8_kernel<96>>(ta, tb, a, grid, stream);
     return launch_as<gemm_fp8_kernel<128>>(ta, tb, a, grid, stream);
 }
 

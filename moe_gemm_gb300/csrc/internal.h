@@ -265,8 +265,10 @@ cudaError_t launch_gemm(const GemmProblem &p, int num_sms, cudaStream_t stream);
 
 // FP8 (e4m3) with a scale per block of 128: quantizers (quant_fp8.cu) and the product
 // (gemm_fp8.cu).
+// chained: the next launch reads these codes as tokens, and may start early (the product asks
+// for its first weights before it waits for the kernel before).
 cudaError_t launch_quant_act_fp8(const uint16_t *a, int64_t M, int64_t K, int64_t lda, void *qa,
-                                 float *sa, bool pow2, cudaStream_t stream);
+                                 float *sa, bool pow2, bool chained, cudaStream_t stream);
 cudaError_t launch_quant_weight_fp8(const float *w, int64_t N, int64_t K, bool pow2, void *qw,
                                     float *sw, cudaStream_t stream);
 struct Fp8Problem {

@@ -63,47 +63,57 @@ __device__ __forceinline__ uint2 codes8_fp8(const float (&x)[8], float s, bool p
                       e4m3x2(y[4], y[5]) | e4m3x2(y[6], y[7]) << 16);
 }
 
-// 16 lanes per (token, group): 8 values each.
-template <bool kPow2, bool kVec>
+// 16 lanes per (token, group), 8 values each; a thread takes kUnits of them, one block's width
+// apart, all loaded before the first is worked on.
+template <bool kPow2, bool kVec, int kUnits>
 __global__ void __launch_bounds__(kActThreads)
-quant_act_fp8_kernel(const uint16_t *a, int64_t lda, int64_t units, int G, uint8_t *qa, float *sa) {
-    griddep_launch_dependents();
+quant_act_fp8_kernel(const uint16_t *a, int64_t lda, int units, int G, int chained, uint8_t *qa,
+                     float *sa) {
+    if (chained) griddep_launch_dependents();
     griddep_wait();
-    const int64_t u = (static_cast<int64_t>(blockIdx.x) * kActThreads + threadIdx.x) >> 4;
+    constexpr int kPerBlock = kActThreads / 16;
+    const int first = blockIdx.x * kPerBlock * kUnits + (threadIdx.x >> 4);
     const int c = threadIdx.x & 15;
-    const bool on = u < units;
-    const int64_t m = on ? u / G : 0;
-    const int g = on ? static_cast<int>(u - m * G) : 0;
-    const uint16_t *src = a + m * lda + g * 128 + c * 8;
-    uint4 v;
-    if (kVec) {
-        v = *reinterpret_cast<const uint4 *>(src);
-    } else {
-        uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+    uint4 v[kUnits];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            w[j] = src[2 * j] | static_cast<uint32_t>(src[2 * j + 1]) << 16;
+    for (int i = 0; i < kUnits; ++i) {
+        const int u = min(first + i * kPerBlock, units - 1);
+        const int m = static_cast<unsigned>(u) / static_cast<unsigned>(G);
+        const uint16_t *src = a + m * lda + (u - m * G) * 128 + c * 8;
+        if (kVec) {
+            v[i] = __ldcs(reinterpret_cast<const uint4 *>(src));
+        } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[j] = src[2 * j] | static_cast<uint32_t>(src[2 * j + 1]) << 16;
+            v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
     }
-    uint32_t mx = amax_bits8(v);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(kFull, mx, o));
-    if (!on) return;
-    const float s = scale_of(bf16_bits_to_f32(mx), kPow2);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    float x[8];
+    for (int i = 0; i < kUnits; ++i) {
+        const int u = first + i * kPerBlock;
+        uint32_t mx = amax_bits8(v[i]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        x[2 * j] = bf16_bits_to_f32(w[j] & 0xFFFFu);
-        x[2 * j + 1] = bf16_bits_to_f32(w[j] >> 16);
+        for (int o = 8; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(kFull, mx, o));
+        const float s = scale_of(bf16_bits_to_f32(mx), kPow2);
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[2 * j] = bf16_bits_to_f32(w[j] & 0xFFFFu);
+            x[2 * j + 1] = bf16_bits_to_f32(w[j] >> 16);
+        }
+        if (u >= units) break;
+        reinterpret_cast<uint2 *>(qa)[static_cast<int64_t>(u) * 16 + c] = codes8_fp8(x, s, kPow2);
+        if (c == 0) sa[u] = s;
     }
-    reinterpret_cast<uint2 *>(qa)[u * 16 + c] = codes8_fp8(x, s, kPow2);
-    if (c == 0) sa[u] = s;
 }
 
 // One CTA per block: 8 warps, a row of 128 values per warp at a time.
 __global__ void __launch_bounds__(256)
 quant_weight_fp8_kernel(const float *w, int N, int K, int pow2, uint8_t *qw, float *sw) {
-    griddep_launch_dependents();
+    // (lets no kernel start early: the product asks for weights before it waits)
     griddep_wait();
     __shared__ float s_max[8];
     const int g = blockIdx.x, b = blockIdx.y;
@@ -155,15 +165,24 @@ cudaError_t launch(void (*kernel)(Params...), dim3 grid, int threads, cudaStream
 }  // namespace
 
 cudaError_t launch_quant_act_fp8(const uint16_t *a, int64_t M, int64_t K, int64_t lda, void *qa,
-                                 float *sa, bool pow2, cudaStream_t stream) {
+                                 float *sa, bool pow2, bool chained, cudaStream_t stream) {
+    // (units are below 2^31 / 128.) A long call takes four units per thread, for more loads
+    // in flight; a decode step has SMs to fill.
     const int G = static_cast<int>(K >> 7);
-    const int64_t units = M * G;
-    const dim3 grid(static_cast<unsigned>((units * 16 + kActThreads - 1) / kActThreads));
+    const int units = static_cast<int>(M * G);
+    const bool many = units >= 1 << 15;
+    const int per = kActThreads / 16 * (many ? 4 : 1);
+    const dim3 grid(static_cast<unsigned>((units + per - 1) / per));
     const bool vec = lda % 8 == 0 && (reinterpret_cast<uintptr_t>(a) & 15) == 0;
-    auto *kernel = pow2 ? (vec ? quant_act_fp8_kernel<true, true> : quant_act_fp8_kernel<true, false>)
-                        : (vec ? quant_act_fp8_kernel<false, true> : quant_act_fp8_kernel<false, false>);
-    return launch(kernel, grid, kActThreads, stream, a, lda, units, G, static_cast<uint8_t *>(qa),
-                  sa);
+    auto *kernel = quant_act_fp8_kernel<false, false, 1>;
+    if (many)
+        kernel = pow2 ? (vec ? quant_act_fp8_kernel<true, true, 4> : quant_act_fp8_kernel<true, false, 4>)
+                      : (vec ? quant_act_fp8_kernel<false, true, 4> : quant_act_fp8_kernel<false, false, 4>);
+    else
+        kernel = pow2 ? (vec ? quant_act_fp8_kernel<true, true, 1> : quant_act_fp8_kernel<true, false, 1>)
+                      : (vec ? quant_act_fp8_kernel<false, true, 1> : quant_act_fp8_kernel<false, false, 1>);
+    return launch(kernel, grid, kActThreads, stream, a, lda, units, G, chained ? 1 : 0,
+                  static_cast<uint8_t *>(qa), sa);
 }
 
 cudaError_t launch_quant_weight_fp8(const float *w, int64_t N, int64_t K, bool pow2, void *qw,
