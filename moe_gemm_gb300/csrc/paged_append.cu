@@ -34,7 +34,7 @@
 namespace w8a8 {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kPerPass = kThreads / 16;      // vectors that a CTA takes at a time
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
@@ -216,7 +216,7 @@ cudaError_t launch_as(const AppendArgs &a, int64_t T, int runs, cudaStream_t str
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_kv_append_kernel<kInt8, kPairs, 3>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, paged_kv_append_kernel<kInt8, kPairs, 2>, a);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
