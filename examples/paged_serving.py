@@ -9,11 +9,13 @@ and their pages serve others. Each step runs
     norm + QKV projection (rmsnorm_linear), K and V into their slots
              (paged_kv_write), attention over the pages (attention_paged),
              output projection (linear), residual
-    norm, router logits, the gate (moe_gate), the expert FFN (moe_ffn), residual
+    norm, router logits, the gate and its experts' FFNs (moe_layer), residual
 
-with random weights. Run it on a GB300:
+with random weights. With --rotate, queries and keys are turned by their positions as
+they are written (paged_kv_append); with --fp8, the projections are those of a checkpoint
+with FP8 blocks (linear_fp8). Run it on a GB300:
 
-    python examples/paged_serving.py [--steps N]
+    python examples/paged_serving.py [--steps N] [--rotate] [--fp8]
 
 It prints what each step served, and at the end how far the answers of a request
 are from serving it alone, prompt in one piece.
@@ -34,9 +36,11 @@ D = 128
 
 class Layer:
     """The weights of one layer: INT8 projections and experts, BF16 norms, an
-    FP32 router with a balance bias and expert groups."""
+    FP32 router with a balance bias and expert groups. rotate: queries and keys are
+    turned by their positions. fp8: projections of FP8 blocks with power-of-two scales."""
 
-    def __init__(self, hidden=512, q_heads=8, kv_heads=2, experts=16, topk=4, inner=256, seed=0):
+    def __init__(self, hidden=512, q_heads=8, kv_heads=2, experts=16, topk=4, inner=256, seed=0,
+                 rotate=False, fp8=False):
         g = torch.Generator(device="cuda").manual_seed(seed)
 
         def normal(*shape, std=0.02):
@@ -44,8 +48,13 @@ class Layer:
 
         self.hidden, self.q_heads, self.kv_heads, self.topk = hidden, q_heads, kv_heads, topk
         self.norm1, self.norm2 = (1 + normal(2, hidden, std=0.1)).to(torch.bfloat16)
-        self.qkv = w8.quant_weight(normal((q_heads + 2 * kv_heads) * D, hidden))
-        self.out = w8.quant_weight(normal(hidden, q_heads * D))
+        self.fp8 = fp8
+        quant = (lambda w: w8.quant_weight_fp8(w, scale_mode=w8.SCALE_POW2)) if fp8 else w8.quant_weight
+        self.qkv = quant(normal((q_heads + 2 * kv_heads) * D, hidden))
+        self.out = quant(normal(hidden, q_heads * D))
+        self.inv_freq = None
+        if rotate:
+            self.inv_freq = (1e4 ** -(torch.arange(D // 2, dtype=torch.float64) / (D // 2))).float().cuda()
         self.router = normal(experts, hidden)
         self.balance = normal(experts)
         up = [w8.quant_weight(normal(2 * inner, hidden)) for _ in range(experts)]
@@ -55,18 +64,30 @@ class Layer:
 
     def __call__(self, x, cache, plan):
         """x [T, hidden] BF16: the new tokens of all requests, packed."""
-        cu_new, kv_lens, slots, _ = plan
+        cu_new, kv_lens, slots, positions = plan
         T, hq, hkv = x.shape[0], self.q_heads, self.kv_heads
-        qkv = w8.rmsnorm_linear(x, self.norm1, 1e-6, *self.qkv).view(T, hq + 2 * hkv, D)
+        if self.fp8:
+            qkv = w8.linear_fp8(w8.rmsnorm(x, self.norm1, 1e-6), *self.qkv,
+                                act_scale_mode=w8.SCALE_POW2)
+        else:
+            qkv = w8.rmsnorm_linear(x, self.norm1, 1e-6, *self.qkv)
+        qkv = qkv.view(T, hq + 2 * hkv, D)
         q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
-        w8.paged_kv_write(k, v, slots, cache.k, cache.v, k_scale=cache.ks, v_scale=cache.vs)
+        pages = dict(k_cache=cache.k, v_cache=cache.v, k_scale=cache.ks, v_scale=cache.vs)
+        if self.inv_freq is None:
+            w8.paged_kv_write(k, v, slots, **pages)
+        else:
+            q = w8.paged_kv_append(q, k, v, positions, slots, self.inv_freq, **pages, q_out=q)
         a = w8.attention_paged(q, cache.k, cache.v, cache.table, kv_lens, cu_new,
                                1 / math.sqrt(D), k_scale=cache.ks, v_scale=cache.vs)
-        x = x + w8.linear(a.view(T, hq * D), *self.out)
+        a = a.view(T, hq * D)
+        if self.fp8:
+            x = x + w8.linear_fp8(a, *self.out, act_scale_mode=w8.SCALE_POW2)
+        else:
+            x = x + w8.linear(a, *self.out)
         y = w8.rmsnorm(x, self.norm2, 1e-6)
-        ids, weights = w8.moe_gate(y.float() @ self.router.T, self.topk, scoring="sigmoid",
-                                   bias=self.balance, n_group=4, topk_group=2)
-        return x + w8.moe_ffn(y, ids, weights, *self.up, *self.down)
+        return x + w8.moe_layer(y, y.float() @ self.router.T, self.topk, *self.up, *self.down,
+                                scoring="sigmoid", bias=self.balance, n_group=4, topk_group=2)[0]
 
 
 class Cache:
@@ -130,8 +151,10 @@ def serve(layer, streams, arrive, chunk=128, pages=256, steps=None, say=None):
 def main(argv=None):
     ap = argparse.ArgumentParser()
     ap.add_argument("--steps", type=int, default=None)
+    ap.add_argument("--rotate", action="store_true")
+    ap.add_argument("--fp8", action="store_true")
     args = ap.parse_args(argv)
-    layer = Layer()
+    layer = Layer(rotate=args.rotate, fp8=args.fp8)
     g = torch.Generator(device="cuda").manual_seed(1)
     prompts, answers = [300, 17, 128, 1, 75], [9, 30, 4, 12, 20]
     streams = [torch.randn(p + a, layer.hidden, generator=g, device="cuda").to(torch.bfloat16)
