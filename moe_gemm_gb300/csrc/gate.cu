@@ -97,8 +97,6 @@ struct GateArgs {
     float scale;
     int32_t *ids;
     float *w;
-    int blocks;             // CTAs of the gate; those behind them take a token of `few` each
-    MoeFewTokens few;
 };
 
 __device__ __forceinline__ float ex2_approx(float v) {
@@ -556,13 +554,14 @@ __device__ __noinline__ void take_token(const MoeFewTokens &f, int t) {
     }
 }
 
-template <int V, typename Tin>
+// kFew: the launch has a CTA for each token of `few`, behind the gate's.
+template <int V, typename Tin, bool kFew>
 __global__ void __launch_bounds__(kGateWarps * 32)
-moe_gate_kernel(const Tin *logits, const GateArgs a) {
+moe_gate_kernel(const Tin *logits, const GateArgs a, const MoeFewTokens few) {
     griddep_launch_dependents();
     griddep_wait();
-    if (blockIdx.x >= a.blocks) {
-        take_token(a.few, blockIdx.x - a.blocks);
+    if (kFew && blockIdx.x >= gridDim.x - few.T) {
+        take_token(few, blockIdx.x - (gridDim.x - few.T));
         return;
     }
     __shared__ int s_list[kGateWarps][32];
@@ -705,9 +704,11 @@ moe_gate_kernel(const Tin *logits, const GateArgs a) {
 }
 
 template <int V, typename Tin>
-cudaError_t launch_v(const Tin *x, const GateArgs &a, cudaStream_t stream) {
+cudaError_t launch_v(const Tin *x, const GateArgs &a, const MoeFewTokens *few,
+                     cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.blocks + a.few.T));
+    cfg.gridDim = dim3(static_cast<unsigned>((a.T + kGateWarps - 1) / kGateWarps +
+                                             (few != nullptr ? few->T : 0)));
     cfg.blockDim = dim3(kGateWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -715,20 +716,23 @@ cudaError_t launch_v(const Tin *x, const GateArgs &a, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, moe_gate_kernel<V, Tin>, x, a);
+    const cudaError_t e =
+        few != nullptr ? cudaLaunchKernelEx(&cfg, moe_gate_kernel<V, Tin, true>, x, a, *few)
+                       : cudaLaunchKernelEx(&cfg, moe_gate_kernel<V, Tin, false>, x, a, MoeFewTokens{});
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
 
 template <typename Tin>
-cudaError_t launch_any(const void *logits, const GateArgs &a, cudaStream_t stream) {
+cudaError_t launch_any(const void *logits, const GateArgs &a, const MoeFewTokens *few,
+                       cudaStream_t stream) {
     const Tin *x = static_cast<const Tin *>(logits);
-    if (a.E <= 32) return launch_v<1>(x, a, stream);
-    if (a.E <= 64) return launch_v<2>(x, a, stream);
-    if (a.E <= 128) return launch_v<4>(x, a, stream);
-    if (a.E <= 256) return launch_v<8>(x, a, stream);
-    if (a.E <= 512) return launch_v<16>(x, a, stream);
-    return launch_v<32>(x, a, stream);
+    if (a.E <= 32) return launch_v<1>(x, a, few, stream);
+    if (a.E <= 64) return launch_v<2>(x, a, few, stream);
+    if (a.E <= 128) return launch_v<4>(x, a, few, stream);
+    if (a.E <= 256) return launch_v<8>(x, a, few, stream);
+    if (a.E <= 512) return launch_v<16>(x, a, few, stream);
+    return launch_v<32>(x, a, few, stream);
 }
 
 }  // namespace
@@ -755,10 +759,8 @@ cudaError_t launch_moe_gate(const GateProblem &p, cudaStream_t stream) {
     a.scale = p.scale;
     a.ids = p.ids;
     a.w = p.w;
-    a.blocks = (a.T + kGateWarps - 1) / kGateWarps;
-    a.few = p.tokens != nullptr ? *p.tokens : MoeFewTokens{};
-    return p.fp32 ? launch_any<float>(p.logits, a, stream)
-                  : launch_any<uint16_t>(p.logits, a, stream);
+    return p.fp32 ? launch_any<float>(p.logits, a, p.tokens, stream)
+                  : launch_any<uint16_t>(p.logits, a, p.tokens, stream);
 }
 
 }  // namespace w8a8

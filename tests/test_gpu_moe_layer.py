@@ -45,7 +45,7 @@ def same(x, logits, k, w, **how):
     (5, 256, 8, 512, 128), (8, 16, 4, 2048, 512), (16, 64, 8, 1024, 640), (17, 33, 5, 640, 256),
     (31, 12, 3, 1280, 896), (32, 64, 16, 512, 256), (32, 4, 4, 256, 384), (32, 9, 1, 128, 1152),
     (1, 1000, 64, 256, 128), (9, 40, 6, 7168, 256), (33, 64, 8, 512, 256), (32, 64, 17, 256, 128),
-    (100, 16, 4, 512, 256)])
+    (100, 16, 4, 512, 256), (32, 16, 16, 4992, 128), (32, 16, 16, 4864, 128), (4, 6, 5, 128, 8192)])
 def test_same_as_gate_and_ffn(T, E, k, H, I):
     x, logits, w = make(T, E, H, I, seed=T + E)
     same(x, logits, k, w)
