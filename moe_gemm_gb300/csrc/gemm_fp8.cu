@@ -17,6 +17,16 @@
 //
 // Warps: 0 loads (TMA), 1 issues the products, 4-7 and 8-11 add up a half of the slice
 // each (128 lanes), 2 and 3 only give up their registers.
+//
+// What bounds it. Few tokens: HBM where slices are wide (8 tokens x 28672 x 8192, 235 MB: 38.9 us,
+// 6.0 TB/s); where they are narrow, the steps: a step takes some 400 cycles to hand a stage
+// and a buffer on, whatever it holds, so those of narrow slices hold 2 or 4 groups (1 x
+// 10240 x 8192: 24 us for 84 MB, 16 x 1024 x 1024: 4.5). Many tokens (gemm_fp8_pair_kernel):
+// tensor memory, which the products' sums and the reads of a group's sums share: 4096
+// x 8192 x 8192 take 209 us, 2.63 PFLOP/s; a form that reads an eighth of the sums takes 170,
+// one that reads half of them 183, and adding costs nothing beside reading. Tried
+// and slower: 16 warps that add up (254 us), reads of 32 columns with two in flight (spills,
+// 449), scales through cp.async (221).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -493,7 +503,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmap_a,
 // rows together (cta_group::2): each holds its 128 tokens and half of the weights, so a
 // group reads and writes 32 KB per SM, and each adds up its own tokens. One thread of the
 // first CTA issues for both; its barriers collect the copies of both and the releases
-// of both CTAs' tensor memory.
+// of both CTAs' tensor memory (4096 x 8192 x 8192: 277 us with single CTAs, 209 with pairs).
 constexpr int kPairTokens = 256, kPairRows = 256;
 constexpr int kPairStageBytes = 2 * 128 * 128;
 constexpr int kPairStages = (kSmemBytes - 1024 - kOffStages - kStagedBytes) / kPairStageBytes;
@@ -813,7 +823,8 @@ cudaError_t launch_gemm_fp8(const Fp8Problem &p, int num_sms, cudaStream_t strea
     a.G = static_cast<int>(p.K >> 7);
     a.m_tiles = (a.M + kTokens - 1) / kTokens;
     // The slice's width: the least waves x width (a wave takes as long as its tiles are
-    // wide), the wider where two are level (fewer reads of the tokens).
+    // wide, and the 16 stand for its ends), the wider where two are level (fewer reads of
+    // the tokens).
     int64_t best = INT64_MAX;
     a.w = 8;
     for (int w = 8; w <= kMaxSlice; w += w < 32 ? 8 : 16) {
@@ -830,11 +841,13 @@ cudaError_t launch_gemm_fp8(const Fp8Problem &p, int num_sms, cudaStream_t strea
     if (e != cudaSuccess) return e;
     a.words = p.out_fp32 || (a.N % 2 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 3) == 0);
     CUtensorMap ta, tb;
-    // Pairs of CTAs, where their waves of tiles take less: a group of a pair's tile takes some
-    // 600 cycles, one of a tile of w rows some 4.4 w.
+    // Pairs of CTAs, where their waves of tiles take less: a tile of theirs takes as long as one of
+    // w = 164 (single CTAs / pairs: 512 x 4096 x 4096, w = 112, 15.4 / 18.4 us; 8192 x 256 x
+    // 2048, w = 128, 9.6 / 11.6; 777 x 4200 x 2048, w = 208, 18.4 / 15.3; 8192 x 512 x 2048, w =
+    // 256, 15.1 / 12.3; 4096 x 8192 x 8192 277 / 209).
     const int64_t m2 = (a.M + kPairTokens - 1) / kPairTokens, n2 = (a.N + kPairRows - 1) / kPairRows;
     const int64_t pairs = num_sms / 2;
-    if ((m2 * n2 + pairs - 1) / pairs * 600 < best * 44 / 10 && m2 * n2 <= INT32_MAX - 4096) {
+    if ((m2 * n2 + pairs - 1) / pairs * (164 + 16) < best && m2 * n2 <= INT32_MAX - 4096) {
         a.m_tiles = static_cast<int>(m2);
         a.tiles = static_cast<int>(m2 * n2);
         a.wide_store = (reinterpret_cast<uintptr_t>(p.y) & 31) == 0 && a.N % per32 == 0;

@@ -21,12 +21,20 @@
 // 8 of up that belong to them), one K group of 128 per step, through a ring of its own in
 // shared memory (cp.async, no barrier with other warps). The ring runs on through the waits.
 //
-// A step of an expert with three and more tokens is eight mma.sync m16n8k16 on fp16 (weights'
-// rows x tokens x 128 K): codes are exact in fp16 and a group's sum in FP32, as in the other
-// products here. K is permuted alike on both sides, so that a lane has 32 consecutive
-// codes of its rows, and of its token's codes. With one or two tokens it is dp4a on the
-// codes as they are: widening 16 x 128 of them takes 80 instructions, 16 warps of
-// which cost more than HBM takes for a tile that is not full.
+// A step of an expert with three and more tokens is four mma.sync m16n8k32 on the int8 codes
+// (weights' rows x tokens x 128 K), of one with one or two tokens dp4a: a group's sum is an exact integer either way. K is permuted alike on both sides, so that a
+// lane has 32 consecutive codes of its rows, and of its token's codes.
+//
+// What bounds it. 16 tokens, 8 of 64 experts (H 4096, I 1536, 1.1 GB): 219 us with the gate, 5.0
+// TB/s; 24 tokens of 256 experts (H 2048, I 640, 554 MB): 100 us, 5.6 TB/s; there the SMs that
+// end their stretch last, 10 % after the mean, and L1's throughput (67 % of its peak: copies,
+// tiles and tokens pass it). One token (156 MB): 45 us, 3.4 TB/s: the streams take 28, the
+// rest are the gate and two launches (4), the routes and the first loads (3), two waits of the
+// grid with h's codes between them (6) and the ends of the streams. Measured on the way (16 tokens):
+// operands widened to fp16, as moe_ffn has them, 246 us; dp4a for up to 8 tokens 435; even
+// stretches instead of equal costs 232; a fifth to a half of the line taken in pieces by warps
+// that are done 240 to 223, but 57 instead of 46 for one token; L2 prefetches during the
+// waits, h's codes made by every CTA, 3 or 6 stages: no gain.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -49,8 +57,8 @@ constexpr int kMaxOutputBytes = 64 << 10;   // d of a CTA's rows, in shared memo
 constexpr int kSyncs = 2;                    // grid-wide waits
 constexpr int kQueue = 8;                    // tiles that a ring is ahead at most
 constexpr unsigned kFull = 0xFFFFFFFFu;
-// What a row of an expert costs, by its tokens: warps that stream alike take so much longer for
-// two tokens, and for the tensor cores' form.
+// What a row of an expert costs, by its tokens: stretches of one length took 190, 222 and 255
+// thousand cycles where all their experts had one, two and more tokens.
 constexpr int kCostOne = 6, kCostTwo = 7, kCostMore = 8;
 
 struct LayerArgs {
@@ -361,7 +369,7 @@ __device__ __forceinline__ uint32_t next_stage(const LayerArgs &a, Routes &r, Fe
     return at;
 }
 
-// A tile of an expert with two and more tokens: 16 rows of weights by up to 8 NT tokens, over
+// A tile of an expert with three and more tokens: 16 rows of weights by up to 8 NT tokens, over
 // all of K. acc: [token tile][the lane's outputs: rows g and g + 8, tokens 2 c and 2 c + 1],
 // g = lane / 4, c = lane % 4.
 template <int NT, bool kUp>

@@ -5,6 +5,10 @@
 //   s = amax / 448, or the smallest power of two that is no smaller;
 //   q = e4m3(x / s), the quotient rounded to FP32 and then to e4m3, ties to even.
 //
+// What bounds the activations': instructions, of the division above all: 4096 x 8192 take 23 us
+// (4.4 TB/s), with powers of two, which are multiplied by their reciprocal, 18.5 (5.4 TB/s); with one
+// unit per thread 29 and 25.
+//
 // 448 is the largest e4m3 number. Of a block of zeros the scale is 0 (power of two:
 // 2^-127) and the codes are 0.
 #include <cuda_bf16.h>

@@ -171,6 +171,10 @@ def test_product_large(M, N, K):
     lim = (2.0 ** -16 + (K // 128 + 1 + K) * 2.0 ** -24) * (x.abs() @ w.abs().T)
     assert torch.all((z - x @ w.T).abs() <= lim)
     assert torch.equal(z.to(torch.bfloat16), y)
+    # and each row is what it is by itself, in whatever tile
+    for r in (0, 200, M - 1):
+        one = w8.gemm_fp8(q[0][r:r + 1], q[1][r:r + 1], q[2], q[3], out_dtype=torch.float32)
+        assert torch.equal(one[0], z[r])
 
 
 @pytest.mark.parametrize("M", [3, 40, 300])
