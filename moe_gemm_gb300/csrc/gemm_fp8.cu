@@ -18,10 +18,10 @@
 // Warps: 0 loads (TMA), 1 issues the products, 4-7 and 8-11 add up a half of the slice
 // each (128 lanes), 2 and 3 only give up their registers.
 //
-// What bounds it. Few tokens: HBM where slices are wide (8 tokens x 28672 x 8192, 235 MB: 38.9 us,
-// 6.0 TB/s); where they are narrow, the steps: a step takes some 400 cycles to hand a stage
-// and a buffer on, whatever it holds, so those of narrow slices hold 2 or 4 groups (1 x
-// 10240 x 8192: 24 us for 84 MB, 16 x 1024 x 1024: 4.5). Many tokens (gemm_fp8_pair_kernel):
+// What bounds it. Up to 32 tokens (gemm_fp8_rows_kernel): HBM (8 tokens x 28672 x 8192, 235 MB:
+// 38.7 us, 6.1 TB/s). Some tens to hundreds: the steps, which take some 400 cycles to hand a
+// stage and a buffer on, whatever they hold, so those of narrow slices hold 2 or 4 groups (64 x
+// 8192 x 4096: 11 us). Many tokens (gemm_fp8_pair_kernel):
 // tensor memory, which the products' sums and the reads of a group's sums share: 4096
 // x 8192 x 8192 take 209 us, 2.63 PFLOP/s; a form that reads an eighth of the sums takes 170,
 // one that reads half of them 183, and adding costs nothing beside reading. Tried
@@ -766,6 +766,239 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
     }
 }
 
+// ------------------------------------------------------------------ few tokens
+// The same product for up to 32 tokens, with the operands the other way round: 128 weight rows, a
+// block of scales, are the lanes, kTok tokens the columns. An instruction reads what it needs
+// and no more, a group's sums are kTok columns, and a store of y is 32 neighbours of a row.
+// It does not matter that the tiles leave SMs idle: half of them take what HBM gives. Against
+// slices: 1 x 10240 x 8192 24.1 -> 15.9 us (5.3 TB/s), 16 x 1024 x 1024 4.9 -> 3.5, 1 x 4096 x
+// 4096 9.6 -> 6.5, 32 x 16384 x 4096 15.4 -> 13.7, 8 x 28672 x 8192 39.1 -> 38.7; level at 32 x
+// 8192 x 4096. What bounds it: HBM, or with few tiles the steps of one (300 ns each).
+constexpr int kRowsMaxTokens = 32;
+constexpr int kRowsThreads = 256;
+constexpr int kRowsTmemCols = 256;
+
+// Groups of a step: 4 with 16 tokens (1 x 4096 x 4096: 6.5 us, with 2 8.2, with 1 10.3), 2 with 32,
+// whose stages are larger (32 x 16384 x 4096: 13.7, with 4 15.0).
+template <int kTok>
+struct RowsShape {
+    static constexpr int kPerStep = kTok == 16 ? 4 : 2;
+    static constexpr int kBufs = kRowsTmemCols / (kPerStep * kTok);
+    static constexpr int kW = 128 * 128, kT = kTok * 128;
+    static constexpr int kStage = kPerStep * (kW + kT);
+    static constexpr int kStages = (kSmemBytes - 1024 - kOffStages) / kStage;
+    static_assert(kStages >= 2 && kStages <= kMaxStages && kBufs >= 2 && kBufs <= kMaxBufs);
+};
+
+template <int kTok>
+__global__ void __launch_bounds__(kRowsThreads, 1)
+gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tmap_a,
+                     const __grid_constant__ CUtensorMap tmap_b, const Fp8Args a) {
+    using Shape = RowsShape<kTok>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    Bars &s = *reinterpret_cast<Bars *>(smem_raw + (base - raw));
+    const uint32_t sW = base + kOffStages;
+    const uint32_t sT = sW + Shape::kStages * Shape::kPerStep * Shape::kW;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < Shape::kStages; ++i) {
+            mbar_init(smem_u32(&s.full[i]), 1);
+            mbar_init(smem_u32(&s.empty[i]), 1);
+        }
+        for (int i = 0; i < Shape::kBufs; ++i) {
+            mbar_init(smem_u32(&s.d_full[i]), 1);
+            mbar_init(smem_u32(&s.d_empty[i]), 4);
+        }
+        mbar_init(smem_u32(&s.drain), 1);
+        s.abort_flag = 0;
+        fence_mbarrier_init();
+        tma_prefetch_desc(&tmap_a);
+        tma_prefetch_desc(&tmap_b);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&s.tmem), kRowsTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s.tmem;
+    volatile int *abort_flag = &s.abort_flag;
+    const int steps = (a.G + Shape::kPerStep - 1) / Shape::kPerStep;
+    griddep_launch_dependents();
+
+    if (warp == 0 && lane == 0) {
+        // ----------------------------------------------------------- TMA producer
+        Ring r;
+        uint32_t issued = 0;
+        bool ok = true;
+        auto groups_of = [&](int step) { return min(Shape::kPerStep, a.G - step * Shape::kPerStep); };
+        auto load_weights = [&](int stage, int step, int n0) {
+            const uint32_t bar = smem_u32(&s.full[stage]);
+            mbar_arrive_expect_tx(bar, groups_of(step) * (Shape::kW + Shape::kT));
+            for (int i = 0; i < groups_of(step); ++i)
+                tma_load_2d(sW + (stage * Shape::kPerStep + i) * Shape::kW, &tmap_b,
+                            (step * Shape::kPerStep + i) * 128, n0, bar);
+        };
+        auto load_tokens = [&](int stage, int step) {
+            for (int i = 0; i < groups_of(step); ++i)
+                tma_load_2d(sT + (stage * Shape::kPerStep + i) * Shape::kT, &tmap_a,
+                            (step * Shape::kPerStep + i) * 128, 0, smem_u32(&s.full[stage]));
+        };
+        // (the first weights before the kernel before has written the tokens' codes)
+        const int ahead = min(Shape::kStages, steps);
+        for (int i = 0; i < ahead; ++i) load_weights(i, i, blockIdx.x * 128);
+        griddep_wait();
+        for (int i = 0; i < ahead; ++i) load_tokens(i, i);
+        issued = ahead;
+        r.idx = ahead == Shape::kStages ? 0 : ahead;
+        r.phase = ahead == Shape::kStages ? 1 : 0;
+        for (int t = blockIdx.x; t < a.tiles && ok; t += gridDim.x) {
+            for (int i = t == blockIdx.x ? ahead : 0; i < steps; ++i) {
+                if (!mbar_wait(smem_u32(&s.empty[r.idx]), r.phase ^ 1u, abort_flag, a.err,
+                               ROLE_PRODUCER, 20, kWaitLimitNs, KID_FP8)) {
+                    ok = false;
+                    break;
+                }
+                load_weights(r.idx, i, t * 128);
+                load_tokens(r.idx, i);
+                r.advance(Shape::kStages);
+                ++issued;
+            }
+        }
+        if (!ok) {           // the copies in flight land before the CTA goes
+            const uint32_t n = Shape::kStages;
+            for (uint32_t i = issued > n ? issued - n : 0; i < issued; ++i) {
+                const unsigned long long t0 = globaltimer_ns();
+                while (!mbar_try_wait(smem_u32(&s.full[i % n]), (i / n) & 1u) &&
+                       globaltimer_ns() - t0 < kWaitLimitNs) {
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // --------------------------------------------------------------- products
+        Ring r, d;
+        bool ok = true;
+        const uint32_t idesc = idesc_e4m3(128, kTok);
+        for (int t = blockIdx.x; t < a.tiles && ok; t += gridDim.x) {
+            for (int i = 0; i < steps; ++i) {
+                ok = mbar_wait(smem_u32(&s.d_empty[d.idx]), d.phase ^ 1u, abort_flag, a.err,
+                               ROLE_MMA, 20, kWaitLimitNs, KID_FP8) &&
+                     mbar_wait(smem_u32(&s.full[r.idx]), r.phase, abort_flag, a.err, ROLE_MMA, 21,
+                               kWaitLimitNs, KID_FP8);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t dw = desc_lo(sW + r.idx * Shape::kPerStep * Shape::kW);
+                const uint32_t dk = desc_lo(sT + r.idx * Shape::kPerStep * Shape::kT);
+                const uint32_t dt = tmem + d.idx * Shape::kPerStep * kTok;
+                const int groups = a.G - i * Shape::kPerStep;
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                        for (int j = 0; j < Shape::kPerStep; ++j) {
+                            if (j >= groups) break;
+                            const uint32_t w = dw + j * (Shape::kW >> 4) + 2 * k;
+                            const uint32_t x = dk + j * (Shape::kT >> 4) + 2 * k;
+                            if (k == 0) mma_e4m3<false>(dt + j * kTok, w, x, idesc);
+                            else mma_e4m3<true>(dt + j * kTok, w, x, idesc);
+                        }
+                    }
+                    mma_commit(smem_u32(&s.empty[r.idx]));
+                    mma_commit(smem_u32(&s.d_full[d.idx]));
+                }
+                __syncwarp();
+                r.advance(Shape::kStages);
+                d.advance(Shape::kBufs);
+            }
+        }
+        if (elect_one()) mma_commit(smem_u32(&s.drain));
+        __syncwarp();
+        const unsigned long long t0 = globaltimer_ns();
+        while (!mbar_try_wait(smem_u32(&s.drain), 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------- sums of groups
+        griddep_wait();
+        const int q = warp & 3;
+        const uint32_t my_tmem = tmem + (static_cast<uint32_t>(q * 32) << 16);
+        const bool mine = lane < a.M;        // a lane brings the scales of token `lane`
+        const float *sa = a.sa + static_cast<int64_t>(mine ? lane : 0) * a.G;
+        Ring d;
+        bool ok = true;
+        for (int t = blockIdx.x; t < a.tiles && ok; t += gridDim.x) {
+            const float *sw = a.sw + static_cast<int64_t>(t) * a.G;
+            float acc[kTok];
+#pragma unroll
+            for (int j = 0; j < kTok; ++j) acc[j] = 0.0f;
+            float fa[Shape::kPerStep], fw[Shape::kPerStep];
+            auto ask = [&](int g) {
+#pragma unroll
+                for (int i = 0; i < Shape::kPerStep; ++i) {
+                    const int at = min(g + i, a.G - 1);
+                    fa[i] = ld_now(sa + at);
+                    fw[i] = ld_now(sw + at);
+                }
+            };
+            ask(0);
+            for (int g = 0; g < a.G; g += Shape::kPerStep) {
+                float f[Shape::kPerStep];
+#pragma unroll
+                for (int i = 0; i < Shape::kPerStep; ++i) f[i] = fa[i] * fw[i];
+                ask(g + Shape::kPerStep);
+                ok = mbar_wait(smem_u32(&s.d_full[d.idx]), d.phase, abort_flag, a.err,
+                               ROLE_EPILOGUE, 20, kWaitLimitNs, KID_FP8);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t v[Shape::kPerStep][kTok / 16][16];
+#pragma unroll
+                for (int i = 0; i < Shape::kPerStep; ++i)
+#pragma unroll
+                    for (int c = 0; c < kTok / 16; ++c)
+                        tmem_ld_16cols(my_tmem + (d.idx * Shape::kPerStep + i) * kTok + 16 * c, v[i][c]);
+#pragma unroll
+                for (int i = 0; i < Shape::kPerStep; ++i)
+#pragma unroll
+                    for (int c = 0; c < kTok / 16; ++c) tmem_wait_ld_dep16(v[i][c]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_relaxed(smem_u32(&s.d_empty[d.idx]));
+                d.advance(Shape::kBufs);
+#pragma unroll
+                for (int i = 0; i < Shape::kPerStep; ++i) {
+                    if (g + i >= a.G) break;         // (an odd last step: what it read is of an older one)
+#pragma unroll
+                    for (int j = 0; j < kTok; ++j)
+                        acc[j] = fmaf(__uint_as_float(v[i][j / 16][j % 16]),
+                                      __shfl_sync(0xFFFFFFFFu, f[i], j), acc[j]);
+                }
+            }
+            const int n = t * 128 + q * 32 + lane;
+            if (!ok || n >= a.N) continue;
+#pragma unroll
+            for (int j = 0; j < kTok; ++j) {
+                if (j >= a.M) break;
+                const int64_t at = static_cast<int64_t>(j) * a.N + n;
+                if (a.out_fp32)
+                    static_cast<float *>(a.y)[at] = acc[j];
+                else
+                    static_cast<__nv_bfloat16 *>(a.y)[at] = __float2bfloat16_rn(acc[j]);
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kRowsTmemCols);
+    }
+}
+
 // A matrix of bytes [rows, K] in boxes of box_rows rows x 128 K.
 bool encode(CUtensorMap *map, const void *ptr, int64_t K, int64_t rows, int box_rows) {
     auto fn = tensor_map_encode_fn();
@@ -779,7 +1012,7 @@ bool encode(CUtensorMap *map, const void *ptr, int64_t K, int64_t rows, int box_
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <auto kernel>
+template <auto kernel, int kCtaThreads = kThreads>
 cudaError_t launch_as(const CUtensorMap &ta, const CUtensorMap &tb, const Fp8Args &a, int grid,
                       cudaStream_t stream) {
     static int attr_done[64] = {0};
@@ -790,7 +1023,8 @@ cudaError_t launch_as(const CUtensorMap &ta, const CUtensorMap &tb, const Fp8Arg
         // setmaxnreg.inc can only take registers that the CTA was launched with
         cudaFuncAttributes fa;
         if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
-        if (fa.numRegs * kThreads < static_cast<int>(256 * kSumRegs + 128 * kOtherRegs))
+        if (kCtaThreads == kThreads &&
+            fa.numRegs * kThreads < static_cast<int>(256 * kSumRegs + 128 * kOtherRegs))
             return cudaErrorInvalidConfiguration;
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
         if (e != cudaSuccess) return e;
@@ -798,7 +1032,7 @@ cudaError_t launch_as(const CUtensorMap &ta, const CUtensorMap &tb, const Fp8Arg
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kCtaThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -841,6 +1075,16 @@ cudaError_t launch_gemm_fp8(const Fp8Problem &p, int num_sms, cudaStream_t strea
     if (e != cudaSuccess) return e;
     a.words = p.out_fp32 || (a.N % 2 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 3) == 0);
     CUtensorMap ta, tb;
+    if (a.M <= kRowsMaxTokens) {
+        a.tiles = (a.N + 127) / 128;
+        const int tok = a.M <= 16 ? 16 : 32;
+        if (!encode(&ta, p.qa, p.K, p.M, tok) || !encode(&tb, p.qw, p.K, p.N, 128))
+            return cudaErrorInvalidValue;
+        const int grid = a.tiles < num_sms ? a.tiles : num_sms;
+        return tok == 16
+                   ? launch_as<gemm_fp8_rows_kernel<16>, kRowsThreads>(ta, tb, a, grid, stream)
+                   : launch_as<gemm_fp8_rows_kernel<32>, kRowsThreads>(ta, tb, a, grid, stream);
+    }
     // Pairs of CTAs, where their waves of tiles take less: a tile of theirs takes as long as one of
     // w = 164 (single CTAs / pairs: 512 x 4096 x 4096, w = 112, 15.4 / 18.4 us; 8192 x 256 x
     // 2048, w = 128, 9.6 / 11.6; 777 x 4200 x 2048, w = 208, 18.4 / 15.3; 8192 x 512 x 2048, w =
