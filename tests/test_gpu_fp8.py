@@ -195,6 +195,22 @@ def test_rows_stand_alone(M):
     assert torch.equal(one[0], want[0])
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("N,K", [(1, 128), (127, 640), (129, 1152), (392, 4736), (20000, 384),
+                                 (40001, 896)])
+def test_few_tokens_as_in_many(N, K, dtype):
+    # up to 32 tokens the weights' rows are the lanes, else the tokens: the sums are the same
+    qa, sa, qw, sw = operands(40, N, K, seed=N)
+    want = w8.gemm_fp8(qa, sa, qw, sw, out_dtype=dtype)
+    for m in (1, 2, 15, 16, 17, 31, 32):
+        y = torch.full((m + 2, N), 7.0, dtype=dtype, device=DEV)
+        for r in (0, 40 - m):
+            w8.gemm_fp8(qa[r:r + m], sa[r:r + m], qw, sw, out_dtype=dtype, out=y[1:m + 1])
+            assert torch.equal(y[1:m + 1], want[r:r + m])
+        assert torch.all(y[0] == 7) and torch.all(y[m + 1] == 7)
+    assert w8.device_error() == 0
+
+
 def test_outputs_anywhere():
     q = operands(50, 264, 256)
     want = w8.gemm_fp8(*q)
