@@ -364,6 +364,9 @@ w8a8_status w8a8_quant_weight_fp8(const float *w, int64_t N, int64_t K, w8a8_sca
  * sum |sa * sw * qa * qw| (tested).
  * Results do not depend on the other rows of the call. No workspace. qa, qw 16-byte aligned;
  * M * K, N * K and M * N below 2^31. M == 0 is a no-op.
+ * Weights are asked for while the kernel before may still run, if that lets its dependents
+ * start early (griddepcontrol.launch_dependents; w8a8_quant_weight_fp8 does not): such a
+ * kernel must not be the one that writes qw. The same holds for w8a8_linear_fp8.
  */
 w8a8_status w8a8_gemm_fp8(const void *qa, const float *sa, const void *qw, const float *sw,
                           void *y, w8a8_dtype y_dtype, int64_t M, int64_t N, int64_t K,
@@ -663,10 +666,10 @@ w8a8_status w8a8_moe_gate(const void *logits, w8a8_dtype logits_dtype, int64_t l
  * the same numbers as w8a8_moe_gate followed by w8a8_moe_ffn, bit for bit (finite x).
  *   x [T, ldx] BF16, logits [T, ld] and the gate's arguments as for w8a8_moe_gate;
  *   weights, scales and y as for w8a8_moe_ffn; ids, w [T, k] out: the gate's choice.
- * For T <= 32 tokens with T * k <= 512 it is two kernels, the gate and a cooperative
- * one that reads the picked experts' weights once (all its CTAs, one per SM, must
- * be resident: it starts when the device has room for them); more tokens run the kernels of
- * those two calls. H, I, k, E as for w8a8_moe_ffn. T == 0 is a no-op.
+ * For T <= 32 tokens with T * k <= 512 and T * k * ceil(H / SMs) <= 16384 it is two kernels, the
+ * gate and a cooperative one that reads the picked experts' weights once (all its CTAs, one
+ * per SM, must be resident: it starts when the device has room for them); everything else
+ * runs the kernels of those two calls. H, I, k, E as for w8a8_moe_ffn. T == 0 is a no-op.
  *   workspace: w8a8_moe_layer_workspace_size bytes, 256-byte aligned; scratch, but calls
  *   that may overlap on the GPU must not share one.
  */

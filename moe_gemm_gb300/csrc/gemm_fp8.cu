@@ -19,7 +19,7 @@
 // each (128 lanes), 2 and 3 only give up their registers.
 //
 // What bounds it. Up to 32 tokens (gemm_fp8_rows_kernel): HBM (8 tokens x 28672 x 8192, 235 MB:
-// 38.7 us, 6.1 TB/s). Some tens to hundreds: the steps, which take some 400 cycles to hand a
+// 38.2 us, 6.2 TB/s). Some tens to hundreds: the steps, which take some 400 cycles to hand a
 // stage and a buffer on, whatever they hold, so those of narrow slices hold 2 or 4 groups (64 x
 // 8192 x 4096: 11 us). Many tokens (gemm_fp8_pair_kernel):
 // tensor memory, which the products' sums and the reads of a group's sums share: 4096
@@ -771,8 +771,8 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
 // block of scales, are the lanes, kTok tokens the columns. An instruction reads what it needs
 // and no more, a group's sums are kTok columns, and a store of y is 32 neighbours of a row.
 // It does not matter that the tiles leave SMs idle: half of them take what HBM gives. Against
-// slices: 1 x 10240 x 8192 24.1 -> 15.9 us (5.3 TB/s), 16 x 1024 x 1024 4.9 -> 3.5, 1 x 4096 x
-// 4096 9.6 -> 6.5, 32 x 16384 x 4096 15.4 -> 13.7, 8 x 28672 x 8192 39.1 -> 38.7; level at 32 x
+// slices: 1 x 10240 x 8192 24.1 -> 15.6 us (5.4 TB/s), 16 x 1024 x 1024 4.9 -> 3.5, 1 x 4096 x
+// 4096 9.6 -> 6.5, 32 x 16384 x 4096 15.4 -> 13.7, 8 x 28672 x 8192 39.1 -> 38.2; level at 32 x
 // 8192 x 4096. What bounds it: HBM, or with few tiles the steps of one (300 ns each).
 constexpr int kRowsMaxTokens = 32;
 constexpr int kRowsThreads = 256;

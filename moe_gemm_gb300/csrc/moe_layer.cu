@@ -22,11 +22,12 @@
 // shared memory (cp.async, no barrier with other warps). The ring runs on through the waits.
 //
 // A step of an expert with three and more tokens is four mma.sync m16n8k32 on the int8 codes
-// (weights' rows x tokens x 128 K), of one with one or two tokens dp4a: a group's sum is an exact integer either way. K is permuted alike on both sides, so that a
-// lane has 32 consecutive codes of its rows, and of its token's codes.
+// (weights' rows x tokens x 128 K), of one with one or two tokens dp4a: a group's sum is an
+// exact integer either way. K is permuted alike on both sides, so that a lane has 32
+// consecutive codes of its rows, and of its token's codes.
 //
-// What bounds it. 16 tokens, 8 of 64 experts (H 4096, I 1536, 1.1 GB): 219 us with the gate, 5.0
-// TB/s; 24 tokens of 256 experts (H 2048, I 640, 554 MB): 100 us, 5.6 TB/s; there the SMs that
+// What bounds it. 16 tokens, 8 of 64 experts (H 4096, I 1536, 1.1 GB): 212 us with the gate, 5.2
+// TB/s; 24 tokens of 256 experts (H 2048, I 640, 554 MB): 98 us, 5.6 TB/s; there the SMs that
 // end their stretch last, 10 % after the mean, and L1's throughput (67 % of its peak: copies,
 // tiles and tokens pass it). One token (156 MB): 45 us, 3.4 TB/s: the streams take 28, the
 // rest are the gate and two launches (4), the routes and the first loads (3), two waits of the

@@ -25,9 +25,9 @@
 //
 // What bounds it: a prompt's tokens with INT8 pages (8192 x 64 + 8 + 8 heads, 319 MB) take 69 us,
 // 4.6 TB/s, with 68 % of the issue slots used; BF16 pages (4097 x 32 + 8 + 8, half a head turned,
-// 101 MB) 15.7 us, 6.4 TB/s of a measured 6.7. 256 threads per token: 77 and 17.3 us (a CTA's
+// 101 MB) 15.8 us, 6.4 TB/s of a measured 6.7. 256 threads per token: 77 and 17.3 us (a CTA's
 // chain of position, sine and barrier in front of half the work), three vectors in flight 75
-// and 17. 32 tokens take 3.5 us, launch and that chain; there a token's heads are
+// and 17. 32 tokens take 3.7 us, launch and that chain; there a token's heads are
 // divided among CTAs.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
