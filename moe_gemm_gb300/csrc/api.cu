@@ -834,6 +834,9 @@ w8a8_status w8a8_paged_kv_append(
     for (const int64_t s : {q_token_stride, q_head_stride, k_token_stride, k_head_stride,
                             v_token_stride, v_head_stride, out_token_stride, out_head_stride})
         if (s < 0 || s % 8 != 0 || s > kMaxElems) return W8A8_ERR_INVALID_ARG;
+    // (queries that share a row to be written to)
+    if ((T > 1 && Hq > 0 && out_token_stride < head_dim) || (Hq > 1 && out_head_stride < head_dim))
+        return W8A8_ERR_INVALID_ARG;
     if ((k_scale == nullptr) != (v_scale == nullptr)) return W8A8_ERR_INVALID_ARG;
     if (T == 0) return W8A8_OK;
     if (!k_bf16 || !v_bf16 || !positions || !slots || !inv_freq || !k_cache || !v_cache ||

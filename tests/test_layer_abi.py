@@ -48,6 +48,14 @@ def test_append(lib):
         assert call(f, APPEND, APPEND_OK, **bad) == INVALID, bad
 
 
+def test_append_outputs_apart(lib):
+    f = lib.w8a8_paged_kv_append
+    for bad in (dict(T=2, ot=0), dict(T=2, ot=120), dict(oh=0), dict(oh=64)):
+        assert call(f, APPEND, APPEND_OK, **bad) == INVALID, bad
+    for good in (dict(Hq=1, oh=0), dict(ot=0), dict(Hq=0, q=None, out=None, ot=0, oh=0)):
+        assert call(f, APPEND, APPEND_OK, **good) == OK, good
+
+
 LAYER = ("x ldx logits ldt ld T k H I E score bias n_group topk_group renorm scale qu su qd sd ids "
          "w y ydt ws wsb stream").split()
 LAYER_OK = dict(x=A, ldx=1024, logits=A, ldt=1, ld=64, T=0, k=8, H=1024, I=512, E=64, score=0,
