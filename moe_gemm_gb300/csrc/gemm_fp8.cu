@@ -19,7 +19,7 @@
 // each (128 lanes), 2 and 3 only give up their registers.
 //
 // What bounds it. Up to 32 tokens (gemm_fp8_rows_kernel): HBM (8 tokens x 28672 x 8192, 235 MB:
-// 38.2 us, 6.2 TB/s). Some tens to hundreds: the steps, which take some 400 cycles to hand a
+// 36.1 us, 6.5 TB/s). Some tens to hundreds: the steps, which take some 400 cycles to hand a
 // stage and a buffer on, whatever they hold, so those of narrow slices hold 2 or 4 groups (64 x
 // 8192 x 4096: 11 us). Many tokens (gemm_fp8_pair_kernel):
 // tensor memory, which the products' sums and the reads of a group's sums share: 4096
@@ -770,9 +770,9 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
 // The same product for up to 32 tokens, with the operands the other way round: 128 weight rows, a
 // block of scales, are the lanes, kTok tokens the columns. An instruction reads what it needs
 // and no more, a group's sums are kTok columns, and a store of y is 32 neighbours of a row.
-// It does not matter that the tiles leave SMs idle: half of them take what HBM gives. Against
+// It does not matter that the tiles leave SMs idle: 100 of them take what HBM gives. Against
 // slices: 1 x 10240 x 8192 24.1 -> 15.6 us (5.4 TB/s), 16 x 1024 x 1024 4.9 -> 3.5, 1 x 4096 x
-// 4096 9.6 -> 6.5, 32 x 16384 x 4096 15.4 -> 13.7, 8 x 28672 x 8192 39.1 -> 38.2; level at 32 x
+// 4096 9.6 -> 6.5, 32 x 16384 x 4096 15.4 -> 13.5, 8 x 28672 x 8192 39.1 -> 36.1; level at 32 x
 // 8192 x 4096. What bounds it: HBM, or with few tiles the steps of one (300 ns each).
 constexpr int kRowsMaxTokens = 32;
 constexpr int kRowsThreads = 256;
@@ -1080,7 +1080,12 @@ cudaError_t launch_gemm_fp8(const Fp8Problem &p, int num_sms, cudaStream_t strea
         const int tok = a.M <= 16 ? 16 : 32;
         if (!encode(&ta, p.qa, p.K, p.M, tok) || !encode(&tb, p.qw, p.K, p.N, 128))
             return cudaErrorInvalidValue;
-        const int grid = a.tiles < num_sms ? a.tiles : num_sms;
+        // As many CTAs as have the same number of tiles each: some SMs' second tiles alone do
+        // not take what HBM gives (against a CTA on every SM: 8 x 28672 x 8192, 112 CTAs, 36.1 / 38.2
+        // us; 1 x 20480 x 4096, 80, 15.5 / 18.2; 32 x 40000 x 4096, 105, 29.2 / 32.7; 8 x 65536 x 2048,
+        // 128, 22.2 / 22.0).
+        const int waves = (a.tiles + num_sms - 1) / num_sms;
+        const int grid = (a.tiles + waves - 1) / waves;
         return tok == 16
                    ? launch_as<gemm_fp8_rows_kernel<16>, kRowsThreads>(ta, tb, a, grid, stream)
                    : launch_as<gemm_fp8_rows_kernel<32>, kRowsThreads>(ta, tb, a, grid, stream);
