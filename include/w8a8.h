@@ -364,9 +364,6 @@ w8a8_status w8a8_quant_weight_fp8(const float *w, int64_t N, int64_t K, w8a8_sca
  * sum |sa * sw * qa * qw| (tested).
  * Results do not depend on the other rows of the call. No workspace. qa, qw 16-byte aligned;
  * M * K, N * K and M * N below 2^31. M == 0 is a no-op.
- * Weights are asked for while the kernel before may still run, if that lets its dependents
- * start early (griddepcontrol.launch_dependents; w8a8_quant_weight_fp8 does not): such a
- * kernel must not be the one that writes qw. The same holds for w8a8_linear_fp8.
  */
 w8a8_status w8a8_gemm_fp8(const void *qa, const float *sa, const void *qw, const float *sw,
                           void *y, w8a8_dtype y_dtype, int64_t M, int64_t N, int64_t K,

@@ -1250,8 +1250,8 @@ w8a8_status check_fp8(const void *a, int64_t a_align, const void *qw, const floa
 }
 
 w8a8_status run_gemm_fp8(const void *qa, const float *sa, const void *qw, const float *sw, void *y,
-                         w8a8_dtype y_dtype, int64_t M, int64_t N, int64_t K, int num_sms,
-                         w8a8_stream_t stream) {
+                         w8a8_dtype y_dtype, int64_t M, int64_t N, int64_t K, bool chained,
+                         int num_sms, w8a8_stream_t stream) {
     w8a8::Fp8Problem p;
     p.qa = qa;
     p.sa = sa;
@@ -1262,6 +1262,7 @@ w8a8_status run_gemm_fp8(const void *qa, const float *sa, const void *qw, const 
     p.M = M;
     p.N = N;
     p.K = K;
+    p.chained = chained;
     return from_cuda(w8a8::launch_gemm_fp8(p, num_sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -1308,7 +1309,7 @@ w8a8_status w8a8_gemm_fp8(const void *qa, const float *sa, const void *qw, const
     w8a8::DeviceInfo info;
     st = check_device(&info);
     if (st != W8A8_OK) return st;
-    return run_gemm_fp8(qa, sa, qw, sw, y, y_dtype, M, N, K, info.num_sms, stream);
+    return run_gemm_fp8(qa, sa, qw, sw, y, y_dtype, M, N, K, false, info.num_sms, stream);
 }
 
 size_t w8a8_linear_fp8_workspace_size(int64_t M, int64_t N, int64_t K) {
@@ -1338,7 +1339,7 @@ w8a8_status w8a8_linear_fp8(const void *a_bf16, int64_t lda, w8a8_scale_mode act
                                    act_mode == W8A8_SCALE_POW2, true,
                                    reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
         return W8A8_ERR_CUDA;
-    return run_gemm_fp8(workspace, sa, qw, sw, y, y_dtype, M, N, K, info.num_sms, stream);
+    return run_gemm_fp8(workspace, sa, qw, sw, y, y_dtype, M, N, K, true, info.num_sms, stream);
 }
 
 w8a8_status w8a8_selftest_wait_timeout(uint32_t limit_us, w8a8_stream_t stream) {

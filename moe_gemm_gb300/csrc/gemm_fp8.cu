@@ -67,6 +67,7 @@ struct Fp8Args {
     int n_mma;                 // the slice in an instruction's N
     int out_fp32, wide_store;  // rows of y allow 32-byte stores
     int words;                 // ... or 4-byte stores
+    int early;                 // the kernel before is the quantizer of the same call
     unsigned long long *err;
 };
 
@@ -285,6 +286,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmap_a,
     tc_fence_after();
     const uint32_t tmem = s.tmem;
     volatile int *abort_flag = &s.abort_flag;
+    if (!a.early) griddep_wait();    // (Fp8Problem::chained)
     griddep_launch_dependents();
 
     if (warp < 4) {
@@ -294,8 +296,8 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmap_a,
             Ring r;
             uint32_t issued = 0;
             bool ok = true;
-            // The first weights are asked for while the kernel before, which may write the
-            // tokens' codes and scales, still runs.
+            // The first weights are asked for while the call's quantizer, which writes the tokens'
+            // codes and scales, still runs.
             const int steps = (a.G + a.per_step - 1) / a.per_step;
             const int ahead = a.stages < steps ? a.stages : steps;
             auto load = [&](const void *map, uint32_t to, int bytes, int step, int row,
@@ -827,6 +829,7 @@ gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tmap_a,
     const uint32_t tmem = s.tmem;
     volatile int *abort_flag = &s.abort_flag;
     const int steps = (a.G + Shape::kPerStep - 1) / Shape::kPerStep;
+    if (!a.early) griddep_wait();    // (Fp8Problem::chained)
     griddep_launch_dependents();
 
     if (warp == 0 && lane == 0) {
@@ -847,7 +850,7 @@ gemm_fp8_rows_kernel(const __grid_constant__ CUtensorMap tmap_a,
                 tma_load_2d(sT + (stage * Shape::kPerStep + i) * Shape::kT, &tmap_a,
                             (step * Shape::kPerStep + i) * 128, 0, smem_u32(&s.full[stage]));
         };
-        // (the first weights before the kernel before has written the tokens' codes)
+        // (the first weights before the call's quantizer has written the tokens' codes)
         const int ahead = min(Shape::kStages, steps);
         for (int i = 0; i < ahead; ++i) load_weights(i, i, blockIdx.x * 128);
         griddep_wait();
@@ -1070,6 +1073,7 @@ cudaError_t launch_gemm_fp8(const Fp8Problem &p, int num_sms, cudaStream_t strea
         }
     }
     a.out_fp32 = p.out_fp32;
+    a.early = p.chained;
     const int per32 = p.out_fp32 ? 8 : 16;
     cudaError_t e = device_error_word(&a.err);
     if (e != cudaSuccess) return e;

@@ -268,8 +268,8 @@ cudaError_t launch_gemm(const GemmProblem &p, int num_sms, cudaStream_t stream);
 
 // FP8 (e4m3) with a scale per block of 128: quantizers (quant_fp8.cu) and the product
 // (gemm_fp8.cu).
-// chained: the next launch reads these codes as tokens, and may start early (the product asks
-// for its first weights before it waits for the kernel before).
+// chained: the next launch is the product of these codes, and may start once this kernel's own wait is
+// over: whatever ran before is done then.
 cudaError_t launch_quant_act_fp8(const uint16_t *a, int64_t M, int64_t K, int64_t lda, void *qa,
                                  float *sa, bool pow2, bool chained, cudaStream_t stream);
 cudaError_t launch_quant_weight_fp8(const float *w, int64_t N, int64_t K, bool pow2, void *qw,
@@ -280,6 +280,9 @@ struct Fp8Problem {
     void *y;                         // [M, N]
     bool out_fp32;
     int64_t M, N, K;
+    // The launch before is the call's chained quantizer: weights may be read before the wait for it. After
+    // any other kernel the product waits first, as what comes before that one may still write them.
+    bool chained;
 };
 cudaError_t launch_gemm_fp8(const Fp8Problem &p, int num_sms, cudaStream_t stream);
 

@@ -73,8 +73,9 @@ template <bool kPow2, bool kVec, int kUnits>
 __global__ void __launch_bounds__(kActThreads)
 quant_act_fp8_kernel(const uint16_t *a, int64_t lda, int units, int G, int chained, uint8_t *qa,
                      float *sa) {
-    if (chained) griddep_launch_dependents();
     griddep_wait();
+    // (behind the wait: when the product starts, all before this kernel is done, writers of weights too)
+    if (chained) griddep_launch_dependents();
     constexpr int kPerBlock = kActThreads / 16;
     const int first = blockIdx.x * kPerBlock * kUnits + (threadIdx.x >> 4);
     const int c = threadIdx.x & 15;
@@ -117,7 +118,6 @@ quant_act_fp8_kernel(const uint16_t *a, int64_t lda, int units, int G, int chain
 // One CTA per block: 8 warps, a row of 128 values per warp at a time.
 __global__ void __launch_bounds__(256)
 quant_weight_fp8_kernel(const float *w, int N, int K, int pow2, uint8_t *qw, float *sw) {
-    // (lets no kernel start early: the product asks for weights before it waits)
     griddep_wait();
     __shared__ float s_max[8];
     const int g = blockIdx.x, b = blockIdx.y;

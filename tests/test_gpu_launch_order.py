@@ -1,0 +1,93 @@
+"""GPU tests that a product reads its weights after the kernels that write them, however early
+the kernels of a stream may start.
+
+Most kernels of the library let the next one start before they are done, and wait for the one
+before them by themselves. So a writer of weights, started early and still waiting for a long
+kernel, may have another call's kernels behind it on the GPU already. The weights here are written
+by paged_kv_append at position 0, which copies its queries' bytes (cos 1, sin 0), behind a
+quantizer that one CTA works at for some hundred microseconds.
+"""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+import moe_gemm_gb300 as w8  # noqa: E402
+
+DEV = torch.device("cuda:0")
+E4M3 = torch.float8_e4m3fn
+N, K = 128, 1024
+
+
+class Late:
+    """Writes `value` into `into` (a multiple of 4096 bytes) behind a long kernel, without a wait."""
+
+    def __init__(self, value, into):
+        def rows(t):
+            return t.view(torch.uint8).view(-1).view(torch.bfloat16).view(-1, 16, 128)
+
+        self.q, self.out = rows(value), rows(into)
+        T = self.q.shape[0]
+        self.kv = torch.zeros(T, 1, 128, dtype=torch.bfloat16, device=DEV)
+        self.pages = [torch.zeros(1, 1, 16, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+        self.pos = torch.zeros(T, dtype=torch.int32, device=DEV)
+        self.slots = torch.full((T,), -1, dtype=torch.int32, device=DEV)
+        self.freq = torch.zeros(8, device=DEV)
+        self.long = torch.ones(1, 1 << 24, dtype=torch.bfloat16, device=DEV)
+        self.codes = torch.empty(1, 1 << 24, dtype=torch.int8, device=DEV)
+        self.scale = torch.empty(1, device=DEV)
+
+    def write(self):
+        w8.quant_act(self.long, qa=self.codes, sa=self.scale)
+        w8.paged_kv_append(self.q, self.kv, self.kv, self.pos, self.slots, self.freq, *self.pages,
+                           q_out=self.out)
+
+
+def check(value, call):
+    """call(weights, out) with weights still to be written gives what it gives with them there."""
+    want = call(value, None)
+    into = torch.zeros_like(value)
+    late = Late(value, into)
+    got = torch.zeros_like(want)
+    late.write()
+    torch.cuda.synchronize()
+    assert torch.equal(into.view(torch.uint8), value.view(torch.uint8))
+    for _ in range(3):
+        into.view(torch.uint8).zero_()
+        got.zero_()
+        torch.cuda.synchronize()
+        late.write()
+        call(into, got)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    assert w8.device_error() == 0
+
+
+def fp8_weights():
+    g = torch.Generator(device=DEV).manual_seed(1)
+    sign = torch.randint(0, 2, (N, K), generator=g, device=DEV) * 2 - 1
+    qw = (torch.randint(1, 9, (N, K), generator=g, device=DEV) * sign).float().to(E4M3)
+    return qw, torch.full((1, K // 128), 0.01, device=DEV)
+
+
+def tokens(M):
+    return torch.randn(M, K, generator=torch.Generator(device=DEV).manual_seed(M), device=DEV).to(
+        torch.bfloat16)
+
+
+@pytest.mark.parametrize("M", [1, 24, 40, 300])
+def test_fp8_product(M):
+    qw, sw = fp8_weights()
+    qa, sa = w8.quant_act_fp8(tokens(M))
+    check(qw, lambda w, out: w8.gemm_fp8(qa, sa, w, sw, out=out))
+
+
+@pytest.mark.parametrize("M", [1, 24, 40, 300])
+def test_fp8_linear(M):
+    qw, sw = fp8_weights()
+    a = tokens(M)
+    ws = torch.empty(w8.linear_fp8_workspace_size(M, N, K), dtype=torch.uint8, device=DEV)
+    check(qw, lambda w, out: w8.linear_fp8(a, w, sw, out=out, workspace=ws))
