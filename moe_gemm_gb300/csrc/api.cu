@@ -115,6 +115,7 @@ w8a8_status run_gemm(const int8_t *qa, const float *sa, const int32_t *offsets, 
         // the int8 codes directly.)
         e = w8a8::launch_widen_codes(qa, R, K, K, workspace, info.num_sms, s, p.sk_cnt,
                                      p.sk_cnt != nullptr ? 2 * w8a8::kSkMaxCtas : 0);
+        p.early = true;
     }
     if (e != cudaSuccess) return W8A8_ERR_CUDA;
     p.qa = qa;
@@ -222,6 +223,7 @@ w8a8_status run_linear(const void *a, int64_t lda, const int32_t *offsets, const
         p.qa = nullptr;   // the tensor-core GEMM reads only the fp16 codes
     }
     if (e != cudaSuccess) return W8A8_ERR_CUDA;
+    p.early = p.act == nullptr;   // behind this call's quantizer
     p.sa = sa;
     p.sw = sw;
     p.qw = qw;
@@ -1143,6 +1145,7 @@ w8a8_status w8a8_moe_ffn(const void *x_bf16, int64_t ldx, const int32_t *topk_id
         p.N = 2 * I;
         p.K = H;
         p.out_fp32 = true;
+        p.early = true;
         e = w8a8::launch_gemm(p, info.num_sms, s);
     }
     // 4. SwiGLU + per-token requantization (fp16 codes: the down GEMM's operand)
@@ -1164,6 +1167,7 @@ w8a8_status w8a8_moe_ffn(const void *x_bf16, int64_t ldx, const int32_t *topk_id
         p.N = H;
         p.K = I;
         p.out_fp32 = true;
+        p.early = true;
         e = w8a8::launch_gemm(p, info.num_sms, s);
     }
     // 6. weighted un-permute into y [T, H]

@@ -124,6 +124,7 @@ struct KParams {
     long long lda;
     int qbuf_off;
     unsigned long long *err;
+    int early;          // GemmProblem::early
     // Stream-K split of dense calls (null sk_cnt: whole tiles only).
     int *sk_cnt;        // [2 * grid] arrival counters of split tiles, zero at launch
     float *sk_part;     // [grid][2][sk_ld][128] FP32 piece partials
@@ -509,7 +510,10 @@ w8a8_gemm_narrow_kernel(const __grid_constant__ CUtensorMap tmap_w,
         tmem_alloc(smem_u32(smem + kOffMisc), kTmemCols);
         tmem_relinquish();
     }
-    if (warp == 2) build_tile_table(p, tt, lane, s_base, s_lo, s_cnt, s_total);
+    if (warp == 2) {
+        if (!p.early) griddep_wait();   // (for all: the barrier below)
+        build_tile_table(p, tt, lane, s_base, s_lo, s_cnt, s_total);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1254,7 +1258,10 @@ w8a8_gemm_wide_kernel(const __grid_constant__ CUtensorMap tmap_w,
         tmem_alloc(smem_u32(smem + kOffMisc), kTmemCols);
         tmem_relinquish();
     }
-    if (warp == 2) build_tile_table(p, kW2Tokens, lane, s_base, s_lo, s_cnt, s_total);
+    if (warp == 2) {
+        if (!p.early) griddep_wait();   // (for all: the barrier below)
+        build_tile_table(p, kW2Tokens, lane, s_base, s_lo, s_cnt, s_total);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1584,8 +1591,8 @@ __device__ __forceinline__ void gemv_produce(const KParams &p, int total, const 
                                              int tt) {
     const int G = p.G;
     // ---------------------------------------------- stage producer
-    // The kernel may start while the quantizer that writes the token
-    // codes still runs (programmatic dependent launch): the first
+    // The kernel may start while the quantizer of its call, which writes the
+    // token codes, still runs (KParams::early): the first
     // stage's weight loads go out at once, its token loads (and all
     // later stages) after griddepcontrol.wait. (Deferring more stages
     // delays the first token loads more than it gains: measured.)
@@ -1685,6 +1692,7 @@ w8a8_gemv_kernel(const __grid_constant__ CUtensorMap tmap_w,
             tma_prefetch_desc(&tmap_w64);
             tma_prefetch_desc(&tmap_q);
         }
+        if (!p.early) griddep_wait();   // (for all: the barrier below)
         build_tile_table(p, tt, lane, s_base, s_lo, s_cnt, s_total);
     }
     __syncthreads();
@@ -2088,6 +2096,7 @@ cudaError_t launch_kernel(const GemmProblem &pr, const PipeShape &ps, int num_sm
     kp.sk_cnt = split ? pr.sk_cnt : nullptr;
     kp.sk_part = split ? pr.sk_part : nullptr;
     kp.sk_ld = split ? pr.sk_ld : 0;
+    kp.early = pr.early ? 1 : 0;
 
     // Programmatic dependent launch: the kernel may start while the staging
     // kernel before it in the stream is still running; its token producer and
@@ -2147,6 +2156,7 @@ cudaError_t launch_wide(const GemmProblem &pr, int num_sms, cudaStream_t stream)
     kp.out_fp32 = pr.out_fp32 ? 1 : 0;
     kp.tile_tokens = kW2Tokens;
     kp.gw = kRasterBand;
+    kp.early = pr.early ? 1 : 0;
     cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void **>(&kp.err), g_device_error);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (pr.R + kW2Tokens - 1) / kW2Tokens * kp.n_tiles;
@@ -2225,6 +2235,7 @@ cudaError_t launch_gemv(const GemmProblem &pr, int num_sms, cudaStream_t stream)
     kp.qbuf_off = qbuf_off;
     kp.b_rows = MR;
     kp.tile_tokens = MR;
+    kp.early = pr.early ? 1 : 0;
     kp.tab_off = tab_off;
     unsigned long long *err = nullptr;
     cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void **>(&err), g_device_error);

@@ -85,6 +85,12 @@ struct GemmProblem {
     int *sk_cnt = nullptr;        // [2 * kSkMaxCtas] counters, zeroed before the GEMM
     float *sk_part = nullptr;     // [kSkMaxCtas][2][sk_ld][128] FP32 partials
     int sk_ld = 0;
+    // The launch before is a kernel of the same call that lets this one start
+    // behind its own wait (the quantizers, widen_codes, swiglu_quant): weights,
+    // their scales and offsets may be read before the wait for it. After any
+    // other kernel the GEMM waits first, as what comes before that one may
+    // still write them.
+    bool early = false;
 };
 
 // Dense calls with at most kGemvMaxTokens token rows run on the CUDA cores

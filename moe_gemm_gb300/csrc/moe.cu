@@ -160,8 +160,8 @@ template <int VPT, int kOut>   // kOut: 0 int8 codes, 1 fp16 codes, 2 h (FP32)
 __global__ void __launch_bounds__(kSwigluThreads)
 swiglu_quant_kernel(const float *__restrict__ U, int I, const int32_t *__restrict__ offsets,
                     int E, void *__restrict__ out, float *__restrict__ sh) {
-    griddep_launch_dependents();
     griddep_wait();   // U comes from the GEMM launched before
+    griddep_launch_dependents();   // (behind it: GemmProblem::early of the down GEMM)
     const int64_t row = blockIdx.x;
     if (offsets != nullptr && row >= offsets[E]) return;
     __shared__ float red[kSwigluThreads / 32];

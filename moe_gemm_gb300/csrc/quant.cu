@@ -82,14 +82,15 @@ __global__ void __launch_bounds__(NT) quant_act_vec_kernel(
     const uint16_t *__restrict__ a, int K, int64_t lda, const int32_t *__restrict__ src_rows,
     void *__restrict__ out, int64_t ldq, float *__restrict__ sa, int *__restrict__ cnt,
     int n_cnt, int pow2) {
-    // A GEMM launched after this kernel as a programmatic dependent may start
-    // its set-up and weight stream now; it waits for this grid (and so for qa
-    // and sa) before it reads the codes. This kernel is itself launched as a
-    // programmatic dependent of the kernel before it (which may have written
-    // the activations, or still read qa/sa): it waits for that grid before
-    // touching either.
-    griddep_launch_dependents();
+    // This kernel is launched as a programmatic dependent of the kernel
+    // before it (which may have written the activations, or still read
+    // qa/sa): it waits for that grid before touching either. A GEMM launched
+    // after this kernel as a programmatic dependent may then start its set-up
+    // and weight stream (GemmProblem::early: everything before this kernel is
+    // done, writers of its weights too); it waits for this grid (and so for
+    // qa and sa) before it reads the codes.
     griddep_wait();
+    griddep_launch_dependents();
     if (kF16 && blockIdx.x == 0)
         for (int i = threadIdx.x; i < n_cnt; i += blockDim.x) cnt[i] = 0;
     __shared__ uint32_t red[NT / 32];
@@ -163,8 +164,8 @@ __global__ void __launch_bounds__(NT) rmsnorm_quant_kernel(
     const uint16_t *__restrict__ x, int K, int64_t ldx, const uint16_t *__restrict__ gamma,
     float eps, void *__restrict__ out, int64_t ldo, float *__restrict__ sa, int *__restrict__ cnt,
     int n_cnt, int pow2) {
-    griddep_launch_dependents();   // as in quant_act_vec_kernel
-    griddep_wait();
+    griddep_wait();                // as in quant_act_vec_kernel
+    griddep_launch_dependents();
     if (kOut == 1 && blockIdx.x == 0)
         for (int i = threadIdx.x; i < n_cnt; i += blockDim.x) cnt[i] = 0;
     constexpr int VPT = 4;
@@ -254,8 +255,8 @@ __global__ void __launch_bounds__(NT) quant_act_stream_kernel(
     const uint16_t *__restrict__ x, int64_t M, int K, int64_t ldx, void *__restrict__ out,
     int64_t ldo, float *__restrict__ sa, int *__restrict__ cnt, int n_cnt, int pow2,
     unsigned long long *__restrict__ err) {
-    griddep_launch_dependents();   // as in quant_act_vec_kernel
-    griddep_wait();
+    griddep_wait();                // as in quant_act_vec_kernel
+    griddep_launch_dependents();
     if (kOut == 1 && blockIdx.x == 0)
         for (int i = threadIdx.x; i < n_cnt; i += blockDim.x) cnt[i] = 0;
     extern __shared__ __align__(16) uint8_t ring[];
@@ -340,8 +341,8 @@ __global__ void __launch_bounds__(kQuantThreads) quant_act_generic_kernel(
     const uint16_t *__restrict__ a, int K, int64_t lda, const int32_t *__restrict__ src_rows,
     void *__restrict__ out, int64_t ldq, float *__restrict__ sa, int *__restrict__ cnt,
     int n_cnt, int pow2) {
-    griddep_launch_dependents();   // as in quant_act_vec_kernel
-    griddep_wait();
+    griddep_wait();                // as in quant_act_vec_kernel
+    griddep_launch_dependents();
     if (kF16 && blockIdx.x == 0)
         for (int i = threadIdx.x; i < n_cnt; i += blockDim.x) cnt[i] = 0;
     __shared__ uint32_t red[kQuantThreads / 32];
@@ -430,14 +431,14 @@ __global__ void __launch_bounds__(256) widen_codes_kernel(const int8_t *__restri
                                                           int64_t rows, int K, int64_t ldq,
                                                           __half *__restrict__ out,
                                                           int *__restrict__ cnt, int n_cnt) {
-    // The GEMM that consumes this copy is launched as a programmatic
-    // dependent: let it start its set-up and weight stream right away. This
-    // kernel is itself a programmatic dependent of the quantizer: wait for
-    // its codes (and so, through the quantizer's own wait, for any GEMM
-    // before it, which may still use the split counters and the staging
-    // copy), before it resets or writes either.
-    griddep_launch_dependents();
+    // This kernel is a programmatic dependent of the quantizer: wait for its
+    // codes (and so, through the quantizer's own wait, for any GEMM before
+    // it, which may still use the split counters and the staging copy),
+    // before it resets or writes either. The GEMM that consumes this copy is
+    // launched as a programmatic dependent: let it start its set-up and
+    // weight stream then (GemmProblem::early).
     griddep_wait();
+    griddep_launch_dependents();
     if (blockIdx.x == 0)
         for (int i = threadIdx.x; i < n_cnt; i += blockDim.x) cnt[i] = 0;
     const int vec_per_row = K >> 4;  // 16 codes per vector

@@ -91,3 +91,56 @@ def test_fp8_linear(M):
     a = tokens(M)
     ws = torch.empty(w8.linear_fp8_workspace_size(M, N, K), dtype=torch.uint8, device=DEV)
     check(qw, lambda w, out: w8.linear_fp8(a, w, sw, out=out, workspace=ws))
+
+
+def int8_weights():
+    # (positive codes: no pair of bytes is a BF16 number that is not finite)
+    g = torch.Generator(device=DEV).manual_seed(2)
+    qw = torch.randint(1, 101, (N, K), generator=g, device=DEV).to(torch.int8)
+    return qw, torch.full((N, K // 128), 0.01, device=DEV)
+
+
+@pytest.mark.parametrize("M", [1, 4, 16, 100, 300])
+def test_int8_product(M):
+    qw, sw = int8_weights()
+    qa, sa = w8.quant_act(tokens(M))
+    ws = torch.empty(w8.gemm_workspace_size(M, N, K), dtype=torch.uint8, device=DEV)
+    check(qw, lambda w, out: w8.gemm(qa, sa, w, sw, torch.bfloat16, out=out, workspace=ws))
+
+
+@pytest.mark.parametrize("M", [1, 4, 16, 100, 300])
+def test_int8_linear(M):
+    qw, sw = int8_weights()
+    a = tokens(M)
+    ws = torch.empty(w8.linear_workspace_size(M, N, K), dtype=torch.uint8, device=DEV)
+    check(qw, lambda w, out: w8.linear(a, w, sw, out=out, workspace=ws))
+
+
+@pytest.mark.parametrize("M", [1, 16, 300])
+def test_int8_weights_alone(M):
+    qw, sw = int8_weights()
+    a = tokens(M)
+    check(qw, lambda w, out: w8.w8a16_gemm(a, w, sw, out=out))
+
+
+@pytest.mark.parametrize("M", [1, 16, 300])
+def test_int8_scales(M):
+    qw, _ = int8_weights()
+    g = torch.Generator(device=DEV).manual_seed(3)
+    sw = torch.exp2(torch.randint(-6, 3, (N, K // 128), generator=g, device=DEV).float())
+    qa, sa = w8.quant_act(tokens(M))
+    check(sw, lambda s, out: w8.gemm(qa, sa, qw, s, torch.bfloat16, out=out))
+
+
+def test_experts_weights():
+    # (one expert; the gate_up weights, then the down weights, written late)
+    g = torch.Generator(device=DEV).manual_seed(4)
+    x = torch.randn(12, 512, generator=g, device=DEV).to(torch.bfloat16)
+    up = torch.randint(1, 101, (1, 256, 512), generator=g, device=DEV).to(torch.int8)
+    down = torch.randint(1, 101, (1, 512, 128), generator=g, device=DEV).to(torch.int8)
+    s_up, s_down = (torch.full(s, 0.01, device=DEV) for s in ((1, 256, 4), (1, 512, 1)))
+    ids = torch.zeros(12, 1, dtype=torch.int32, device=DEV)
+    w = torch.ones(12, 1, device=DEV)
+    ws = torch.empty(w8.moe_ffn_workspace_size(12, 1, 512, 128, 1), dtype=torch.uint8, device=DEV)
+    check(up, lambda q, out: w8.moe_ffn(x, ids, w, q, s_up, down, s_down, out=out, workspace=ws))
+    check(down, lambda q, out: w8.moe_ffn(x, ids, w, up, s_up, q, s_down, out=out, workspace=ws))
