@@ -97,7 +97,8 @@ struct Routes {
     int pair[kMoeFewMaxPairs];
     int part[kWarps];
     Stretch stretch[2][kWarps];              // of both products
-    float w[kMoeFewMaxPairs];                // of the pairs; 0 where there is no expert
+    float w[kMoeFewMaxPairs];                // of the pairs
+    bool routed[kMoeFewMaxPairs];            // whether they have an expert
     int n;
     int abort;
 };
@@ -189,7 +190,8 @@ __device__ __forceinline__ void make_routes(const LayerArgs &a, Routes &r) {
     if (threadIdx.x < n) {
         id = a.ids[threadIdx.x];
         if (id < 0 || id >= a.E) id = -1;
-        r.w[threadIdx.x] = id >= 0 ? a.w[threadIdx.x] : 0.0f;
+        r.w[threadIdx.x] = a.w[threadIdx.x];
+        r.routed[threadIdx.x] = id >= 0;
         // (an expert's pairs come in any order: each is a column of its own)
         if (id >= 0) place = atomicAdd(&r.count[id], 1);
     }
@@ -631,9 +633,9 @@ moe_layer_kernel(const LayerArgs a) {
     for (int i = threadIdx.x; i < a.T * L; i += kThreads) {
         const int t = i / L, n = i - t * L;
         float acc = 0.0f;
-        // (the gate gives a place without an expert the weight 0: s_d is not written there)
+        // (s_d is not written where there is no expert; a weight of 0 counts, as its d may not be finite)
         for (int j = t * a.k; j < (t + 1) * a.k; ++j)
-            if (r.w[j] != 0.0f) acc = fmaf(r.w[j], s_d[j * L + n], acc);
+            if (r.routed[j]) acc = fmaf(r.w[j], s_d[j * L + n], acc);
         const int64_t at = static_cast<int64_t>(t) * a.H + r0 + n;
         if (a.out_fp32)
             static_cast<float *>(a.y)[at] = acc;

@@ -85,6 +85,21 @@ def test_tokens_without_experts():
     assert torch.all(y == 0) and torch.all(ids == -1)
 
 
+@pytest.mark.parametrize("T", [1, 9])
+def test_weights_of_zero(T):
+    # an expert that counts 0 times still gives NaN where its output is not finite
+    x, logits, (qu, su, qd, sd) = make(T, 6, 256, 128)
+    sd[2, ::3] = 3e38
+    sd[4, 1::3] = 3e38
+    for how in (dict(scale=0.0), dict(scoring="softmax", renormalize=False)):
+        logits[:, 2] = logits[:, 4] = -200.0       # (the softmax of -200 is 0 in FP32)
+        y, ids, ww = w8.moe_layer(x, logits, 6, qu, su, qd, sd, **how)
+        want = w8.moe_ffn(x, *w8.moe_gate(logits, 6, **how), qu, su, qd, sd)
+        assert torch.all((ww == 0) == (((ids == 2) | (ids == 4)) | ("scale" in how)))
+        assert torch.any(torch.isnan(want)) and not torch.all(torch.isnan(want))
+        assert torch.equal(y.view(torch.int16), want.view(torch.int16))
+
+
 def test_zero_and_unaligned_rows():
     x, logits, w = make(7, 16, 512, 256)
     x[3] = 0
