@@ -747,8 +747,10 @@ w8a8_status w8a8_paged_kv_write(const void *k_bf16, int64_t k_token_stride, int6
  *        sin times amplitude. (a, b) are elements i and rot / 2 + i of a head
  *        or, interleaved, 2 i and 2 i + 1; elements rot .. 127 stay as they are;
  *   q_out [T, Hq, 128] BF16 with the given strides: the queries, rounded once; it may be
- *        q itself (same strides). Rows must not overlap: strides below 128 are refused
- *        where there are several. Hq 0 (q and q_out NULL): keys and values only.
+ *        q itself (same strides). Otherwise its rows share no memory with one another's, nor
+ *        with q's, k's or v's (which may lie beside them, a token's in one row of a matrix):
+ *        refused where they do, and where they interleave with other token strides.
+ *        Hq 0 (q and q_out NULL): keys and values only.
  * k is turned in FP32, and rounded once: to BF16 pages, or to INT8 codes with the scale
  * amax / 127 of the turned vector. v is written as w8a8_paged_kv_write does.
  * Angles are exact to 2^-23 of a turn at any position for inv_freq up to 1 in magnitude

@@ -316,6 +316,61 @@ w8a8_status check_ffn_shape(int64_t T, int64_t k, int64_t H, int64_t I, int64_t 
     return W8A8_OK;
 }
 
+// Rows of 128 BF16 values at p + t * ts + h * hs, h < heads.
+struct HeadRows {
+    const void *p;
+    int64_t ts, hs, heads;
+};
+
+// Whether x + n * step, |n| < T, comes within 128 of 0.
+bool near_zero(int64_t x, int64_t step, int64_t T) {
+    int64_t n = step > 0 ? -x / step : 0;
+    n = n > T - 1 ? T - 1 : n < 1 - T ? 1 - T : n;
+    for (int64_t i = n - 1; i <= n + 1; ++i) {
+        const int64_t y = x + i * step;
+        if (i > -T && i < T && y > -128 && y < 128) return true;
+    }
+    return false;
+}
+
+// Whether two of T tokens' rows share memory (token strides of 128 and more where T > 1, head
+// strides where heads > 1).
+bool rows_overlap(const HeadRows &a, int64_t T) {
+    if (T < 2 || a.heads < 2 || a.ts >= (a.heads - 1) * a.hs + 128 || a.hs >= (T - 1) * a.ts + 128)
+        return false;
+    for (int64_t h = 1; h < a.heads; ++h)
+        if (near_zero(h * a.hs, a.ts, T)) return true;
+    return false;
+}
+
+// Whether rows of a and rows of b share memory. Where their memory interleaves, rows are told apart
+// only with the same token stride, and with the same head stride or few heads.
+bool rows_meet(HeadRows a, HeadRows b, int64_t T) {
+    if (a.heads == 0 || b.heads == 0) return false;
+    if (T < 2) a.ts = b.ts = 0;
+    if (a.heads < 2) a.hs = b.heads < 2 ? 0 : b.hs;
+    if (b.heads < 2) b.hs = a.hs;
+    const int64_t d = (static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.p)) -
+                       static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.p))) / 2;
+    const int64_t wide_a = (a.heads - 1) * a.hs + 128, wide_b = (b.heads - 1) * b.hs + 128;
+    if (d >= wide_a + (T - 1) * a.ts || -d >= wide_b + (T - 1) * b.ts) return false;
+    if (a.ts != b.ts) return true;
+    if (a.ts > 0) {                  // (a token's heads beside one another, as in one projection's rows)
+        const int64_t r = (d % a.ts + a.ts) % a.ts;
+        if (r >= wide_a && r + wide_b <= a.ts) return false;
+    }
+    if (a.hs == b.hs) {
+        for (int64_t j = 1 - a.heads; j < b.heads; ++j)
+            if (near_zero(d + j * a.hs, a.ts, T)) return true;
+        return false;
+    }
+    if (a.heads * b.heads > 65536) return true;
+    for (int64_t i = 0; i < a.heads; ++i)
+        for (int64_t j = 0; j < b.heads; ++j)
+            if (near_zero(d + j * b.hs - i * a.hs, a.ts, T)) return true;
+    return false;
+}
+
 // Validates the gate's arguments and fills its problem.
 w8a8_status check_gate(const void *logits, w8a8_dtype logits_dtype, int64_t ld, int64_t T,
                        int64_t E, int64_t k, w8a8_gate_score score, const float *bias,
@@ -837,7 +892,10 @@ w8a8_status w8a8_paged_kv_append(
                             v_token_stride, v_head_stride, out_token_stride, out_head_stride})
         if (s < 0 || s % 8 != 0 || s > kMaxElems) return W8A8_ERR_INVALID_ARG;
     // (queries that share a row to be written to)
-    if ((T > 1 && Hq > 0 && out_token_stride < head_dim) || (Hq > 1 && out_head_stride < head_dim))
+    const HeadRows q{q_bf16, q_token_stride, q_head_stride, Hq};
+    const HeadRows out{q_out, out_token_stride, out_head_stride, Hq};
+    if ((T > 1 && Hq > 0 && out_token_stride < head_dim) ||
+        (Hq > 1 && out_head_stride < head_dim) || rows_overlap(out, T))
         return W8A8_ERR_INVALID_ARG;
     if ((k_scale == nullptr) != (v_scale == nullptr)) return W8A8_ERR_INVALID_ARG;
     if (T == 0) return W8A8_OK;
@@ -846,6 +904,12 @@ w8a8_status w8a8_paged_kv_append(
         !aligned(k_bf16, 16) || !aligned(v_bf16, 16) || !aligned(k_cache, 16) ||
         !aligned(v_cache, 16) || !aligned(positions, 4) || !aligned(slots, 4) ||
         !aligned(inv_freq, 4) || !aligned(k_scale, 4) || !aligned(v_scale, 4))
+        return W8A8_ERR_INVALID_ARG;
+    // (rows to be written to that other CTAs read)
+    const bool in_place = q.p == out.p && (T < 2 || q.ts == out.ts) && (Hq < 2 || q.hs == out.hs);
+    if ((!in_place && rows_meet(out, q, T)) ||
+        rows_meet(out, {k_bf16, k_token_stride, k_head_stride, Hkv}, T) ||
+        rows_meet(out, {v_bf16, v_token_stride, v_head_stride, Hkv}, T))
         return W8A8_ERR_INVALID_ARG;
     w8a8::DeviceInfo info;
     w8a8_status st = check_device(&info);

@@ -225,3 +225,21 @@ def test_refusals():
     refused(k=k[:, :1], v=v[:, :1])
     refused(amplitude=float("nan"))
     refused(k_scale=None)
+
+
+@pytest.mark.parametrize("T", [1, 3, 600])
+def test_outputs_beside_or_refused(T):
+    q, k, v, slots, pos, cache = make(T, 6, 2, 16, True, 9000)
+    f = freqs(128)
+    want = w8.paged_kv_append(q, k, v, pos, slots, f, **cache)
+    rows = torch.zeros(T, 16, D, dtype=torch.bfloat16, device=DEV)     # q k v and room for q_out
+    rows[:, :6], rows[:, 6:8], rows[:, 8:10] = q, k, v
+    parts = dict(q=rows[:, :6], k=rows[:, 6:8], v=rows[:, 8:10], positions=pos, slots=slots,
+                 inv_freq=f, **cache)
+    before = rows.clone()
+    got = w8.paged_kv_append(**parts, q_out=rows[:, 10:])
+    assert torch.equal(got, want) and torch.equal(rows[:, :10], before[:, :10])
+    for out in (rows[:, 1:7], rows[:, 9:15], rows.view(-1)[64:64 + T * 768].view(T, 6, D)):
+        with pytest.raises(w8.W8A8Error):
+            w8.paged_kv_append(**parts, q_out=out)
+    assert torch.equal(rows[:, :10], before[:, :10])

@@ -56,6 +56,72 @@ def test_append_outputs_apart(lib):
         assert call(f, APPEND, APPEND_OK, **good) == OK, good
 
 
+# A projection's rows: 64 query, 8 key and 8 value heads of 128 side by side, in bytes from A.
+QKV = dict(APPEND_OK, T=3, qt=10240, kt=10240, vt=10240, ot=10240, k=A + 64 * 256, v=A + 72 * 256)
+AWAY = A + (1 << 24)
+
+
+def written_rows_are_refused(lib, **change):
+    """Whether the call is refused for its operands; without a GPU, one that is not is for that."""
+    return call(lib.w8a8_paged_kv_append, APPEND, QKV, **change) == INVALID
+
+
+def brute_force(T, a, b, same):
+    """Whether two rows of 128 share memory; a, b: (address, token stride, head stride, heads)."""
+    def rows(x):
+        return [x[0] // 2 + t * x[1] + h * x[2] for t in range(T) for h in range(x[3])]
+    p, q = rows(a), rows(b)
+    return any(abs(x - y) < 128 and not (same and i == j)
+               for i, x in enumerate(p) for j, y in enumerate(q))
+
+
+def test_append_rows_that_share_memory(lib):
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("calls that are not refused would run on addresses that are none")
+    for bad in (dict(out=AWAY, Hq=2, T=2, ot=128, oh=128), dict(out=AWAY, Hq=3, T=2, ot=256, oh=128),
+                dict(out=AWAY, Hq=2, T=4, ot=128, oh=384),          # rows of q_out
+                dict(out=A + 256), dict(out=A - 256), dict(out=A + 240), dict(ot=10368), dict(oh=256),
+                dict(ot=8192), dict(out=A + 10240 * 2), dict(qh=256),   # q_out and q
+                dict(out=A + 70 * 256, Hq=2), dict(q=AWAY, k=A), dict(q=AWAY, v=A + 63 * 256),
+                dict(q=AWAY, k=A + 200 * 256)):                     # q_out and k or v
+        assert written_rows_are_refused(lib, **bad), bad
+    for good in (dict(), dict(T=1), dict(T=1, ot=0), dict(out=AWAY), dict(out=AWAY, ot=8192),
+                 dict(out=AWAY, ot=128, oh=384), dict(out=AWAY, Hq=2, T=4, ot=256, oh=128),
+                 dict(out=AWAY, Hq=2, T=3, ot=128, oh=384), dict(Hq=0, q=None, out=None),
+                 dict(Hq=1, oh=0, qh=128), dict(q=AWAY), dict(q=AWAY, out=A + 3 * 20480 - 16, k=AWAY, v=AWAY)):
+        assert not written_rows_are_refused(lib, **good), good
+
+
+def test_append_rows_against_every_pair(lib):
+    # where strides agree, the answer is that of a comparison of every two rows
+    import random
+
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("calls that are not refused would run on addresses that are none")
+    rng = random.Random(7)
+    seen = set()
+    for _ in range(3000):
+        T, Hq, Hkv = rng.randint(1, 4), rng.randint(1, 4), rng.randint(1, 3)
+        ts, hs = 8 * rng.randint(16, 160), 8 * rng.randint(16, 90)
+        kh = rng.choice([hs, 8 * rng.randint(0, 90)])
+        out = A + 16 * rng.randint(-200, 200)
+        q, k = A + 16 * rng.randint(-500, 500), A + 16 * rng.randint(-500, 500)
+        if rng.random() < 0.2:
+            q = out
+        if rng.random() < 0.5:
+            q = AWAY
+        got = written_rows_are_refused(lib, T=T, Hq=Hq, Hkv=Hkv, q=q, k=k, v=AWAY * 2, out=out, qt=ts,
+                                       kt=ts, vt=ts, ot=ts, qh=hs, oh=hs, kh=kh, vh=kh)
+        o = (out, ts, hs, Hq)
+        want = (brute_force(T, o, o, True) or brute_force(T, o, (q, ts, hs, Hq), q == out)
+                or brute_force(T, o, (k, ts, kh, Hkv), False))
+        assert got == want, (T, Hq, Hkv, ts, hs, kh, out, q, k)
+        seen.add((got, q == out))
+    assert len(seen) == 4
+
+
 LAYER = ("x ldx logits ldt ld T k H I E score bias n_group topk_group renorm scale qu su qd sd ids "
          "w y ydt ws wsb stream").split()
 LAYER_OK = dict(x=A, ldx=1024, logits=A, ldt=1, ld=64, T=0, k=8, H=1024, I=512, E=64, score=0,
