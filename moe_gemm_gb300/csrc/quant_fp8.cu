@@ -97,7 +97,8 @@ quant_act_fp8_kernel(const uint16_t *a, int64_t lda, int units, int G, int chain
     }
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-        const int u = first + i * kPerBlock;
+        // (behind the last unit: that one again, the same values, so that every lane is at every shuffle)
+        const int u = min(first + i * kPerBlock, units - 1);
         uint32_t mx = amax_bits8(v[i]);
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(kFull, mx, o));
@@ -109,7 +110,6 @@ quant_act_fp8_kernel(const uint16_t *a, int64_t lda, int units, int G, int chain
             x[2 * j] = bf16_bits_to_f32(w[j] & 0xFFFFu);
             x[2 * j + 1] = bf16_bits_to_f32(w[j] >> 16);
         }
-        if (u >= units) break;
         reinterpret_cast<uint2 *>(qa)[static_cast<int64_t>(u) * 16 + c] = codes8_fp8(x, s, kPow2);
         if (c == 0) sa[u] = s;
     }

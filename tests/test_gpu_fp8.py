@@ -86,6 +86,22 @@ def test_quant_act_rows_anywhere():
 
 
 @pytest.mark.parametrize("mode", [w8.SCALE_AMAX, w8.SCALE_POW2])
+@pytest.mark.parametrize("M,K", [(4097, 1152), (4095, 1152), (32771, 128), (2341, 1920)])
+def test_quant_act_units_left_over(M, K, mode):
+    # four units per thread, and an odd number of units that ends inside them
+    assert M * (K // 128) % 2 == 1 and M * (K // 128) >= 1 << 15
+    g = torch.Generator(device=DEV).manual_seed(M)
+    a = torch.randn(M, K + 3, generator=g, device=DEV).to(torch.bfloat16)
+    check_act(a[:, 3:], mode)                            # rows at odd addresses
+    check_act(a[:, :K].contiguous(), mode)
+    # nothing behind the last unit
+    qa = torch.full((M + 1, K), 0x11, dtype=torch.uint8, device=DEV)
+    sa = torch.full((M + 1, K // 128), 7.0, device=DEV)
+    w8.quant_act_fp8(a[:, 3:], qa[:M].view(E4M3), sa[:M], scale_mode=mode)
+    assert torch.all(qa[M] == 0x11) and torch.all(sa[M] == 7)
+
+
+@pytest.mark.parametrize("mode", [w8.SCALE_AMAX, w8.SCALE_POW2])
 @pytest.mark.parametrize("N,K", [(1, 128), (128, 128), (200, 384), (515, 1024)])
 def test_quant_weight(N, K, mode):
     w = torch.randn(N, K, device=DEV) * 0.02
