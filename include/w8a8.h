@@ -341,15 +341,17 @@ w8a8_status w8a8_w8a16_grouped_gemm(const void *a_bf16, int64_t lda, const int32
  *   sa = amax / 448 of a token's group (IEEE division), or with W8A8_SCALE_POW2 the
  *   smallest power of two >= amax / 448 (exponent in [-127, 127]);
  *   qa = e4m3(a / sa): the quotient rounded to FP32 (exact for powers of two), then to
- *   e4m3, ties to even.
- * A group of zeros has codes 0 and scale 0 (2^-127). Inputs must be finite. qa 16-byte
- * aligned. M == 0 is a no-op.
+ *   e4m3, ties to even; 448 at most.
+ * A group whose scale is 0 (zeros; 2^-127 as a power of two) has codes 0. Inputs must be
+ * finite. qa 16-byte aligned. M == 0 is a no-op.
  */
 w8a8_status w8a8_quant_act_fp8(const void *a_bf16, int64_t M, int64_t K, int64_t lda, void *qa,
                                float *sa, w8a8_scale_mode mode, w8a8_stream_t stream);
 
 /* Weights: w [N, K] float (16-byte aligned); qw [N, K] codes, sw [ceil(N / 128), K / 128], in
- * the same way over [128, 128] blocks. N <= 8,388,480; N == 0 is a no-op. */
+ * the same way over [128, 128] blocks. N <= 8,388,480; N == 0 is a no-op.
+ * (Only here can amax / 448 be so small that it is rounded to few bits: with a scale of a few
+ * 2^-149 the largest codes stop at 448 * scale, and a block below 225 * 2^-149 has scale 0.) */
 w8a8_status w8a8_quant_weight_fp8(const float *w, int64_t N, int64_t K, w8a8_scale_mode mode,
                                   void *qw, float *sw, w8a8_stream_t stream);
 
@@ -360,8 +362,9 @@ w8a8_status w8a8_quant_weight_fp8(const float *w, int64_t N, int64_t K, w8a8_sca
  * Any scales whose products sa * sw are finite. The products of two e4m3 numbers are
  * exact in FP32; the tensor cores sum a group's in FP32 (128 additions, each off by 2^-23 of
  * its result at most), then the groups are added in K order, acc = fma(P, sa * sw, acc).
- * FP32 outputs are within (2^-16 + (K / 128 + 1) * 2^-24) * T of the exact value, T =
- * sum |sa * sw * qa * qw| (tested).
+ * FP32 outputs are within (2^-16 + (K / 128 + 1) * 2^-24) * T + 2^-149 * U of the exact value,
+ * T = sum |sa * sw * qa * qw|, U = K / 128 + the sum of |qa * qw| over the groups whose
+ * |sa * sw| is below 2^-126 and so rounded to a multiple of 2^-149 (tested).
  * Results do not depend on the other rows of the call. No workspace. qa, qw 16-byte aligned;
  * M * K, N * K and M * N below 2^31. M == 0 is a no-op.
  */

@@ -9,8 +9,8 @@
 // (4.4 TB/s), with powers of two, which are multiplied by their reciprocal, 18.5 (5.4 TB/s); with one
 // unit per thread 29 and 25.
 //
-// 448 is the largest e4m3 number. Of a block of zeros the scale is 0 (power of two:
-// 2^-127) and the codes are 0.
+// 448 is the largest e4m3 number. Of a block of zeros, or below 225 * 2^-149, the scale is 0 (power of
+// two: 2^-127) and the codes are 0.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -27,8 +27,8 @@ constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr float kTop = 448.0f;
 constexpr int kActThreads = 256;
 
-// Two e4m3 codes, the first in the low byte (round to nearest even; no value here passes
-// 448 by half a step).
+// Two e4m3 codes, the first in the low byte (round to nearest even, 448 at most: values are larger only
+// where amax / 448 is a few 2^-149 and was rounded down, 667 at most).
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));

@@ -117,6 +117,70 @@ def test_quant_weight(N, K, mode):
     assert torch.equal(qw.cpu().view(torch.uint8), want)
 
 
+def test_quant_weight_smallest():
+    # scales of a few 2^-149: amax / 448 rounds to 1 of them for 225 to 672, to 2 up to 1120
+    step = 2.0 ** -149
+    k = torch.zeros(256, 384, dtype=torch.int32)
+    k[:128, :128] = torch.arange(128 * 128).view(128, 128) % 668
+    k[:128, 128:256] = torch.arange(128)[None] % 225
+    k[:128, 256:] = torch.arange(128 * 128).view(128, 128) % 226
+    k[128:, :128] = torch.arange(128 * 128).view(128, 128) % 1001
+    k[::3] *= -1
+    w = torch.where(k < 0, (-k) | (-1 << 31), k).to(torch.int32).view(torch.float32)
+    assert torch.equal(w.double(), k.double() * step)
+    qw, sw = w8.quant_weight_fp8(w.to(DEV))
+    s = torch.tensor([[1, 0, 1], [2, 0, 0]]).double()
+    assert torch.equal(sw.double().cpu(), s * step)
+    s = s.repeat_interleave(128, 0).repeat_interleave(128, 1)
+    x = torch.where(s > 0, k / torch.where(s > 0, s, 1.0), 0.0).clamp(-448, 448)
+    assert torch.equal(qw.cpu().view(torch.uint8) & 0x7F, x.abs().float().to(E4M3).view(torch.uint8))
+    assert torch.equal(qw.float().cpu().sign(), x.float().to(E4M3).float().sign())
+    qw, sw = w8.quant_weight_fp8(w.to(DEV), scale_mode=w8.SCALE_POW2)
+    assert torch.all(sw == 2.0 ** -127) and torch.all(qw.float() == 0)
+
+
+@pytest.mark.parametrize("M", [3, 20, 40, 300, 1200])
+def test_smallest_scales(M):
+    """Scale products from 2^-160 to 2^-120. Below 2^-126 they are rounded to multiples of
+    2^-149 (off by 2^-150, times the group's sum of |qa qw|), below 2^-150 to 0; and each addition
+    of a group is off by 2^-150 where its result is below 2^-126. BF16: half a step there, 2^-134."""
+    N, K = 520, 1152
+    g = torch.Generator(device=DEV).manual_seed(M)
+    qa = torch.randint(-8, 9, (M, K), generator=g, device=DEV).float().to(E4M3)
+    qw = torch.randint(-8, 9, (N, K), generator=g, device=DEV).float().to(E4M3)
+
+    def scales(rows):
+        e = torch.randint(-80, -59, (rows, K // 128), generator=g, device=DEV).float()
+        return torch.exp2(e) * (1 + torch.rand(rows, K // 128, generator=g, device=DEV))
+
+    sa, sw = scales(M), scales(-(-N // 128))
+    want, T = exact(qa, sa, qw, sw)
+    f = sa.double()[:, None] * sw.double()[None]                         # [M, blocks, G]
+    small = torch.where(f < 2.0 ** -126, 1.0, 0.0).repeat_interleave(128, 1)[:, :N]
+    U = (torch.einsum("mgk,ngk->mng", qa.double().abs().view(M, -1, 128),
+                      qw.double().abs().view(N, -1, 128)) * small).sum(-1) + K // 128
+    assert 0 < small.mean() < 1
+    lim = (2.0 ** -16 + (K // 128 + 1) * 2.0 ** -24) * T + 2.0 ** -149 * U
+    y = w8.gemm_fp8(qa, sa, qw, sw, out_dtype=torch.float32)
+    assert torch.all((y.double() - want).abs() <= lim)
+    y = w8.gemm_fp8(qa, sa, qw, sw)
+    assert torch.all((y.double() - want).abs() <= lim * (1 + 2.0 ** -8) + 2.0 ** -8 * want.abs() + 2.0 ** -134)
+
+
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_scale_products_that_vanish(M):
+    # products of 2^-160 are 0 and of 1.5 * 2^-149 are 2^-148: a bound relative to T alone would not hold
+    qa = torch.full((M, 128), 448.0, device=DEV).to(E4M3)
+    qw = torch.full((256, 128), 448.0, device=DEV).to(E4M3)
+    sa = torch.full((M, 1), 2.0 ** -80, device=DEV)
+    sw = torch.tensor([[2.0 ** -80], [1.5 * 2.0 ** -69]], device=DEV)
+    y = w8.gemm_fp8(qa, sa, qw, sw, out_dtype=torch.float32).double()
+    want, T = exact(qa, sa, qw, sw)
+    assert torch.all(y[:, :128] == 0) and torch.all(T[:, :128] > 2.0 ** -136)
+    assert torch.all(y[:, 128:] == 128 * 448.0 ** 2 * 2.0 ** -148)
+    assert torch.all((y - want).abs() <= 2.0 ** -16 * T + 2.0 ** -149 * (1 + 128 * 448.0 ** 2))
+
+
 def operands(M, N, K, seed=0, mode=w8.SCALE_AMAX):
     g = torch.Generator(device=DEV).manual_seed(seed)
     a = torch.randn(M, K, generator=g, device=DEV)
