@@ -663,13 +663,15 @@ w8a8_status w8a8_moe_gate(const void *logits, w8a8_dtype logits_dtype, int64_t l
 
 /*
  * A whole mixture-of-experts layer: w8a8_moe_gate, then the FFN of the picked experts,
- * the same numbers as w8a8_moe_gate followed by w8a8_moe_ffn, bit for bit (finite x).
+ * the same numbers as w8a8_moe_gate followed by w8a8_moe_ffn, bit for bit, where x and each
+ * token's h (silu(gate) * up) are finite.
  *   x [T, ldx] BF16, logits [T, ld] and the gate's arguments as for w8a8_moe_gate;
  *   weights, scales and y as for w8a8_moe_ffn; ids, w [T, k] out: the gate's choice.
  * For T <= 32 tokens with T * k <= 512 and T * k * ceil(H / SMs) <= 16384 it is two kernels, the
  * gate and a cooperative one that reads the picked experts' weights once (all its CTAs, one
- * per SM, must be resident: it starts when the device has room for them); everything else
- * runs the kernels of those two calls. H, I, k, E as for w8a8_moe_ffn. T == 0 is a no-op.
+ * per SM, must be resident: it starts when the device has room for them, and a stream that may
+ * use a part of the SMs only is refused with W8A8_ERR_CUDA: there the two calls themselves
+ * are for); everything else runs the kernels of those two calls. H, I, k, E as for w8a8_moe_ffn. T == 0 is a no-op.
  *   workspace: w8a8_moe_layer_workspace_size bytes, 256-byte aligned; scratch, but calls
  *   that may overlap on the GPU must not share one.
  */
