@@ -19,9 +19,9 @@
 // each (128 lanes), 2 and 3 only give up their registers.
 //
 // What bounds it. Up to 32 tokens (gemm_fp8_rows_kernel): HBM (8 tokens x 28672 x 8192, 235 MB:
-// 36.1 us, 6.5 TB/s). Some tens to hundreds: the steps, which take some 400 cycles to hand a
+// 38.0 us, 6.2 TB/s). Some tens to hundreds: the steps, which take some 400 cycles to hand a
 // stage and a buffer on, whatever they hold, so those of narrow slices hold 2 or 4 groups (64 x
-// 8192 x 4096: 11 us). Many tokens (gemm_fp8_pair_kernel):
+// 8192 x 4096: 12.4 us). Many tokens (gemm_fp8_pair_kernel):
 // tensor memory, which the products' sums and the reads of a group's sums share: 4096
 // x 8192 x 8192 take 209 us, 2.63 PFLOP/s; a form that reads an eighth of the sums takes 170,
 // one that reads half of them 183, and adding costs nothing beside reading. Tried
@@ -505,7 +505,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmap_a,
 // rows together (cta_group::2): each holds its 128 tokens and half of the weights, so a
 // group reads and writes 32 KB per SM, and each adds up its own tokens. One thread of the
 // first CTA issues for both; its barriers collect the copies of both and the releases
-// of both CTAs' tensor memory (4096 x 8192 x 8192: 277 us with single CTAs, 209 with pairs).
+// of both CTAs' tensor memory (4096 x 8192 x 8192: 319 us with single CTAs, 209 with pairs).
 constexpr int kPairTokens = 256, kPairRows = 256;
 constexpr int kPairStageBytes = 2 * 128 * 128;
 constexpr int kPairStages = (kSmemBytes - 1024 - kOffStages - kStagedBytes) / kPairStageBytes;
@@ -541,8 +541,8 @@ __device__ __forceinline__ uint32_t in_first(uint32_t saddr) {
 }
 // (Relaxed, and waited for with the CTA's scope: what the barrier guards is tensor memory, whose
 // reads have completed before. A release or an acquire over the cluster would wait for
-// the thread's outstanding loads and drop what L1 holds, twice per group: 277 -> 546 us at
-// 4096 x 8192 x 8192.)
+// the thread's outstanding loads and drop what L1 holds, twice per group: 546 us instead of 226
+// at 4096 x 8192 x 8192.)
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -626,8 +626,8 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
             for (int t = first; t < a.tiles && ok; t += pairs) {
                 const PairTile p = pair_tile(t, a.m_tiles, n_tiles);
                 for (int g = 0; g < a.G; ++g) {
-                    if (!mbar_wait(smem_u32(&s.empty[r.idx]), r.phase ^ 1u, abort_flag, a.err, ROLE_PRODUCER, 10,
- kWaitLimitNs, KID_FP8)) {
+                    if (!mbar_wait(smem_u32(&s.empty[r.idx]), r.phase ^ 1u, abort_flag, a.err,
+                                   ROLE_PRODUCER, 10, kWaitLimitNs, KID_FP8)) {
                         ok = false;
                         break;
                     }
@@ -661,10 +661,10 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
             const uint32_t idesc = idesc_e4m3(kPairTokens, kPairRows);
             for (int t = first; t < a.tiles && ok; t += pairs) {
                 for (int g = 0; g < a.G; ++g) {
-                    ok = mbar_wait(smem_u32(&s.d_empty[d.idx]), d.phase ^ 1u, abort_flag, a.err, ROLE_MMA, 10,
- kWaitLimitNs, KID_FP8) &&
-                         mbar_wait(smem_u32(&s.full[r.idx]), r.phase, abort_flag, a.err, ROLE_MMA, 11,
- kWaitLimitNs, KID_FP8);
+                    ok = mbar_wait(smem_u32(&s.d_empty[d.idx]), d.phase ^ 1u, abort_flag, a.err,
+                                   ROLE_MMA, 10, kWaitLimitNs, KID_FP8) &&
+                         mbar_wait(smem_u32(&s.full[r.idx]), r.phase, abort_flag, a.err, ROLE_MMA,
+                                   11, kWaitLimitNs, KID_FP8);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     tc_fence_after();
@@ -771,17 +771,18 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmap_a,
 // ------------------------------------------------------------------ few tokens
 // The same product for up to 32 tokens, with the operands the other way round: 128 weight rows, a
 // block of scales, are the lanes, kTok tokens the columns. An instruction reads what it needs
-// and no more, a group's sums are kTok columns, and a store of y is 32 neighbours of a row.
-// It does not matter that the tiles leave SMs idle: 100 of them take what HBM gives. Against
-// slices: 1 x 10240 x 8192 24.1 -> 15.6 us (5.4 TB/s), 16 x 1024 x 1024 4.9 -> 3.5, 1 x 4096 x
-// 4096 9.6 -> 6.5, 32 x 16384 x 4096 15.4 -> 13.5, 8 x 28672 x 8192 39.1 -> 36.1; level at 32 x
-// 8192 x 4096. What bounds it: HBM, or with few tiles the steps of one (300 ns each).
+// and no more, a group's sums are kTok columns, and a store of y is 32 neighbours of a row. Against
+// slices: 1 x 10240 x 8192 25.7 -> 16.8 us, 16 x 1024 x 1024 5.1 -> 3.8, 1 x 4096 x 4096 9.6 ->
+// 7.2, 32 x 16384 x 4096 16.5 -> 15.0, 8 x 28672 x 8192 41.7 -> 38.0; level at 32 x 8192 x
+// 4096. What bounds it: HBM from some 100 tiles on (80 take 5.0 TB/s, 112 6.2); with fewer, what an
+// SM takes in, 64 KB of weights a step in 0.55 us (one tile's 2, 8 and 16 steps: 3.8, 7.2 and
+// 11.6 us).
 constexpr int kRowsMaxTokens = 32;
 constexpr int kRowsThreads = 256;
 constexpr int kRowsTmemCols = 256;
 
-// Groups of a step: 4 with 16 tokens (1 x 4096 x 4096: 6.5 us, with 2 8.2, with 1 10.3), 2 with 32,
-// whose stages are larger (32 x 16384 x 4096: 13.7, with 4 15.0).
+// Groups of a step: 4 with 16 tokens (1 x 4096 x 4096: 7.2 us, with 2 8.9), 2 with 32, whose stages are
+// larger (32 x 16384 x 4096: 15.0, with 4 16.2; 32 x 8192 x 4096: 11.0 and 10.5).
 template <int kTok>
 struct RowsShape {
     static constexpr int kPerStep = kTok == 16 ? 4 : 2;
@@ -1085,9 +1086,9 @@ cudaError_t launch_gemm_fp8(const Fp8Problem &p, int num_sms, cudaStream_t strea
         if (!encode(&ta, p.qa, p.K, p.M, tok) || !encode(&tb, p.qw, p.K, p.N, 128))
             return cudaErrorInvalidValue;
         // As many CTAs as have the same number of tiles each: some SMs' second tiles alone do
-        // not take what HBM gives (against a CTA on every SM: 8 x 28672 x 8192, 112 CTAs, 36.1 / 38.2
-        // us; 1 x 20480 x 4096, 80, 15.5 / 18.2; 32 x 40000 x 4096, 105, 29.2 / 32.7; 8 x 65536 x 2048,
-        // 128, 22.2 / 22.0).
+        // not take what HBM gives (against a CTA on every SM: 8 x 28672 x 8192, 112 CTAs, 38.0 / 40.7
+        // us; 1 x 20480 x 4096, 80, 16.5 / 19.2; 32 x 40000 x 4096, 105, 30.9 / 35.3; 8 x 65536 x 2048,
+        // 128, 24.0 / 24.2).
         const int waves = (a.tiles + num_sms - 1) / num_sms;
         const int grid = (a.tiles + waves - 1) / waves;
         return tok == 16
@@ -1095,9 +1096,9 @@ cudaError_t launch_gemm_fp8(const Fp8Problem &p, int num_sms, cudaStream_t strea
                    : launch_as<gemm_fp8_rows_kernel<32>, kRowsThreads>(ta, tb, a, grid, stream);
     }
     // Pairs of CTAs, where their waves of tiles take less: a tile of theirs takes as long as one of
-    // w = 164 (single CTAs / pairs: 512 x 4096 x 4096, w = 112, 15.4 / 18.4 us; 8192 x 256 x
-    // 2048, w = 128, 9.6 / 11.6; 777 x 4200 x 2048, w = 208, 18.4 / 15.3; 8192 x 512 x 2048, w =
-    // 256, 15.1 / 12.3; 4096 x 8192 x 8192 277 / 209).
+    // w = 164 (single CTAs / pairs: 512 x 4096 x 4096, w = 112, 15.8 / 18.5 us; 8192 x 256 x
+    // 2048, w = 128, 9.9 / 11.6; 777 x 4200 x 2048, w = 208, 19.1 / 15.2; 8192 x 512 x 2048, w =
+    // 256, 16.0 / 12.5; 4096 x 8192 x 8192 319 / 209).
     const int64_t m2 = (a.M + kPairTokens - 1) / kPairTokens, n2 = (a.N + kPairRows - 1) / kPairRows;
     const int64_t pairs = num_sms / 2;
     if ((m2 * n2 + pairs - 1) / pairs * (164 + 16) < best && m2 * n2 <= INT32_MAX - 4096) {

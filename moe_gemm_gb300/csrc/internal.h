@@ -240,7 +240,7 @@ constexpr int kMaxExperts = 1024;
 // The experts of a few tokens in one kernel (moe_layer.cu), after the gate, whose
 // launch makes moe_few_tokens() as well: the tokens' codes and scales, and zeros.
 // (8 of 64 experts, H 4096, I 1536, this kernel / the six of moe_ffn, with the gate: 1 token 45 / 77
-// us, 16 tokens 213 / 299, 32 tokens 301 / 311; 8 of 256, H 2048, I 640: 19 / 37, 91 / 127, 132 /
+// us, 16 tokens 221 / 299, 32 tokens 302 / 311; 8 of 256, H 2048, I 640: 19 / 37, 92 / 127, 134 /
 // 179. Experts with more than 32 tokens would need tiles that its registers do not hold.)
 constexpr int64_t kMoeFewMaxTokens = 32;
 constexpr int64_t kMoeFewMaxPairs = 512;

@@ -26,10 +26,12 @@
 // exact integer either way. K is permuted alike on both sides, so that a lane has 32
 // consecutive codes of its rows, and of its token's codes.
 //
-// What bounds it. 16 tokens, 8 of 64 experts (H 4096, I 1536, 1.1 GB): 212 us with the gate, 5.2
-// TB/s; 24 tokens of 256 experts (H 2048, I 640, 554 MB): 98 us, 5.6 TB/s; there the SMs that
-// end their stretch last, 10 % after the mean, and L1's throughput (67 % of its peak: copies,
-// tiles and tokens pass it). One token (156 MB): 45 us, 3.4 TB/s: the streams take 28, the
+// What bounds it. 16 tokens, 8 of 64 experts (H 4096, I 1536, 1.1 GB): 221 us with the gate, 5.0
+// TB/s; 24 tokens of 256 experts (H 2048, I 640, 554 MB): 100 us, 5.6 TB/s; there the SMs that
+// end their stretch last, 10 % after the mean (L1 at 52 % of its peak, issue slots 36 %). 32 tokens of
+// 64 experts (1.2 GB): 302 us, 4.1 TB/s: most experts have three tokens and more, whose steps ask for
+// the tokens' codes and use them at once (L1 35 %, issue slots 28 %: latency). One token (156 MB):
+// 45 us, 3.4 TB/s: the streams take 28, the
 // rest are the gate and two launches (4), the routes and the first loads (3), two waits of the
 // grid with h's codes between them (6) and the ends of the streams. Measured on the way (16 tokens):
 // operands widened to fp16, as moe_ffn has them, 246 us; dp4a for up to 8 tokens 435; even
