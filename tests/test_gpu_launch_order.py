@@ -144,3 +144,16 @@ def test_experts_weights():
     ws = torch.empty(w8.moe_ffn_workspace_size(12, 1, 512, 128, 1), dtype=torch.uint8, device=DEV)
     check(up, lambda q, out: w8.moe_ffn(x, ids, w, q, s_up, down, s_down, out=out, workspace=ws))
     check(down, lambda q, out: w8.moe_ffn(x, ids, w, up, s_up, q, s_down, out=out, workspace=ws))
+
+
+def test_int8_offsets():
+    # (where the experts' rows end; the rest of the 4096 bytes is not read)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    a = torch.randn(40, 256, generator=g, device=DEV).to(torch.bfloat16)
+    qw = torch.randint(-127, 128, (4, 128, 256), generator=g, device=DEV).to(torch.int8)
+    sw = torch.full((4, 128, 2), 0.01, device=DEV)
+    ends = torch.zeros(1024, dtype=torch.int32, device=DEV)
+    ends[:5] = torch.tensor([0, 7, 7, 23, 40], device=DEV)
+    ws = torch.empty(w8.grouped_linear_workspace_size(40, 4, 128, 256), dtype=torch.uint8, device=DEV)
+    check(ends, lambda o, out: w8.grouped_linear(a, o[:5], qw, sw, out=out, workspace=ws))
+    check(ends, lambda o, out: w8.w8a16_grouped_gemm(a, o[:5], qw, sw, out=out))
